@@ -31,6 +31,12 @@ Conveniences that allocate the outputs:
     prologue(q_raw, k_raw, v_raw, g_raw, b_raw, w_q, w_k, w_v, state=None) -> dict
     chunk_fwd_prologue(q_raw, k_raw, v_raw, g_raw, b_raw, w_q, w_k, w_v, state=None, S0=None)
         -> (o, S_T, state)
+Latent attention, for the attention layers between such mixers (latent.py):
+    latent_fwd(q, kv, k_rope, lens=None, scale=None) -> (o, lse)
+    latent_bwd(q, kv, k_rope, o, lse, d_o, lens=None, scale=None) -> dict of dq, dkv, dk_rope
+    latent_step(q, cache, table, lens, scale) -> o
+    latent_steps(q, draft, tree, cache, table, lens, scale) -> o
+    and the C ABI's own gdn_latent_fwd, _bwd, _step, _steps with their workspace queries
 """
 from __future__ import annotations
 
@@ -50,8 +56,10 @@ SYMBOLS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_ws",
            "gdn_chunk_fwd_noalloc", "gdn_recurrent_step", "gdn_recurrent_steps",
            "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd", "gdn_prologue",
            "gdn_recurrent_step_prologue", "gdn_chunk_fwd_decoupled",
-           "gdn_recurrent_step_decoupled", "gdn_chunk_fwd_prologue", "gdn_status_str",
-           "gdn_abi_version")
+           "gdn_recurrent_step_decoupled", "gdn_chunk_fwd_prologue",
+           "gdn_latent_fwd_workspace_size", "gdn_latent_fwd", "gdn_latent_bwd_workspace_size",
+           "gdn_latent_bwd", "gdn_latent_steps_workspace_size", "gdn_latent_step",
+           "gdn_latent_steps", "gdn_status_str", "gdn_abi_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -114,6 +122,20 @@ def lib() -> ctypes.CDLL:
         L.gdn_chunk_fwd_prologue.argtypes = [vp, vp, vp, fp, fp, fp, fp, fp, vp, vp, vp, vp, vp,
                                              vp, fp, vp, fp, i, i, i, i, i, i, f, i, i, i, vp]
         L.gdn_chunk_fwd_prologue.restype = i
+        L.gdn_latent_fwd_workspace_size.argtypes = [i] * 8 + [ctypes.POINTER(sz)]
+        L.gdn_latent_fwd_workspace_size.restype = i
+        L.gdn_latent_fwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, sz] + [i] * 7 + [f, i, vp]
+        L.gdn_latent_fwd.restype = i
+        L.gdn_latent_bwd_workspace_size.argtypes = [i] * 8 + [ctypes.POINTER(sz)]
+        L.gdn_latent_bwd_workspace_size.restype = i
+        L.gdn_latent_bwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, sz] + [i] * 7 + [f, i, vp]
+        L.gdn_latent_bwd.restype = i
+        L.gdn_latent_steps_workspace_size.argtypes = [i] * 6 + [ctypes.POINTER(sz)]
+        L.gdn_latent_steps_workspace_size.restype = i
+        L.gdn_latent_step.argtypes = [vp, vp, vp, vp, vp, fp, vp, sz] + [i] * 7 + [f, i, vp]
+        L.gdn_latent_step.restype = i
+        L.gdn_latent_steps.argtypes = [vp, vp, vp, vp, vp, vp, vp, fp, vp, sz] + [i] * 8 + [f, i, vp]
+        L.gdn_latent_steps.restype = i
         L.gdn_status_str.argtypes = [i]
         L.gdn_status_str.restype = ctypes.c_char_p
         L.gdn_abi_version.argtypes = []
@@ -627,3 +649,9 @@ def gdn_recurrent_step_prologue(q_raw, k_raw, v_raw, g_raw, b_raw, w_q, w_k, w_v
         _dtype_code(q_raw), gate, _stream(stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_recurrent_step_prologue")
+
+
+from .latent import (  # noqa: E402  (needs the names above)
+    gdn_latent_bwd, gdn_latent_bwd_workspace_size, gdn_latent_fwd, gdn_latent_fwd_workspace_size,
+    gdn_latent_step, gdn_latent_steps, gdn_latent_steps_workspace_size, latent_bwd, latent_fwd,
+    latent_step, latent_steps)

@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libgdn.so")
 OBJ_DIR = os.path.join(os.path.dirname(HERE), "_build", "obj")
 SOURCES = ["gdn_api.cpp", "recurrent_step.hip", "chunk_fwd.hip", "chunk_fwd_ws.hip", "chunk_fwd_seg.hip",
            "chunk_fwd_wsc.hip", "recurrent_multi.hip", "chunk_bwd.hip",
-           "prologue.hip"]
+           "prologue.hip", "latent_api.cpp", "latent_fwd.hip", "latent_bwd.hip", "latent_step.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

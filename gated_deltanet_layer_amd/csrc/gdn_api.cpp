@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/gdn.h"
+#include "api_checks.h"
 #include "chunk_bwd.h"
 #include "prologue.h"
 
@@ -39,35 +40,9 @@ hipError_t recurrent_multi_launch(bool bf16, bool channel, int K, int V, const v
 
 namespace {
 
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) == 0; }
-bool aligned16(const void *p) { return aligned(p, 16); }
-
-Range range(const void *p, unsigned long long bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + (uintptr_t)bytes};
-}
-
-bool overlap(Range a, Range b) {
-    if (a.lo == a.hi || b.lo == b.hi) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
+using namespace gdn_checks;
 
 bool kv_supported(int x) { return x == 64 || x == 128; }
-
-// n = a * b * c * d without overflow past 2^62, or -1.
-long long prod(long long a, long long b, long long c = 1, long long d = 1) {
-    const long long lim = 1LL << 62;
-    long long n = a;
-    for (long long f : {b, c, d}) {
-        if (f != 0 && n > lim / f) return -1;
-        n *= f;
-    }
-    return n;
-}
 
 // The chunk kernels address a chunk's rows with 32-bit per-lane offsets from a
 // wave-uniform base: 64 rows of H * max(K, V) elements of at most 4 bytes must

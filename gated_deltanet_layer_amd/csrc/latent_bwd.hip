@@ -1,0 +1,394 @@
+// latent_bwd.hip -- gradients of the expanded latent attention (gfx950).
+//
+//   P_ij = exp(s_ij - lse_i),  D_i = do_i . o_i,  dS_ij = scale P_ij (do_i . v_j - D_i)
+//   dv_j = sum_i P_ij do_i,  dk_j = sum_i dS_ij q_i,  dq_i = sum_j dS_ij k_j
+//   dk_rope_j = sum over heads of the rotary part of dk_j
+//
+// No atomics, so results do not depend on the order in which workgroups run:
+// one kernel owns key rows and walks the query rows that see them (dk, dv), one
+// owns query rows and walks their keys (dq); the scores are computed in both.
+// The rotary part of dk is written per head in fp32 and added over the heads in
+// order by a last kernel.
+#include "latent.h"
+
+namespace gdn {
+
+struct BwdWs {
+    long rope, bytes;   // float D[B][Tq][H] first, then float dk_rope[B][Tk][H][64]
+    __host__ __device__ BwdWs(int B, int Tq, int Tk, int H) {
+        rope = ((long)B * Tq * H * 4 + 255) & ~255L;
+        bytes = rope + (long)B * Tk * H * LATENT_ROPE * 4;
+    }
+};
+
+// D_i = do_i . o_i, one wave 64 / (DV / 8) rows at a time.
+template <typename T, int DV>
+__global__ __launch_bounds__(256) void latent_bwd_dot_kernel(const T *o, const T *d_o, float *D, long nrows)
+{
+    constexpr int LPR = DV / 8;   // lanes a row, 8 values each
+    const long row = ((long)blockIdx.x * 256 + threadIdx.x) / LPR;
+    const int at = (threadIdx.x % LPR) * 8;
+    float s = 0.f;
+    if (row < nrows) {
+        const Frag<T> x = load_frag<T>(o + row * DV + at), y = load_frag<T>(d_o + row * DV + at);
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += (float)x.v[e] * (float)y.v[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s += x.lo[e] * y.lo[e] + x.hi[e] * y.hi[e];
+        }
+    }
+#pragma unroll
+    for (int d = LPR / 2; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
+    if (row < nrows && at == 0) D[row] = s;
+}
+
+// dk_rope[b][t] = sum over heads, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void latent_bwd_rope_kernel(const float *part, T *dk_rope, long nrows, int H)
+{
+    const long row = (long)blockIdx.x * 16 + threadIdx.x / 16;
+    const int at = (threadIdx.x & 15) * 4;
+    if (row >= nrows) return;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < H; ++h)
+        s += *reinterpret_cast<const f32x4 *>(part + (row * H + h) * LATENT_ROPE + at);
+    store4(dk_rope + row * LATENT_ROPE + at, s);
+}
+
+template <typename T, int DN, int DV> struct BwdCfg {
+    static constexpr int NG = sizeof(T) == 2 ? 2 : 1;      // 16-row groups a wave owns
+    static constexpr int OWN = 64 * NG;                    // rows a workgroup owns (keys or queries)
+    static constexpr int ST = sizeof(T) == 2 ? 64 : 32;    // rows a tile that walks by
+    static constexpr int DK = DN + LATENT_ROPE;
+    static constexpr int KCPR = DK * (int)sizeof(T) / 16, VCPR = DV * (int)sizeof(T) / 16;
+    static constexpr int KBYTES = ST * KCPR * 16, VBYTES = ST * VCPR * 16;
+    static constexpr int BUF = KBYTES + VBYTES;            // [ST][DK] and [ST][DV]
+    static constexpr int ROWS = 2 * ST * 4;                // lse and D of the tile's rows
+};
+
+// Copies rows r0 .. r0 + ST - 1 of a [.., DK] and a [.., DV] matrix; rows from n
+// on read as zeros.  Columns of the first from DN on come from `rope` if given.
+template <typename T, int DN, int DV, typename C>
+__device__ __forceinline__ void bwd_load_tile(char *buf, const T *x, long xs, const T *rope, const T *y,
+                                              long ys, int r0, int n)
+{
+    const int tid = threadIdx.x, wbase = (tid & ~63) * 16;
+    constexpr int EPC = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < C::ST * C::KCPR / 256; ++i) {
+        const int slot = i * 256 + tid, row = slot / C::KCPR, ch = (slot % C::KCPR) ^ (row & 7);
+        const int r = r0 + row, col = ch * EPC;
+        const void *src = !rope || col < DN ? (const void *)(x + r * xs + col)
+                                            : (const void *)(rope + (long)r * LATENT_ROPE + (col - DN));
+        if (r >= n) src = &latent_zero;
+        g2lds16(src, buf + i * 4096 + wbase);
+    }
+#pragma unroll
+    for (int i = 0; i < C::ST * C::VCPR / 256; ++i) {
+        const int slot = i * 256 + tid, row = slot / C::VCPR, ch = (slot % C::VCPR) ^ (row & 7);
+        const int r = r0 + row;
+        const void *src = r < n ? (const void *)(y + r * ys + ch * EPC) : (const void *)&latent_zero;
+        g2lds16(src, buf + C::KBYTES + i * 4096 + wbase);
+    }
+}
+
+// dk and dv.  A wave owns 16 NG keys: k and v of them stay in registers as B
+// operands, dk^T and dv^T as accumulators.  Scores have query rows on the
+// accumulator's rows, so P and dS feed the gradient products as B operands
+// straight from the registers; q and do come from LDS, along the rows for the
+// scores and across them for the gradients.
+template <typename T, int DN, int DV>
+__global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, int ntiles)
+{
+    typedef BwdCfg<T, DN, DV> C;
+    constexpr int NG = C::NG, ST = C::ST, DK = C::DK, NKB = DK / 32, NVB = DV / 32, NKC = DK / 16, NVC = DV / 16;
+    extern __shared__ char lds[];
+    const int BH = a.B * a.H;
+    const int bh = blockIdx.x % BH, tile = blockIdx.x / BH;   // the first keys are seen by most rows
+    const int b = bh / a.H, h = bh % a.H;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int off = a.Tk - a.Tq, n = live_len(a.lens, b, a.Tk);
+    const int k0 = tile * C::OWN, w0 = k0 + wave * 16 * NG;
+    const long qs = (long)a.H * DK, kvs = (long)a.H * (DN + DV), os = (long)a.H * DV;
+    const T *q = (const T *)a.q + ((long)b * a.Tq * a.H + h) * DK;
+    const T *d_o = (const T *)a.d_o + ((long)b * a.Tq * a.H + h) * DV;
+    const T *kv = (const T *)a.kv + ((long)b * a.Tk * a.H + h) * (DN + DV);
+    const T *kr = (const T *)a.k_rope + (long)b * a.Tk * LATENT_ROPE;
+    const float *lse = a.lse + (long)b * a.Tq * a.H + h, *Dw = (const float *)a.ws + (long)b * a.Tq * a.H + h;
+    const float c = a.scale * LOG2E;
+    float *stat = (float *)(lds + 2 * C::BUF);   // [2][2][ST]
+
+    Frag<T> kf[NG][NKB], vf[NG][NVB];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int key = w0 + 16 * g + r16;
+        const bool live = key < n;
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+            const int col = 32 * kb + 8 * gq;
+            const T *p = 32 * kb < DN ? kv + key * kvs + col : kr + (long)key * LATENT_ROPE + (col - DN);
+            kf[g][kb] = live ? load_frag<T>(p) : zero_frag<T>();
+        }
+#pragma unroll
+        for (int vb = 0; vb < NVB; ++vb)
+            vf[g][vb] = live ? load_frag<T>(kv + key * kvs + DN + 32 * vb + 8 * gq) : zero_frag<T>();
+    }
+    f32x4 dk[NKC][NG], dv[NVC][NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int i = 0; i < NKC; ++i) dk[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NVC; ++i) dv[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // query rows that are no padding and see the workgroup's first key
+    const int qn = min(a.Tq, n - off), qfirst = max(0, k0 - off) / ST * ST;
+    const int nt = k0 < n && qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0;
+    auto load = [&](int j) {
+        const int r0 = qfirst + j * ST, buf = j & 1;
+        bwd_load_tile<T, DK, DV, C>(lds + buf * C::BUF, q, qs, (const T *)nullptr, d_o, os, r0, qn);
+        if (wave < 2 && (threadIdx.x & 63) < ST) {   // lse by the first wave, D by the second
+            const int r = r0 + (threadIdx.x & 63);
+            const void *src = r >= qn ? (const void *)&latent_zero : (wave ? Dw : lse) + (long)r * a.H;
+            g2lds4(src, (char *)(stat + (buf * 2 + wave) * ST));
+        }
+    };
+    if (nt > 0) load(0);
+    for (int j = 0; j < nt; ++j) {
+        const char *qt = lds + (j & 1) * C::BUF, *dt = qt + C::KBYTES;
+        const float *st = stat + (j & 1) * 2 * ST;
+        const int r0 = qfirst + j * ST;
+        wait_vm<0>();
+        lds_barrier();
+        if (j + 1 < nt) load(j + 1);
+        if (off + r0 + ST - 1 < w0 || w0 >= n) continue;   // no row of the tile sees a key of this wave
+        const bool part = off + r0 < w0 + 16 * NG - 1 || r0 + ST > qn;
+#pragma unroll
+        for (int t = 0; t < ST / 32; ++t) {
+            f32x4 s[2][NG], dp[2][NG];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    dp[u][g] = s[u][g];
+                }
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) {
+                    const Frag<T> f = row_frag<T, C::KCPR>(qt, 32 * t + 16 * u, kb);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, kf[g][kb]);
+                }
+#pragma unroll
+                for (int vb = 0; vb < NVB; ++vb) {
+                    const Frag<T> f = row_frag<T, C::VCPR>(dt, 32 * t + 16 * u, vb);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, vf[g][vb]);
+                }
+                const int row = 32 * t + 16 * u + 4 * gq;
+                const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + row), dd = *reinterpret_cast<const f32x4 *>(st + ST + row);
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float p = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e] * LOG2E));
+                        if (part && (off + r0 + row + e < w0 + 16 * g + r16 || r0 + row + e >= qn)) p = 0.f;
+                        s[u][g][e] = p;
+                        dp[u][g][e] = p * (dp[u][g][e] - dd[e]);
+                    }
+            }
+            // P and dS rounded to the storage type for the matrix cores (half a
+            // step each, as the gradients themselves); scale is applied at the end
+            Frag<T> pf[NG], sf[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                pf[g] = reg_frag<T>(s[0][g], s[1][g]);
+                sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+            }
+            const int ra = 32 * t + 4 * gq, rb = ra + 16;
+#pragma unroll
+            for (int i = 0; i < NVC; ++i) {
+                const Frag<T> f = col_frag<T, C::VCPR>(dt, ra, rb, i);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dv[i][g] = mma(dv[i][g], f, pf[g]);
+            }
+#pragma unroll
+            for (int i = 0; i < NKC; ++i) {
+                const Frag<T> f = col_frag<T, C::KCPR>(qt, ra, rb, i);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dk[i][g] = mma(dk[i][g], f, sf[g]);
+            }
+        }
+    }
+    T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV);
+    float *rope = (float *)((char *)a.ws + BwdWs(a.B, a.Tq, a.Tk, a.H).rope);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int key = w0 + 16 * g + r16;
+        if (key >= a.Tk) continue;
+#pragma unroll
+        for (int i = 0; i < NKC; ++i) {
+            const f32x4 v = dk[i][g] * a.scale;
+            if (16 * i < DN) store4(dkv + key * kvs + 16 * i + 4 * gq, v);
+            else store4(rope + (((long)b * a.Tk + key) * a.H + h) * LATENT_ROPE + (16 * i - DN) + 4 * gq, v);
+        }
+#pragma unroll
+        for (int i = 0; i < NVC; ++i) store4(dkv + key * kvs + DN + 16 * i + 4 * gq, dv[i][g]);
+    }
+}
+
+// dq.  A wave owns 16 NG query rows, q and do of them in registers; scores are
+// transposed as in the forward pass, and dS^T feeds dq^T = K^T dS^T from the
+// registers.
+template <typename T, int DN, int DV>
+__global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, int ntiles)
+{
+    typedef BwdCfg<T, DN, DV> C;
+    constexpr int NG = C::NG, ST = C::ST, DK = C::DK, NKB = DK / 32, NVB = DV / 32, NKC = DK / 16;
+    extern __shared__ char lds[];
+    const int BH = a.B * a.H;
+    const int bh = blockIdx.x % BH, tile = ntiles - 1 - (int)(blockIdx.x / BH);
+    const int b = bh / a.H, h = bh % a.H;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int off = a.Tk - a.Tq, n = live_len(a.lens, b, a.Tk);
+    const int q0 = tile * C::OWN, w0 = q0 + wave * 16 * NG;
+    const long qs = (long)a.H * DK, kvs = (long)a.H * (DN + DV), os = (long)a.H * DV;
+    const T *q = (const T *)a.q + ((long)b * a.Tq * a.H + h) * DK;
+    const T *d_o = (const T *)a.d_o + ((long)b * a.Tq * a.H + h) * DV;
+    const T *kv = (const T *)a.kv + ((long)b * a.Tk * a.H + h) * (DN + DV);
+    const T *kr = (const T *)a.k_rope + (long)b * a.Tk * LATENT_ROPE;
+    const float *lse = a.lse + (long)b * a.Tq * a.H + h, *Dw = (const float *)a.ws + (long)b * a.Tq * a.H + h;
+    const float c = a.scale * LOG2E;
+
+    int pos[NG];
+    float ls[NG], dd[NG];
+    Frag<T> qf[NG][NKB], of[NG][NVB];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int row = w0 + 16 * g + r16;
+        const bool live = row < a.Tq && off + row < n;
+        pos[g] = live ? off + row : -1;
+        ls[g] = live ? lse[(long)row * a.H] * LOG2E : 0.f;
+        dd[g] = live ? Dw[(long)row * a.H] : 0.f;
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb)
+            qf[g][kb] = live ? load_frag<T>(q + row * qs + 32 * kb + 8 * gq) : zero_frag<T>();
+#pragma unroll
+        for (int vb = 0; vb < NVB; ++vb)
+            of[g][vb] = live ? load_frag<T>(d_o + row * os + 32 * vb + 8 * gq) : zero_frag<T>();
+    }
+    f32x4 dq[NKC][NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < NKC; ++i) dq[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int last = min(n, off + min(q0 + C::OWN, a.Tq));
+    const int nt = (off + q0 < n) ? (last + ST - 1) / ST : 0;
+    const int wlast = min(n, off + min(w0 + 16 * NG, a.Tq)), wfull = off + w0 + 1;
+    if (nt > 0) bwd_load_tile<T, DN, DV, C>(lds, kv, kvs, kr, kv + DN, kvs, 0, n);
+    for (int j = 0; j < nt; ++j) {
+        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::KBYTES;
+        const int k0 = j * ST;
+        wait_vm<0>();
+        lds_barrier();
+        if (j + 1 < nt) bwd_load_tile<T, DN, DV, C>(lds + ((j + 1) & 1) * C::BUF, kv, kvs, kr, kv + DN, kvs, k0 + ST, n);
+        if (k0 >= wlast || off + w0 >= n) continue;
+        const bool part = k0 + ST > wfull || k0 + ST > n;
+#pragma unroll
+        for (int t = 0; t < ST / 32; ++t) {
+            f32x4 s[2][NG], dp[2][NG];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    dp[u][g] = s[u][g];
+                }
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) {
+                    const Frag<T> f = row_frag<T, C::KCPR>(kt, 32 * t + 16 * u, kb);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, qf[g][kb]);
+                }
+#pragma unroll
+                for (int vb = 0; vb < NVB; ++vb) {
+                    const Frag<T> f = row_frag<T, C::VCPR>(vt, 32 * t + 16 * u, vb);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, of[g][vb]);
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float p = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[g]));
+                        if (part && k0 + 32 * t + 16 * u + 4 * gq + e > pos[g]) p = 0.f;
+                        dp[u][g][e] = p * (dp[u][g][e] - dd[g]);
+                    }
+            }
+            Frag<T> sf[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+            const int ra = 32 * t + 4 * gq, rb = ra + 16;
+#pragma unroll
+            for (int i = 0; i < NKC; ++i) {
+                const Frag<T> f = col_frag<T, C::KCPR>(kt, ra, rb, i);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dq[i][g] = mma(dq[i][g], f, sf[g]);
+            }
+        }
+    }
+    T *dqp = (T *)a.dq + ((long)b * a.Tq * a.H + h) * DK;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int row = w0 + 16 * g + r16;
+        if (row >= a.Tq) continue;
+#pragma unroll
+        for (int i = 0; i < NKC; ++i)
+            store4(dqp + row * qs + 16 * i + 4 * gq, pos[g] >= 0 ? dq[i][g] * a.scale : f32x4{0.f, 0.f, 0.f, 0.f});
+    }
+}
+
+template <typename T, int DN, int DV>
+static hipError_t bwd_launch(const LatentBwdArgs &a, hipStream_t st)
+{
+    typedef BwdCfg<T, DN, DV> C;
+    const BwdWs lay(a.B, a.Tq, a.Tk, a.H);
+    const long BH = (long)a.B * a.H, qrows = BH * a.Tq, krows = (long)a.B * a.Tk;
+    const int nq = (a.Tq + C::OWN - 1) / C::OWN, nk = (a.Tk + C::OWN - 1) / C::OWN;
+    auto kkv = latent_bwd_kv_kernel<T, DN, DV>;
+    auto kq = latent_bwd_q_kernel<T, DN, DV>;
+    const int lkv = 2 * C::BUF + 2 * C::ROWS, lq = 2 * C::BUF;
+    hipError_t e = hipFuncSetAttribute((const void *)kkv, hipFuncAttributeMaxDynamicSharedMemorySize, lkv);
+    if (e == hipSuccess) e = hipFuncSetAttribute((const void *)kq, hipFuncAttributeMaxDynamicSharedMemorySize, lq);
+    if (e != hipSuccess) return e;
+    float *D = (float *)a.ws;
+    if (qrows > 0) {
+        hipLaunchKernelGGL((latent_bwd_dot_kernel<T, DV>), dim3((unsigned)((qrows * (DV / 8) + 255) / 256)), dim3(256), 0, st,
+                           (const T *)a.o, (const T *)a.d_o, D, qrows);
+        hipLaunchKernelGGL(kq, dim3((unsigned)(BH * nq)), dim3(256), lq, st, a, nq);
+    }
+    if (krows > 0) {
+        hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk)), dim3(256), lkv, st, a, nk);
+        hipLaunchKernelGGL((latent_bwd_rope_kernel<T>), dim3((unsigned)((krows + 15) / 16)), dim3(256), 0, st,
+                           (const float *)((const char *)a.ws + lay.rope), (T *)a.dk_rope, krows, a.H);
+    }
+    return hipGetLastError();
+}
+
+hipError_t latent_bwd_launch(bool bf16, int dn, int dv, const LatentBwdArgs &a, hipStream_t st)
+{
+    if (bf16) {
+        if (dn == 128) return dv == 128 ? bwd_launch<__bf16, 128, 128>(a, st) : bwd_launch<__bf16, 128, 64>(a, st);
+        return dv == 128 ? bwd_launch<__bf16, 64, 128>(a, st) : bwd_launch<__bf16, 64, 64>(a, st);
+    }
+    if (dn == 128) return dv == 128 ? bwd_launch<float, 128, 128>(a, st) : bwd_launch<float, 128, 64>(a, st);
+    return dv == 128 ? bwd_launch<float, 64, 128>(a, st) : bwd_launch<float, 64, 64>(a, st);
+}
+
+unsigned long long latent_bwd_workspace(int B, int Tq, int Tk, int H) { return (unsigned long long)BwdWs(B, Tq, Tk, H).bytes; }
+
+} // namespace gdn

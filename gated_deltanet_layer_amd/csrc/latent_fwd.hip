@@ -1,0 +1,206 @@
+// latent_fwd.hip -- expanded latent attention, causal forward (gfx950).
+//
+//   s_ij = scale (q_i^nope . k_j^nope + q_i^rope . k_j^rope),  j <= p_i = Tk - Tq + i
+//   o_i = sum_j softmax_j(s_ij) v_j,   lse_i = log sum_j exp s_ij
+//
+// One workgroup of four waves owns RT = 64 NR query rows of one head and walks
+// the key tiles once, keeping the running maximum and sum of every row.  Scores
+// are computed transposed (keys on the accumulator's rows, query rows on its
+// lanes): a lane then holds four consecutive keys of one query row, so the
+// softmax needs two cross-lane steps a tile, and the weights feed the second
+// product (o^T = V^T P^T) as its B operand straight from the registers.
+#include "latent.h"
+
+namespace gdn {
+
+template <typename T, int DN, int DV> struct FwdCfg {
+    static constexpr int NR = sizeof(T) == 2 ? 2 : 1;      // 16-row groups a wave
+    static constexpr int NW = 4;
+    static constexpr int RT = 16 * NR * NW;                // query rows a workgroup
+    static constexpr int KT = sizeof(T) == 2 ? 64 : 32;    // keys a tile
+    static constexpr int DK = DN + LATENT_ROPE;
+    static constexpr int KCPR = DK * (int)sizeof(T) / 16, VCPR = DV * (int)sizeof(T) / 16;
+    static constexpr int KBYTES = KT * KCPR * 16, VBYTES = KT * VCPR * 16;
+    static constexpr int BUF = KBYTES + VBYTES;
+};
+
+// Enqueue the copies of keys k0 .. k0 + KT - 1 into a tile buffer.
+template <typename T, int DN, int DV, typename C>
+__device__ __forceinline__ void fwd_load_tile(char *buf, const T *kv, const T *kr, long kvs, int k0, int n)
+{
+    const int tid = threadIdx.x, wbase = (tid & ~63) * 16;
+    constexpr int EPC = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < C::KT * C::KCPR / 256; ++i) {
+        const int slot = i * 256 + tid, row = slot / C::KCPR, ch = (slot % C::KCPR) ^ (row & 7);
+        const int key = k0 + row, col = ch * EPC;
+        const void *src = col < DN ? (const void *)(kv + key * kvs + col)
+                                   : (const void *)(kr + (long)key * LATENT_ROPE + (col - DN));
+        if (key >= n) src = &latent_zero;
+        g2lds16(src, buf + i * 4096 + wbase);
+    }
+#pragma unroll
+    for (int i = 0; i < C::KT * C::VCPR / 256; ++i) {
+        const int slot = i * 256 + tid, row = slot / C::VCPR, ch = (slot % C::VCPR) ^ (row & 7);
+        const int key = k0 + row;
+        const void *src = key < n ? (const void *)(kv + key * kvs + DN + ch * EPC) : (const void *)&latent_zero;
+        g2lds16(src, buf + C::KBYTES + i * 4096 + wbase);
+    }
+}
+
+template <typename T, int DN, int DV>
+__global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int ntiles)
+{
+    typedef FwdCfg<T, DN, DV> C;
+    constexpr int NR = C::NR, KT = C::KT, DK = C::DK, NKB = DK / 32, NS = KT / 16, NCB = DV / 16;
+    extern __shared__ char lds[];
+    const int BH = a.B * a.H;
+    const int bh = blockIdx.x % BH, tile = ntiles - 1 - (int)(blockIdx.x / BH);   // longest rows first
+    const int b = bh / a.H, h = bh % a.H;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int off = a.Tk - a.Tq, n = live_len(a.lens, b, a.Tk);
+    const int q0 = tile * C::RT, w0 = q0 + wave * 16 * NR;   // first row of the workgroup, of the wave
+    const long qs = (long)a.H * DK, kvs = (long)a.H * (DN + DV), os = (long)a.H * DV;
+    const T *q = (const T *)a.q + ((long)b * a.Tq * a.H + h) * DK;
+    const T *kv = (const T *)a.kv + ((long)b * a.Tk * a.H + h) * (DN + DV);
+    const T *kr = (const T *)a.k_rope + (long)b * a.Tk * LATENT_ROPE;
+    const float c = a.scale * LOG2E;
+
+    int pos[NR];   // position of this lane's rows; -1: the row sees nothing
+    Frag<T> qf[NR][NKB];
+#pragma unroll
+    for (int g = 0; g < NR; ++g) {
+        const int row = w0 + 16 * g + r16;
+        const bool live = row < a.Tq && off + row < n;
+        pos[g] = live ? off + row : -1;
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb)
+            qf[g][kb] = live ? load_frag<T>(q + row * qs + 32 * kb + 8 * gq) : zero_frag<T>();
+    }
+    f32x4 acc[NCB][NR];
+    float m[NR], l[NR];
+#pragma unroll
+    for (int g = 0; g < NR; ++g) {
+        m[g] = -INFINITY;
+        l[g] = 0.f;
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) acc[cb][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // keys that any row of the workgroup, of this wave, may see
+    const int last = min(n, off + min(q0 + C::RT, a.Tq));
+    const int nt = (off + q0 < n) ? (last + KT - 1) / KT : 0;
+    const int wlast = min(n, off + min(w0 + 16 * NR, a.Tq)), wfull = off + w0 + 1;
+    if (nt > 0) fwd_load_tile<T, DN, DV, C>(lds, kv, kr, kvs, 0, n);
+    for (int j = 0; j < nt; ++j) {
+        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::KBYTES;
+        const int k0 = j * KT;
+        wait_vm<0>();
+        lds_barrier();
+        if (j + 1 < nt) fwd_load_tile<T, DN, DV, C>(lds + ((j + 1) & 1) * C::BUF, kv, kr, kvs, k0 + KT, n);
+        if (k0 >= wlast || off + w0 >= n) continue;   // nothing for this wave in the tile
+        f32x4 s[NS][NR];
+#pragma unroll
+        for (int t = 0; t < NS; ++t) {
+#pragma unroll
+            for (int g = 0; g < NR; ++g) s[t][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const Frag<T> kf = row_frag<T, C::KCPR>(kt, 16 * t, kb);
+#pragma unroll
+                for (int g = 0; g < NR; ++g) s[t][g] = mma(s[t][g], kf, qf[g][kb]);
+            }
+        }
+        if (k0 + KT > wfull || k0 + KT > n) {   // the tile reaches past some row's last key
+#pragma unroll
+            for (int t = 0; t < NS; ++t)
+#pragma unroll
+                for (int g = 0; g < NR; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (k0 + 16 * t + 4 * gq + e > pos[g]) s[t][g][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < NS; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][g][e]);
+            mx = rows_max(mx);
+            const bool up = (mx - m[g]) * c > RAISE;   // false while both are -inf
+            if (__any(up)) {
+                const float mn = up ? mx : m[g];
+                const float al = up ? exp2_hw((m[g] - mn) * c) : 1.f;
+                m[g] = mn;
+                l[g] *= al;
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb) acc[cb][g] *= al;
+            }
+            const float mb = m[g] == -INFINITY ? 0.f : m[g] * c;
+#pragma unroll
+            for (int t = 0; t < NS; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p = exp2_hw(__builtin_fmaf(s[t][g][e], c, -mb));
+                    s[t][g][e] = p;
+                    l[g] += p;
+                }
+        }
+        // weights rounded to the storage type for the matrix cores (half a step
+        // each, as the output itself); their sum is the unrounded one
+#pragma unroll
+        for (int t = 0; t < NS; t += 2) {
+            Frag<T> pf[NR];
+#pragma unroll
+            for (int g = 0; g < NR; ++g) pf[g] = reg_frag<T>(s[t][g], s[t + 1][g]);
+#pragma unroll
+            for (int cb = 0; cb < NCB; ++cb) {
+                const Frag<T> vf = col_frag<T, C::VCPR>(vt, 16 * t + 4 * gq, 16 * t + 16 + 4 * gq, cb);
+#pragma unroll
+                for (int g = 0; g < NR; ++g) acc[cb][g] = mma(acc[cb][g], vf, pf[g]);
+            }
+        }
+    }
+    T *o = (T *)a.o + ((long)b * a.Tq * a.H + h) * DV;
+#pragma unroll
+    for (int g = 0; g < NR; ++g) {
+        const int row = w0 + 16 * g + r16;
+        const float ls = rows_sum(l[g]);
+        const bool seen = pos[g] >= 0;
+        const float inv = seen ? 1.f / ls : 0.f;
+        if (row < a.Tq) {
+#pragma unroll
+            for (int cb = 0; cb < NCB; ++cb) store4(o + row * os + 16 * cb + 4 * gq, seen ? acc[cb][g] * inv : f32x4{0.f, 0.f, 0.f, 0.f});
+            if (a.lse && gq == 0)
+                a.lse[((long)b * a.Tq + row) * a.H + h] =
+                    seen ? (m[g] * c + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+        }
+    }
+}
+
+template <typename T, int DN, int DV>
+static hipError_t fwd_launch(const LatentFwdArgs &a, hipStream_t st)
+{
+    typedef FwdCfg<T, DN, DV> C;
+    const int ntiles = (a.Tq + C::RT - 1) / C::RT;
+    auto k = latent_fwd_kernel<T, DN, DV>;
+    const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * C::BUF);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k, dim3((unsigned)((long)ntiles * a.B * a.H)), dim3(256), 2 * C::BUF, st, a, ntiles);
+    return hipGetLastError();
+}
+
+hipError_t latent_fwd_launch(bool bf16, int dn, int dv, const LatentFwdArgs &a, hipStream_t st)
+{
+    if (bf16) {
+        if (dn == 128) return dv == 128 ? fwd_launch<__bf16, 128, 128>(a, st) : fwd_launch<__bf16, 128, 64>(a, st);
+        return dv == 128 ? fwd_launch<__bf16, 64, 128>(a, st) : fwd_launch<__bf16, 64, 64>(a, st);
+    }
+    if (dn == 128) return dv == 128 ? fwd_launch<float, 128, 128>(a, st) : fwd_launch<float, 128, 64>(a, st);
+    return dv == 128 ? fwd_launch<float, 64, 128>(a, st) : fwd_launch<float, 64, 64>(a, st);
+}
+
+unsigned long long latent_fwd_workspace(bool, int, int, int, int, int) { return 0; }
+
+} // namespace gdn

@@ -1,6 +1,7 @@
 /*
  * gdn.h -- C ABI of the MI355X (gfx950) Gated DeltaNet mixer: prologue, forward,
- * decode, verify and backward.
+ * decode, verify and backward; and of the latent attention that a hybrid stack puts
+ * between such layers (gdn_latent_*).
  *
  * The operation (Atomic-GDN2 model card, section 2.1 "Gated DeltaNet-2"), for
  * every batch row b and head h independently, token by token:
@@ -379,6 +380,110 @@ GDN_API gdn_status gdn_recurrent_step_prologue(const void *q_raw, const void *k_
                                                void *cs_v_out, float *S, void *o, int N, int H,
                                                int K, int V, float g_cap, gdn_act act,
                                                gdn_dtype dtype, gdn_gate gate, void *stream);
+
+/*
+ * Latent attention: the attention layer that stands between Gated DeltaNet layers
+ * in the hybrid of the Atomic-GDN2 card (section 2.2), in the same four modes:
+ * forward and backward over whole sequences, one token, M drafted tokens.
+ *
+ * Every token has one latent vector c_t (r values) and one rotary key (dr values)
+ * for all heads.  The EXPANDED form works on the keys and values that the
+ * up-projection makes of the latents, the ABSORBED form on the latents, with the
+ * up-projections folded into the query (q^nope W_uk) and the output (W_uv).  The
+ * projections and the rotation are the caller's.  Storage types are those of
+ * gdn_dtype; scores, softmax statistics, sums and lse are fp32; for GDN_BF16 the
+ * softmax weights are rounded to bf16 for the matrix cores.  Every pointer apart
+ * from lens, lse, table (4 bytes) and tree (8 bytes) needs 16-byte alignment, a
+ * workspace 256 bytes; a workspace's contents on entry do not matter, on return
+ * they are unspecified, and calls that share one must not run concurrently.
+ * Outputs and the workspace overlap neither inputs nor each other.  scale: finite
+ * and > 0.  Results are the same on every call with the same arguments.
+ * NOT checked: live inputs are finite (what lies behind a sequence's live length,
+ * or in cache slots behind it, may hold anything).
+ *
+ * Expanded causal forward.
+ *
+ *   q      [B, Tq, H, dn + dr] dtype    (first dn: without rotation)
+ *   kv     [B, Tk, H, dn + dv] dtype    the up-projected latents: key part, value
+ *   k_rope [B, Tk, dr]         dtype    one for all heads
+ *   lens   [B] int32 live keys of each sequence (clamped to 0 .. Tk), or NULL (Tk)
+ *   o      [B, Tq, H, dv]      dtype
+ *   lse    [B, Tq, H]          fp32, or NULL
+ *
+ * Tq <= Tk.  Query i has position p = Tk - Tq + i (Tq = Tk: a whole sequence,
+ * Tq < Tk: its last rows over all keys) and sees the keys j <= p, j < lens[b].  A
+ * row at p >= lens[b] is padding: o = 0, lse = -inf.  dn and dv: 64 or 128, dr: 64
+ * (GDN_ENOTSUP otherwise, and for B * H * Tq >= 2^28 or B * H * ceil(Tk / 64) >=
+ * 2^24).  Any size may be 0.  Long rows with few workgroups are split over the
+ * keys; the pieces stand in the workspace (at least
+ * gdn_latent_fwd_workspace_size bytes; NULL when that is 0).
+ */
+GDN_API gdn_status gdn_latent_fwd_workspace_size(int B, int Tq, int Tk, int H, int dn, int dr, int dv,
+                                                 gdn_dtype dtype, size_t *bytes);
+GDN_API gdn_status gdn_latent_fwd(const void *q, const void *kv, const void *k_rope, const int *lens,
+                                  void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                  int B, int Tq, int Tk, int H, int dn, int dr, int dv, float scale,
+                                  gdn_dtype dtype, void *stream);
+
+/*
+ * Gradients of gdn_latent_fwd.  q .. lse as given to and written by the forward
+ * (lse is required), d_o [B, Tq, H, dv] dtype; writes dq, dkv and dk_rope in the
+ * layouts of q, kv and k_rope (dk_rope is the sum over the heads).  Gradients of
+ * padding rows and keys are 0.  Deterministic: no atomics.
+ */
+GDN_API gdn_status gdn_latent_bwd_workspace_size(int B, int Tq, int Tk, int H, int dn, int dr, int dv,
+                                                 gdn_dtype dtype, size_t *bytes);
+GDN_API gdn_status gdn_latent_bwd(const void *q, const void *kv, const void *k_rope, const int *lens,
+                                  const void *o, const float *lse, const void *d_o,
+                                  void *dq, void *dkv, void *dk_rope,
+                                  void *workspace, size_t workspace_bytes,
+                                  int B, int Tq, int Tk, int H, int dn, int dr, int dv, float scale,
+                                  gdn_dtype dtype, void *stream);
+
+/*
+ * Absorbed form, one token of N sequences over a paged cache.
+ *
+ *   q      [N, H, r + dr]            dtype   (q^nope W_uk, then the rotary part)
+ *   cache  [pages, page, r + dr]     dtype   a token's latent, then its rotary key
+ *   table  [N, width] int32          token t of sequence n is slot t % page of page
+ *                                    table[n, t / page]
+ *   lens   [N] int32                 cached tokens (clamped to 0 .. width * page),
+ *                                    the new token's own among them
+ *   o      [N, H, r] dtype           lse [N, H] fp32 or NULL
+ *
+ * A table entry outside 0 .. pages - 1 holds no tokens (they are not seen); entries
+ * behind a sequence's last page are not read.  A sequence with no token gives
+ * o = 0, lse = -inf.  r: 256 or 512, dr: 64, any page >= 1 (GDN_ENOTSUP otherwise,
+ * and where pages * page, N * width or the call's tiles or rows pass 32 bits).
+ */
+GDN_API gdn_status gdn_latent_step(const void *q, const void *cache, const int *table, const int *lens,
+                                   void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                   int N, int H, int r, int dr, int pages, int page, int width,
+                                   float scale, gdn_dtype dtype, void *stream);
+
+/*
+ * Absorbed form, M drafted tokens of N sequences: a tree of drafts behind the
+ * cached tokens (the verification step of speculative decoding; the mixer's is
+ * gdn_recurrent_steps).  As gdn_latent_step, with
+ *
+ *   q      [N, M, H, r + dr] dtype   o [N, M, H, r] dtype   lse [N, M, H] fp32 or NULL
+ *   draft  [N, M, r + dr]    dtype   the drafted tokens' own rows, which are not in the
+ *                                    cache: only what is accepted need be appended
+ *   tree   [N, M] int64 or NULL      bit j of tree[n, m]: draft m sees draft j (itself:
+ *                                    bit m; bits from M on are ignored).  NULL: a chain,
+ *                                    draft m sees the drafts 0 .. m
+ *
+ * Every draft sees all lens[n] cached tokens.  M: 0 .. 64.  A row that sees nothing
+ * gives o = 0, lse = -inf.  The workspace query serves both calls (gdn_latent_step:
+ * M = 1).
+ */
+GDN_API gdn_status gdn_latent_steps_workspace_size(int N, int M, int H, int r, int dr,
+                                                   gdn_dtype dtype, size_t *bytes);
+GDN_API gdn_status gdn_latent_steps(const void *q, const void *draft, const long long *tree,
+                                    const void *cache, const int *table, const int *lens,
+                                    void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                    int N, int M, int H, int r, int dr, int pages, int page, int width,
+                                    float scale, gdn_dtype dtype, void *stream);
 
 /* Static English text for a status code (never NULL). */
 GDN_API const char *gdn_status_str(gdn_status s);
