@@ -2,7 +2,7 @@
 // kernels (gfx950): latent_fwd.hip, latent_bwd.hip, latent_step.hip.
 //
 // All of them keep operand tiles in LDS as rows of 16-byte chunks whose index is
-// XOR-ed with the row (latent_off), read matrix-core operands from them either
+// XOR-ed with the row, read matrix-core operands from them either
 // along a row (row_frag: contraction over the row's columns) or across rows
 // (col_frag: contraction over the rows, through gfx950's transposing LDS read
 // for bf16), and hold scores so that an accumulator tile feeds the next product
@@ -59,52 +59,86 @@ hipError_t latent_step_launch(bool bf16, int r, const LatentStepArgs &a, hipStre
 unsigned long long latent_step_workspace(bool bf16, int N, int M, int H, int r);
 
 #ifdef __HIPCC__
-// Sixteen zero bytes: the source of every tile row behind the last live key, so
-// that what such rows hold in memory (it may be NaN) never meets a product.
-static __device__ const uint4 latent_zero = {0u, 0u, 0u, 0u};
+// Zeros: the source of every tile row behind the last live key, so that what such
+// rows hold in memory (it may be NaN) never meets a product.  One row of the widest
+// kind (512 fp32 values).
+static __device__ const uint4 latent_zero[128] = {};
 
-// Byte offset of the 16-byte chunk `ch` of row `row`, rows of CPR chunks (a
-// multiple of 8): the low three bits of the chunk index are XOR-ed with the row,
-// so that eight rows read at one chunk index fall on distinct banks.
-template <int CPR> __device__ __forceinline__ int latent_off(int row, int ch) {
+// LDS tiles are rows of CPR 16-byte chunks (a multiple of 8); the low three bits of
+// a chunk's index are XOR-ed with its row, so that eight rows read at one chunk
+// index fall on distinct banks.  The functions below split an address into a part
+// per lane, computed once, and one that folds into the instruction's offset.
+
+// Operand with rows `row` (of this lane) and columns 32 kb + 8 gq .. +7.
+template <typename T, int CPR> __device__ __forceinline__ int row_base(int row) {
     static_assert(CPR % 8 == 0, "rows are a multiple of 128 bytes");
+    const int ch = sizeof(T) == 2 ? lane_gq() : 2 * lane_gq();
     return row * (CPR * 16) + ((ch ^ (row & 7)) << 4);
 }
-
-// Operand with rows row0 + r16 and columns 32 kb + 8 gq .. +7.
-template <typename T, int CPR> __device__ __forceinline__ Frag<T> row_frag(const char *M, int row0, int kb);
-template <int CPR> __device__ __forceinline__ Frag<__bf16> row_frag_bf(const char *M, int row0, int kb) {
-    return {*reinterpret_cast<const bf16x8 *>(M + latent_off<CPR>(row0 + lane_r16(), 4 * kb + lane_gq()))};
-}
-template <int CPR> __device__ __forceinline__ Frag<float> row_frag_f(const char *M, int row0, int kb) {
-    const int row = row0 + lane_r16(), ch = 8 * kb + 2 * lane_gq();
-    return {*reinterpret_cast<const f32x4 *>(M + latent_off<CPR>(row, ch)),
-            *reinterpret_cast<const f32x4 *>(M + latent_off<CPR>(row, ch + 1))};
-}
-template <typename T, int CPR> __device__ __forceinline__ Frag<T> row_frag(const char *M, int row0, int kb) {
-    if constexpr (sizeof(T) == 2) return row_frag_bf<CPR>(M, row0, kb);
-    else return row_frag_f<CPR>(M, row0, kb);
+template <typename T> __device__ __forceinline__ Frag<T> row_frag(const char *M, int base, int kb) {
+    if constexpr (sizeof(T) == 2) {
+        return {*reinterpret_cast<const bf16x8 *>(M + (base ^ ((kb & 1) << 6)) + (kb >> 1) * 128)};
+    } else {
+        return {*reinterpret_cast<const f32x4 *>(M + base + kb * 128),
+                *reinterpret_cast<const f32x4 *>(M + (base ^ 16) + kb * 128)};
+    }
 }
 
-// Operand with rows = columns 16 cb + r16 of the tile and contraction slots =
-// tile rows rowA + 0..3, rowB + 0..3 (rowA and rowB of this lane's group,
-// multiples of 4).
-template <typename T, int CPR>
-__device__ __forceinline__ Frag<T> col_frag(const char *M, int rowA, int rowB, int cb) {
+// Operand with rows = columns 16 cb + r16 of the tile and contraction slots = tile
+// rows row + 0..3 and row + STEP + 0..3 (`row`: of this lane's group, a multiple of
+// 4 whose low three bits are those of the row given to col_base; STEP: 4 or 16).
+template <typename T, int CPR> __device__ __forceinline__ int col_base(int row) {
     const int r16 = lane_r16();
     if constexpr (sizeof(T) == 2) {
-        const int ch = 2 * cb + ((r16 & 3) >> 1), sub = 8 * (r16 & 1), dr = r16 >> 2;
-        return {cat8(lds_read_tr(lds_u32(M + latent_off<CPR>(rowA + dr, ch) + sub)),
-                     lds_read_tr(lds_u32(M + latent_off<CPR>(rowB + dr, ch) + sub)))};
+        row += r16 >> 2;
+        return row * (CPR * 16) + ((((r16 & 3) >> 1) ^ (row & 7)) << 4) + 8 * (r16 & 1);
     } else {
-        const int ch = 4 * cb + (r16 >> 2), sub = 4 * (r16 & 3);
+        return row * (CPR * 16) + (((r16 >> 2) ^ (row & 7)) << 4) + 4 * (r16 & 3);
+    }
+}
+template <typename T, int CPR, int STEP>
+__device__ __forceinline__ Frag<T> col_frag(const char *M, int base, int cb) {
+    static_assert(STEP == 4 || STEP == 16, "");
+    constexpr int FLIP = STEP == 4 ? 64 : 0;   // row + 4 has bit 2 of its low three bits changed
+    if constexpr (sizeof(T) == 2) {
+        const int at = base ^ ((cb & 3) << 5);
+        const char *m = M + (cb >> 2) * 128;
+        return {cat8(lds_read_tr(lds_u32(m + at)), lds_read_tr(lds_u32(m + (at ^ FLIP) + STEP * CPR * 16)))};
+    } else {
+        const int at = base ^ ((cb & 1) << 6);
+        const char *m = M + (cb >> 1) * 128;
         Frag<T> f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            f.lo[e] = *reinterpret_cast<const float *>(M + latent_off<CPR>(rowA + e, ch) + sub);
-            f.hi[e] = *reinterpret_cast<const float *>(M + latent_off<CPR>(rowB + e, ch) + sub);
+            f.lo[e] = *reinterpret_cast<const float *>(m + (at ^ (e << 4)) + e * CPR * 16);
+            f.hi[e] = *reinterpret_cast<const float *>(m + (at ^ (e << 4) ^ FLIP) + (STEP + e) * CPR * 16);
         }
         return f;
+    }
+}
+
+// Enqueue the copy of rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes
+// apart, x: row 0) into an LDS tile by 256 threads; rows from n on read as zeros.
+// One instruction of the workgroup covers 256 / CPR rows, a multiple of 8, so the
+// lane's offset within them is the same for all.
+template <int CPR, int ROWS>
+__device__ __forceinline__ void load_rows(char *tile, const char *x, long stride, int r0, int n)
+{
+    constexpr int RP = 256 / CPR;
+    static_assert(RP % 8 == 0 && ROWS % RP == 0, "");
+    const int tid = threadIdx.x, row = tid / CPR, ch = (tid % CPR) ^ (row & 7);
+    char *dst = tile + (tid & ~63) * 16;
+    const char *p = x + r0 * stride;
+    if (r0 + ROWS <= n) {
+        const unsigned off = (unsigned)(row * (int)stride + ch * 16);
+#pragma unroll
+        for (int i = 0; i < ROWS / RP; ++i) g2lds16s(p + i * RP * stride, off, dst + i * 4096);
+    } else {
+#pragma unroll
+        for (int i = 0; i < ROWS / RP; ++i) {
+            const char *src = r0 + i * RP + row < n ? p + (i * RP + row) * stride + ch * 16 : (const char *)latent_zero;
+            g2lds16(src, dst + i * 4096);
+        }
     }
 }
 

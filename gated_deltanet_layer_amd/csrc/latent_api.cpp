@@ -37,6 +37,8 @@ gdn_status expanded_sizes(int B, int Tq, int Tk, int H, int dn, int dr, int dv, 
     if ((dn != 64 && dn != 128) || (dv != 64 && dv != 128) || dr != gdn::LATENT_ROPE) return GDN_ENOTSUP;
     // grids: workgroups * 256 threads < 2^32
     const long long rows = prod(B, H, Tq), tiles = prod(B, H, ((long long)Tk + 63) / 64);
+    // a lane's offset within the 32 rows that one copy covers: 32 bits
+    if (H > (1 << 15)) return GDN_ENOTSUP;
     if (rows >= (1LL << 28) || tiles >= (1LL << 24) || prod(B, Tk) >= (1LL << 28)) return GDN_ENOTSUP;
     return GDN_OK;
 }
@@ -47,9 +49,8 @@ gdn_status absorbed_sizes(int N, int M, int H, int r, int dr, gdn_dtype dtype)
     if (N < 0 || M < 0 || H < 0 || r <= 0 || dr <= 0) return GDN_EINVAL;
     if (prod(N, M, H, 4LL * ((long long)r + dr)) < 0) return GDN_EINVAL;
     if ((r != 256 && r != 512) || dr != gdn::LATENT_ROPE || M > 64) return GDN_ENOTSUP;
-    // the join kernel's grid: a workgroup of 256 threads for four rows
-    const long long rows = prod(M, H);
-    if (rows > (1LL << 20) || prod(N, (rows + 3) / 4) >= (1LL << 24)) return GDN_ENOTSUP;
+    // the join kernel's grid: a workgroup of 256 threads a row
+    if (prod(M, H) > (1LL << 20) || prod(N, M, H) >= (1LL << 24)) return GDN_ENOTSUP;
     return GDN_OK;
 }
 

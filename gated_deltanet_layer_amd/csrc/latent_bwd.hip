@@ -62,37 +62,11 @@ template <typename T, int DN, int DV> struct BwdCfg {
     static constexpr int OWN = 64 * NG;                    // rows a workgroup owns (keys or queries)
     static constexpr int ST = sizeof(T) == 2 ? 64 : 32;    // rows a tile that walks by
     static constexpr int DK = DN + LATENT_ROPE;
-    static constexpr int KCPR = DK * (int)sizeof(T) / 16, VCPR = DV * (int)sizeof(T) / 16;
-    static constexpr int KBYTES = ST * KCPR * 16, VBYTES = ST * VCPR * 16;
-    static constexpr int BUF = KBYTES + VBYTES;            // [ST][DK] and [ST][DV]
+    static constexpr int ES = (int)sizeof(T), NCPR = DN * ES / 16, RCPR = LATENT_ROPE * ES / 16, VCPR = DV * ES / 16;
+    // a tile: [ST][DN] and [ST][64] of the rows' two key parts, [ST][DV]
+    static constexpr int OFF_R = ST * NCPR * 16, OFF_V = OFF_R + ST * RCPR * 16, BUF = OFF_V + ST * VCPR * 16;
     static constexpr int ROWS = 2 * ST * 4;                // lse and D of the tile's rows
 };
-
-// Copies rows r0 .. r0 + ST - 1 of a [.., DK] and a [.., DV] matrix; rows from n
-// on read as zeros.  Columns of the first from DN on come from `rope` if given.
-template <typename T, int DN, int DV, typename C>
-__device__ __forceinline__ void bwd_load_tile(char *buf, const T *x, long xs, const T *rope, const T *y,
-                                              long ys, int r0, int n)
-{
-    const int tid = threadIdx.x, wbase = (tid & ~63) * 16;
-    constexpr int EPC = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int i = 0; i < C::ST * C::KCPR / 256; ++i) {
-        const int slot = i * 256 + tid, row = slot / C::KCPR, ch = (slot % C::KCPR) ^ (row & 7);
-        const int r = r0 + row, col = ch * EPC;
-        const void *src = !rope || col < DN ? (const void *)(x + r * xs + col)
-                                            : (const void *)(rope + (long)r * LATENT_ROPE + (col - DN));
-        if (r >= n) src = &latent_zero;
-        g2lds16(src, buf + i * 4096 + wbase);
-    }
-#pragma unroll
-    for (int i = 0; i < C::ST * C::VCPR / 256; ++i) {
-        const int slot = i * 256 + tid, row = slot / C::VCPR, ch = (slot % C::VCPR) ^ (row & 7);
-        const int r = r0 + row;
-        const void *src = r < n ? (const void *)(y + r * ys + ch * EPC) : (const void *)&latent_zero;
-        g2lds16(src, buf + C::KBYTES + i * 4096 + wbase);
-    }
-}
 
 // dk and dv.  A wave owns 16 NG keys: k and v of them stay in registers as B
 // operands, dk^T and dv^T as accumulators.  Scores have query rows on the
@@ -132,8 +106,8 @@ __global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
             kf[g][kb] = live ? load_frag<T>(p) : zero_frag<T>();
         }
 #pragma unroll
-        for (int vb = 0; vb < NVB; ++vb)
-            vf[g][vb] = live ? load_frag<T>(kv + key * kvs + DN + 32 * vb + 8 * gq) : zero_frag<T>();
+        for (int v = 0; v < NVB; ++v)
+            vf[g][v] = live ? load_frag<T>(kv + key * kvs + DN + 32 * v + 8 * gq) : zero_frag<T>();
     }
     f32x4 dk[NKC][NG], dv[NVC][NG];
 #pragma unroll
@@ -149,16 +123,21 @@ __global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
     const int nt = k0 < n && qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0;
     auto load = [&](int j) {
         const int r0 = qfirst + j * ST, buf = j & 1;
-        bwd_load_tile<T, DK, DV, C>(lds + buf * C::BUF, q, qs, (const T *)nullptr, d_o, os, r0, qn);
+        char *to = lds + buf * C::BUF;
+        load_rows<C::NCPR, ST>(to, (const char *)q, qs * C::ES, r0, qn);
+        load_rows<C::RCPR, ST>(to + C::OFF_R, (const char *)(q + DN), qs * C::ES, r0, qn);
+        load_rows<C::VCPR, ST>(to + C::OFF_V, (const char *)d_o, os * C::ES, r0, qn);
         if (wave < 2 && (threadIdx.x & 63) < ST) {   // lse by the first wave, D by the second
             const int r = r0 + (threadIdx.x & 63);
             const void *src = r >= qn ? (const void *)&latent_zero : (wave ? Dw : lse) + (long)r * a.H;
             g2lds4(src, (char *)(stat + (buf * 2 + wave) * ST));
         }
     };
+    const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = row_base<T, C::VCPR>(r16);
+    const int nc = col_base<T, C::NCPR>(4 * gq), rc = col_base<T, C::RCPR>(4 * gq), vc = col_base<T, C::VCPR>(4 * gq);
     if (nt > 0) load(0);
     for (int j = 0; j < nt; ++j) {
-        const char *qt = lds + (j & 1) * C::BUF, *dt = qt + C::KBYTES;
+        const char *qt = lds + (j & 1) * C::BUF, *dt = qt + C::OFF_V;
         const float *st = stat + (j & 1) * 2 * ST;
         const int r0 = qfirst + j * ST;
         wait_vm<0>();
@@ -166,7 +145,7 @@ __global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
         if (j + 1 < nt) load(j + 1);
         if (off + r0 + ST - 1 < w0 || w0 >= n) continue;   // no row of the tile sees a key of this wave
         const bool part = off + r0 < w0 + 16 * NG - 1 || r0 + ST > qn;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < ST / 32; ++t) {
             f32x4 s[2][NG], dp[2][NG];
 #pragma unroll
@@ -178,16 +157,20 @@ __global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
                 }
 #pragma unroll
                 for (int kb = 0; kb < NKB; ++kb) {
-                    const Frag<T> f = row_frag<T, C::KCPR>(qt, 32 * t + 16 * u, kb);
+                    const Frag<T> f = kb < DN / 32
+                        ? row_frag<T>(qt + (32 * t + 16 * u) * C::NCPR * 16, nb, kb)
+                        : row_frag<T>(qt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rb, kb - DN / 32);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, kf[g][kb]);
+                    if (kb % 3 == 2) GDN_SCHED_FENCE();
                 }
 #pragma unroll
-                for (int vb = 0; vb < NVB; ++vb) {
-                    const Frag<T> f = row_frag<T, C::VCPR>(dt, 32 * t + 16 * u, vb);
+                for (int v = 0; v < NVB; ++v) {
+                    const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::VCPR * 16, vb, v);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, vf[g][vb]);
+                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, vf[g][v]);
                 }
+                GDN_SCHED_FENCE();
                 const int row = 32 * t + 16 * u + 4 * gq;
                 const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + row), dd = *reinterpret_cast<const f32x4 *>(st + ST + row);
 #pragma unroll
@@ -208,18 +191,20 @@ __global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
                 pf[g] = reg_frag<T>(s[0][g], s[1][g]);
                 sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
             }
-            const int ra = 32 * t + 4 * gq, rb = ra + 16;
 #pragma unroll
             for (int i = 0; i < NVC; ++i) {
-                const Frag<T> f = col_frag<T, C::VCPR>(dt, ra, rb, i);
+                const Frag<T> f = col_frag<T, C::VCPR, 16>(dt + 32 * t * C::VCPR * 16, vc, i);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dv[i][g] = mma(dv[i][g], f, pf[g]);
+                if (i % 2 == 1) GDN_SCHED_FENCE();
             }
 #pragma unroll
             for (int i = 0; i < NKC; ++i) {
-                const Frag<T> f = col_frag<T, C::KCPR>(qt, ra, rb, i);
+                const Frag<T> f = i < DN / 16 ? col_frag<T, C::NCPR, 16>(qt + 32 * t * C::NCPR * 16, nc, i)
+                                              : col_frag<T, C::RCPR, 16>(qt + C::OFF_R + 32 * t * C::RCPR * 16, rc, i - DN / 16);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dk[i][g] = mma(dk[i][g], f, sf[g]);
+                if (i % 2 == 1) GDN_SCHED_FENCE();
             }
         }
     }
@@ -277,8 +262,8 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
         for (int kb = 0; kb < NKB; ++kb)
             qf[g][kb] = live ? load_frag<T>(q + row * qs + 32 * kb + 8 * gq) : zero_frag<T>();
 #pragma unroll
-        for (int vb = 0; vb < NVB; ++vb)
-            of[g][vb] = live ? load_frag<T>(d_o + row * os + 32 * vb + 8 * gq) : zero_frag<T>();
+        for (int v = 0; v < NVB; ++v)
+            of[g][v] = live ? load_frag<T>(d_o + row * os + 32 * v + 8 * gq) : zero_frag<T>();
     }
     f32x4 dq[NKC][NG];
 #pragma unroll
@@ -289,16 +274,24 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
     const int last = min(n, off + min(q0 + C::OWN, a.Tq));
     const int nt = (off + q0 < n) ? (last + ST - 1) / ST : 0;
     const int wlast = min(n, off + min(w0 + 16 * NG, a.Tq)), wfull = off + w0 + 1;
-    if (nt > 0) bwd_load_tile<T, DN, DV, C>(lds, kv, kvs, kr, kv + DN, kvs, 0, n);
+    auto load = [&](int j) {
+        char *to = lds + (j & 1) * C::BUF;
+        load_rows<C::NCPR, ST>(to, (const char *)kv, kvs * C::ES, j * ST, n);
+        load_rows<C::RCPR, ST>(to + C::OFF_R, (const char *)kr, LATENT_ROPE * C::ES, j * ST, n);
+        load_rows<C::VCPR, ST>(to + C::OFF_V, (const char *)(kv + DN), kvs * C::ES, j * ST, n);
+    };
+    const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = row_base<T, C::VCPR>(r16);
+    const int nc = col_base<T, C::NCPR>(4 * gq), rc = col_base<T, C::RCPR>(4 * gq);
+    if (nt > 0) load(0);
     for (int j = 0; j < nt; ++j) {
-        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::KBYTES;
+        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
         const int k0 = j * ST;
         wait_vm<0>();
         lds_barrier();
-        if (j + 1 < nt) bwd_load_tile<T, DN, DV, C>(lds + ((j + 1) & 1) * C::BUF, kv, kvs, kr, kv + DN, kvs, k0 + ST, n);
+        if (j + 1 < nt) load(j + 1);
         if (k0 >= wlast || off + w0 >= n) continue;
         const bool part = k0 + ST > wfull || k0 + ST > n;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < ST / 32; ++t) {
             f32x4 s[2][NG], dp[2][NG];
 #pragma unroll
@@ -310,16 +303,20 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
                 }
 #pragma unroll
                 for (int kb = 0; kb < NKB; ++kb) {
-                    const Frag<T> f = row_frag<T, C::KCPR>(kt, 32 * t + 16 * u, kb);
+                    const Frag<T> f = kb < DN / 32
+                        ? row_frag<T>(kt + (32 * t + 16 * u) * C::NCPR * 16, nb, kb)
+                        : row_frag<T>(kt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rb, kb - DN / 32);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, qf[g][kb]);
+                    if (kb % 3 == 2) GDN_SCHED_FENCE();
                 }
 #pragma unroll
-                for (int vb = 0; vb < NVB; ++vb) {
-                    const Frag<T> f = row_frag<T, C::VCPR>(vt, 32 * t + 16 * u, vb);
+                for (int v = 0; v < NVB; ++v) {
+                    const Frag<T> f = row_frag<T>(vt + (32 * t + 16 * u) * C::VCPR * 16, vb, v);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, of[g][vb]);
+                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, of[g][v]);
                 }
+                GDN_SCHED_FENCE();
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -332,12 +329,13 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
             Frag<T> sf[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
-            const int ra = 32 * t + 4 * gq, rb = ra + 16;
 #pragma unroll
             for (int i = 0; i < NKC; ++i) {
-                const Frag<T> f = col_frag<T, C::KCPR>(kt, ra, rb, i);
+                const Frag<T> f = i < DN / 16 ? col_frag<T, C::NCPR, 16>(kt + 32 * t * C::NCPR * 16, nc, i)
+                                              : col_frag<T, C::RCPR, 16>(kt + C::OFF_R + 32 * t * C::RCPR * 16, rc, i - DN / 16);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dq[i][g] = mma(dq[i][g], f, sf[g]);
+                if (i % 2 == 1) GDN_SCHED_FENCE();
             }
         }
     }

@@ -19,34 +19,10 @@ template <typename T, int DN, int DV> struct FwdCfg {
     static constexpr int RT = 16 * NR * NW;                // query rows a workgroup
     static constexpr int KT = sizeof(T) == 2 ? 64 : 32;    // keys a tile
     static constexpr int DK = DN + LATENT_ROPE;
-    static constexpr int KCPR = DK * (int)sizeof(T) / 16, VCPR = DV * (int)sizeof(T) / 16;
-    static constexpr int KBYTES = KT * KCPR * 16, VBYTES = KT * VCPR * 16;
-    static constexpr int BUF = KBYTES + VBYTES;
+    static constexpr int ES = (int)sizeof(T), NCPR = DN * ES / 16, RCPR = LATENT_ROPE * ES / 16, VCPR = DV * ES / 16;
+    // a tile: [KT][DN] keys, [KT][64] rotary keys, [KT][DV] values
+    static constexpr int OFF_R = KT * NCPR * 16, OFF_V = OFF_R + KT * RCPR * 16, BUF = OFF_V + KT * VCPR * 16;
 };
-
-// Enqueue the copies of keys k0 .. k0 + KT - 1 into a tile buffer.
-template <typename T, int DN, int DV, typename C>
-__device__ __forceinline__ void fwd_load_tile(char *buf, const T *kv, const T *kr, long kvs, int k0, int n)
-{
-    const int tid = threadIdx.x, wbase = (tid & ~63) * 16;
-    constexpr int EPC = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int i = 0; i < C::KT * C::KCPR / 256; ++i) {
-        const int slot = i * 256 + tid, row = slot / C::KCPR, ch = (slot % C::KCPR) ^ (row & 7);
-        const int key = k0 + row, col = ch * EPC;
-        const void *src = col < DN ? (const void *)(kv + key * kvs + col)
-                                   : (const void *)(kr + (long)key * LATENT_ROPE + (col - DN));
-        if (key >= n) src = &latent_zero;
-        g2lds16(src, buf + i * 4096 + wbase);
-    }
-#pragma unroll
-    for (int i = 0; i < C::KT * C::VCPR / 256; ++i) {
-        const int slot = i * 256 + tid, row = slot / C::VCPR, ch = (slot % C::VCPR) ^ (row & 7);
-        const int key = k0 + row;
-        const void *src = key < n ? (const void *)(kv + key * kvs + DN + ch * EPC) : (const void *)&latent_zero;
-        g2lds16(src, buf + C::KBYTES + i * 4096 + wbase);
-    }
-}
 
 template <typename T, int DN, int DV>
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int ntiles)
@@ -91,13 +67,20 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
     const int last = min(n, off + min(q0 + C::RT, a.Tq));
     const int nt = (off + q0 < n) ? (last + KT - 1) / KT : 0;
     const int wlast = min(n, off + min(w0 + 16 * NR, a.Tq)), wfull = off + w0 + 1;
-    if (nt > 0) fwd_load_tile<T, DN, DV, C>(lds, kv, kr, kvs, 0, n);
+    auto load = [&](int j) {
+        char *buf = lds + (j & 1) * C::BUF;
+        load_rows<C::NCPR, KT>(buf, (const char *)kv, kvs * C::ES, j * KT, n);
+        load_rows<C::RCPR, KT>(buf + C::OFF_R, (const char *)kr, LATENT_ROPE * C::ES, j * KT, n);
+        load_rows<C::VCPR, KT>(buf + C::OFF_V, (const char *)(kv + DN), kvs * C::ES, j * KT, n);
+    };
+    const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = col_base<T, C::VCPR>(4 * gq);
+    if (nt > 0) load(0);
     for (int j = 0; j < nt; ++j) {
-        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::KBYTES;
+        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
         const int k0 = j * KT;
         wait_vm<0>();
         lds_barrier();
-        if (j + 1 < nt) fwd_load_tile<T, DN, DV, C>(lds + ((j + 1) & 1) * C::BUF, kv, kr, kvs, k0 + KT, n);
+        if (j + 1 < nt) load(j + 1);
         if (k0 >= wlast || off + w0 >= n) continue;   // nothing for this wave in the tile
         f32x4 s[NS][NR];
 #pragma unroll
@@ -106,7 +89,9 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
             for (int g = 0; g < NR; ++g) s[t][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb) {
-                const Frag<T> kf = row_frag<T, C::KCPR>(kt, 16 * t, kb);
+                const Frag<T> kf = kb < DN / 32
+                    ? row_frag<T>(kt + 16 * t * C::NCPR * 16, nb, kb)
+                    : row_frag<T>(kt + C::OFF_R + 16 * t * C::RCPR * 16, rb, kb - DN / 32);
 #pragma unroll
                 for (int g = 0; g < NR; ++g) s[t][g] = mma(s[t][g], kf, qf[g][kb]);
             }
@@ -156,7 +141,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
             for (int g = 0; g < NR; ++g) pf[g] = reg_frag<T>(s[t][g], s[t + 1][g]);
 #pragma unroll
             for (int cb = 0; cb < NCB; ++cb) {
-                const Frag<T> vf = col_frag<T, C::VCPR>(vt, 16 * t + 4 * gq, 16 * t + 16 + 4 * gq, cb);
+                const Frag<T> vf = col_frag<T, C::VCPR, 16>(vt + 16 * t * C::VCPR * 16, vb, cb);
 #pragma unroll
                 for (int g = 0; g < NR; ++g) acc[cb][g] = mma(acc[cb][g], vf, pf[g]);
             }
