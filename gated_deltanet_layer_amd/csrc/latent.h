@@ -118,13 +118,13 @@ __device__ __forceinline__ Frag<T> col_frag(const char *M, int base, int cb) {
 }
 
 // Enqueue the copy of rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes
-// apart, x: row 0) into an LDS tile by 256 threads; rows from n on read as zeros.
-// One instruction of the workgroup covers 256 / CPR rows, a multiple of 8, so the
+// apart, x: row 0) into an LDS tile by NTHR threads; rows from n on read as zeros.
+// One instruction of the workgroup covers NTHR / CPR rows, a multiple of 8, so the
 // lane's offset within them is the same for all.
-template <int CPR, int ROWS>
+template <int CPR, int ROWS, int NTHR = 256>
 __device__ __forceinline__ void load_rows(char *tile, const char *x, long stride, int r0, int n)
 {
-    constexpr int RP = 256 / CPR;
+    constexpr int RP = NTHR / CPR;
     static_assert(RP % 8 == 0 && ROWS % RP == 0, "");
     const int tid = threadIdx.x, row = tid / CPR, ch = (tid % CPR) ^ (row & 7);
     char *dst = tile + (tid & ~63) * 16;
@@ -132,12 +132,12 @@ __device__ __forceinline__ void load_rows(char *tile, const char *x, long stride
     if (r0 + ROWS <= n) {
         const unsigned off = (unsigned)(row * (int)stride + ch * 16);
 #pragma unroll
-        for (int i = 0; i < ROWS / RP; ++i) g2lds16s(p + i * RP * stride, off, dst + i * 4096);
+        for (int i = 0; i < ROWS / RP; ++i) g2lds16s(p + i * RP * stride, off, dst + i * NTHR * 16);
     } else {
 #pragma unroll
         for (int i = 0; i < ROWS / RP; ++i) {
             const char *src = r0 + i * RP + row < n ? p + (i * RP + row) * stride + ch * 16 : (const char *)latent_zero;
-            g2lds16(src, dst + i * 4096);
+            g2lds16(src, dst + i * NTHR * 16);
         }
     }
 }

@@ -66,25 +66,35 @@ template <typename T, int DN, int DV> struct BwdCfg {
     // a tile: [ST][DN] and [ST][64] of the rows' two key parts, [ST][DV]
     static constexpr int OFF_R = ST * NCPR * 16, OFF_V = OFF_R + ST * RCPR * 16, BUF = OFF_V + ST * VCPR * 16;
     static constexpr int ROWS = 2 * ST * 4;                // lse and D of the tile's rows
+    static constexpr int HAND = 2 * 2 * NG * 1024;         // two blocks of P, one pair of waves
+    static constexpr int KV_LDS = 3 * (BUF + ROWS) + 4 * HAND;
+    static_assert(KV_LDS <= 160 * 1024, "LDS");
 };
 
-// dk and dv.  A wave owns 16 NG keys: k and v of them stay in registers as B
-// operands, dk^T and dv^T as accumulators.  Scores have query rows on the
-// accumulator's rows, so P and dS feed the gradient products as B operands
-// straight from the registers; q and do come from LDS, along the rows for the
-// scores and across them for the gradients.
+// dk and dv.  Four pairs of waves; a pair owns 16 NG keys.  The first of the pair
+// computes the scores and P and adds up dv^T (k and dv in its registers), the second
+// takes P over, computes dP and dS and adds up dk^T (v and dk in its registers): the
+// same number of products for both, and of q and do each reads from LDS one along
+// the rows and the other across them, where one wave for both would not have the
+// registers for 32 keys, and with 16 keys would read twice as much.  The second is
+// one block of 32 query rows behind, so neither waits for the other inside a block.
+// Scores have query rows on the accumulator's rows: P and dS feed the gradient
+// products as B operands straight from the registers, and P changes hands between
+// equal lanes.
 template <typename T, int DN, int DV>
-__global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, int ntiles)
+__global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, int ntiles)
 {
     typedef BwdCfg<T, DN, DV> C;
     constexpr int NG = C::NG, ST = C::ST, DK = C::DK, NKB = DK / 32, NVB = DV / 32, NKC = DK / 16, NVC = DV / 16;
+    constexpr int BPT = ST / 32;   // blocks a tile
     extern __shared__ char lds[];
     const int BH = a.B * a.H;
     const int bh = blockIdx.x % BH, tile = blockIdx.x / BH;   // the first keys are seen by most rows
     const int b = bh / a.H, h = bh % a.H;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int pair = wave & 3, lane = threadIdx.x & 63;
     const int off = a.Tk - a.Tq, n = live_len(a.lens, b, a.Tk);
-    const int k0 = tile * C::OWN, w0 = k0 + wave * 16 * NG;
+    const int k0 = tile * C::OWN, w0 = k0 + pair * 16 * NG;
     const long qs = (long)a.H * DK, kvs = (long)a.H * (DN + DV), os = (long)a.H * DV;
     const T *q = (const T *)a.q + ((long)b * a.Tq * a.H + h) * DK;
     const T *d_o = (const T *)a.d_o + ((long)b * a.Tq * a.H + h) * DV;
@@ -92,69 +102,70 @@ __global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
     const T *kr = (const T *)a.k_rope + (long)b * a.Tk * LATENT_ROPE;
     const float *lse = a.lse + (long)b * a.Tq * a.H + h, *Dw = (const float *)a.ws + (long)b * a.Tq * a.H + h;
     const float c = a.scale * LOG2E;
-    float *stat = (float *)(lds + 2 * C::BUF);   // [2][2][ST]
-
-    Frag<T> kf[NG][NKB], vf[NG][NVB];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const int key = w0 + 16 * g + r16;
-        const bool live = key < n;
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-            const int col = 32 * kb + 8 * gq;
-            const T *p = 32 * kb < DN ? kv + key * kvs + col : kr + (long)key * LATENT_ROPE + (col - DN);
-            kf[g][kb] = live ? load_frag<T>(p) : zero_frag<T>();
-        }
-#pragma unroll
-        for (int v = 0; v < NVB; ++v)
-            vf[g][v] = live ? load_frag<T>(kv + key * kvs + DN + 32 * v + 8 * gq) : zero_frag<T>();
-    }
-    f32x4 dk[NKC][NG], dv[NVC][NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-#pragma unroll
-        for (int i = 0; i < NKC; ++i) dk[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < NVC; ++i) dv[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    float *stat = (float *)(lds + 3 * C::BUF);                  // [3][2][ST]: lse and D of the rows
+    char *hand = lds + 3 * (C::BUF + C::ROWS) + pair * C::HAND; // [2][2 NG][64 lanes] f32x4: P, block by block
 
     // query rows that are no padding and see the workgroup's first key
     const int qn = min(a.Tq, n - off), qfirst = max(0, k0 - off) / ST * ST;
-    const int nt = k0 < n && qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0;
+    const int nt = k0 < n && qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0, nblk = nt * BPT;
     auto load = [&](int j) {
-        const int r0 = qfirst + j * ST, buf = j & 1;
+        const int r0 = qfirst + j * ST, buf = j % 3;
         char *to = lds + buf * C::BUF;
-        load_rows<C::NCPR, ST>(to, (const char *)q, qs * C::ES, r0, qn);
-        load_rows<C::RCPR, ST>(to + C::OFF_R, (const char *)(q + DN), qs * C::ES, r0, qn);
-        load_rows<C::VCPR, ST>(to + C::OFF_V, (const char *)d_o, os * C::ES, r0, qn);
-        if (wave < 2 && (threadIdx.x & 63) < ST) {   // lse by the first wave, D by the second
-            const int r = r0 + (threadIdx.x & 63);
-            const void *src = r >= qn ? (const void *)&latent_zero : (wave ? Dw : lse) + (long)r * a.H;
+        load_rows<C::NCPR, ST, 512>(to, (const char *)q, qs * C::ES, r0, qn);
+        load_rows<C::RCPR, ST, 512>(to + C::OFF_R, (const char *)(q + DN), qs * C::ES, r0, qn);
+        load_rows<C::VCPR, ST, 512>(to + C::OFF_V, (const char *)d_o, os * C::ES, r0, qn);
+        if (wave < 2 && lane < ST) {   // lse by the first wave, D by the second
+            const int r = r0 + lane;
+            const void *src = r >= qn ? (const void *)latent_zero : (wave ? Dw : lse) + (long)r * a.H;
             g2lds4(src, (char *)(stat + (buf * 2 + wave) * ST));
         }
     };
-    const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = row_base<T, C::VCPR>(r16);
-    const int nc = col_base<T, C::NCPR>(4 * gq), rc = col_base<T, C::RCPR>(4 * gq), vc = col_base<T, C::VCPR>(4 * gq);
+    // before block i: block i - 1 of P is whole, and where a tile begins it is there
+    auto sync = [&](int i) {
+        if (i < nblk && i % BPT == 0) {
+            wait_vm<0>();
+            lds_barrier();
+            if (i / BPT + 1 < nt) load(i / BPT + 1);   // over the tile before the one that block i - 1 is of
+        } else {
+            lds_barrier();
+        }
+    };
+    auto seen = [&](int i) {   // whether a row of block i sees a key of the wave
+        return off + qfirst + i * 32 + 31 >= w0 && w0 < n;
+    };
     if (nt > 0) load(0);
-    for (int j = 0; j < nt; ++j) {
-        const char *qt = lds + (j & 1) * C::BUF, *dt = qt + C::OFF_V;
-        const float *st = stat + (j & 1) * 2 * ST;
-        const int r0 = qfirst + j * ST;
-        wait_vm<0>();
-        lds_barrier();
-        if (j + 1 < nt) load(j + 1);
-        if (off + r0 + ST - 1 < w0 || w0 >= n) continue;   // no row of the tile sees a key of this wave
-        const bool part = off + r0 < w0 + 16 * NG - 1 || r0 + ST > qn;
+
+    if (wave < 4) {
+        const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vc = col_base<T, C::VCPR>(4 * gq);
+        Frag<T> kf[NG][NKB];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int key = w0 + 16 * g + r16;
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const int col = 32 * kb + 8 * gq;
+                const T *p = 32 * kb < DN ? kv + key * kvs + col : kr + (long)key * LATENT_ROPE + (col - DN);
+                kf[g][kb] = key < n ? load_frag<T>(p) : zero_frag<T>();
+            }
+        }
+        f32x4 dv[NVC][NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < NVC; ++i) dv[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int t = 0; t < ST / 32; ++t) {
-            f32x4 s[2][NG], dp[2][NG];
+        for (int i = 0; i <= nblk; ++i) {
+            sync(i);
+            if (i == nblk || !seen(i)) continue;
+            const char *qt = lds + i / BPT % 3 * C::BUF, *dt = qt + C::OFF_V;
+            const float *st = stat + i / BPT % 3 * 2 * ST;
+            const int t = i % BPT, r0 = qfirst + i * 32;
+            const bool part = off + r0 < w0 + 16 * NG - 1 || r0 + 32 > qn;
+            f32x4 s[2][NG];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    dp[u][g] = s[u][g];
-                }
+                for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int kb = 0; kb < NKB; ++kb) {
                     const Frag<T> f = kb < DN / 32
@@ -162,66 +173,111 @@ __global__ __launch_bounds__(256, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
                         : row_frag<T>(qt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rb, kb - DN / 32);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, kf[g][kb]);
-                    if (kb % 3 == 2) GDN_SCHED_FENCE();
                 }
+                const int row = 16 * u + 4 * gq;
+                const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 32 * t + row) * LOG2E;
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
+                if (part) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const bool hide = (off + r0 + row + e < w0 + 16 * g + r16) | (r0 + row + e >= qn);
+                            s[u][g][e] = hide ? 0.f : s[u][g][e];
+                        }
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    *reinterpret_cast<f32x4 *>(hand + (((i & 1) * 2 + u) * NG + g) * 1024 + lane * 16) = s[u][g];
+            }
+            // P (and below dS) rounded to the storage type for the matrix cores: half
+            // a step each, as the gradients themselves
+            Frag<T> pf[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
+#pragma unroll
+            for (int v = 0; v < NVC; ++v) {
+                const Frag<T> f = col_frag<T, C::VCPR, 16>(dt + 32 * t * C::VCPR * 16, vc, v);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dv[v][g] = mma(dv[v][g], f, pf[g]);
+            }
+        }
+        T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV) + DN;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int key = w0 + 16 * g + r16;
+            if (key >= a.Tk) continue;
+#pragma unroll
+            for (int v = 0; v < NVC; ++v) store4(dkv + key * kvs + 16 * v + 4 * gq, dv[v][g]);
+        }
+    } else {
+        const int vb = row_base<T, C::VCPR>(r16), nc = col_base<T, C::NCPR>(4 * gq), rc = col_base<T, C::RCPR>(4 * gq);
+        Frag<T> vf[NG][NVB];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int key = w0 + 16 * g + r16;
+#pragma unroll
+            for (int v = 0; v < NVB; ++v)
+                vf[g][v] = key < n ? load_frag<T>(kv + key * kvs + DN + 32 * v + 8 * gq) : zero_frag<T>();
+        }
+        f32x4 dk[NKC][NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < NKC; ++i) dk[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int i = 0; i <= nblk; ++i) {
+            sync(i);
+            if (i == 0 || !seen(i - 1)) continue;
+            const int k = i - 1, t = k % BPT;
+            const char *qt = lds + k / BPT % 3 * C::BUF, *dt = qt + C::OFF_V;
+            const float *st = stat + (k / BPT % 3 * 2 + 1) * ST;
+            f32x4 dp[2][NG];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int v = 0; v < NVB; ++v) {
                     const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::VCPR * 16, vb, v);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, vf[g][v]);
                 }
-                GDN_SCHED_FENCE();
-                const int row = 32 * t + 16 * u + 4 * gq;
-                const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + row), dd = *reinterpret_cast<const f32x4 *>(st + ST + row);
+                const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 32 * t + 16 * u + 4 * gq);
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
+                for (int g = 0; g < NG; ++g) {
+                    const f32x4 p = *reinterpret_cast<const f32x4 *>(hand + (((k & 1) * 2 + u) * NG + g) * 1024 + lane * 16);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float p = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e] * LOG2E));
-                        if (part && (off + r0 + row + e < w0 + 16 * g + r16 || r0 + row + e >= qn)) p = 0.f;
-                        s[u][g][e] = p;
-                        dp[u][g][e] = p * (dp[u][g][e] - dd[e]);
-                    }
+                    for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
+                }
             }
-            // P and dS rounded to the storage type for the matrix cores (half a
-            // step each, as the gradients themselves); scale is applied at the end
-            Frag<T> pf[NG], sf[NG];
+            Frag<T> sf[NG];
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                pf[g] = reg_frag<T>(s[0][g], s[1][g]);
-                sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+            for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+#pragma unroll
+            for (int v = 0; v < NKC; ++v) {
+                const Frag<T> f = v < DN / 16 ? col_frag<T, C::NCPR, 16>(qt + 32 * t * C::NCPR * 16, nc, v)
+                                              : col_frag<T, C::RCPR, 16>(qt + C::OFF_R + 32 * t * C::RCPR * 16, rc, v - DN / 16);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dk[v][g] = mma(dk[v][g], f, sf[g]);
             }
+        }
+        T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV);
+        float *rope = (float *)((char *)a.ws + BwdWs(a.B, a.Tq, a.Tk, a.H).rope);
 #pragma unroll
-            for (int i = 0; i < NVC; ++i) {
-                const Frag<T> f = col_frag<T, C::VCPR, 16>(dt + 32 * t * C::VCPR * 16, vc, i);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) dv[i][g] = mma(dv[i][g], f, pf[g]);
-                if (i % 2 == 1) GDN_SCHED_FENCE();
-            }
+        for (int g = 0; g < NG; ++g) {
+            const int key = w0 + 16 * g + r16;
+            if (key >= a.Tk) continue;
 #pragma unroll
             for (int i = 0; i < NKC; ++i) {
-                const Frag<T> f = i < DN / 16 ? col_frag<T, C::NCPR, 16>(qt + 32 * t * C::NCPR * 16, nc, i)
-                                              : col_frag<T, C::RCPR, 16>(qt + C::OFF_R + 32 * t * C::RCPR * 16, rc, i - DN / 16);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) dk[i][g] = mma(dk[i][g], f, sf[g]);
-                if (i % 2 == 1) GDN_SCHED_FENCE();
+                const f32x4 v = dk[i][g] * a.scale;
+                if (16 * i < DN) store4(dkv + key * kvs + 16 * i + 4 * gq, v);
+                else store4(rope + (((long)b * a.Tk + key) * a.H + h) * LATENT_ROPE + (16 * i - DN) + 4 * gq, v);
             }
         }
-    }
-    T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV);
-    float *rope = (float *)((char *)a.ws + BwdWs(a.B, a.Tq, a.Tk, a.H).rope);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const int key = w0 + 16 * g + r16;
-        if (key >= a.Tk) continue;
-#pragma unroll
-        for (int i = 0; i < NKC; ++i) {
-            const f32x4 v = dk[i][g] * a.scale;
-            if (16 * i < DN) store4(dkv + key * kvs + 16 * i + 4 * gq, v);
-            else store4(rope + (((long)b * a.Tk + key) * a.H + h) * LATENT_ROPE + (16 * i - DN) + 4 * gq, v);
-        }
-#pragma unroll
-        for (int i = 0; i < NVC; ++i) store4(dkv + key * kvs + DN + 16 * i + 4 * gq, dv[i][g]);
     }
 }
 
@@ -359,7 +415,7 @@ static hipError_t bwd_launch(const LatentBwdArgs &a, hipStream_t st)
     const int nq = (a.Tq + C::OWN - 1) / C::OWN, nk = (a.Tk + C::OWN - 1) / C::OWN;
     auto kkv = latent_bwd_kv_kernel<T, DN, DV>;
     auto kq = latent_bwd_q_kernel<T, DN, DV>;
-    const int lkv = 2 * C::BUF + 2 * C::ROWS, lq = 2 * C::BUF;
+    const int lkv = C::KV_LDS, lq = 2 * C::BUF;
     hipError_t e = hipFuncSetAttribute((const void *)kkv, hipFuncAttributeMaxDynamicSharedMemorySize, lkv);
     if (e == hipSuccess) e = hipFuncSetAttribute((const void *)kq, hipFuncAttributeMaxDynamicSharedMemorySize, lq);
     if (e != hipSuccess) return e;
@@ -370,7 +426,7 @@ static hipError_t bwd_launch(const LatentBwdArgs &a, hipStream_t st)
         hipLaunchKernelGGL(kq, dim3((unsigned)(BH * nq)), dim3(256), lq, st, a, nq);
     }
     if (krows > 0) {
-        hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk)), dim3(256), lkv, st, a, nk);
+        hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk)), dim3(512), lkv, st, a, nk);
         hipLaunchKernelGGL((latent_bwd_rope_kernel<T>), dim3((unsigned)((krows + 15) / 16)), dim3(256), 0, st,
                            (const float *)((const char *)a.ws + lay.rope), (T *)a.dk_rope, krows, a.H);
     }
