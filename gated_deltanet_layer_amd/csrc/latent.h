@@ -64,54 +64,60 @@ unsigned long long latent_step_workspace(bool bf16, int N, int M, int H, int r);
 // kind (512 fp32 values).
 static __device__ const uint4 latent_zero[128] = {};
 
-// LDS tiles are rows of CPR 16-byte chunks (a multiple of 8); the low three bits of
-// a chunk's index are XOR-ed with its row, so that eight rows read at one chunk
-// index fall on distinct banks.  The functions below split an address into a part
-// per lane, computed once, and one that folds into the instruction's offset.
+// LDS tiles are rows of CPR 16-byte chunks (8, or a multiple of 16); the chunk index
+// is XOR-ed with a function of the row.  The LDS serves 16 chunks (64 banks) a clock.
+// A 16-byte read goes by groups of 16 lanes, measured as {0-3, 12-15, 20-23, 24-27},
+// {4-11, 16-19, 28-31} and the same from 32 on: for row_frag, rows 0-3 and 12-15 at
+// one chunk index with rows 4-11 at the next.  col_frag reads eight rows at a pair of
+// chunks.  Both fall on 16 distinct slots of 256 bytes if what tells eight rows apart
+// moves whole pairs, and the row's bit 3 swaps the chunks of a pair and the halves of
+// the eight (with rows XOR-ed by their low bits alone, each row_frag took twice as
+// long).  The functions below split an address into a part per lane, computed once,
+// and one that folds into the instruction's offset.
+template <int CPR> __device__ __forceinline__ constexpr int swz(int row) {
+    static_assert(CPR == 8 || CPR % 16 == 0, "");
+    return CPR == 8 ? (((row >> 1) & 3) << 1) ^ (((row >> 3) & 1) * 5) : ((row & 7) << 1) ^ (((row >> 3) & 1) * 9);
+}
 
 // Operand with rows `row` (of this lane) and columns 32 kb + 8 gq .. +7.
 template <typename T, int CPR> __device__ __forceinline__ int row_base(int row) {
-    static_assert(CPR % 8 == 0, "rows are a multiple of 128 bytes");
     const int ch = sizeof(T) == 2 ? lane_gq() : 2 * lane_gq();
-    return row * (CPR * 16) + ((ch ^ (row & 7)) << 4);
+    return row * (CPR * 16) + ((ch ^ swz<CPR>(row)) << 4);
 }
 template <typename T> __device__ __forceinline__ Frag<T> row_frag(const char *M, int base, int kb) {
     if constexpr (sizeof(T) == 2) {
-        return {*reinterpret_cast<const bf16x8 *>(M + (base ^ ((kb & 1) << 6)) + (kb >> 1) * 128)};
+        return {*reinterpret_cast<const bf16x8 *>(M + (base ^ ((kb & 3) << 6)) + (kb >> 2) * 256)};
     } else {
-        return {*reinterpret_cast<const f32x4 *>(M + base + kb * 128),
-                *reinterpret_cast<const f32x4 *>(M + (base ^ 16) + kb * 128)};
+        base ^= (kb & 1) << 7;
+        M += (kb >> 1) * 256;
+        return {*reinterpret_cast<const f32x4 *>(M + base), *reinterpret_cast<const f32x4 *>(M + (base ^ 16))};
     }
 }
 
 // Operand with rows = columns 16 cb + r16 of the tile and contraction slots = tile
-// rows row + 0..3 and row + STEP + 0..3 (`row`: of this lane's group, a multiple of
-// 4 whose low three bits are those of the row given to col_base; STEP: 4 or 16).
+// rows row + 0..3 and row + 16 + 0..3 (`row`: 4 gq and a multiple of 16).
 template <typename T, int CPR> __device__ __forceinline__ int col_base(int row) {
     const int r16 = lane_r16();
     if constexpr (sizeof(T) == 2) {
         row += r16 >> 2;
-        return row * (CPR * 16) + ((((r16 & 3) >> 1) ^ (row & 7)) << 4) + 8 * (r16 & 1);
+        return row * (CPR * 16) + ((((r16 & 3) >> 1) ^ swz<CPR>(row)) << 4) + 8 * (r16 & 1);
     } else {
-        return row * (CPR * 16) + (((r16 >> 2) ^ (row & 7)) << 4) + 4 * (r16 & 3);
+        return row * (CPR * 16) + (((r16 >> 2) ^ swz<CPR>(row)) << 4) + 4 * (r16 & 3);
     }
 }
-template <typename T, int CPR, int STEP>
-__device__ __forceinline__ Frag<T> col_frag(const char *M, int base, int cb) {
-    static_assert(STEP == 4 || STEP == 16, "");
-    constexpr int FLIP = STEP == 4 ? 64 : 0;   // row + 4 has bit 2 of its low three bits changed
+template <typename T, int CPR> __device__ __forceinline__ Frag<T> col_frag(const char *M, int base, int cb) {
     if constexpr (sizeof(T) == 2) {
-        const int at = base ^ ((cb & 3) << 5);
-        const char *m = M + (cb >> 2) * 128;
-        return {cat8(lds_read_tr(lds_u32(m + at)), lds_read_tr(lds_u32(m + (at ^ FLIP) + STEP * CPR * 16)))};
+        const char *m = M + (base ^ ((cb & 7) << 5)) + (cb >> 3) * 256;
+        return {cat8(lds_read_tr(lds_u32(m)), lds_read_tr(lds_u32(m + 16 * CPR * 16)))};
     } else {
-        const int at = base ^ ((cb & 1) << 6);
-        const char *m = M + (cb >> 1) * 128;
+        static_assert(CPR % 16 == 0, "");
+        const int at = base ^ ((cb & 3) << 6);
+        const char *m = M + (cb >> 2) * 256;
         Frag<T> f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            f.lo[e] = *reinterpret_cast<const float *>(m + (at ^ (e << 4)) + e * CPR * 16);
-            f.hi[e] = *reinterpret_cast<const float *>(m + (at ^ (e << 4) ^ FLIP) + (STEP + e) * CPR * 16);
+        for (int e = 0; e < 4; ++e) {   // row + e: bits 1 and 2 of the chunk index
+            f.lo[e] = *reinterpret_cast<const float *>(m + (at ^ (e << 5)) + e * CPR * 16);
+            f.hi[e] = *reinterpret_cast<const float *>(m + (at ^ (e << 5)) + (16 + e) * CPR * 16);
         }
         return f;
     }
@@ -120,23 +126,25 @@ __device__ __forceinline__ Frag<T> col_frag(const char *M, int base, int cb) {
 // Enqueue the copy of rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes
 // apart, x: row 0) into an LDS tile by NTHR threads; rows from n on read as zeros.
 // One instruction of the workgroup covers NTHR / CPR rows, a multiple of 8, so the
-// lane's offset within them is the same for all.
+// lane's offset within them is the same for all, but for row bit 3 where it is 8.
 template <int CPR, int ROWS, int NTHR = 256>
 __device__ __forceinline__ void load_rows(char *tile, const char *x, long stride, int r0, int n)
 {
     constexpr int RP = NTHR / CPR;
     static_assert(RP % 8 == 0 && ROWS % RP == 0, "");
-    const int tid = threadIdx.x, row = tid / CPR, ch = (tid % CPR) ^ (row & 7);
+    const int tid = threadIdx.x, row = tid / CPR, ch = ((tid % CPR) ^ swz<CPR>(row)) * 16;
     char *dst = tile + (tid & ~63) * 16;
     const char *p = x + r0 * stride;
     if (r0 + ROWS <= n) {
-        const unsigned off = (unsigned)(row * (int)stride + ch * 16);
+        const unsigned off = (unsigned)(row * (int)stride + ch);
 #pragma unroll
-        for (int i = 0; i < ROWS / RP; ++i) g2lds16s(p + i * RP * stride, off, dst + i * NTHR * 16);
+        for (int i = 0; i < ROWS / RP; ++i)
+            g2lds16s(p + i * RP * stride, RP == 8 && (i & 1) ? (unsigned)(row * (int)stride + (ch ^ 144)) : off, dst + i * NTHR * 16);
     } else {
 #pragma unroll
         for (int i = 0; i < ROWS / RP; ++i) {
-            const char *src = r0 + i * RP + row < n ? p + (i * RP + row) * stride + ch * 16 : (const char *)latent_zero;
+            const char *src = r0 + i * RP + row < n ? p + (i * RP + row) * stride + (RP == 8 && (i & 1) ? ch ^ 144 : ch)
+                                                    : (const char *)latent_zero;
             g2lds16(src, dst + i * NTHR * 16);
         }
     }

@@ -21,27 +21,17 @@ struct BwdWs {
     }
 };
 
-// D_i = do_i . o_i, one wave 64 / (DV / 8) rows at a time.
-template <typename T, int DV>
-__global__ __launch_bounds__(256) void latent_bwd_dot_kernel(const T *o, const T *d_o, float *D, long nrows)
-{
-    constexpr int LPR = DV / 8;   // lanes a row, 8 values each
-    const long row = ((long)blockIdx.x * 256 + threadIdx.x) / LPR;
-    const int at = (threadIdx.x % LPR) * 8;
+// This lane's share of a row's do . o (the four 16-lane rows hold its columns).
+template <typename T> __device__ __forceinline__ float frag_dot(const Frag<T> &x, const Frag<T> &y) {
     float s = 0.f;
-    if (row < nrows) {
-        const Frag<T> x = load_frag<T>(o + row * DV + at), y = load_frag<T>(d_o + row * DV + at);
-        if constexpr (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += (float)x.v[e] * (float)y.v[e];
-        } else {
+        for (int e = 0; e < 8; ++e) s += (float)x.v[e] * (float)y.v[e];
+    } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s += x.lo[e] * y.lo[e] + x.hi[e] * y.hi[e];
-        }
+        for (int e = 0; e < 4; ++e) s += x.lo[e] * y.lo[e] + x.hi[e] * y.hi[e];
     }
-#pragma unroll
-    for (int d = LPR / 2; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
-    if (row < nrows && at == 0) D[row] = s;
+    return s;
 }
 
 // dk_rope[b][t] = sum over heads, in order.
@@ -200,7 +190,7 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
             for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
 #pragma unroll
             for (int v = 0; v < NVC; ++v) {
-                const Frag<T> f = col_frag<T, C::VCPR, 16>(dt + 32 * t * C::VCPR * 16, vc, v);
+                const Frag<T> f = col_frag<T, C::VCPR>(dt + 32 * t * C::VCPR * 16, vc, v);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dv[v][g] = mma(dv[v][g], f, pf[g]);
             }
@@ -259,8 +249,8 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
             for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
 #pragma unroll
             for (int v = 0; v < NKC; ++v) {
-                const Frag<T> f = v < DN / 16 ? col_frag<T, C::NCPR, 16>(qt + 32 * t * C::NCPR * 16, nc, v)
-                                              : col_frag<T, C::RCPR, 16>(qt + C::OFF_R + 32 * t * C::RCPR * 16, rc, v - DN / 16);
+                const Frag<T> f = v < DN / 16 ? col_frag<T, C::NCPR>(qt + 32 * t * C::NCPR * 16, nc, v)
+                                              : col_frag<T, C::RCPR>(qt + C::OFF_R + 32 * t * C::RCPR * 16, rc, v - DN / 16);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dk[v][g] = mma(dk[v][g], f, sf[g]);
             }
@@ -281,9 +271,9 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
     }
 }
 
-// dq.  A wave owns 16 NG query rows, q and do of them in registers; scores are
-// transposed as in the forward pass, and dS^T feeds dq^T = K^T dS^T from the
-// registers.
+// dq, and D for the kernel above, which is launched after this one.  A wave owns 16
+// NG query rows, q and do of them in registers; scores are transposed as in the
+// forward pass, and dS^T feeds dq^T = K^T dS^T from the registers.
 template <typename T, int DN, int DV>
 __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, int ntiles)
 {
@@ -301,7 +291,9 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
     const T *d_o = (const T *)a.d_o + ((long)b * a.Tq * a.H + h) * DV;
     const T *kv = (const T *)a.kv + ((long)b * a.Tk * a.H + h) * (DN + DV);
     const T *kr = (const T *)a.k_rope + (long)b * a.Tk * LATENT_ROPE;
-    const float *lse = a.lse + (long)b * a.Tq * a.H + h, *Dw = (const float *)a.ws + (long)b * a.Tq * a.H + h;
+    const T *o = (const T *)a.o + ((long)b * a.Tq * a.H + h) * DV;
+    const float *lse = a.lse + (long)b * a.Tq * a.H + h;
+    float *Dw = (float *)a.ws + (long)b * a.Tq * a.H + h;
     const float c = a.scale * LOG2E;
 
     int pos[NG];
@@ -313,13 +305,18 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
         const bool live = row < a.Tq && off + row < n;
         pos[g] = live ? off + row : -1;
         ls[g] = live ? lse[(long)row * a.H] * LOG2E : 0.f;
-        dd[g] = live ? Dw[(long)row * a.H] : 0.f;
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb)
             qf[g][kb] = live ? load_frag<T>(q + row * qs + 32 * kb + 8 * gq) : zero_frag<T>();
 #pragma unroll
         for (int v = 0; v < NVB; ++v)
             of[g][v] = live ? load_frag<T>(d_o + row * os + 32 * v + 8 * gq) : zero_frag<T>();
+        float dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < NVB; ++v)
+            if (live) dot += frag_dot<T>(of[g][v], load_frag<T>(o + row * os + 32 * v + 8 * gq));
+        dd[g] = rows_sum(dot);
+        if (live && gq == 0) Dw[(long)row * a.H] = dd[g];
     }
     f32x4 dq[NKC][NG];
 #pragma unroll
@@ -387,8 +384,8 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
             for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
 #pragma unroll
             for (int i = 0; i < NKC; ++i) {
-                const Frag<T> f = i < DN / 16 ? col_frag<T, C::NCPR, 16>(kt + 32 * t * C::NCPR * 16, nc, i)
-                                              : col_frag<T, C::RCPR, 16>(kt + C::OFF_R + 32 * t * C::RCPR * 16, rc, i - DN / 16);
+                const Frag<T> f = i < DN / 16 ? col_frag<T, C::NCPR>(kt + 32 * t * C::NCPR * 16, nc, i)
+                                              : col_frag<T, C::RCPR>(kt + C::OFF_R + 32 * t * C::RCPR * 16, rc, i - DN / 16);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dq[i][g] = mma(dq[i][g], f, sf[g]);
                 if (i % 2 == 1) GDN_SCHED_FENCE();
@@ -411,7 +408,7 @@ static hipError_t bwd_launch(const LatentBwdArgs &a, hipStream_t st)
 {
     typedef BwdCfg<T, DN, DV> C;
     const BwdWs lay(a.B, a.Tq, a.Tk, a.H);
-    const long BH = (long)a.B * a.H, qrows = BH * a.Tq, krows = (long)a.B * a.Tk;
+    const long BH = (long)a.B * a.H, krows = (long)a.B * a.Tk;
     const int nq = (a.Tq + C::OWN - 1) / C::OWN, nk = (a.Tk + C::OWN - 1) / C::OWN;
     auto kkv = latent_bwd_kv_kernel<T, DN, DV>;
     auto kq = latent_bwd_q_kernel<T, DN, DV>;
@@ -419,17 +416,11 @@ static hipError_t bwd_launch(const LatentBwdArgs &a, hipStream_t st)
     hipError_t e = hipFuncSetAttribute((const void *)kkv, hipFuncAttributeMaxDynamicSharedMemorySize, lkv);
     if (e == hipSuccess) e = hipFuncSetAttribute((const void *)kq, hipFuncAttributeMaxDynamicSharedMemorySize, lq);
     if (e != hipSuccess) return e;
-    float *D = (float *)a.ws;
-    if (qrows > 0) {
-        hipLaunchKernelGGL((latent_bwd_dot_kernel<T, DV>), dim3((unsigned)((qrows * (DV / 8) + 255) / 256)), dim3(256), 0, st,
-                           (const T *)a.o, (const T *)a.d_o, D, qrows);
-        hipLaunchKernelGGL(kq, dim3((unsigned)(BH * nq)), dim3(256), lq, st, a, nq);
-    }
-    if (krows > 0) {
-        hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk)), dim3(512), lkv, st, a, nk);
+    if (BH * nq > 0) hipLaunchKernelGGL(kq, dim3((unsigned)(BH * nq)), dim3(256), lq, st, a, nq);
+    if (BH * nk > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk)), dim3(512), lkv, st, a, nk);
+    if (krows > 0)
         hipLaunchKernelGGL((latent_bwd_rope_kernel<T>), dim3((unsigned)((krows + 15) / 16)), dim3(256), 0, st,
                            (const float *)((const char *)a.ws + lay.rope), (T *)a.dk_rope, krows, a.H);
-    }
     return hipGetLastError();
 }
 

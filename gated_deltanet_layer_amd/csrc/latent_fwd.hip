@@ -141,7 +141,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
             for (int g = 0; g < NR; ++g) pf[g] = reg_frag<T>(s[t][g], s[t + 1][g]);
 #pragma unroll
             for (int cb = 0; cb < NCB; ++cb) {
-                const Frag<T> vf = col_frag<T, C::VCPR, 16>(vt + 16 * t * C::VCPR * 16, vb, cb);
+                const Frag<T> vf = col_frag<T, C::VCPR>(vt + 16 * t * C::VCPR * 16, vb, cb);
 #pragma unroll
                 for (int g = 0; g < NR; ++g) acc[cb][g] = mma(acc[cb][g], vf, pf[g]);
             }

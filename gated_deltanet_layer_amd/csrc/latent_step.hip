@@ -32,13 +32,13 @@ template <typename T, int R, bool SPLIT, int G, int NW> struct StepCfg {
     static constexpr int ES = (int)sizeof(T), CPR = R * ES / 16, RCPR = LATENT_ROPE * ES / 16;
     static constexpr int OFF_R = KT * CPR * 16;             // a tile: [KT][R] latents, [KT][64] rotary keys
     static constexpr int TILE = OFF_R + KT * RCPR * 16;
-    static constexpr int PCPR = KT * ES / 16;               // 8
-    static constexpr int OFF_P = 2 * TILE;                  // weights [RT][KT]
-    static constexpr int OFF_MX = OFF_P + (SPLIT ? RT * PCPR * 16 : 0);   // [NS][RT] maxima, then sums
+    static constexpr int PF = 64 * 8 * ES;                  // an operand of weights: 16 rows, 32 keys
+    static constexpr int OFF_P = 2 * TILE;                  // [G][KT / 32] of them
+    static constexpr int OFF_MX = OFF_P + (SPLIT ? G * KT / 32 * PF : 0);   // [NS][RT] maxima, then sums
     static constexpr int OFF_KV = OFF_MX + (SPLIT ? NS * RT * 4 : 0);     // [2][KT] bytes: key is there
     static constexpr int OFF_SCAN = OFF_KV + 2 * KT;        // [NW + 2] ints
     static constexpr int BYTES = OFF_SCAN + (NW + 2) * 4;
-    static_assert(PCPR == 8 && BYTES <= 160 * 1024 && (!SPLIT || NS <= NW), "");
+    static_assert(BYTES <= 160 * 1024 && (!SPLIT || NS <= NW), "");
 };
 
 // Rows of a workgroup.  fp32 has registers for 16.
@@ -184,19 +184,19 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
                 const char *q = (const char *)(((uintptr_t)rhi << 32) | rlo);
 #pragma unroll
                 for (int k = 0; k < CPR / 64; ++k)
-                    g2lds16s(q, (unsigned)((k * 64 + (lane ^ ((wave * WR + i) & 7))) * 16), dst + (i * CPR / 64 + k) * 1024);
+                    g2lds16s(q, (unsigned)((k * 64 + (lane ^ swz<CPR>(wave * WR + i))) * 16), dst + (i * CPR / 64 + k) * 1024);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < WR * CPR / 64; ++i) {
                 const int row = i * (64 / CPR) + lane / CPR;
-                g2lds16(row_ptr(row) + (((lane % CPR) ^ ((wave * WR + row) & 7)) * 16), dst + i * 1024);
+                g2lds16(row_ptr(row) + ((lane % CPR) ^ swz<CPR>(wave * WR + row)) * 16, dst + i * 1024);
             }
         }
         char *rdst = lds + buf * C::TILE + C::OFF_R + wave * WR * C::RCPR * 16;
 #pragma unroll
         for (int i = 0; i < WR * C::RCPR / 64; ++i) {
-            const int row = i * (64 / C::RCPR) + lane / C::RCPR, ch = (lane % C::RCPR) ^ ((wave * WR + row) & 7);
+            const int row = i * (64 / C::RCPR) + lane / C::RCPR, ch = (lane % C::RCPR) ^ swz<C::RCPR>(wave * WR + row);
             const char *q = row_ptr(row);   // a row that is not there: the first of the zeros
             g2lds16(__shfl((int)there, row, 64) ? q + R * C::ES + ch * 16 : q, rdst + i * 1024);
         }
@@ -205,10 +205,12 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
     // lane parts of the LDS addresses; first product: this wave's slab of keys (SPLIT)
     const int slab = SPLIT ? wave : 0, row0 = SPLIT ? 0 : wave * 16 * G;
     const int nb = row_base<T, CPR>(16 * slab + r16), rb = row_base<T, C::RCPR>(16 * slab + r16);
-    constexpr int PC = 8 / C::ES;   // 16-column blocks in 128 bytes
-    static_assert(CB % PC == 0, "a wave's columns begin at whole 128 bytes");
-    const int vb = col_base<T, CPR>(SPLIT ? 8 * gq : 4 * gq), pb = row_base<T, C::PCPR>(r16);
-    const int vcol = SPLIT ? wave * CB / PC * 128 : 0;
+    // second product: this wave's first 16-column block, as a part inside 256 bytes
+    // and whole ones
+    constexpr int PC = 16 / C::ES;
+    static_assert(CB % PC == 0 || PC % CB == 0, "");
+    const int col0 = SPLIT ? wave * CB : 0;
+    const int vb = col_base<T, CPR>(4 * gq) ^ (col0 % PC * 16 * C::ES), vcol = col0 / PC * 256;
     Frag<T> qf[G][NKB];
     unsigned long long bits[G];
     f32x4 acc[CB][G];
@@ -307,8 +309,8 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
                         p[e] = exp2_hw(__builtin_fmaf(s[rg][e], c, -mb));
                         l[rg] += p[e];
                     }
-                    const int row = 16 * rg + r16, col = 16 * wave + 4 * gq, ch = col * C::ES / 16, sub = col * C::ES & 15;
-                    store4((T *)(lds + C::OFF_P + (row * C::PCPR + (ch ^ (row & 7))) * 16 + sub), p);
+                    // as the lane's own half of the operand of 32 keys
+                    store4((T *)(lds + C::OFF_P + (rg * KT / 32 + wave / 2) * C::PF + lane * 8 * C::ES) + 4 * (wave & 1), p);
                 }
             }
             lds_barrier();
@@ -316,10 +318,10 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
             for (int kk = 0; kk < KT / 32; ++kk) {
                 Frag<T> pf[G];
 #pragma unroll
-                for (int rg = 0; rg < G; ++rg) pf[rg] = row_frag<T>(lds + C::OFF_P + 16 * rg * C::PCPR * 16, pb, kk);
+                for (int rg = 0; rg < G; ++rg) pf[rg] = load_frag<T>((const T *)(lds + C::OFF_P + (rg * KT / 32 + kk) * C::PF) + lane * 8);
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
-                    const Frag<T> vf = col_frag<T, CPR, 4>(tile + 32 * kk * CPR * 16 + vcol, vb, cb);
+                    const Frag<T> vf = col_frag<T, CPR>(tile + 32 * kk * CPR * 16 + vcol, vb, cb);
 #pragma unroll
                     for (int rg = 0; rg < G; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
                 }
@@ -384,7 +386,7 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
                 for (int rg = 0; rg < G; ++rg) pf[rg] = reg_frag<T>(s[t][rg], s[t + 1][rg]);
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
-                    const Frag<T> vf = col_frag<T, CPR, 16>(tile + 16 * t * CPR * 16, vb, cb);
+                    const Frag<T> vf = col_frag<T, CPR>(tile + 16 * t * CPR * 16, vb, cb);
 #pragma unroll
                     for (int rg = 0; rg < G; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
                     if (cb % 4 == 3) GDN_SCHED_FENCE();
