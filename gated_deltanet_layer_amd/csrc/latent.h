@@ -49,6 +49,8 @@ struct LatentStepArgs {
     float scale;
     int N, M, H, drafts;          // drafts: M, or 0 without drafted rows
     int pages, page, width;       // pages in the cache, tokens a page, table columns
+    unsigned page_mul;            // t / page = t page_mul >> page_shift for t < 2^30 (set by the launcher)
+    int page_shift;
 };
 
 hipError_t latent_fwd_launch(bool bf16, int dn, int dv, const LatentFwdArgs &a, hipStream_t st);

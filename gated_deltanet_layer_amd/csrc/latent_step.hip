@@ -20,31 +20,46 @@ namespace gdn {
 
 constexpr int STEP_CUS = 256;   // one workgroup a compute unit: two tiles fill its LDS
 
-// SPLIT: the waves divide each tile's keys for the scores and the output columns for
-// the second product, every wave for all 16 G rows.  Otherwise every wave owns 16 G
-// rows and takes all keys and columns for them.
-template <typename T, int R, bool SPLIT, int G, int NW> struct StepCfg {
-    static constexpr int NTHR = 64 * NW, D = R + LATENT_ROPE;
-    static constexpr int RT = SPLIT ? 16 * G : 16 * G * NW;
+// Up to 32 rows: four waves divide each tile's keys for the scores and the output
+// columns for the second product, every wave for all 16 G rows.
+template <typename T, int R, int G> struct StepCfg {
+    static constexpr int NW = 4, D = R + LATENT_ROPE, RT = 16 * G;
     static constexpr int KT = sizeof(T) == 2 ? 64 : 32;
     static constexpr int NS = KT / 16;                      // 16-key slabs
-    static constexpr int CB = SPLIT ? R / 16 / NW : R / 16; // 16-column blocks of the output a wave
+    static constexpr int CB = R / 16 / NW;                  // 16-column blocks of the output a wave
     static constexpr int ES = (int)sizeof(T), CPR = R * ES / 16, RCPR = LATENT_ROPE * ES / 16;
     static constexpr int OFF_R = KT * CPR * 16;             // a tile: [KT][R] latents, [KT][64] rotary keys
     static constexpr int TILE = OFF_R + KT * RCPR * 16;
     static constexpr int PF = 64 * 8 * ES;                  // an operand of weights: 16 rows, 32 keys
     static constexpr int OFF_P = 2 * TILE;                  // [G][KT / 32] of them
-    static constexpr int OFF_MX = OFF_P + (SPLIT ? G * KT / 32 * PF : 0);   // [NS][RT] maxima, then sums
-    static constexpr int OFF_KV = OFF_MX + (SPLIT ? NS * RT * 4 : 0);     // [2][KT] bytes: key is there
+    static constexpr int OFF_MX = OFF_P + G * KT / 32 * PF; // [NS][RT] maxima, then sums
+    static constexpr int OFF_KV = OFF_MX + NS * RT * 4;     // [2][KT] bytes: key is there
     static constexpr int OFF_SCAN = OFF_KV + 2 * KT;        // [NW + 2] ints
     static constexpr int BYTES = OFF_SCAN + (NW + 2) * 4;
-    static_assert(BYTES <= 160 * 1024 && (!SPLIT || NS <= NW), "");
+    static_assert(BYTES <= 160 * 1024, "");
+};
+
+// More rows (bf16): 64 a workgroup, four waves for the scores, four for the second
+// product; see latent_step_wide_kernel.
+template <int R> struct WideCfg {
+    static constexpr int D = R + LATENT_ROPE, RT = 64, KT = 32, NB = 4;   // NB tile buffers
+    static constexpr int CB = R / 64;
+    static constexpr int CPR = R / 8, RCPR = LATENT_ROPE / 8;
+    static constexpr int OFF_R = KT * CPR * 16, TILE = OFF_R + KT * RCPR * 16;
+    static constexpr int OFF_P = NB * TILE;                 // [2][4] operands of weights, 1 KB each
+    static constexpr int OFF_AL = OFF_P + 2 * 4 * 1024;     // [2][64] factors of a raised maximum
+    static constexpr int OFF_FIN = OFF_AL + 2 * 64 * 4;     // [2][2][64] sums and maxima of a finished sequence
+    static constexpr int OFF_KV = OFF_FIN + 2 * 2 * 64 * 4; // [NB][KT] bytes: key is there
+    static constexpr int OFF_ID = OFF_KV + NB * KT;         // [4][KT] pages
+    static constexpr int OFF_SCAN = OFF_ID + 4 * KT * 4;    // [8 + 2] ints
+    static constexpr int BYTES = OFF_SCAN + 10 * 4;
+    static_assert(BYTES <= 160 * 1024, "");
 };
 
 // Rows of a workgroup.  fp32 has registers for 16.
 __host__ __device__ inline int step_rt(bool bf16, int rows)
 {
-    return !bf16 || rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    return !bf16 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 // Workgroups that may share the key tiles of one row tile.
@@ -76,24 +91,30 @@ struct StepPos {
     int n, t, len, nkt;
 };
 
-template <typename T, int R, bool SPLIT, int G, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs a, int ntile, int max_shares)
+// The tile after p; called only while one is left.
+template <int KT> __device__ __forceinline__ StepPos step_after(const LatentStepArgs &a, StepPos p)
 {
-    typedef StepCfg<T, R, SPLIT, G, NW> C;
-    constexpr int D = C::D, KT = C::KT, RT = C::RT, NKB = D / 32, NS = C::NS, CPR = C::CPR, CB = C::CB;
-    extern __shared__ char lds[];
-    const int share = blockIdx.x % max_shares, rt = blockIdx.x / max_shares;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), r16 = lane_r16(), gq = lane_gq();
-    const int rows = a.M * a.H;
-    const float c = a.scale * LOG2E;
-    const StepWs lay(a.N, ntile, RT, R);
-    int *prefix = (int *)a.ws;
-    float *part = (float *)((char *)a.ws + lay.part);
+    if (++p.t == p.nkt) {
+        p.t = 0;
+        do {
+            ++p.n;
+            p.len = __builtin_amdgcn_readfirstlane(step_len(a, p.n));
+            p.nkt = step_tiles(p.len, a.drafts, KT);
+        } while (p.nkt == 0 && p.n + 1 < a.N);
+    }
+    return p;
+}
 
-    // tiles before each sequence: every thread adds up a run of sequences, then a scan
-    int *scan = (int *)(lds + C::OFF_SCAN);
-    const int per = (a.N + C::NTHR - 1) / C::NTHR, s0 = min(a.N, tid * per), s1 = min(a.N, s0 + per);
+// This workgroup's share [g0, g1) of all key tiles and its first tile; false if it
+// has none.  Every thread adds up the tiles of a run of sequences, then a scan over
+// the workgroup; `first` also writes the tiles before each sequence for the join.
+// scan: [NW + 2] ints of LDS.
+template <int NW, int KT>
+__device__ __forceinline__ bool step_share(const LatentStepArgs &a, int share, int max_shares, bool first, int *scan,
+                                           int &g0, int &g1, StepPos &cur)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int per = (a.N + 64 * NW - 1) / (64 * NW), s0 = min(a.N, tid * per), s1 = min(a.N, s0 + per);
     int mine = 0;
     for (int n = s0; n < s1; ++n) mine += step_tiles(step_len(a, n), a.drafts, KT);
     int incl = mine;
@@ -112,16 +133,17 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
     }
     total = __builtin_amdgcn_readfirstlane(total);
     const int shares = min(max_shares, total);   // none without a tile
-    if (share == 0 && rt == 0) {
-        int at = incl - mine;
+    if (first) {
+        int *prefix = (int *)a.ws, at = incl - mine;
         for (int n = s0; n < s1; ++n) {
             prefix[n] = at;
             at += step_tiles(step_len(a, n), a.drafts, KT);
         }
         if (tid == 0) prefix[a.N] = total;
     }
-    if (share >= shares) return;
-    const int g0 = (int)((long)share * total / shares), g1 = (int)((long)(share + 1) * total / shares);
+    if (share >= shares) return false;
+    g0 = (int)((long)share * total / shares);
+    g1 = (int)((long)(share + 1) * total / shares);
     if (g0 >= incl - mine && g0 < incl) {
         int at = incl - mine;
         for (int n = s0; n < s1; ++n) {
@@ -134,23 +156,71 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
         }
     }
     __syncthreads();
-
-    StepPos cur, nxt;
     cur.n = __builtin_amdgcn_readfirstlane(scan[NW]);
     cur.t = __builtin_amdgcn_readfirstlane(scan[NW + 1]);
     cur.len = __builtin_amdgcn_readfirstlane(step_len(a, cur.n));
     cur.nkt = step_tiles(cur.len, a.drafts, KT);
-    auto after = [&](StepPos p) {   // called only while a tile is left
-        if (++p.t == p.nkt) {
-            p.t = 0;
-            do {
-                ++p.n;
-                p.len = __builtin_amdgcn_readfirstlane(step_len(a, p.n));
-                p.nkt = step_tiles(p.len, a.drafts, KT);
-            } while (p.nkt == 0 && p.n + 1 < a.N);
-        }
-        return p;
-    };
+    return true;
+}
+
+__device__ __forceinline__ int step_page(const LatentStepArgs &a, int t) {
+    return (int)(((unsigned long long)(unsigned)t * a.page_mul) >> a.page_shift);
+}
+
+// Row of key `key` of p's sequence and whether it is there; id: its page.
+template <int ROWB>
+__device__ __forceinline__ const char *step_row(const LatentStepArgs &a, const StepPos &p, int key, int id, bool &there)
+{
+    there = false;
+    if (key < p.len) {
+        there = id >= 0 && id < a.pages;   // any other page holds nothing
+        if (there) return (const char *)a.cache + ((long)id * a.page + (key - step_page(a, key) * a.page)) * ROWB;
+    } else if (key - p.len < a.drafts) {
+        there = true;
+        return (const char *)a.draft + ((long)p.n * a.M + (key - p.len)) * ROWB;
+    }
+    return (const char *)latent_zero;
+}
+
+// -inf where the row does not see the key: s of keys first .. first + 3, `there` their
+// flags, bit: the drafts that the row sees.  Without branches: the compiler has lost
+// the masked value of a vector element that two nested ones decide.
+__device__ __forceinline__ f32x4 step_mask(f32x4 s, unsigned there, int first, int len, unsigned long long bit)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int d = first + e - len;
+        const unsigned in = d < 0 ? 1u : (unsigned)(bit >> (d & 63));
+        s[e] = (in & (there >> (8 * e)) & 1u) ? s[e] : -INFINITY;
+    }
+    return s;
+}
+
+// The drafts that query row `row` of sequence n sees.
+__device__ __forceinline__ unsigned long long step_bits(const LatentStepArgs &a, int n, int row, bool live)
+{
+    if (!live || !a.drafts) return 0ull;
+    const int node = row / a.H;
+    if (a.tree) return (unsigned long long)a.tree[(long)n * a.M + node];
+    return node >= 63 ? ~0ull : (2ull << node) - 1;
+}
+
+template <typename T, int R, int G>
+__global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, int ntile, int max_shares)
+{
+    typedef StepCfg<T, R, G> C;
+    constexpr int D = C::D, KT = C::KT, RT = C::RT, NKB = D / 32, NS = C::NS, CPR = C::CPR, CB = C::CB, NW = C::NW;
+    extern __shared__ char lds[];
+    const int share = blockIdx.x % max_shares, rt = blockIdx.x / max_shares;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int rows = a.M * a.H;
+    const float c = a.scale * LOG2E;
+    float *part = (float *)((char *)a.ws + StepWs(a.N, ntile, RT, R).part);
+    int g0, g1;
+    StepPos cur, nxt;
+    if (!step_share<NW, KT>(a, share, max_shares, share == 0 && rt == 0, (int *)(lds + C::OFF_SCAN), g0, g1, cur)) return;
+
     // The wave copies WR rows of a tile; its lanes look up one each (lanes beyond
     // WR repeat them): page() the page of the lane's row, a tile ahead of its use,
     // load_tile() the copies into buffer `buf`.
@@ -158,19 +228,12 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
     const int krow = wave * WR + (lane & (WR - 1));
     auto page = [&](const StepPos &p) {
         const int key = p.t * KT + krow;
-        return key < p.len ? a.table[(long)p.n * a.width + key / a.page] : -1;
+        return key < p.len ? a.table[(long)p.n * a.width + step_page(a, key)] : -1;
     };
     auto load_tile = [&](const StepPos &p, int id, int buf) {
         const int key = p.t * KT + krow;
-        const char *src = (const char *)latent_zero;
-        bool there = false;
-        if (key < p.len) {
-            there = id >= 0 && id < a.pages;   // any other page holds nothing
-            if (there) src = (const char *)a.cache + ((long)id * a.page + key % a.page) * (D * C::ES);
-        } else if (key - p.len < a.drafts) {
-            there = true;
-            src = (const char *)a.draft + ((long)p.n * a.M + (key - p.len)) * (D * C::ES);
-        }
+        bool there;
+        const char *src = step_row<D * C::ES>(a, p, key, id, there);
         if (lane < WR) lds[C::OFF_KV + buf * KT + krow] = there;
         const int lo = (int)(uintptr_t)src, hi = (int)((uintptr_t)src >> 32);
         auto row_ptr = [&](int row) {   // of a row that differs by lane
@@ -202,14 +265,13 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
         }
     };
 
-    // lane parts of the LDS addresses; first product: this wave's slab of keys (SPLIT)
-    const int slab = SPLIT ? wave : 0, row0 = SPLIT ? 0 : wave * 16 * G;
-    const int nb = row_base<T, CPR>(16 * slab + r16), rb = row_base<T, C::RCPR>(16 * slab + r16);
+    // lane parts of the LDS addresses; first product: this wave's slab of keys
+    const int nb = row_base<T, CPR>(16 * wave + r16), rb = row_base<T, C::RCPR>(16 * wave + r16);
     // second product: this wave's first 16-column block, as a part inside 256 bytes
     // and whole ones
     constexpr int PC = 16 / C::ES;
     static_assert(CB % PC == 0 || PC % CB == 0, "");
-    const int col0 = SPLIT ? wave * CB : 0;
+    const int col0 = wave * CB;
     const int vb = col_base<T, CPR>(4 * gq) ^ (col0 % PC * 16 * C::ES), vcol = col0 / PC * 256;
     Frag<T> qf[G][NKB];
     unsigned long long bits[G];
@@ -219,23 +281,20 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
     bool fresh = true;
     load_tile(cur, idn, 0);
     if (g0 + 1 < g1) {
-        nxt = after(cur);
+        nxt = step_after<KT>(a, cur);
         idn = page(nxt);
     }
     for (int g = g0;; ++g, buf ^= 1) {
         if (fresh) {
 #pragma unroll
             for (int rg = 0; rg < G; ++rg) {
-                const int row = rt * RT + row0 + 16 * rg + r16;
+                const int row = rt * RT + 16 * rg + r16;
                 const bool live = row < rows;
                 const T *q = (const T *)a.q + ((long)cur.n * rows + (live ? row : 0)) * D;
 #pragma unroll
                 for (int kb = 0; kb < NKB; ++kb)
                     qf[rg][kb] = live ? load_frag<T>(q + 32 * kb + 8 * gq) : zero_frag<T>();
-                const int node = row / a.H;
-                bits[rg] = !live || !a.drafts ? 0ull
-                         : a.tree ? (unsigned long long)a.tree[(long)cur.n * a.M + node]
-                         : node >= 63 ? ~0ull : (2ull << node) - 1;
+                bits[rg] = step_bits(a, cur.n, row, live);
                 m[rg] = -INFINITY;
                 l[rg] = 0.f;
 #pragma unroll
@@ -247,189 +306,108 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
         wait_vm<0>();
         lds_barrier();
         StepPos aft = nxt;
-        if (g + 2 < g1) aft = after(nxt);
+        if (g + 2 < g1) aft = step_after<KT>(a, nxt);
         if (more) load_tile(nxt, idn, buf ^ 1);
         if (g + 2 < g1) idn = page(aft);
 
-        const char *tile = lds + buf * C::TILE, *there4 = lds + C::OFF_KV + buf * KT + 16 * slab + 4 * gq;
-        const int key = cur.t * KT + 16 * slab + 4 * gq;   // first of this lane's four, in the first slab
-        // -inf where the row does not see the key.  Without branches: the compiler
-        // has lost the masked value of a vector element that two nested ones decide.
-        auto mask = [&](f32x4 s, unsigned there, int first, unsigned long long bit) {
+        const char *tile = lds + buf * C::TILE, *there4 = lds + C::OFF_KV + buf * KT + 16 * wave + 4 * gq;
+        const int key = cur.t * KT + 16 * wave + 4 * gq;   // first of this lane's four, in the first slab
+        float *mx = (float *)(lds + C::OFF_MX);
+        f32x4 s[G];
+        if (wave < NS) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = first + e - cur.len;
-                const unsigned in = d < 0 ? 1u : (unsigned)(bit >> (d & 63));
-                s[e] = (in & (there >> (8 * e)) & 1u) ? s[e] : -INFINITY;
+            for (int rg = 0; rg < G; ++rg) s[rg] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const Frag<T> kf = kb < R / 32 ? row_frag<T>(tile, nb, kb) : row_frag<T>(tile + C::OFF_R, rb, kb - R / 32);
+#pragma unroll
+                for (int rg = 0; rg < G; ++rg) s[rg] = mma(s[rg], kf, qf[rg][kb]);
             }
-            return s;
-        };
-        if constexpr (SPLIT) {
-            float *mx = (float *)(lds + C::OFF_MX);
-            f32x4 s[G];
+            const unsigned there = *reinterpret_cast<const unsigned *>(there4);
+            if (__any(there != 0x01010101u || key + 3 >= cur.len)) {
+#pragma unroll
+                for (int rg = 0; rg < G; ++rg) s[rg] = step_mask(s[rg], there, key, cur.len, bits[rg]);
+            }
+#pragma unroll
+            for (int rg = 0; rg < G; ++rg) {
+                const float t = rows_max(fmaxf(fmaxf(s[rg][0], s[rg][1]), fmaxf(s[rg][2], s[rg][3])));
+                if (gq == 0) mx[wave * RT + 16 * rg + r16] = t;
+            }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int rg = 0; rg < G; ++rg) {
+            float t = mx[16 * rg + r16];
+#pragma unroll
+            for (int w = 1; w < NS; ++w) t = fmaxf(t, mx[w * RT + 16 * rg + r16]);
+            const bool up = (t - m[rg]) * c > RAISE;   // false while both are -inf
+            if (__any(up)) {
+                const float mn = up ? t : m[rg], al = up ? exp2_hw((m[rg] - mn) * c) : 1.f;
+                m[rg] = mn;
+                l[rg] *= al;
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) acc[cb][rg] *= al;
+            }
             if (wave < NS) {
-#pragma unroll
-                for (int rg = 0; rg < G; ++rg) s[rg] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    const Frag<T> kf = kb < R / 32 ? row_frag<T>(tile, nb, kb) : row_frag<T>(tile + C::OFF_R, rb, kb - R / 32);
-#pragma unroll
-                    for (int rg = 0; rg < G; ++rg) s[rg] = mma(s[rg], kf, qf[rg][kb]);
-                }
-                const unsigned there = *reinterpret_cast<const unsigned *>(there4);
-                if (__any(there != 0x01010101u || key + 3 >= cur.len)) {
-#pragma unroll
-                    for (int rg = 0; rg < G; ++rg) s[rg] = mask(s[rg], there, key, bits[rg]);
-                }
-#pragma unroll
-                for (int rg = 0; rg < G; ++rg) {
-                    const float t = rows_max(fmaxf(fmaxf(s[rg][0], s[rg][1]), fmaxf(s[rg][2], s[rg][3])));
-                    if (gq == 0) mx[wave * RT + 16 * rg + r16] = t;
-                }
-            }
-            lds_barrier();
-#pragma unroll
-            for (int rg = 0; rg < G; ++rg) {
-                float t = mx[16 * rg + r16];
-#pragma unroll
-                for (int w = 1; w < NS; ++w) t = fmaxf(t, mx[w * RT + 16 * rg + r16]);
-                const bool up = (t - m[rg]) * c > RAISE;   // false while both are -inf
-                if (__any(up)) {
-                    const float mn = up ? t : m[rg], al = up ? exp2_hw((m[rg] - mn) * c) : 1.f;
-                    m[rg] = mn;
-                    l[rg] *= al;
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) acc[cb][rg] *= al;
-                }
-                if (wave < NS) {
-                    const float mb = m[rg] == -INFINITY ? 0.f : m[rg] * c;
-                    f32x4 p;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = exp2_hw(__builtin_fmaf(s[rg][e], c, -mb));
-                        l[rg] += p[e];
-                    }
-                    // as the lane's own half of the operand of 32 keys
-                    store4((T *)(lds + C::OFF_P + (rg * KT / 32 + wave / 2) * C::PF + lane * 8 * C::ES) + 4 * (wave & 1), p);
-                }
-            }
-            lds_barrier();
-#pragma unroll
-            for (int kk = 0; kk < KT / 32; ++kk) {
-                Frag<T> pf[G];
-#pragma unroll
-                for (int rg = 0; rg < G; ++rg) pf[rg] = load_frag<T>((const T *)(lds + C::OFF_P + (rg * KT / 32 + kk) * C::PF) + lane * 8);
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                    const Frag<T> vf = col_frag<T, CPR>(tile + 32 * kk * CPR * 16 + vcol, vb, cb);
-#pragma unroll
-                    for (int rg = 0; rg < G; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
-                }
-            }
-        } else {
-            f32x4 s[NS][G];
-#pragma unroll
-            for (int t = 0; t < NS; ++t) {
-#pragma unroll
-                for (int rg = 0; rg < G; ++rg) s[t][rg] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    const Frag<T> kf = kb < R / 32 ? row_frag<T>(tile + 16 * t * CPR * 16, nb, kb)
-                                                   : row_frag<T>(tile + C::OFF_R + 16 * t * C::RCPR * 16, rb, kb - R / 32);
-#pragma unroll
-                    for (int rg = 0; rg < G; ++rg) s[t][rg] = mma(s[t][rg], kf, qf[rg][kb]);
-                    if (kb % 3 == 2) GDN_SCHED_FENCE();   // bounds the operands in flight: registers
-                }
-            }
-            unsigned there[NS], all = 0x01010101u;
-#pragma unroll
-            for (int t = 0; t < NS; ++t) {
-                there[t] = *reinterpret_cast<const unsigned *>(there4 + 16 * t);
-                all &= there[t];
-            }
-            if (__any(all != 0x01010101u || key + KT - 13 >= cur.len)) {
-#pragma unroll
-                for (int t = 0; t < NS; ++t)
-#pragma unroll
-                    for (int rg = 0; rg < G; ++rg) s[t][rg] = mask(s[t][rg], there[t], key + 16 * t, bits[rg]);
-            }
-#pragma unroll
-            for (int rg = 0; rg < G; ++rg) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int t = 0; t < NS; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][rg][e]);
-                mx = rows_max(mx);
-                const bool up = (mx - m[rg]) * c > RAISE;
-                if (__any(up)) {
-                    const float mn = up ? mx : m[rg], al = up ? exp2_hw((m[rg] - mn) * c) : 1.f;
-                    m[rg] = mn;
-                    l[rg] *= al;
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) acc[cb][rg] *= al;
-                }
                 const float mb = m[rg] == -INFINITY ? 0.f : m[rg] * c;
+                f32x4 p;
 #pragma unroll
-                for (int t = 0; t < NS; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p = exp2_hw(__builtin_fmaf(s[t][rg][e], c, -mb));
-                        s[t][rg][e] = p;
-                        l[rg] += p;
-                    }
-            }
-#pragma unroll
-            for (int t = 0; t < NS; t += 2) {
-                Frag<T> pf[G];
-#pragma unroll
-                for (int rg = 0; rg < G; ++rg) pf[rg] = reg_frag<T>(s[t][rg], s[t + 1][rg]);
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                    const Frag<T> vf = col_frag<T, CPR>(tile + 16 * t * CPR * 16, vb, cb);
-#pragma unroll
-                    for (int rg = 0; rg < G; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
-                    if (cb % 4 == 3) GDN_SCHED_FENCE();
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = exp2_hw(__builtin_fmaf(s[rg][e], c, -mb));
+                    l[rg] += p[e];
                 }
+                // as the lane's own half of the operand of 32 keys
+                store4((T *)(lds + C::OFF_P + (rg * KT / 32 + wave / 2) * C::PF + lane * 8 * C::ES) + 4 * (wave & 1), p);
+            }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int kk = 0; kk < KT / 32; ++kk) {
+            Frag<T> pf[G];
+#pragma unroll
+            for (int rg = 0; rg < G; ++rg) pf[rg] = load_frag<T>((const T *)(lds + C::OFF_P + (rg * KT / 32 + kk) * C::PF) + lane * 8);
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                const Frag<T> vf = col_frag<T, CPR>(tile + 32 * kk * CPR * 16 + vcol, vb, cb);
+#pragma unroll
+                for (int rg = 0; rg < G; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
             }
         }
         if (!more || nxt.n != cur.n) {
             // the sequence's (or the share's) last tile: the rows' sums, then write
-            float *mx = (float *)(lds + C::OFF_MX), ls[G];
+            float ls[G];
 #pragma unroll
             for (int rg = 0; rg < G; ++rg) ls[rg] = rows_sum(l[rg]);
-            if constexpr (SPLIT) {
-                lds_barrier();
+            lds_barrier();
 #pragma unroll
-                for (int rg = 0; rg < G; ++rg)
-                    if (gq == 0 && wave < NS) mx[wave * RT + 16 * rg + r16] = ls[rg];
-                lds_barrier();
+            for (int rg = 0; rg < G; ++rg)
+                if (gq == 0 && wave < NS) mx[wave * RT + 16 * rg + r16] = ls[rg];
+            lds_barrier();
 #pragma unroll
-                for (int rg = 0; rg < G; ++rg) {
-                    ls[rg] = 0.f;
+            for (int rg = 0; rg < G; ++rg) {
+                ls[rg] = 0.f;
 #pragma unroll
-                    for (int w = 0; w < NS; ++w) ls[rg] += mx[w * RT + 16 * rg + r16];
-                }
+                for (int w = 0; w < NS; ++w) ls[rg] += mx[w * RT + 16 * rg + r16];
             }
             const bool whole = kt0 == 0 && cur.t + 1 == cur.nkt;
             const long slot = ((long)share * 2 + (kt0 == 0 ? 1 : 0)) * ntile + rt;
             float *po = part + slot * RT * (R + 1), *pl = po + RT * R;
 #pragma unroll
             for (int rg = 0; rg < G; ++rg) {
-                const int lr = row0 + 16 * rg + r16, row = rt * RT + lr;
+                const int lr = 16 * rg + r16, row = rt * RT + lr;
                 const bool seen = ls[rg] > 0.f;
                 const float inv = seen ? 1.f / ls[rg] : 0.f;
                 const float lg = seen ? m[rg] * c + __builtin_amdgcn_logf(ls[rg]) : -INFINITY;
                 if (row >= rows) continue;
-                T *o = (T *)a.o + ((long)cur.n * rows + row) * R + (SPLIT ? 16 * wave * CB : 0) + 4 * gq;
-                float *w = po + (long)lr * R + (SPLIT ? 16 * wave * CB : 0) + 4 * gq;
+                T *o = (T *)a.o + ((long)cur.n * rows + row) * R + 16 * wave * CB + 4 * gq;
+                float *w = po + (long)lr * R + 16 * wave * CB + 4 * gq;
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
                     const f32x4 v = seen ? acc[cb][rg] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
                     if (whole) store4(o + 16 * cb, v);
                     else store4(w + 16 * cb, v);
                 }
-                if (gq == 0 && (!SPLIT || wave == 0)) {
+                if (gq == 0 && wave == 0) {
                     if (!whole) pl[lr] = lg;
                     else if (a.lse) a.lse[(long)cur.n * rows + row] = lg * LN2;
                 }
@@ -440,6 +418,251 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_step_kernel(LatentStepArgs 
         }
         cur = nxt;
         nxt = aft;
+    }
+}
+
+// 64 rows of a sequence.  Four waves hold the queries of 16 rows each and compute
+// the scores and weights of a tile of 32 keys; four waves hold 64 rows by a quarter
+// of the output columns and multiply the weights with the values, a tile behind.  So
+// neither needs more registers than two waves a SIMD have, and the matrix cores of
+// each SIMD get the products of one kind while the other's wave works on its softmax
+// or, the second kind, on the copies of the tiles to come.  Weights change hands as whole operands, a lane's own eight values.
+template <int R>
+__global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs a, int ntile, int max_shares)
+{
+    typedef __bf16 T;
+    typedef WideCfg<R> C;
+    constexpr int D = C::D, KT = C::KT, RT = C::RT, NKB = D / 32, CPR = C::CPR, CB = C::CB, NB = C::NB;
+    constexpr int WR = KT / 4;                 // rows of a tile that one of the copying waves copies
+    constexpr int NV = WR * CPR / 64 + 2;      // its copies a step: latents, rotary keys, pages
+    extern __shared__ char lds[];
+    const int share = blockIdx.x % max_shares, rt = blockIdx.x / max_shares;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int rows = a.M * a.H;
+    const float c = a.scale * LOG2E;
+    float *part = (float *)((char *)a.ws + StepWs(a.N, ntile, RT, R).part);
+    int g0, g1;
+    StepPos pos;
+    if (!step_share<8, KT>(a, share, max_shares, share == 0 && rt == 0, (int *)(lds + C::OFF_SCAN), g0, g1, pos)) return;
+    const int nt = g1 - g0;
+    float *alpha = (float *)(lds + C::OFF_AL), *fin = (float *)(lds + C::OFF_FIN);
+
+    if (wave < 4) {
+        const int row = rt * RT + wave * 16 + r16;
+        const bool live = row < rows;
+        const int nb = row_base<T, CPR>(r16), rb = row_base<T, C::RCPR>(r16);
+        Frag<T> qf[NKB];
+        unsigned long long bits = 0;
+        float m = -INFINITY, l = 0.f;
+        int n = -1;
+        StepPos p = pos;
+        for (int i = 0;; ++i) {
+            lds_barrier();   // tile i is there
+            if (i == nt) break;
+            if (p.n != n) {   // another sequence
+                n = p.n;
+                const T *q = (const T *)a.q + ((long)n * rows + (live ? row : 0)) * D;
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) qf[kb] = live ? load_frag<T>(q + 32 * kb + 8 * gq) : zero_frag<T>();
+                bits = step_bits(a, n, row, live);
+                m = -INFINITY;
+                l = 0.f;
+            }
+            const char *tile = lds + i % NB * C::TILE;
+            f32x4 s[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const Frag<T> kf = kb < R / 32 ? row_frag<T>(tile + 16 * t * CPR * 16, nb, kb)
+                                                   : row_frag<T>(tile + C::OFF_R + 16 * t * C::RCPR * 16, rb, kb - R / 32);
+                    s[t] = mma(s[t], kf, qf[kb]);
+                }
+            const int key = p.t * KT + 4 * gq;
+            const char *there4 = lds + C::OFF_KV + i % NB * KT + 4 * gq;
+            const unsigned th0 = *reinterpret_cast<const unsigned *>(there4), th1 = *reinterpret_cast<const unsigned *>(there4 + 16);
+            if (__any((th0 & th1) != 0x01010101u || key + 19 >= p.len)) {
+                s[0] = step_mask(s[0], th0, key, p.len, bits);
+                s[1] = step_mask(s[1], th1, key + 16, p.len, bits);
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(s[0][e], s[1][e]));
+            mx = rows_max(mx);
+            const bool up = (mx - m) * c > RAISE;   // false while both are -inf
+            const float mn = up ? mx : m, al = up ? exp2_hw((m - mn) * c) : 1.f;
+            m = mn;
+            l *= al;
+            if (gq == 0) alpha[(i & 1) * 64 + wave * 16 + r16] = al;
+            const float mb = m == -INFINITY ? 0.f : m * c;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[t][e] = exp2_hw(__builtin_fmaf(s[t][e], c, -mb));
+                    l += s[t][e];
+                }
+            const Frag<T> pf = reg_frag<T>(s[0], s[1]);
+            *reinterpret_cast<bf16x8 *>(lds + C::OFF_P + ((i & 1) * 4 + wave) * 1024 + lane * 16) = pf.v;
+            if (i + 1 == nt || p.t + 1 == p.nkt) {   // the sequence's (or the share's) last tile
+                const float ls = rows_sum(l);
+                if (gq == 0) {
+                    fin[(i & 1) * 128 + wave * 16 + r16] = ls;
+                    fin[(i & 1) * 128 + 64 + wave * 16 + r16] = m * c;
+                }
+            }
+            if (i + 1 < nt) p = step_after<KT>(a, p);
+        }
+    } else {
+        const int w = wave - 4, col0 = w * CB;   // 16-column blocks of this wave
+
+        // The copies.  Tile i (counted from g0) stands in buffer i % NB.  Step i
+        // enqueues tile i + 2, from row addresses worked out in the step before; works
+        // out those of i + 3, from pages enqueued two steps before; and enqueues the
+        // pages of i + 5.  Every step has NV copies a wave, so that all but those of
+        // the step before have arrived when NV are left.
+        const int krow = w * WR + (lane & (WR - 1));
+        int *ids = (int *)(lds + C::OFF_ID);
+        int lo = 0, hi = 0;
+        bool there = false;
+        auto load_ids = [&](const StepPos &p, int i) {   // [i % 4][KT]
+            const int key = p.t * KT + krow;
+            const void *src = key < p.len ? (const void *)(a.table + (long)p.n * a.width + step_page(a, key)) : (const void *)latent_zero;
+            if (lane < WR) g2lds4(src, (char *)(ids + i % 4 * KT + w * WR));
+        };
+        auto address = [&](const StepPos &p, int i) {
+            const char *src = step_row<D * 2>(a, p, p.t * KT + krow, ids[i % 4 * KT + krow], there);
+            lo = (int)(uintptr_t)src;
+            hi = (int)((uintptr_t)src >> 32);
+        };
+        auto load_tile = [&](int i) {
+            if (lane < WR) lds[C::OFF_KV + i % NB * KT + krow] = there;
+            auto row_ptr = [&](int row) {   // of a row that differs by lane
+                return (const char *)(((uintptr_t)(unsigned)__shfl(hi, row, 64) << 32) | (unsigned)__shfl(lo, row, 64));
+            };
+            char *dst = lds + i % NB * C::TILE + w * WR * CPR * 16;
+            if constexpr (CPR == 64) {   // a row is one instruction: its address is uniform
+#pragma unroll
+                for (int k = 0; k < WR; ++k) {
+                    const unsigned rlo = (unsigned)__builtin_amdgcn_readlane(lo, k), rhi = (unsigned)__builtin_amdgcn_readlane(hi, k);
+                    g2lds16s((const char *)(((uintptr_t)rhi << 32) | rlo), (unsigned)((lane ^ swz<CPR>(w * WR + k)) * 16), dst + k * 1024);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < WR * CPR / 64; ++k) {
+                    const int row = k * (64 / CPR) + lane / CPR;
+                    g2lds16(row_ptr(row) + ((lane % CPR) ^ swz<CPR>(w * WR + row)) * 16, dst + k * 1024);
+                }
+            }
+            const int row = lane / C::RCPR, ch = (lane % C::RCPR) ^ swz<C::RCPR>(w * WR + row);
+            const char *q = row_ptr(row);   // a row that is not there: the first of the zeros
+            g2lds16(__shfl((int)there, row, 64) ? q + R * 2 + ch * 16 : q, lds + i % NB * C::TILE + C::OFF_R + w * WR * C::RCPR * 16);
+        };
+        static_assert(WR * C::RCPR == 64, "one copy of rotary keys a wave");
+        StepPos ahead[6];   // of tiles i .. i + 5
+        ahead[0] = pos;
+#pragma unroll
+        for (int k = 1; k < 6; ++k) ahead[k] = k < nt ? step_after<KT>(a, ahead[k - 1]) : ahead[k - 1];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load_ids(ahead[k], k);
+        wait_vm<0>();
+        address(ahead[0], 0);
+        load_tile(0);
+        if (1 < nt) {
+            address(ahead[1], 1);
+            load_tile(1);
+        }
+        address(ahead[2], 2);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the first pages have been read
+        load_ids(ahead[4], 4);
+        wait_vm<0>();
+        auto step = [&](int i) {
+            if (i + 1 < nt) wait_vm<NV>();
+            else wait_vm<0>();
+            lds_barrier();
+            if (i + 2 < nt) {
+                load_tile(i + 2);
+                load_ids(ahead[5], i + 5);
+                address(ahead[3], i + 3);
+            }
+        };
+
+        const int vb = col_base<T, CPR>(4 * gq) ^ (col0 % 8 * 32), vcol = col0 / 8 * 256;
+        f32x4 acc[CB][4];
+        StepPos p = pos;   // of the tile before
+        bool fresh = true;
+        int kt0 = pos.t;
+        for (int i = 0;; ++i) {
+            step(i);
+            if (i > 0) {
+                const int k = i - 1;
+                if (fresh) {
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                        for (int rg = 0; rg < 4; ++rg) acc[cb][rg] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    fresh = false;
+                }
+                Frag<T> pf[4];
+                float al[4];
+                bool up = false;
+#pragma unroll
+                for (int rg = 0; rg < 4; ++rg) {
+                    pf[rg] = {*reinterpret_cast<const bf16x8 *>(lds + C::OFF_P + ((k & 1) * 4 + rg) * 1024 + lane * 16)};
+                    al[rg] = alpha[(k & 1) * 64 + rg * 16 + r16];
+                    up |= al[rg] != 1.f;
+                }
+                if (__any(up)) {
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                        for (int rg = 0; rg < 4; ++rg) acc[cb][rg] *= al[rg];
+                }
+                const char *tile = lds + k % NB * C::TILE + vcol;
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) {
+                    const Frag<T> vf = col_frag<T, CPR>(tile, vb, cb);
+#pragma unroll
+                    for (int rg = 0; rg < 4; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
+                }
+                if (i == nt || p.t + 1 == p.nkt) {
+                    const bool whole = kt0 == 0 && p.t + 1 == p.nkt;
+                    const long slot = ((long)share * 2 + (kt0 == 0 ? 1 : 0)) * ntile + rt;
+                    float *po = part + slot * RT * (R + 1), *pl = po + RT * R;
+#pragma unroll
+                    for (int rg = 0; rg < 4; ++rg) {
+                        const int lr = 16 * rg + r16, row = rt * RT + lr;
+                        const float ls = fin[(k & 1) * 128 + lr], mc = fin[(k & 1) * 128 + 64 + lr];
+                        const bool seen = ls > 0.f;
+                        const float inv = seen ? 1.f / ls : 0.f;
+                        const float lg = seen ? mc + __builtin_amdgcn_logf(ls) : -INFINITY;
+                        if (row >= rows) continue;
+                        T *o = (T *)a.o + ((long)p.n * rows + row) * R + 16 * col0 + 4 * gq;
+                        float *f = po + (long)lr * R + 16 * col0 + 4 * gq;
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb) {
+                            const f32x4 v = seen ? acc[cb][rg] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
+                            if (whole) store4(o + 16 * cb, v);
+                            else store4(f + 16 * cb, v);
+                        }
+                        if (gq == 0 && w == 0) {
+                            if (!whole) pl[lr] = lg;
+                            else if (a.lse) a.lse[(long)p.n * rows + row] = lg * LN2;
+                        }
+                    }
+                    fresh = true;
+                    kt0 = 0;
+                }
+            }
+            if (i == nt) break;
+            p = ahead[0];
+#pragma unroll
+            for (int k = 0; k < 5; ++k) ahead[k] = ahead[k + 1];
+            if (i + 6 < nt) ahead[5] = step_after<KT>(a, ahead[5]);
+        }
     }
 }
 
@@ -512,32 +735,42 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentStepArgs a, int 
         a.lse[(long)n * rows + row] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
 }
 
-template <typename T, int R, bool SPLIT, int G, int NW>
-static hipError_t step_launch(const LatentStepArgs &a, hipStream_t st)
+template <typename T, int R, typename K>
+static hipError_t step_enqueue(K k, int rt, int threads, int lds, const LatentStepArgs &a, hipStream_t st)
 {
-    typedef StepCfg<T, R, SPLIT, G, NW> C;
-    const int rows = a.M * a.H, ntile = (rows + C::RT - 1) / C::RT, shares = step_shares(ntile);
-    auto k = latent_step_kernel<T, R, SPLIT, G, NW>;
-    const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+    const int rows = a.M * a.H, ntile = (rows + rt - 1) / rt, shares = step_shares(ntile);
+    const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k, dim3(ntile * shares), dim3(C::NTHR), C::BYTES, st, a, ntile, shares);
-    hipLaunchKernelGGL((latent_join_kernel<T, R>), dim3(a.N * rows), dim3(256), 0, st, a, ntile, shares, C::RT);
+    hipLaunchKernelGGL(k, dim3(ntile * shares), dim3(threads), lds, st, a, ntile, shares);
+    hipLaunchKernelGGL((latent_join_kernel<T, R>), dim3(a.N * rows), dim3(256), 0, st, a, ntile, shares, rt);
     return hipGetLastError();
+}
+
+template <typename T, int R, int G> static hipError_t step_launch(const LatentStepArgs &a, hipStream_t st)
+{
+    typedef StepCfg<T, R, G> C;
+    return step_enqueue<T, R>(latent_step_kernel<T, R, G>, C::RT, 256, C::BYTES, a, st);
 }
 
 template <int R> static hipError_t step_bf16(const LatentStepArgs &a, hipStream_t st)
 {
     switch (step_rt(true, a.M * a.H)) {
-    case 16: return step_launch<__bf16, R, true, 1, 4>(a, st);
-    case 32: return step_launch<__bf16, R, true, 2, 4>(a, st);
-    case 64: return step_launch<__bf16, R, false, 1, 4>(a, st);
-    default: return step_launch<__bf16, R, false, 1, 8>(a, st);
+    case 16: return step_launch<__bf16, R, 1>(a, st);
+    case 32: return step_launch<__bf16, R, 2>(a, st);
+    default: return step_enqueue<__bf16, R>(latent_step_wide_kernel<R>, WideCfg<R>::RT, 512, WideCfg<R>::BYTES, a, st);
     }
 }
 
-hipError_t latent_step_launch(bool bf16, int r, const LatentStepArgs &a, hipStream_t st)
+hipError_t latent_step_launch(bool bf16, int r, const LatentStepArgs &given, hipStream_t st)
 {
-    if (!bf16) return r == 512 ? step_launch<float, 512, true, 1, 4>(a, st) : step_launch<float, 256, true, 1, 4>(a, st);
+    // with L = ceil(log2 page), mul = floor(2^(30 + L) / page) + 1: mul page - 2^(30 + L)
+    // is at most 2^L, so t of it stays below 2^(30 + L) and the quotient is exact
+    LatentStepArgs a = given;
+    int L = 0;
+    while ((1LL << L) < a.page) ++L;
+    a.page_shift = 30 + L;
+    a.page_mul = (unsigned)((1ULL << (30 + L)) / (unsigned)a.page + 1);
+    if (!bf16) return r == 512 ? step_launch<float, 512, 1>(a, st) : step_launch<float, 256, 1>(a, st);
     return r == 512 ? step_bf16<512>(a, st) : step_bf16<256>(a, st);
 }
 
