@@ -63,8 +63,8 @@ unsigned long long latent_step_workspace(bool bf16, int N, int M, int H, int r);
 #ifdef __HIPCC__
 // Zeros: the source of every tile row behind the last live key, so that what such
 // rows hold in memory (it may be NaN) never meets a product.  One row of the widest
-// kind (512 fp32 values).
-static __device__ const uint4 latent_zero[128] = {};
+// kind (512 + 64 fp32 values).
+static __device__ const uint4 latent_zero[144] = {};
 
 // LDS tiles are rows of CPR 16-byte chunks (8, or a multiple of 16); the chunk index
 // is XOR-ed with a function of the row.  The LDS serves 16 chunks (64 banks) a clock.
@@ -152,6 +152,19 @@ __device__ __forceinline__ void load_rows(char *tile, const char *x, long stride
     }
 }
 
+// g2lds16, g2lds16s and g2lds4 for the middle of other work: without the memory
+// clobber, so that LDS reads of other buffers may move across them.  They keep their
+// order among themselves and to the waits and barriers, which are volatile too.
+__device__ __forceinline__ void copy16(const void *src, const char *lds) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_addr(lds)) : "m0");
+}
+__device__ __forceinline__ void copy16s(const void *base, unsigned off, const char *lds) {   // base: uniform
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_addr(lds)) : "m0");
+}
+__device__ __forceinline__ void copy4(const void *src, const char *lds) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_addr(lds)) : "m0");
+}
+
 // Operand straight from global memory: 8 values of this lane's row.
 template <typename T> __device__ __forceinline__ Frag<T> load_frag(const T *p) {
     if constexpr (sizeof(T) == 2) return {*reinterpret_cast<const bf16x8 *>(p)};
@@ -172,6 +185,19 @@ template <typename T> __device__ __forceinline__ Frag<T> zero_frag() {
 template <typename T> __device__ __forceinline__ void store4(T *p, f32x4 v) {
     if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4 *>(p) = cvt4(v);
     else *reinterpret_cast<f32x4 *>(p) = v;
+}
+
+// Order for the scheduler: AHEAD LDS reads, then after every group of M matrix
+// products R more reads, as long as reads are left.  Left to itself the compiler puts
+// each read right before its product and waits for it there.
+template <int AHEAD, int READS, int PRODUCTS, int R, int M> __device__ __forceinline__ void pipeline() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = AHEAD; i < READS; i += R) {
+        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS, 0);
 }
 
 // Maximum and sum over the four 16-lane rows of a wave, per lane of a row.

@@ -50,8 +50,8 @@ template <int R> struct WideCfg {
     static constexpr int OFF_AL = OFF_P + 2 * 4 * 1024;     // [2][64] factors of a raised maximum
     static constexpr int OFF_FIN = OFF_AL + 2 * 64 * 4;     // [2][2][64] sums and maxima of a finished sequence
     static constexpr int OFF_KV = OFF_FIN + 2 * 2 * 64 * 4; // [NB][KT] bytes: key is there
-    static constexpr int OFF_ID = OFF_KV + NB * KT;         // [4][KT] pages
-    static constexpr int OFF_SCAN = OFF_ID + 4 * KT * 4;    // [8 + 2] ints
+    static constexpr int OFF_ID = OFF_KV + NB * KT;         // [4][4][64] pages, by lane of the copying waves
+    static constexpr int OFF_SCAN = OFF_ID + 4 * 4 * 64 * 4;    // [8 + 2] ints
     static constexpr int BYTES = OFF_SCAN + 10 * 4;
     static_assert(BYTES <= 160 * 1024, "");
 };
@@ -84,6 +84,13 @@ __device__ __forceinline__ int step_len(const LatentStepArgs &a, int n) {
     const int v = a.lens[n];
     return v < 0 ? 0 : v > cap ? cap : v;
 }
+// The same of a sequence that is uniform, by a scalar load: waiting for it does not
+// wait for copies in flight.
+__device__ __forceinline__ int step_len_uniform(const LatentStepArgs &a, int n) {
+    const int cap = (int)min((long)a.width * a.page, 0x7fffffffL);
+    const int v = ((const __attribute__((address_space(4))) int *)(uintptr_t)a.lens)[__builtin_amdgcn_readfirstlane(n)];
+    return v < 0 ? 0 : v > cap ? cap : v;
+}
 __device__ __forceinline__ int step_tiles(int len, int drafts, int kt) { return (len + drafts + kt - 1) / kt; }
 
 // A key tile: tile t of the nkt of sequence n, whose cached length is len.
@@ -98,7 +105,7 @@ template <int KT> __device__ __forceinline__ StepPos step_after(const LatentStep
         p.t = 0;
         do {
             ++p.n;
-            p.len = __builtin_amdgcn_readfirstlane(step_len(a, p.n));
+            p.len = step_len_uniform(a, p.n);
             p.nkt = step_tiles(p.len, a.drafts, KT);
         } while (p.nkt == 0 && p.n + 1 < a.N);
     }
@@ -158,7 +165,7 @@ __device__ __forceinline__ bool step_share(const LatentStepArgs &a, int share, i
     __syncthreads();
     cur.n = __builtin_amdgcn_readfirstlane(scan[NW]);
     cur.t = __builtin_amdgcn_readfirstlane(scan[NW + 1]);
-    cur.len = __builtin_amdgcn_readfirstlane(step_len(a, cur.n));
+    cur.len = step_len_uniform(a, cur.n);
     cur.nkt = step_tiles(cur.len, a.drafts, KT);
     return true;
 }
@@ -167,19 +174,15 @@ __device__ __forceinline__ int step_page(const LatentStepArgs &a, int t) {
     return (int)(((unsigned long long)(unsigned)t * a.page_mul) >> a.page_shift);
 }
 
-// Row of key `key` of p's sequence and whether it is there; id: its page.
+// Row of key `key` of p's sequence (latent_zero: it is not there); id: its page.
 template <int ROWB>
-__device__ __forceinline__ const char *step_row(const LatentStepArgs &a, const StepPos &p, int key, int id, bool &there)
+__device__ __forceinline__ const char *step_row(const LatentStepArgs &a, const StepPos &p, int key, int id)
 {
-    there = false;
-    if (key < p.len) {
-        there = id >= 0 && id < a.pages;   // any other page holds nothing
-        if (there) return (const char *)a.cache + ((long)id * a.page + (key - step_page(a, key) * a.page)) * ROWB;
-    } else if (key - p.len < a.drafts) {
-        there = true;
-        return (const char *)a.draft + ((long)p.n * a.M + (key - p.len)) * ROWB;
-    }
-    return (const char *)latent_zero;
+    const bool cached = key < p.len;
+    const bool there = cached ? id >= 0 && id < a.pages : key - p.len < a.drafts;   // any other page holds nothing
+    const long slot = (long)id * a.page + (key - step_page(a, key) * a.page), node = (long)p.n * a.M + (key - p.len);
+    const char *src = cached ? (const char *)a.cache + slot * ROWB : (const char *)a.draft + node * ROWB;
+    return there ? src : (const char *)latent_zero;
 }
 
 // -inf where the row does not see the key: s of keys first .. first + 3, `there` their
@@ -232,9 +235,8 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
     };
     auto load_tile = [&](const StepPos &p, int id, int buf) {
         const int key = p.t * KT + krow;
-        bool there;
-        const char *src = step_row<D * C::ES>(a, p, key, id, there);
-        if (lane < WR) lds[C::OFF_KV + buf * KT + krow] = there;
+        const char *src = step_row<D * C::ES>(a, p, key, id);
+        if (lane < WR) lds[C::OFF_KV + buf * KT + krow] = src != (const char *)latent_zero;
         const int lo = (int)(uintptr_t)src, hi = (int)((uintptr_t)src >> 32);
         auto row_ptr = [&](int row) {   // of a row that differs by lane
             return (const char *)(((uintptr_t)(unsigned)__shfl(hi, row, 64) << 32) | (unsigned)__shfl(lo, row, 64));
@@ -260,8 +262,7 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
 #pragma unroll
         for (int i = 0; i < WR * C::RCPR / 64; ++i) {
             const int row = i * (64 / C::RCPR) + lane / C::RCPR, ch = (lane % C::RCPR) ^ swz<C::RCPR>(wave * WR + row);
-            const char *q = row_ptr(row);   // a row that is not there: the first of the zeros
-            g2lds16(__shfl((int)there, row, 64) ? q + R * C::ES + ch * 16 : q, rdst + i * 1024);
+            g2lds16(row_ptr(row) + R * C::ES + ch * 16, rdst + i * 1024);
         }
     };
 
@@ -481,6 +482,7 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
                                                    : row_frag<T>(tile + C::OFF_R + 16 * t * C::RCPR * 16, rb, kb - R / 32);
                     s[t] = mma(s[t], kf, qf[kb]);
                 }
+            pipeline<12, 2 * NKB, 2 * NKB, 2, 2>();
             const int key = p.t * KT + 4 * gq;
             const char *there4 = lds + C::OFF_KV + i % NB * KT + 4 * gq;
             const unsigned th0 = *reinterpret_cast<const unsigned *>(there4), th1 = *reinterpret_cast<const unsigned *>(there4 + 16);
@@ -519,150 +521,160 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
     } else {
         const int w = wave - 4, col0 = w * CB;   // 16-column blocks of this wave
 
-        // The copies.  Tile i (counted from g0) stands in buffer i % NB.  Step i
-        // enqueues tile i + 2, from row addresses worked out in the step before; works
-        // out those of i + 3, from pages enqueued two steps before; and enqueues the
-        // pages of i + 5.  Every step has NV copies a wave, so that all but those of
-        // the step before have arrived when NV are left.
+        // The copies.  Tile i (counted from g0) stands in buffer i % NB.  Step i enqueues
+        // tile i + 2; works out the row addresses of i + 3, from pages enqueued two steps
+        // before; and enqueues the pages of i + 5: one copy after each few products.
+        // Behind the share's last tile all of this goes to that tile again.  Every step
+        // has NV copies a wave, so that all but those of the step before have arrived
+        // when NV are left.
         const int krow = w * WR + (lane & (WR - 1));
-        int *ids = (int *)(lds + C::OFF_ID);
-        int lo = 0, hi = 0;
-        bool there = false;
-        auto load_ids = [&](const StepPos &p, int i) {   // [i % 4][KT]
+        const char *ids = lds + C::OFF_ID;   // [4][4 waves][64 lanes]
+        constexpr bool WHOLE = CPR == 64;    // a row is one copy: its address is uniform
+        const char *row = nullptr;           // of tile i + 2
+        auto load_ids = [&](const StepPos &p, int i) {
             const int key = p.t * KT + krow;
             const void *src = key < p.len ? (const void *)(a.table + (long)p.n * a.width + step_page(a, key)) : (const void *)latent_zero;
-            if (lane < WR) g2lds4(src, (char *)(ids + i % 4 * KT + w * WR));
+            copy4(src, ids + (i % 4 * 4 + w) * 256);
         };
-        auto address = [&](const StepPos &p, int i) {
-            const char *src = step_row<D * 2>(a, p, p.t * KT + krow, ids[i % 4 * KT + krow], there);
-            lo = (int)(uintptr_t)src;
-            hi = (int)((uintptr_t)src >> 32);
+        auto page_id = [&](int i) { return *reinterpret_cast<const int *>(ids + (i % 4 * 4 + w) * 256 + lane * 4); };
+        auto address = [&](const StepPos &p, int id) { return step_row<D * 2>(a, p, p.t * KT + krow, id); };
+        auto of_row = [&](const char *p, int r) {   // of a row that differs by lane
+            const int lo = (int)(uintptr_t)p, hi = (int)((uintptr_t)p >> 32);
+            return (const char *)(((uintptr_t)(unsigned)__shfl(hi, r, 64) << 32) | (unsigned)__shfl(lo, r, 64));
         };
-        auto load_tile = [&](int i) {
-            if (lane < WR) lds[C::OFF_KV + i % NB * KT + krow] = there;
-            auto row_ptr = [&](int row) {   // of a row that differs by lane
-                return (const char *)(((uintptr_t)(unsigned)__shfl(hi, row, 64) << 32) | (unsigned)__shfl(lo, row, 64));
-            };
-            char *dst = lds + i % NB * C::TILE + w * WR * CPR * 16;
-            if constexpr (CPR == 64) {   // a row is one instruction: its address is uniform
-#pragma unroll
-                for (int k = 0; k < WR; ++k) {
-                    const unsigned rlo = (unsigned)__builtin_amdgcn_readlane(lo, k), rhi = (unsigned)__builtin_amdgcn_readlane(hi, k);
-                    g2lds16s((const char *)(((uintptr_t)rhi << 32) | rlo), (unsigned)((lane ^ swz<CPR>(w * WR + k)) * 16), dst + k * 1024);
-                }
+        auto load_row = [&](const char *p, int i, int k) {   // k < CB: as many as the wave has column blocks
+            char *dst = lds + i % NB * C::TILE + w * WR * CPR * 16 + k * 1024;
+            if constexpr (WHOLE) {
+                const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(uintptr_t)p, k);
+                const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)((uintptr_t)p >> 32), k);
+                copy16s((const char *)(((uintptr_t)hi << 32) | lo), (unsigned)((lane ^ swz<CPR>(w * WR + k)) * 16), dst);
             } else {
-#pragma unroll
-                for (int k = 0; k < WR * CPR / 64; ++k) {
-                    const int row = k * (64 / CPR) + lane / CPR;
-                    g2lds16(row_ptr(row) + ((lane % CPR) ^ swz<CPR>(w * WR + row)) * 16, dst + k * 1024);
-                }
+                const int r = k * (64 / CPR) + lane / CPR;
+                copy16(of_row(p, r) + ((lane % CPR) ^ swz<CPR>(w * WR + r)) * 16, dst);
             }
-            const int row = lane / C::RCPR, ch = (lane % C::RCPR) ^ swz<C::RCPR>(w * WR + row);
-            const char *q = row_ptr(row);   // a row that is not there: the first of the zeros
-            g2lds16(__shfl((int)there, row, 64) ? q + R * 2 + ch * 16 : q, lds + i % NB * C::TILE + C::OFF_R + w * WR * C::RCPR * 16);
         };
-        static_assert(WR * C::RCPR == 64, "one copy of rotary keys a wave");
-        StepPos ahead[6];   // of tiles i .. i + 5
-        ahead[0] = pos;
+        const int rrow = lane / C::RCPR, rch = ((lane % C::RCPR) ^ swz<C::RCPR>(w * WR + rrow)) * 16 + R * 2;
+        auto load_rope = [&](const char *p, const char *from, int i) {   // p: the lane's row; from: row rrow
+            lds[C::OFF_KV + i % NB * KT + krow] = p != (const char *)latent_zero;   // equal lanes write equal bytes
+            copy16(from + rch, lds + i % NB * C::TILE + C::OFF_R + w * WR * C::RCPR * 16);
+        };
+        static_assert(WR * C::RCPR == 64 && WR * CPR / 64 == CB, "");
+        StepPos pa = pos, pi = pos;   // of the tiles whose addresses, and pages, come next
+        int na = 0, ni = 0;
+        auto advance = [&](StepPos &p, int &n) {
+            if (++n < nt) p = step_after<KT>(a, p);
+        };
 #pragma unroll
-        for (int k = 1; k < 6; ++k) ahead[k] = k < nt ? step_after<KT>(a, ahead[k - 1]) : ahead[k - 1];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) load_ids(ahead[k], k);
-        wait_vm<0>();
-        address(ahead[0], 0);
-        load_tile(0);
-        if (1 < nt) {
-            address(ahead[1], 1);
-            load_tile(1);
+        for (int k = 0; k < 4; ++k) {
+            load_ids(pi, k);
+            advance(pi, ni);
         }
-        address(ahead[2], 2);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the first pages have been read
-        load_ids(ahead[4], 4);
         wait_vm<0>();
-        auto step = [&](int i) {
-            if (i + 1 < nt) wait_vm<NV>();
-            else wait_vm<0>();
-            lds_barrier();
-            if (i + 2 < nt) {
-                load_tile(i + 2);
-                load_ids(ahead[5], i + 5);
-                address(ahead[3], i + 3);
-            }
-        };
+        for (int k = 0; k < 2; ++k) {
+            const char *r = address(pa, page_id(k));
+#pragma unroll
+            for (int b = 0; b < CB; ++b) load_row(r, k, b);
+            load_rope(r, of_row(r, rrow), k);
+            advance(pa, na);
+        }
+        row = address(pa, page_id(2));
+        advance(pa, na);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the first pages have been read
+        load_ids(pi, 4);
+        advance(pi, ni);
+        wait_vm<0>();
 
         const int vb = col_base<T, CPR>(4 * gq) ^ (col0 % 8 * 32), vcol = col0 / 8 * 256;
         f32x4 acc[CB][4];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int rg = 0; rg < 4; ++rg) acc[cb][rg] = f32x4{0.f, 0.f, 0.f, 0.f};
         StepPos p = pos;   // of the tile before
-        bool fresh = true;
         int kt0 = pos.t;
-        for (int i = 0;; ++i) {
-            step(i);
-            if (i > 0) {
-                const int k = i - 1;
-                if (fresh) {
+        lds_barrier();   // step 0
 #pragma unroll
-                    for (int cb = 0; cb < CB; ++cb)
+        for (int k = 0; k < CB; ++k) load_row(row, 2, k);
+        load_rope(row, of_row(row, rrow), 2);
+        load_ids(pi, 5);
+        advance(pi, ni);
+        row = address(pa, page_id(3));
+        advance(pa, na);
+#pragma unroll 1
+        for (int i = 1; i <= nt; ++i) {
+            wait_vm<NV>();
+            lds_barrier();
+            const int k = i - 1;
+            Frag<T> pf[4];
+            float al[4];
+            bool up = false;
 #pragma unroll
-                        for (int rg = 0; rg < 4; ++rg) acc[cb][rg] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    fresh = false;
-                }
-                Frag<T> pf[4];
-                float al[4];
-                bool up = false;
+            for (int rg = 0; rg < 4; ++rg) {
+                pf[rg] = {*reinterpret_cast<const bf16x8 *>(lds + C::OFF_P + ((k & 1) * 4 + rg) * 1024 + lane * 16)};
+                al[rg] = alpha[(k & 1) * 64 + rg * 16 + r16];
+                up |= al[rg] != 1.f;
+            }
+            if (__any(up)) {
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                    for (int rg = 0; rg < 4; ++rg) acc[cb][rg] *= al[rg];
+            }
+            const char *tile = lds + k % NB * C::TILE + vcol;
+            constexpr int AHEAD = CB < 4 ? CB : 4;   // operands read before their products
+            Frag<T> vf[CB];
+#pragma unroll
+            for (int cb = 0; cb < AHEAD; ++cb) vf[cb] = col_frag<T, CPR>(tile, vb, cb);
+            const int id = page_id(i + 3);
+            const char *from = of_row(row, rrow), *next = nullptr;
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                GDN_SCHED_FENCE();
+                if (cb + AHEAD < CB) vf[cb + AHEAD] = col_frag<T, CPR>(tile, vb, cb + AHEAD);
+                load_row(row, i + 2, cb);
+                if (cb == 0) load_ids(pi, i + 5);
+                if (cb == 1) load_rope(row, from, i + 2);
+                if (cb == 2) next = address(pa, id);
+#pragma unroll
+                for (int rg = 0; rg < 4; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf[cb], pf[rg]);
+            }
+            row = next;
+            advance(pi, ni);
+            advance(pa, na);
+            if (i == nt || p.t + 1 == p.nkt) {
+                const bool whole = kt0 == 0 && p.t + 1 == p.nkt;
+                const long slot = ((long)share * 2 + (kt0 == 0 ? 1 : 0)) * ntile + rt;
+                float *po = part + slot * RT * (R + 1), *pl = po + RT * R;
 #pragma unroll
                 for (int rg = 0; rg < 4; ++rg) {
-                    pf[rg] = {*reinterpret_cast<const bf16x8 *>(lds + C::OFF_P + ((k & 1) * 4 + rg) * 1024 + lane * 16)};
-                    al[rg] = alpha[(k & 1) * 64 + rg * 16 + r16];
-                    up |= al[rg] != 1.f;
-                }
-                if (__any(up)) {
+                    const int lr = 16 * rg + r16, row = rt * RT + lr;
+                    const float ls = fin[(k & 1) * 128 + lr], mc = fin[(k & 1) * 128 + 64 + lr];
+                    const bool seen = ls > 0.f;
+                    const float inv = seen ? 1.f / ls : 0.f;
+                    const float lg = seen ? mc + __builtin_amdgcn_logf(ls) : -INFINITY;
+                    if (row >= rows) continue;
+                    T *o = (T *)a.o + ((long)p.n * rows + row) * R + 16 * col0 + 4 * gq;
+                    float *f = po + (long)lr * R + 16 * col0 + 4 * gq;
 #pragma unroll
-                    for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-                        for (int rg = 0; rg < 4; ++rg) acc[cb][rg] *= al[rg];
-                }
-                const char *tile = lds + k % NB * C::TILE + vcol;
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                    const Frag<T> vf = col_frag<T, CPR>(tile, vb, cb);
-#pragma unroll
-                    for (int rg = 0; rg < 4; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
-                }
-                if (i == nt || p.t + 1 == p.nkt) {
-                    const bool whole = kt0 == 0 && p.t + 1 == p.nkt;
-                    const long slot = ((long)share * 2 + (kt0 == 0 ? 1 : 0)) * ntile + rt;
-                    float *po = part + slot * RT * (R + 1), *pl = po + RT * R;
-#pragma unroll
-                    for (int rg = 0; rg < 4; ++rg) {
-                        const int lr = 16 * rg + r16, row = rt * RT + lr;
-                        const float ls = fin[(k & 1) * 128 + lr], mc = fin[(k & 1) * 128 + 64 + lr];
-                        const bool seen = ls > 0.f;
-                        const float inv = seen ? 1.f / ls : 0.f;
-                        const float lg = seen ? mc + __builtin_amdgcn_logf(ls) : -INFINITY;
-                        if (row >= rows) continue;
-                        T *o = (T *)a.o + ((long)p.n * rows + row) * R + 16 * col0 + 4 * gq;
-                        float *f = po + (long)lr * R + 16 * col0 + 4 * gq;
-#pragma unroll
-                        for (int cb = 0; cb < CB; ++cb) {
-                            const f32x4 v = seen ? acc[cb][rg] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
-                            if (whole) store4(o + 16 * cb, v);
-                            else store4(f + 16 * cb, v);
-                        }
-                        if (gq == 0 && w == 0) {
-                            if (!whole) pl[lr] = lg;
-                            else if (a.lse) a.lse[(long)p.n * rows + row] = lg * LN2;
-                        }
+                    for (int cb = 0; cb < CB; ++cb) {
+                        const f32x4 v = seen ? acc[cb][rg] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
+                        if (whole) store4(o + 16 * cb, v);
+                        else store4(f + 16 * cb, v);
                     }
-                    fresh = true;
-                    kt0 = 0;
+                    if (gq == 0 && w == 0) {
+                        if (!whole) pl[lr] = lg;
+                        else if (a.lse) a.lse[(long)p.n * rows + row] = lg * LN2;
+                    }
                 }
-            }
-            if (i == nt) break;
-            p = ahead[0];
 #pragma unroll
-            for (int k = 0; k < 5; ++k) ahead[k] = ahead[k + 1];
-            if (i + 6 < nt) ahead[5] = step_after<KT>(a, ahead[5]);
+                for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                    for (int rg = 0; rg < 4; ++rg) acc[cb][rg] = f32x4{0.f, 0.f, 0.f, 0.f};
+                kt0 = 0;
+            }
+            if (i < nt) p = step_after<KT>(a, p);
         }
+        wait_vm<0>();   // copies into this LDS end before it is given away
     }
 }
 
