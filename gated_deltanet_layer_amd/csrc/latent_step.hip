@@ -308,6 +308,9 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
         lds_barrier();
         StepPos aft = nxt;
         if (g + 2 < g1) aft = step_after<KT>(a, nxt);
+        // the pages arrived with the tile: nothing of their use moves up to where it would
+        // wait for them, and with them for every copy in flight
+        asm volatile("" : "+v"(idn));
         if (more) load_tile(nxt, idn, buf ^ 1);
         if (g + 2 < g1) idn = page(aft);
 
@@ -523,7 +526,7 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
 
         // The copies.  Tile i (counted from g0) stands in buffer i % NB.  Step i enqueues
         // tile i + 2; works out the row addresses of i + 3, from pages enqueued two steps
-        // before; and enqueues the pages of i + 5: one copy after each few products.
+        // before; and enqueues the pages of i + 5.
         // Behind the share's last tile all of this goes to that tile again.  Every step
         // has NV copies a wave, so that all but those of the step before have arrived
         // when NV are left.
@@ -605,6 +608,9 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
             wait_vm<NV>();
             lds_barrier();
             const int k = i - 1;
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) load_row(row, i + 2, cb);   // at once: their latency is what a step waits for
+            GDN_SCHED_FENCE();
             Frag<T> pf[4];
             float al[4];
             bool up = false;
@@ -631,7 +637,6 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
             for (int cb = 0; cb < CB; ++cb) {
                 GDN_SCHED_FENCE();
                 if (cb + AHEAD < CB) vf[cb + AHEAD] = col_frag<T, CPR>(tile, vb, cb + AHEAD);
-                load_row(row, i + 2, cb);
                 if (cb == 0) load_ids(pi, i + 5);
                 if (cb == 1) load_rope(row, from, i + 2);
                 if (cb == 2) next = address(pa, id);
@@ -679,44 +684,40 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
 }
 
 // Joins the pieces of every sequence that more than one share worked on, and
-// writes the sequences that have no key at all.  One workgroup a (sequence, row):
-// four waves, each a quarter of the pieces, four of them in flight.
-template <typename T, int R>
+// writes the sequences that have no key at all.  WPR waves a row, each with every
+// WPR-th piece: four where few rows have many pieces, else one.
+template <typename T, int R, int WPR>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentStepArgs a, int ntile, int max_shares, int RT)
 {
     constexpr int PER = R / 64;   // columns a lane
-    __shared__ float sums[4][R];
-    __shared__ float tops[4];
-    const int rows = a.M * a.H, n = blockIdx.x / rows, row = blockIdx.x % rows;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const StepWs lay(a.N, ntile, RT, R);
+    const int rows = a.M * a.H, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const long at = (long)blockIdx.x * (4 / WPR) + wave / WPR;   // of the N * rows rows
+    if (at >= (long)a.N * rows) return;
+    const int n = (int)(at / rows), row = (int)(at % rows), w0 = wave % WPR;
     const int *prefix = (const int *)a.ws;
     const int c0 = prefix[n], c1 = prefix[n + 1], total = prefix[a.N], shares = min(max_shares, total);
     int wf = 0, wl = -1;
     if (c1 > c0) {
         wf = (int)(((long)(c0 + 1) * shares - 1) / total);
         wl = (int)(((long)c1 * shares - 1) / total);
-        if (wf == wl) return;   // written by its one share
+        if (wf == wl) return;   // written by its one share (all waves of the row agree)
     }
     // piece w of the sequence: the last of share wf, the first of the others
     const long step = (long)2 * ntile * RT * (R + 1);
-    const float *first = (const float *)((const char *)a.ws + lay.part) + (long)(row / RT) * RT * (R + 1);
+    const float *first = (const float *)((const char *)a.ws + StepWs(a.N, ntile, RT, R).part) + (long)(row / RT) * RT * (R + 1);
     const float *last = first + (long)ntile * RT * (R + 1);
     const int lr = row % RT;
     auto piece = [&](int w) { return (w == wf ? last : first) + w * step; };
     float top = -INFINITY;
-    for (int w = wf + threadIdx.x; w <= wl; w += 256) top = fmaxf(top, piece(w)[RT * R + lr]);
+    for (int w = wf + lane; w <= wl; w += 64) top = fmaxf(top, piece(w)[RT * R + lr]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     float sum[PER], ls = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) sum[i] = 0.f;
     if (top != -INFINITY) {
 #pragma unroll 4
-        for (int w = wf + wave; w <= wl; w += 4) {
+        for (int w = wf + w0; w <= wl; w += WPR) {
             const float *p = piece(w);
             const float f = exp2_hw(p[RT * R + lr] - top);
             ls += f;
@@ -728,23 +729,30 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentStepArgs a, int 
             }
         }
     }
-    __syncthreads();
-    if (lane == 0) tops[wave] = ls;
+    if constexpr (WPR > 1) {   // one row a workgroup
+        __shared__ float sums[4][R], parts[4];
+        if (lane == 0) parts[wave] = ls;
+#pragma unroll
+        for (int i = 0; i < PER; i += 4)
+            *reinterpret_cast<f32x4 *>(&sums[wave][i * 64 + lane * 4]) = f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]};
+        __syncthreads();
+        if (wave > 0) return;
+        ls = parts[0] + parts[1] + parts[2] + parts[3];
+#pragma unroll
+        for (int i = 0; i < PER; i += 4)
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(&sums[w][i * 64 + lane * 4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[i + e] += v[e];
+            }
+    }
+    const float inv = ls > 0.f ? 1.f / ls : 0.f;
+    T *o = (T *)a.o + at * R;
 #pragma unroll
     for (int i = 0; i < PER; i += 4)
-        *reinterpret_cast<f32x4 *>(&sums[wave][i * 64 + lane * 4]) = f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]};
-    __syncthreads();
-    ls = tops[0] + tops[1] + tops[2] + tops[3];
-    const float inv = ls > 0.f ? 1.f / ls : 0.f;
-    const int col = threadIdx.x * 4;
-    if (col < R) {
-        f32x4 v = *reinterpret_cast<const f32x4 *>(&sums[0][col]);
-#pragma unroll
-        for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const f32x4 *>(&sums[w][col]);
-        store4((T *)a.o + ((long)n * rows + row) * R + col, v * inv);
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[(long)n * rows + row] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+        store4(o + i * 64 + lane * 4, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]} * inv);
+    if (a.lse && lane == 0) a.lse[at] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
 }
 
 template <typename T, int R, typename K>
@@ -754,7 +762,11 @@ static hipError_t step_enqueue(K k, int rt, int threads, int lds, const LatentSt
     const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k, dim3(ntile * shares), dim3(threads), lds, st, a, ntile, shares);
-    hipLaunchKernelGGL((latent_join_kernel<T, R>), dim3(a.N * rows), dim3(256), 0, st, a, ntile, shares, rt);
+    // pieces a sequence: about shares / N
+    if (shares > 4 * a.N)
+        hipLaunchKernelGGL((latent_join_kernel<T, R, 4>), dim3(a.N * rows), dim3(256), 0, st, a, ntile, shares, rt);
+    else
+        hipLaunchKernelGGL((latent_join_kernel<T, R, 1>), dim3((a.N * rows + 3) / 4), dim3(256), 0, st, a, ntile, shares, rt);
     return hipGetLastError();
 }
 
