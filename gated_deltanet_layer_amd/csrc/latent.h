@@ -56,7 +56,7 @@ struct LatentStepArgs {
 hipError_t latent_fwd_launch(bool bf16, int dn, int dv, const LatentFwdArgs &a, hipStream_t st);
 unsigned long long latent_fwd_workspace(bool bf16, int B, int Tq, int Tk, int H, int dv);
 hipError_t latent_bwd_launch(bool bf16, int dn, int dv, const LatentBwdArgs &a, hipStream_t st);
-unsigned long long latent_bwd_workspace(int B, int Tq, int Tk, int H);
+unsigned long long latent_bwd_workspace(bool bf16, int B, int Tq, int Tk, int H, int dn, int dv);
 hipError_t latent_step_launch(bool bf16, int r, const LatentStepArgs &a, hipStream_t st);
 unsigned long long latent_step_workspace(bool bf16, int N, int M, int H, int r);
 

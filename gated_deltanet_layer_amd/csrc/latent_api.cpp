@@ -147,7 +147,7 @@ gdn_status gdn_latent_bwd_workspace_size(int B, int Tq, int Tk, int H, int dn, i
     if (!bytes) return GDN_EINVAL;
     const gdn_status st = expanded_sizes(B, Tq, Tk, H, dn, dr, dv, dtype);
     if (st != GDN_OK) return st;
-    *bytes = (size_t)gdn::latent_bwd_workspace(B, Tq, Tk, H);
+    *bytes = (size_t)gdn::latent_bwd_workspace(dtype == GDN_BF16, B, Tq, Tk, H, dn, dv);
     return GDN_OK;
 }
 
@@ -168,7 +168,7 @@ gdn_status gdn_latent_bwd(const void *q, const void *kv, const void *k_rope, con
     for (const void *p : {(const void *)lens, (const void *)lse})
         if (p && !aligned(p, 4)) return GDN_EINVAL;
     if (workspace && !aligned(workspace, 256)) return GDN_EINVAL;
-    const unsigned long long need = st == GDN_OK ? gdn::latent_bwd_workspace(B, Tq, Tk, H) : 0;
+    const unsigned long long need = st == GDN_OK ? gdn::latent_bwd_workspace(dtype == GDN_BF16, B, Tq, Tk, H, dn, dv) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EINVAL;
     const Range in[] = {range(q, qrows * (dn + dr) * es), range(kv, krows * (dn + dv) * es), range(k_rope, ks * dr * es),
                         range(lens, lens ? (long long)B * 4 : 0), range(o, qrows * dv * es), range(lse, qrows * 4),

@@ -8,16 +8,50 @@
 // one kernel owns key rows and walks the query rows that see them (dk, dv), one
 // owns query rows and walks their keys (dq); the scores are computed in both.
 // The rotary part of dk is written per head in fp32 and added over the heads in
-// order by a last kernel.
+// order by a last kernel, with the pieces of what was cut.
 #include "latent.h"
 
 namespace gdn {
 
+// How a call is cut.  Where the workgroups that own rows are too few for the device,
+// the rows that walk by are cut into pieces, one workgroup each; the pieces' sums
+// stand in the workspace and the last kernel adds them up in order.  The longest walk
+// of a causal call is otherwise its time.
+struct BwdPlan {
+    int kp, qp;        // pieces of the keys (dq), of the query rows (dk, dv)
+    int kstep, qstep;  // rows of a piece, whole tiles
+};
+
+inline int bwd_pieces(long wgs, long fill, int tiles) {   // pieces of four tiles or more
+    if (wgs <= 0 || wgs >= fill || tiles < 8) return 1;
+    const long n = (fill + wgs - 1) / wgs;
+    return (int)(n > tiles / 4 ? tiles / 4 : n > 16 ? 16 : n);
+}
+
+inline BwdPlan bwd_plan(bool bf16, int B, int Tq, int Tk, int H)
+{
+    const int own = bf16 ? 128 : 64, st = bf16 ? 64 : 32;
+    const long bh = (long)B * H;
+    const int nk = (Tk + st - 1) / st, nq = (Tq + st - 1) / st;
+    const int kp = bwd_pieces(bh * ((Tq + own - 1) / own), 512, nk), qp = bwd_pieces(bh * ((Tk + own - 1) / own), 256, nq);
+    BwdPlan p;
+    p.kstep = (nk + kp - 1) / kp * st;
+    p.qstep = (nq + qp - 1) / qp * st;
+    p.kp = kp > 1 ? (Tk + p.kstep - 1) / p.kstep : 1;
+    p.qp = qp > 1 ? (Tq + p.qstep - 1) / p.qstep : 1;
+    return p;
+}
+
+// Workspace, all float: D[B][Tq][H]; dk_rope[qp][B][Tk][H][64]; where there are pieces,
+// dq[kp][B][Tq][H][DK] and dkv[qp][B][Tk][H][DN + DV].
 struct BwdWs {
-    long rope, bytes;   // float D[B][Tq][H] first, then float dk_rope[B][Tk][H][64]
-    __host__ __device__ BwdWs(int B, int Tq, int Tk, int H) {
-        rope = ((long)B * Tq * H * 4 + 255) & ~255L;
-        bytes = rope + (long)B * Tk * H * LATENT_ROPE * 4;
+    long rope, dq, dkv, bytes;
+    __host__ __device__ BwdWs(const BwdPlan &p, int B, int Tq, int Tk, int H, int dn, int dv) {
+        const long qr = (long)B * Tq * H, kr = (long)B * Tk * H;
+        rope = (qr * 4 + 255) & ~255L;
+        dq = rope + p.qp * kr * LATENT_ROPE * 4;
+        dkv = dq + (p.kp > 1 ? p.kp * qr * (dn + LATENT_ROPE) * 4 : 0);
+        bytes = dkv + (p.qp > 1 ? p.qp * kr * (dn + dv) * 4 : 0);
     }
 };
 
@@ -32,19 +66,6 @@ template <typename T> __device__ __forceinline__ float frag_dot(const Frag<T> &x
         for (int e = 0; e < 4; ++e) s += x.lo[e] * y.lo[e] + x.hi[e] * y.hi[e];
     }
     return s;
-}
-
-// dk_rope[b][t] = sum over heads, in order.
-template <typename T>
-__global__ __launch_bounds__(256) void latent_bwd_rope_kernel(const float *part, T *dk_rope, long nrows, int H)
-{
-    const long row = (long)blockIdx.x * 16 + threadIdx.x / 16;
-    const int at = (threadIdx.x & 15) * 4;
-    if (row >= nrows) return;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    for (int h = 0; h < H; ++h)
-        s += *reinterpret_cast<const f32x4 *>(part + (row * H + h) * LATENT_ROPE + at);
-    store4(dk_rope + row * LATENT_ROPE + at, s);
 }
 
 template <typename T, int DN, int DV> struct BwdCfg {
@@ -71,15 +92,16 @@ template <typename T, int DN, int DV> struct BwdCfg {
 // Scores have query rows on the accumulator's rows: P and dS feed the gradient
 // products as B operands straight from the registers, and P changes hands between
 // equal lanes.
-template <typename T, int DN, int DV>
-__global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, int ntiles)
+template <typename T, int DN, int DV, bool CUT>
+__global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, BwdPlan plan)
 {
     typedef BwdCfg<T, DN, DV> C;
     constexpr int NG = C::NG, ST = C::ST, DK = C::DK, NKB = DK / 32, NVB = DV / 32, NKC = DK / 16, NVC = DV / 16;
     constexpr int BPT = ST / 32;   // blocks a tile
     extern __shared__ char lds[];
     const int BH = a.B * a.H;
-    const int bh = blockIdx.x % BH, tile = blockIdx.x / BH;   // the first keys are seen by most rows
+    const int bh = blockIdx.x % BH, piece = CUT ? blockIdx.x / BH % plan.qp : 0;
+    const int tile = blockIdx.x / BH / (CUT ? plan.qp : 1);   // the first keys are seen by most rows
     const int b = bh / a.H, h = bh % a.H;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
     const int pair = wave & 3, lane = threadIdx.x & 63;
@@ -95,8 +117,9 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
     float *stat = (float *)(lds + 3 * C::BUF);                  // [3][2][ST]: lse and D of the rows
     char *hand = lds + 3 * (C::BUF + C::ROWS) + pair * C::HAND; // [2][2 NG][64 lanes] f32x4: P, block by block
 
-    // query rows that are no padding and see the workgroup's first key
-    const int qn = min(a.Tq, n - off), qfirst = max(0, k0 - off) / ST * ST;
+    // query rows that are no padding and see the workgroup's first key (of the piece)
+    const int qn = min(min(a.Tq, n - off), CUT ? (piece + 1) * plan.qstep : a.Tq);
+    const int qfirst = max(CUT ? piece * plan.qstep : 0, max(0, k0 - off) / ST * ST);
     const int nt = k0 < n && qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0, nblk = nt * BPT;
     auto load = [&](int j) {
         const int r0 = qfirst + j * ST, buf = j % 3;
@@ -123,6 +146,8 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
     auto seen = [&](int i) {   // whether a row of block i sees a key of the wave
         return off + qfirst + i * 32 + 31 >= w0 && w0 < n;
     };
+    const BwdWs lay(plan, a.B, a.Tq, a.Tk, a.H, DN, DV);
+    if (CUT && nt == 0) return;   // the last kernel knows which pieces there are
     if (nt > 0) load(0);
 
     if (wave < 4) {
@@ -196,12 +221,16 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
             }
         }
         T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV) + DN;
+        float *part = (float *)((char *)a.ws + lay.dkv) + ((piece * (long)a.B + b) * a.Tk * a.H + h) * (DN + DV) + DN;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const int key = w0 + 16 * g + r16;
             if (key >= a.Tk) continue;
 #pragma unroll
-            for (int v = 0; v < NVC; ++v) store4(dkv + key * kvs + 16 * v + 4 * gq, dv[v][g]);
+            for (int v = 0; v < NVC; ++v) {
+                if (CUT) store4(part + key * kvs + 16 * v + 4 * gq, dv[v][g]);
+                else store4(dkv + key * kvs + 16 * v + 4 * gq, dv[v][g]);
+            }
         }
     } else {
         const int vb = row_base<T, C::VCPR>(r16), nc = col_base<T, C::NCPR>(4 * gq), rc = col_base<T, C::RCPR>(4 * gq);
@@ -256,7 +285,8 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
             }
         }
         T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV);
-        float *rope = (float *)((char *)a.ws + BwdWs(a.B, a.Tq, a.Tk, a.H).rope);
+        float *rope = (float *)((char *)a.ws + lay.rope);
+        float *part = (float *)((char *)a.ws + lay.dkv) + ((piece * (long)a.B + b) * a.Tk * a.H + h) * (DN + DV);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const int key = w0 + 16 * g + r16;
@@ -264,8 +294,10 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
 #pragma unroll
             for (int i = 0; i < NKC; ++i) {
                 const f32x4 v = dk[i][g] * a.scale;
-                if (16 * i < DN) store4(dkv + key * kvs + 16 * i + 4 * gq, v);
-                else store4(rope + (((long)b * a.Tk + key) * a.H + h) * LATENT_ROPE + (16 * i - DN) + 4 * gq, v);
+                if (16 * i >= DN)
+                    store4(rope + (((piece * (long)a.B + b) * a.Tk + key) * a.H + h) * LATENT_ROPE + (16 * i - DN) + 4 * gq, v);
+                else if (CUT) store4(part + key * kvs + 16 * i + 4 * gq, v);
+                else store4(dkv + key * kvs + 16 * i + 4 * gq, v);
             }
         }
     }
@@ -274,14 +306,16 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
 // dq, and D for the kernel above, which is launched after this one.  A wave owns 16
 // NG query rows, q and do of them in registers; scores are transposed as in the
 // forward pass, and dS^T feeds dq^T = K^T dS^T from the registers.
-template <typename T, int DN, int DV>
-__global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, int ntiles)
+template <typename T, int DN, int DV, bool CUT>
+__global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, int ntiles, BwdPlan plan)
 {
     typedef BwdCfg<T, DN, DV> C;
     constexpr int NG = C::NG, ST = C::ST, DK = C::DK, NKB = DK / 32, NVB = DV / 32, NKC = DK / 16;
+    constexpr bool BF = sizeof(T) == 2;
     extern __shared__ char lds[];
     const int BH = a.B * a.H;
-    const int bh = blockIdx.x % BH, tile = ntiles - 1 - (int)(blockIdx.x / BH);
+    const int bh = blockIdx.x % BH, piece = CUT ? blockIdx.x / BH % plan.kp : 0;
+    const int tile = ntiles - 1 - (int)(blockIdx.x / BH / (CUT ? plan.kp : 1));
     const int b = bh / a.H, h = bh % a.H;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
     const int off = a.Tk - a.Tq, n = live_len(a.lens, b, a.Tk);
@@ -316,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
         for (int v = 0; v < NVB; ++v)
             if (live) dot += frag_dot<T>(of[g][v], load_frag<T>(o + row * os + 32 * v + 8 * gq));
         dd[g] = rows_sum(dot);
-        if (live && gq == 0) Dw[(long)row * a.H] = dd[g];
+        if (live && gq == 0 && piece == 0) Dw[(long)row * a.H] = dd[g];
     }
     f32x4 dq[NKC][NG];
 #pragma unroll
@@ -325,7 +359,9 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
         for (int i = 0; i < NKC; ++i) dq[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int last = min(n, off + min(q0 + C::OWN, a.Tq));
-    const int nt = (off + q0 < n) ? (last + ST - 1) / ST : 0;
+    const int all = (off + q0 < n) ? (last + ST - 1) / ST : 0;
+    const int j0 = CUT ? piece * plan.kstep / ST : 0, nt = CUT ? min(all, j0 + plan.kstep / ST) : all;
+    if (CUT && piece > 0 && nt <= j0) return;   // the last kernel knows which pieces there are
     const int wlast = min(n, off + min(w0 + 16 * NG, a.Tq)), wfull = off + w0 + 1;
     auto load = [&](int j) {
         char *to = lds + (j & 1) * C::BUF;
@@ -335,8 +371,8 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
     };
     const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = row_base<T, C::VCPR>(r16);
     const int nc = col_base<T, C::NCPR>(4 * gq), rc = col_base<T, C::RCPR>(4 * gq);
-    if (nt > 0) load(0);
-    for (int j = 0; j < nt; ++j) {
+    if (nt > j0) load(j0);
+    for (int j = j0; j < nt; ++j) {
         const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
         const int k0 = j * ST;
         wait_vm<0>();
@@ -361,7 +397,6 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
                         : row_frag<T>(kt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rb, kb - DN / 32);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, qf[g][kb]);
-                    if (kb % 3 == 2) GDN_SCHED_FENCE();
                 }
 #pragma unroll
                 for (int v = 0; v < NVB; ++v) {
@@ -369,6 +404,7 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
 #pragma unroll
                     for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, of[g][v]);
                 }
+                if (BF) pipeline<4, NKB + NVB, (NKB + NVB) * NG, 1, NG>();
                 GDN_SCHED_FENCE();
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
@@ -388,39 +424,100 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
                                               : col_frag<T, C::RCPR>(kt + C::OFF_R + 32 * t * C::RCPR * 16, rc, i - DN / 16);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dq[i][g] = mma(dq[i][g], f, sf[g]);
-                if (i % 2 == 1) GDN_SCHED_FENCE();
             }
+            if (BF) pipeline<4, 2 * NKC, NKC * NG, 2, NG>();
         }
     }
     T *dqp = (T *)a.dq + ((long)b * a.Tq * a.H + h) * DK;
+    float *sum = (float *)((char *)a.ws + BwdWs(plan, a.B, a.Tq, a.Tk, a.H, DN, DV).dq) + ((piece * (long)a.B + b) * a.Tq * a.H + h) * DK;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         const int row = w0 + 16 * g + r16;
         if (row >= a.Tq) continue;
 #pragma unroll
-        for (int i = 0; i < NKC; ++i)
-            store4(dqp + row * qs + 16 * i + 4 * gq, pos[g] >= 0 ? dq[i][g] * a.scale : f32x4{0.f, 0.f, 0.f, 0.f});
+        for (int i = 0; i < NKC; ++i) {
+            const f32x4 v = pos[g] >= 0 ? dq[i][g] * a.scale : f32x4{0.f, 0.f, 0.f, 0.f};
+            if (CUT) store4(sum + row * qs + 16 * i + 4 * gq, v);
+            else store4(dqp + row * qs + 16 * i + 4 * gq, v);
+        }
     }
+}
+
+// dk_rope[b][t], the sum over pieces and heads, and where there are pieces the sums of
+// dq and dkv over them; all in order.  The first nr workgroups take 16 rows of dk_rope
+// each, the next ones 4 x 256 values of dq, the others of dkv.  A piece counts for the
+// rows that its workgroup has worked on.
+template <typename T, int DN, int DV>
+__global__ __launch_bounds__(256) void latent_bwd_sum_kernel(LatentBwdArgs a, BwdPlan plan, int nr, int ndq)
+{
+    typedef BwdCfg<T, DN, DV> C;
+    const BwdWs lay(plan, a.B, a.Tq, a.Tk, a.H, DN, DV);
+    const int off = a.Tk - a.Tq;
+    // pieces of the query rows that the owner of key t walks: [first, end)
+    auto walked = [&](int b, int t, int &first, int &end) {
+        const int n = live_len(a.lens, b, a.Tk), k0 = t / C::OWN * C::OWN, qn = min(a.Tq, n - off);
+        const int q0 = max(0, k0 - off) / C::ST * C::ST;
+        const bool any = k0 < n && q0 < qn;
+        first = any ? q0 / plan.qstep : 0;
+        end = any ? (qn - 1) / plan.qstep + 1 : 0;
+    };
+    if ((int)blockIdx.x < nr) {
+        const long krows = (long)a.B * a.Tk, row = (long)blockIdx.x * 16 + threadIdx.x / 16;
+        const int at = (threadIdx.x & 15) * 4;
+        if (row >= krows) return;
+        int first = 0, end = 1;
+        if (plan.qp > 1) walked((int)(row / a.Tk), (int)(row % a.Tk), first, end);
+        const float *part = (const float *)((const char *)a.ws + lay.rope);
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        for (int p = first; p < end; ++p)
+#pragma unroll 4
+            for (int h = 0; h < a.H; ++h)
+                s += *reinterpret_cast<const f32x4 *>(part + ((p * krows + row) * a.H + h) * LATENT_ROPE + at);
+        store4((T *)a.dk_rope + row * LATENT_ROPE + at, s);
+        return;
+    }
+    const bool isq = (int)blockIdx.x < nr + ndq;
+    const int W = isq ? C::DK : DN + DV, T_ = isq ? a.Tq : a.Tk;
+    const long at = ((long)(blockIdx.x - nr - (isq ? 0 : ndq)) * 256 + threadIdx.x) * 4, size = (long)a.B * T_ * a.H * W;
+    if (at >= size) return;
+    const int b = (int)(at / W / a.H / T_), t = (int)(at / W / a.H % T_);
+    int first = 0, end;
+    if (isq) {   // the owner of row t walks the keys up to its last row's position
+        const int n = live_len(a.lens, b, a.Tk), q0 = t / C::OWN * C::OWN;
+        const int last = min(n, off + min(q0 + C::OWN, a.Tq));
+        end = off + q0 < n ? (last - 1) / plan.kstep + 1 : 1;   // piece 0 always writes
+    } else {
+        walked(b, t, first, end);
+    }
+    const float *part = (const float *)((const char *)a.ws + (isq ? lay.dq : lay.dkv)) + at;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int p = first; p < end; ++p) s += *reinterpret_cast<const f32x4 *>(part + p * size);
+    store4((T *)(isq ? a.dq : a.dkv) + at, s);
+}
+
+static hipError_t allow_lds(const void *kernel, int bytes) {
+    return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 template <typename T, int DN, int DV>
 static hipError_t bwd_launch(const LatentBwdArgs &a, hipStream_t st)
 {
     typedef BwdCfg<T, DN, DV> C;
-    const BwdWs lay(a.B, a.Tq, a.Tk, a.H);
+    const BwdPlan plan = bwd_plan(sizeof(T) == 2, a.B, a.Tq, a.Tk, a.H);
     const long BH = (long)a.B * a.H, krows = (long)a.B * a.Tk;
     const int nq = (a.Tq + C::OWN - 1) / C::OWN, nk = (a.Tk + C::OWN - 1) / C::OWN;
-    auto kkv = latent_bwd_kv_kernel<T, DN, DV>;
-    auto kq = latent_bwd_q_kernel<T, DN, DV>;
-    const int lkv = C::KV_LDS, lq = 2 * C::BUF;
-    hipError_t e = hipFuncSetAttribute((const void *)kkv, hipFuncAttributeMaxDynamicSharedMemorySize, lkv);
-    if (e == hipSuccess) e = hipFuncSetAttribute((const void *)kq, hipFuncAttributeMaxDynamicSharedMemorySize, lq);
+    auto kkv = plan.qp > 1 ? latent_bwd_kv_kernel<T, DN, DV, true> : latent_bwd_kv_kernel<T, DN, DV, false>;
+    auto kq = plan.kp > 1 ? latent_bwd_q_kernel<T, DN, DV, true> : latent_bwd_q_kernel<T, DN, DV, false>;
+    hipError_t e = allow_lds((const void *)kkv, C::KV_LDS);
+    if (e == hipSuccess) e = allow_lds((const void *)kq, 2 * C::BUF);
     if (e != hipSuccess) return e;
-    if (BH * nq > 0) hipLaunchKernelGGL(kq, dim3((unsigned)(BH * nq)), dim3(256), lq, st, a, nq);
-    if (BH * nk > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk)), dim3(512), lkv, st, a, nk);
+    if (BH * nq > 0) hipLaunchKernelGGL(kq, dim3((unsigned)(BH * nq * plan.kp)), dim3(256), 2 * C::BUF, st, a, nq, plan);
+    if (BH * nk > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk * plan.qp)), dim3(512), C::KV_LDS, st, a, plan);
+    auto groups = [](long values) { return (int)((values + 1023) / 1024); };
+    const int nr = (int)((krows + 15) / 16), ndq = plan.kp > 1 ? groups(BH * a.Tq * C::DK) : 0;
+    const int ndkv = plan.qp > 1 ? groups(BH * a.Tk * (DN + DV)) : 0;
     if (krows > 0)
-        hipLaunchKernelGGL((latent_bwd_rope_kernel<T>), dim3((unsigned)((krows + 15) / 16)), dim3(256), 0, st,
-                           (const float *)((const char *)a.ws + lay.rope), (T *)a.dk_rope, krows, a.H);
+        hipLaunchKernelGGL((latent_bwd_sum_kernel<T, DN, DV>), dim3(nr + ndq + ndkv), dim3(256), 0, st, a, plan, nr, ndq);
     return hipGetLastError();
 }
 
@@ -434,6 +531,9 @@ hipError_t latent_bwd_launch(bool bf16, int dn, int dv, const LatentBwdArgs &a, 
     return dv == 128 ? bwd_launch<float, 64, 128>(a, st) : bwd_launch<float, 64, 64>(a, st);
 }
 
-unsigned long long latent_bwd_workspace(int B, int Tq, int Tk, int H) { return (unsigned long long)BwdWs(B, Tq, Tk, H).bytes; }
+unsigned long long latent_bwd_workspace(bool bf16, int B, int Tq, int Tk, int H, int dn, int dv)
+{
+    return (unsigned long long)BwdWs(bwd_plan(bf16, B, Tq, Tk, H), B, Tq, Tk, H, dn, dv).bytes;
+}
 
 } // namespace gdn

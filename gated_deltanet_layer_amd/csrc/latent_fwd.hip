@@ -3,7 +3,7 @@
 //   s_ij = scale (q_i^nope . k_j^nope + q_i^rope . k_j^rope),  j <= p_i = Tk - Tq + i
 //   o_i = sum_j softmax_j(s_ij) v_j,   lse_i = log sum_j exp s_ij
 //
-// One workgroup of four waves owns RT = 64 NR query rows of one head and walks
+// A workgroup of four waves owns RT = 64 NR query rows of one head and walks
 // the key tiles once, keeping the running maximum and sum of every row.  Scores
 // are computed transposed (keys on the accumulator's rows, query rows on its
 // lanes): a lane then holds four consecutive keys of one query row, so the
@@ -13,8 +13,7 @@
 
 namespace gdn {
 
-template <typename T, int DN, int DV> struct FwdCfg {
-    static constexpr int NR = sizeof(T) == 2 ? 2 : 1;      // 16-row groups a wave
+template <typename T, int DN, int DV, int NR> struct FwdCfg {   // NR: 16-row groups a wave
     static constexpr int NW = 4;
     static constexpr int RT = 16 * NR * NW;                // query rows a workgroup
     static constexpr int KT = sizeof(T) == 2 ? 64 : 32;    // keys a tile
@@ -24,14 +23,47 @@ template <typename T, int DN, int DV> struct FwdCfg {
     static constexpr int OFF_R = KT * NCPR * 16, OFF_V = OFF_R + KT * RCPR * 16, BUF = OFF_V + KT * VCPR * 16;
 };
 
-template <typename T, int DN, int DV>
-__global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int ntiles)
+// How a call is cut: 16-row groups a wave, and pieces of the keys.
+struct FwdPlan {
+    int nr, pieces, keys;   // keys a piece, whole tiles
+};
+
+// Rows: two groups a wave (each key operand serves two products) once that gives
+// every compute unit a workgroup; below that, one (333 rows, 16 heads: 13.5 us from
+// 14.4).  Keys: where there is less than two workgroups a unit and a row has eight
+// tiles or more, in pieces of four tiles or more, enough to fill the units twice (four
+// where there is a workgroup a unit already: causal rows differ); the longest row of a
+// causal call is otherwise its time (bf16, one row of 16 heads over 8192 keys 246 us,
+// in pieces 36; 64 rows of 8 heads over 4096: 111, 25; fp32, 4 heads of 2048: 211, 101;
+// from 512 workgroups on pieces cost more than they give: 2 x 16 heads of 2048 64, 70).
+inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
 {
-    typedef FwdCfg<T, DN, DV> C;
-    constexpr int NR = C::NR, KT = C::KT, DK = C::DK, NKB = DK / 32, NS = KT / 16, NCB = DV / 16;
+    const long bh = (long)B * H;
+    const int kt = bf16 ? 64 : 32, nt = (Tk + kt - 1) / kt;
+    FwdPlan p = {bf16 && bh * ((Tq + 127) / 128) >= 256 ? 2 : 1, 1, nt * kt};
+    const long wgs = bh * ((Tq + 64 * p.nr - 1) / (64 * p.nr));
+    if (wgs > 0 && wgs < 512 && nt >= 8) {
+        long n = wgs < 256 ? (512 + wgs - 1) / wgs : 4;
+        if (n > nt / 4) n = nt / 4;
+        if (n > 32) n = 32;
+        const int each = (int)((nt + n - 1) / n);
+        p.keys = each * kt;
+        p.pieces = (nt + each - 1) / each;
+    }
+    return p;
+}
+
+// Workspace of a call in pieces: float o[pieces][rows][DV], then float lse (base 2)
+// [pieces][rows], rows = B Tq H.
+template <typename T, int DN, int DV, int NR, bool CUT>
+__global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int ntiles, FwdPlan plan)
+{
+    typedef FwdCfg<T, DN, DV, NR> C;
+    constexpr int KT = C::KT, DK = C::DK, NKB = DK / 32, NS = KT / 16, NCB = DV / 16;
     extern __shared__ char lds[];
     const int BH = a.B * a.H;
-    const int bh = blockIdx.x % BH, tile = ntiles - 1 - (int)(blockIdx.x / BH);   // longest rows first
+    const int bh = blockIdx.x % BH, piece = CUT ? blockIdx.x / BH % plan.pieces : 0;
+    const int tile = ntiles - 1 - (int)(blockIdx.x / BH / (CUT ? plan.pieces : 1));   // longest rows first
     const int b = bh / a.H, h = bh % a.H;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
     const int off = a.Tk - a.Tq, n = live_len(a.lens, b, a.Tk);
@@ -65,7 +97,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
 
     // keys that any row of the workgroup, of this wave, may see
     const int last = min(n, off + min(q0 + C::RT, a.Tq));
-    const int nt = (off + q0 < n) ? (last + KT - 1) / KT : 0;
+    const int all = (off + q0 < n) ? (last + KT - 1) / KT : 0;
+    const int j0 = CUT ? piece * plan.keys / KT : 0, nt = CUT ? min(all, j0 + plan.keys / KT) : all;
     const int wlast = min(n, off + min(w0 + 16 * NR, a.Tq)), wfull = off + w0 + 1;
     auto load = [&](int j) {
         char *buf = lds + (j & 1) * C::BUF;
@@ -74,8 +107,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
         load_rows<C::VCPR, KT>(buf + C::OFF_V, (const char *)(kv + DN), kvs * C::ES, j * KT, n);
     };
     const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = col_base<T, C::VCPR>(4 * gq);
-    if (nt > 0) load(0);
-    for (int j = 0; j < nt; ++j) {
+    if (nt > j0) load(j0);
+    for (int j = j0; j < nt; ++j) {
         const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
         const int k0 = j * KT;
         wait_vm<0>();
@@ -96,6 +129,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
                 for (int g = 0; g < NR; ++g) s[t][g] = mma(s[t][g], kf, qf[g][kb]);
             }
         }
+        if (sizeof(T) == 2) pipeline<4, NS * NKB, NS * NKB * NR, 1, NR>();
         if (k0 + KT > wfull || k0 + KT > n) {   // the tile reaches past some row's last key
 #pragma unroll
             for (int t = 0; t < NS; ++t)
@@ -146,34 +180,86 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
                 for (int g = 0; g < NR; ++g) acc[cb][g] = mma(acc[cb][g], vf, pf[g]);
             }
         }
+        if (sizeof(T) == 2) pipeline<4, NS * NCB, NS / 2 * NCB * NR, 2, NR>();
     }
     T *o = (T *)a.o + ((long)b * a.Tq * a.H + h) * DV;
+    const long rows = (long)a.B * a.Tq * a.H;
+    float *po = (float *)a.ws + piece * rows * DV + ((long)b * a.Tq * a.H + h) * DV;
+    float *pl = (float *)a.ws + plan.pieces * rows * DV + piece * rows;
 #pragma unroll
     for (int g = 0; g < NR; ++g) {
         const int row = w0 + 16 * g + r16;
         const float ls = rows_sum(l[g]);
-        const bool seen = pos[g] >= 0;
+        // a row of a piece may see none of its keys, while its maximum still is -inf
+        const bool seen = pos[g] >= (CUT ? j0 * KT : 0) && (!CUT || m[g] != -INFINITY);
         const float inv = seen ? 1.f / ls : 0.f;
-        if (row < a.Tq) {
+        if (row >= a.Tq) continue;
+        if (seen || !CUT) {
 #pragma unroll
-            for (int cb = 0; cb < NCB; ++cb) store4(o + row * os + 16 * cb + 4 * gq, seen ? acc[cb][g] * inv : f32x4{0.f, 0.f, 0.f, 0.f});
-            if (a.lse && gq == 0)
-                a.lse[((long)b * a.Tq + row) * a.H + h] =
-                    seen ? (m[g] * c + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+            for (int cb = 0; cb < NCB; ++cb) {
+                const f32x4 v = seen ? acc[cb][g] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
+                if (CUT) store4(po + row * os + 16 * cb + 4 * gq, v);
+                else store4(o + row * os + 16 * cb + 4 * gq, v);
+            }
+        }
+        const float lg = seen ? m[g] * c + __builtin_amdgcn_logf(ls) : -INFINITY;
+        const long at = ((long)b * a.Tq + row) * a.H + h;
+        if (gq == 0) {
+            if (CUT) pl[at] = lg;
+            else if (a.lse) a.lse[at] = lg * LN2;
         }
     }
 }
 
-template <typename T, int DN, int DV>
-static hipError_t fwd_launch(const LatentFwdArgs &a, hipStream_t st)
+// Joins the pieces of every row; DV / 4 lanes a row.
+template <typename T, int DV>
+__global__ __launch_bounds__(256) void latent_fwd_join_kernel(LatentFwdArgs a, int pieces)
 {
-    typedef FwdCfg<T, DN, DV> C;
+    constexpr int LPR = DV / 4;
+    const long rows = (long)a.B * a.Tq * a.H, row = (long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const int at = threadIdx.x % LPR * 4;
+    if (row >= rows) return;
+    const float *po = (const float *)a.ws, *pl = po + pieces * rows * DV;
+    float top = -INFINITY, ls = 0.f;
+    for (int i = 0; i < pieces; ++i) top = fmaxf(top, pl[i * rows + row]);
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (top != -INFINITY)
+        for (int i = 0; i < pieces; ++i) {
+            const float lg = pl[i * rows + row];
+            if (lg == -INFINITY) continue;   // nothing was written
+            const float f = exp2_hw(lg - top);
+            ls += f;
+            sum += f * *reinterpret_cast<const f32x4 *>(po + (i * rows + row) * DV + at);
+        }
+    store4((T *)a.o + row * DV + at, ls > 0.f ? sum * (1.f / ls) : sum);
+    if (a.lse && at == 0) a.lse[row] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+}
+
+template <typename T, int DN, int DV, int NR, bool CUT>
+static hipError_t fwd_enqueue(const LatentFwdArgs &a, const FwdPlan &plan, hipStream_t st)
+{
+    typedef FwdCfg<T, DN, DV, NR> C;
     const int ntiles = (a.Tq + C::RT - 1) / C::RT;
-    auto k = latent_fwd_kernel<T, DN, DV>;
+    auto k = latent_fwd_kernel<T, DN, DV, NR, CUT>;
     const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * C::BUF);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k, dim3((unsigned)((long)ntiles * a.B * a.H)), dim3(256), 2 * C::BUF, st, a, ntiles);
+    hipLaunchKernelGGL(k, dim3((unsigned)((long)ntiles * a.B * a.H * plan.pieces)), dim3(256), 2 * C::BUF, st, a, ntiles, plan);
+    if (CUT) {
+        const long rows = (long)a.B * a.Tq * a.H, per = 256 / (DV / 4);
+        hipLaunchKernelGGL((latent_fwd_join_kernel<T, DV>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a, plan.pieces);
+    }
     return hipGetLastError();
+}
+
+template <typename T, int DN, int DV> static hipError_t fwd_launch(const LatentFwdArgs &a, hipStream_t st)
+{
+    constexpr bool BF = sizeof(T) == 2;
+    const FwdPlan plan = fwd_plan(BF, a.B, a.Tq, a.Tk, a.H);
+    if constexpr (BF) {
+        if (plan.nr == 2)
+            return plan.pieces > 1 ? fwd_enqueue<T, DN, DV, 2, true>(a, plan, st) : fwd_enqueue<T, DN, DV, 2, false>(a, plan, st);
+    }
+    return plan.pieces > 1 ? fwd_enqueue<T, DN, DV, 1, true>(a, plan, st) : fwd_enqueue<T, DN, DV, 1, false>(a, plan, st);
 }
 
 hipError_t latent_fwd_launch(bool bf16, int dn, int dv, const LatentFwdArgs &a, hipStream_t st)
@@ -186,6 +272,10 @@ hipError_t latent_fwd_launch(bool bf16, int dn, int dv, const LatentFwdArgs &a, 
     return dv == 128 ? fwd_launch<float, 64, 128>(a, st) : fwd_launch<float, 64, 64>(a, st);
 }
 
-unsigned long long latent_fwd_workspace(bool, int, int, int, int, int) { return 0; }
+unsigned long long latent_fwd_workspace(bool bf16, int B, int Tq, int Tk, int H, int dv)
+{
+    const FwdPlan plan = fwd_plan(bf16, B, Tq, Tk, H);
+    return plan.pieces > 1 ? (unsigned long long)plan.pieces * B * Tq * H * (dv + 1) * 4 : 0;
+}
 
 } // namespace gdn

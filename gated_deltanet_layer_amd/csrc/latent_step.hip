@@ -274,6 +274,7 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
     static_assert(CB % PC == 0 || PC % CB == 0, "");
     const int col0 = wave * CB;
     const int vb = col_base<T, CPR>(4 * gq) ^ (col0 % PC * 16 * C::ES), vcol = col0 / PC * 256;
+    constexpr int MMAS = C::ES == 2 ? 1 : 8;   // instructions of one mma
     Frag<T> qf[G][NKB];
     unsigned long long bits[G];
     f32x4 acc[CB][G];
@@ -327,6 +328,7 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
 #pragma unroll
                 for (int rg = 0; rg < G; ++rg) s[rg] = mma(s[rg], kf, qf[rg][kb]);
             }
+            pipeline<8, NKB * C::ES / 2, NKB * G * MMAS, C::ES / 2, G * MMAS>();
             const unsigned there = *reinterpret_cast<const unsigned *>(there4);
             if (__any(there != 0x01010101u || key + 3 >= cur.len)) {
 #pragma unroll
@@ -376,6 +378,8 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
 #pragma unroll
                 for (int rg = 0; rg < G; ++rg) acc[cb][rg] = mma(acc[cb][rg], vf, pf[rg]);
             }
+            constexpr int RD = C::ES == 2 ? 2 : 8;   // LDS reads of an operand across the rows
+            pipeline<G * C::ES / 2 + 4 * RD, G * C::ES / 2 + CB * RD, CB * G * MMAS, RD, G * MMAS>();
         }
         if (!more || nxt.n != cur.n) {
             // the sequence's (or the share's) last tile: the rows' sums, then write

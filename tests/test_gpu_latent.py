@@ -198,6 +198,20 @@ def test_backward_longer(B, Tq, Tk, H, dt):
     _check_bwd(_expanded(B, Tq, Tk, H, 128, 128, dt, seed=13), dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dn,dv", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("B,Tq,Tk,H,lens", [
+    (3, 700, 700, 2, [700, 70, 0]), (2, 300, 1200, 1, [1200, 930]), (2, 513, 1025, 2, [1025, 513]), (1, 640, 640, 3, None)])
+def test_calls_cut_into_pieces(B, Tq, Tk, H, dn, dv, dt, lens):
+    """Few workgroups and long walks: keys (fwd, dq) and query rows (dkv) are cut; ragged
+    lengths end inside a piece, before one, and before every row."""
+    _say(f"pieces B{B} Tq{Tq} Tk{Tk} H{H} dn{dn} dv{dv} {dt} lens {lens}")
+    assert gdn.gdn_latent_fwd_workspace_size(B, Tq, Tk, H, dn, 64, dv, DT[dt]) > 0
+    d = _expanded(B, Tq, Tk, H, dn, dv, dt, lens=lens, seed=23)
+    _check_fwd(d, dt)
+    _check_bwd(d, dt)
+
+
 def test_backward_without_queries_writes_zeros():
     kv, kr = torch.randn(1, 5, 2, 128, device=DEV), torch.randn(1, 5, 64, device=DEV)
     q = torch.zeros(1, 0, 2, 128, device=DEV)

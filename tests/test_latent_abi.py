@@ -122,6 +122,20 @@ def test_absorbed_unsupported(L, call, kw):
     assert call(L, nb=1 << 35, **kw) == gdn.GDN_ENOTSUP
 
 
+def test_fwd_in_pieces_needs_its_workspace(L):
+    n = ctypes.c_size_t(0)
+    a = dict(B=1, Tq=3, Tk=4096, H=2)
+    assert L.gdn_latent_fwd_workspace_size(1, 3, 4096, 2, 128, 64, 128, 1, ctypes.byref(n)) == gdn.GDN_OK and n.value > 0
+    assert _fwd(L, ws=None, **a) == gdn.GDN_EINVAL
+    assert _fwd(L, nb=n.value - 1, **a) == gdn.GDN_EINVAL
+    assert _fwd(L, ws=_p(4), **a) == gdn.GDN_EINVAL   # over o
+
+
+def test_rows_too_wide_for_32_bit_offsets_are_refused(L):
+    assert _fwd(L, B=1, Tq=1, Tk=1, H=(1 << 15) + 1) == gdn.GDN_ENOTSUP
+    assert _bwd(L, B=1, Tq=1, Tk=1, H=(1 << 15) + 1) == gdn.GDN_ENOTSUP
+
+
 def test_steps_takes_at_most_64_drafts(L):
     assert _steps(L, M=65) == gdn.GDN_ENOTSUP
 
