@@ -81,6 +81,13 @@ template <int CPR> __device__ __forceinline__ constexpr int swz(int row) {
     return CPR == 8 ? (((row >> 1) & 3) << 1) ^ (((row >> 3) & 1) * 5) : ((row & 7) << 1) ^ (((row >> 3) & 1) * 9);
 }
 
+// Keeps what is computed from x where it is used: addresses that the compiler moved out
+// of a long loop would stay in registers that the loop needs.
+__device__ __forceinline__ int pin(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // Operand with rows `row` (of this lane) and columns 32 kb + 8 gq .. +7.
 template <typename T, int CPR> __device__ __forceinline__ int row_base(int row) {
     const int ch = sizeof(T) == 2 ? lane_gq() : 2 * lane_gq();

@@ -352,7 +352,6 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
         for (int v = 0; v < NVB; ++v)
             if (live) dot += frag_dot<T>(of[g][v], load_frag<T>(o + row * os + 32 * v + 8 * gq));
         dd[g] = rows_sum(dot);
-        if (live && gq == 0 && piece == 0) Dw[(long)row * a.H] = dd[g];
     }
     f32x4 dq[NKC][NG];
 #pragma unroll
@@ -373,57 +372,106 @@ __global__ __launch_bounds__(256, 2) void latent_bwd_q_kernel(LatentBwdArgs a, i
     };
     const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = row_base<T, C::VCPR>(r16);
     const int nc = col_base<T, C::NCPR>(4 * gq), rc = col_base<T, C::RCPR>(4 * gq);
+    // of 32 keys (block t of tile j): P, and dP in the same layout
+    auto products = [&](int j, int t, f32x4 (&s)[2][NG], f32x4 (&dp)[2][NG]) {
+        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
+        const int k0 = j * ST;
+        const bool part = k0 + ST > wfull || k0 + ST > n;
+        const int nbl = pin(nb), rbl = pin(rb), vbl = pin(vb);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                dp[u][g] = s[u][g];
+            }
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const Frag<T> f = kb < DN / 32
+                    ? row_frag<T>(kt + (32 * t + 16 * u) * C::NCPR * 16, nbl, kb)
+                    : row_frag<T>(kt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rbl, kb - DN / 32);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, qf[g][kb]);
+            }
+#pragma unroll
+            for (int v = 0; v < NVB; ++v) {
+                const Frag<T> f = row_frag<T>(vt + (32 * t + 16 * u) * C::VCPR * 16, vbl, v);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, of[g][v]);
+            }
+            if (BF) pipeline<4, NKB + NVB, (NKB + NVB) * NG, 1, NG>();
+            GDN_SCHED_FENCE();
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[g]));
+            if (part) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[u][g][e] = k0 + 32 * t + 16 * u + 4 * gq + e > pos[g] ? 0.f : s[u][g][e];
+            }
+        }
+    };
+    if (BF && all <= 2) {
+        // The first rows, of few keys: o, rounded to bf16, is as large as v there, and
+        // the error that its rounding leaves in D, the same for all keys of a row, would
+        // be as large as the rounding of dS (a sixth more error in dq over 30 rows; rows
+        // of n keys have it 1 / sqrt(n) as large).  They have D from P and dP themselves.
+        float sum[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+        for (int j = 0; j < all; ++j) {
+            if (j == 0) load(0);
+            wait_vm<0>();
+            lds_barrier();
+            if (j + 1 < all) load(j + 1);
+#pragma unroll 1
+            for (int t = 0; t < ST / 32; ++t) {
+                f32x4 s[2][NG], dp[2][NG];
+                products(j, t, s, dp);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[g] += s[u][g][e] * dp[u][g][e];
+            }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int g = 0; g < NG; ++g) dd[g] = rows_sum(sum[g]);
+    }
+    if (piece == 0 && gq == 0) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            if (pos[g] >= 0) Dw[(long)(w0 + 16 * g + r16) * a.H] = dd[g];
+    }
     if (nt > j0) load(j0);
     for (int j = j0; j < nt; ++j) {
-        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
+        const char *kt = lds + (j & 1) * C::BUF;
         const int k0 = j * ST;
         wait_vm<0>();
         lds_barrier();
         if (j + 1 < nt) load(j + 1);
         if (k0 >= wlast || off + w0 >= n) continue;
-        const bool part = k0 + ST > wfull || k0 + ST > n;
 #pragma unroll 1
         for (int t = 0; t < ST / 32; ++t) {
             f32x4 s[2][NG], dp[2][NG];
+            products(j, t, s, dp);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    dp[u][g] = s[u][g];
-                }
-#pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    const Frag<T> f = kb < DN / 32
-                        ? row_frag<T>(kt + (32 * t + 16 * u) * C::NCPR * 16, nb, kb)
-                        : row_frag<T>(kt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rb, kb - DN / 32);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, qf[g][kb]);
-                }
-#pragma unroll
-                for (int v = 0; v < NVB; ++v) {
-                    const Frag<T> f = row_frag<T>(vt + (32 * t + 16 * u) * C::VCPR * 16, vb, v);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, of[g][v]);
-                }
-                if (BF) pipeline<4, NKB + NVB, (NKB + NVB) * NG, 1, NG>();
-                GDN_SCHED_FENCE();
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float p = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[g]));
-                        if (part && k0 + 32 * t + 16 * u + 4 * gq + e > pos[g]) p = 0.f;
-                        dp[u][g][e] = p * (dp[u][g][e] - dd[g]);
-                    }
-            }
+                for (int g = 0; g < NG; ++g) dp[u][g] = s[u][g] * (dp[u][g] - dd[g]);
+            const int ncl = pin(nc), rcl = pin(rc);
             Frag<T> sf[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
 #pragma unroll
             for (int i = 0; i < NKC; ++i) {
-                const Frag<T> f = i < DN / 16 ? col_frag<T, C::NCPR>(kt + 32 * t * C::NCPR * 16, nc, i)
-                                              : col_frag<T, C::RCPR>(kt + C::OFF_R + 32 * t * C::RCPR * 16, rc, i - DN / 16);
+                const Frag<T> f = i < DN / 16 ? col_frag<T, C::NCPR>(kt + 32 * t * C::NCPR * 16, ncl, i)
+                                              : col_frag<T, C::RCPR>(kt + C::OFF_R + 32 * t * C::RCPR * 16, rcl, i - DN / 16);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) dq[i][g] = mma(dq[i][g], f, sf[g]);
             }

@@ -142,7 +142,8 @@ def test_what_lies_behind_a_sequence_is_not_touched(dt):
 def _bwd_tol(d, o, lse, scale, u):
     """Tolerances of dq, dkv, dk_rope: the terms' absolute values times what each may
     be off.  P: 2 ds + 8 e (and the rounding u in dv); dP - D: (DV + 2) e sums of
-    absolute products; dS: u."""
+    absolute products, and in D u |do| |o|, by which do . o of the rounded o may be off
+    the sum of P dP, which the kernel takes for the first rows; dS: u."""
     Q, K, V = ref.heads(d["q"], d["kv"], d["k_rope"])
     B, H, Tq, D = Q.shape
     Tk = K.shape[2]
@@ -157,6 +158,7 @@ def _bwd_tol(d, o, lse, scale, u):
     ds = (D + 4) * E * scale * np.where(see, np.abs(Q) @ np.abs(K).swapaxes(2, 3), 0) + 4 * E * np.abs(L) + 8 * E
     dp, Dv = dO @ V.swapaxes(2, 3), (dO * O).sum(-1, keepdims=True)
     off = (V.shape[-1] + 4) * E * (np.abs(dO) @ np.abs(V).swapaxes(2, 3) + (np.abs(dO) * np.abs(O)).sum(-1, keepdims=True))
+    off = off + u * (np.abs(dO) * np.abs(O)).sum(-1, keepdims=True)
     eS = scale * p * ((u + ds + 4 * E) * np.abs(dp - Dv) + off)   # error of dS
     S = scale * p * np.abs(dp - Dv)
     nq, nk = (Tk + 8) * E, (Tq * 1 + 8) * E
