@@ -132,6 +132,23 @@ template <typename T, int CPR> __device__ __forceinline__ Frag<T> col_frag(const
     }
 }
 
+// Copies into LDS for the middle of other work: as g2lds16, g2lds16s and g2lds4, but
+// without the memory clobber, so that LDS reads of other buffers may move across them
+// (they keep their order among themselves and to the waits and barriers, which are
+// volatile too), and with addresses that the caller has in scalar registers.
+__device__ __forceinline__ unsigned lds_at(const char *lds) {   // uniform
+    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)lds;
+}
+__device__ __forceinline__ void copy16(const void *src, const char *lds) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");
+}
+__device__ __forceinline__ void copy16s(const void *base, unsigned off, const char *lds) {   // base: uniform
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_at(lds)) : "m0");
+}
+__device__ __forceinline__ void copy4(const void *src, const char *lds) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");
+}
+
 // Enqueue the copy of rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes
 // apart, x: row 0) into an LDS tile by NTHR threads; rows from n on read as zeros.
 // One instruction of the workgroup covers NTHR / CPR rows, a multiple of 8, so the
@@ -142,34 +159,20 @@ __device__ __forceinline__ void load_rows(char *tile, const char *x, long stride
     constexpr int RP = NTHR / CPR;
     static_assert(RP % 8 == 0 && ROWS % RP == 0, "");
     const int tid = threadIdx.x, row = tid / CPR, ch = ((tid % CPR) ^ swz<CPR>(row)) * 16;
-    char *dst = tile + (tid & ~63) * 16;
-    const char *p = x + r0 * stride;
+    const char *dst = tile + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024, *p = x + r0 * stride;
     if (r0 + ROWS <= n) {
         const unsigned off = (unsigned)(row * (int)stride + ch);
 #pragma unroll
         for (int i = 0; i < ROWS / RP; ++i)
-            g2lds16s(p + i * RP * stride, RP == 8 && (i & 1) ? (unsigned)(row * (int)stride + (ch ^ 144)) : off, dst + i * NTHR * 16);
+            copy16s(p + i * RP * stride, RP == 8 && (i & 1) ? (unsigned)(row * (int)stride + (ch ^ 144)) : off, dst + i * NTHR * 16);
     } else {
 #pragma unroll
         for (int i = 0; i < ROWS / RP; ++i) {
             const char *src = r0 + i * RP + row < n ? p + (i * RP + row) * stride + (RP == 8 && (i & 1) ? ch ^ 144 : ch)
                                                     : (const char *)latent_zero;
-            g2lds16(src, dst + i * NTHR * 16);
+            copy16(src, dst + i * NTHR * 16);
         }
     }
-}
-
-// g2lds16, g2lds16s and g2lds4 for the middle of other work: without the memory
-// clobber, so that LDS reads of other buffers may move across them.  They keep their
-// order among themselves and to the waits and barriers, which are volatile too.
-__device__ __forceinline__ void copy16(const void *src, const char *lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_addr(lds)) : "m0");
-}
-__device__ __forceinline__ void copy16s(const void *base, unsigned off, const char *lds) {   // base: uniform
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_addr(lds)) : "m0");
-}
-__device__ __forceinline__ void copy4(const void *src, const char *lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_addr(lds)) : "m0");
 }
 
 // Operand straight from global memory: 8 values of this lane's row.

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
         if (wave < 2 && lane < ST) {   // lse by the first wave, D by the second
             const int r = r0 + lane;
             const void *src = r >= qn ? (const void *)latent_zero : (wave ? Dw : lse) + (long)r * a.H;
-            g2lds4(src, (char *)(stat + (buf * 2 + wave) * ST));
+            copy4(src, (char *)(stat + (buf * 2 + wave) * ST));
         }
     };
     // before block i: block i - 1 of P is whole, and where a tile begins it is there
