@@ -61,6 +61,8 @@ hipError_t latent_step_launch(bool bf16, int r, const LatentStepArgs &a, hipStre
 unsigned long long latent_step_workspace(bool bf16, int N, int M, int H, int r);
 
 #ifdef __HIPCC__
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
 // Zeros: the source of every tile row behind the last live key, so that what such
 // rows hold in memory (it may be NaN) never meets a product.  One row of the widest
 // kind (512 + 64 fp32 values).

@@ -35,11 +35,11 @@ gdn_status expanded_sizes(int B, int Tq, int Tk, int H, int dn, int dr, int dv, 
     if (B < 0 || Tq < 0 || Tk < 0 || H < 0 || dn <= 0 || dr <= 0 || dv <= 0 || Tq > Tk) return GDN_EINVAL;
     if (prod(B, Tk, H, 4LL * ((long long)dn + dr + dv)) < 0) return GDN_EINVAL;
     if ((dn != 64 && dn != 128) || (dv != 64 && dv != 128) || dr != gdn::LATENT_ROPE) return GDN_ENOTSUP;
-    // grids: workgroups * 256 threads < 2^32
+    // grids: workgroups * 256 threads < 2^32 (16 rows of B Tk a workgroup)
     const long long rows = prod(B, H, Tq), tiles = prod(B, H, ((long long)Tk + 63) / 64);
     // a lane's offset within the 32 rows that one copy covers: 32 bits
     if (H > (1 << 15)) return GDN_ENOTSUP;
-    if (rows >= (1LL << 28) || tiles >= (1LL << 24) || prod(B, Tk) >= (1LL << 28)) return GDN_ENOTSUP;
+    if (rows >= (1LL << 28) || tiles >= (1LL << 24) || prod(B, Tk) >= (1LL << 27)) return GDN_ENOTSUP;
     return GDN_OK;
 }
 

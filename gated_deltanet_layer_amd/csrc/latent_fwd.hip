@@ -190,8 +190,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
     for (int g = 0; g < NR; ++g) {
         const int row = w0 + 16 * g + r16;
         const float ls = rows_sum(l[g]);
-        // a row of a piece may see none of its keys, while its maximum still is -inf
-        const bool seen = pos[g] >= (CUT ? j0 * KT : 0) && (!CUT || m[g] != -INFINITY);
+        // a row of a piece may see none of its keys: its sum is 0 (and a NaN where scores are)
+        const bool seen = pos[g] >= (CUT ? j0 * KT : 0) && (!CUT || ls != 0.f);
         const float inv = seen ? 1.f / ls : 0.f;
         if (row >= a.Tq) continue;
         if (seen || !CUT) {
@@ -223,16 +223,15 @@ __global__ __launch_bounds__(256) void latent_fwd_join_kernel(LatentFwdArgs a, i
     float top = -INFINITY, ls = 0.f;
     for (int i = 0; i < pieces; ++i) top = fmaxf(top, pl[i * rows + row]);
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    if (top != -INFINITY)
-        for (int i = 0; i < pieces; ++i) {
-            const float lg = pl[i * rows + row];
-            if (lg == -INFINITY) continue;   // nothing was written
-            const float f = exp2_hw(lg - top);
-            ls += f;
-            sum += f * *reinterpret_cast<const f32x4 *>(po + (i * rows + row) * DV + at);
-        }
-    store4((T *)a.o + row * DV + at, ls > 0.f ? sum * (1.f / ls) : sum);
-    if (a.lse && at == 0) a.lse[row] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+    for (int i = 0; i < pieces; ++i) {
+        const float lg = pl[i * rows + row];
+        if (lg == -INFINITY) continue;   // nothing was written
+        const float f = exp2_hw(lg - top);
+        ls += f;
+        sum += f * *reinterpret_cast<const f32x4 *>(po + (i * rows + row) * DV + at);
+    }
+    store4((T *)a.o + row * DV + at, ls != 0.f ? sum * (1.f / ls) : sum);
+    if (a.lse && at == 0) a.lse[row] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
 }
 
 template <typename T, int DN, int DV, int NR, bool CUT>

@@ -199,6 +199,32 @@ __device__ __forceinline__ f32x4 step_mask(f32x4 s, unsigned there, int first, i
     return s;
 }
 
+// A draft that a row does not see has the weight 0 in it, and 0 times a NaN or an
+// infinity (a batch of trees padded with drafts that hold anything) is a NaN: rows
+// from .. to - 1 of a tile are made finite between the two products, by each wave for
+// the columns that it alone multiplies, chunks ch0 .. ch0 + NCH - 1.  A row that sees
+// such a draft has its NaN from the score.
+template <typename T, int CPR, int NCH> __device__ __forceinline__ void step_finite(char *tile, int from, int to, int ch0)
+{
+    const unsigned top = sizeof(T) == 2 ? 0x7f80u : 0x7f800000u;   // an exponent of ones
+    for (int i = from * NCH + (threadIdx.x & 63); i < to * NCH; i += 64) {
+        const int row = i / NCH;
+        u32x4 *at = reinterpret_cast<u32x4 *>(tile + row * (CPR * 16) + (((ch0 + i % NCH) ^ swz<CPR>(row)) << 4));
+        u32x4 v = *at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 2) {
+                v[e] &= (v[e] & top) == top ? 0xffff0000u : ~0u;
+                v[e] &= (v[e] >> 16 & top) == top ? 0x0000ffffu : ~0u;
+            } else {
+                v[e] = (v[e] & top) == top ? 0u : v[e];
+            }
+        }
+        *at = v;
+    }
+    asm volatile("" ::: "memory");
+}
+
 // The drafts that query row `row` of sequence n sees.
 __device__ __forceinline__ unsigned long long step_bits(const LatentStepArgs &a, int n, int row, bool live)
 {
@@ -367,6 +393,9 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
             }
         }
         lds_barrier();
+        if (a.drafts && (cur.t + 1) * KT > cur.len)
+            step_finite<T, CPR, CB * 16 / PC>(lds + buf * C::TILE, max(0, cur.len - cur.t * KT),
+                                              min(KT, cur.len + a.drafts - cur.t * KT), col0 * 16 / PC);
 #pragma unroll
         for (int kk = 0; kk < KT / 32; ++kk) {
             Frag<T> pf[G];
@@ -403,7 +432,7 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
 #pragma unroll
             for (int rg = 0; rg < G; ++rg) {
                 const int lr = 16 * rg + r16, row = rt * RT + lr;
-                const bool seen = ls[rg] > 0.f;
+                const bool seen = ls[rg] != 0.f;   // a NaN shows
                 const float inv = seen ? 1.f / ls[rg] : 0.f;
                 const float lg = seen ? m[rg] * c + __builtin_amdgcn_logf(ls[rg]) : -INFINITY;
                 if (row >= rows) continue;
@@ -631,6 +660,9 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
                     for (int rg = 0; rg < 4; ++rg) acc[cb][rg] *= al[rg];
             }
             const char *tile = lds + k % NB * C::TILE + vcol;
+            if (a.drafts && (p.t + 1) * KT > p.len)
+                step_finite<T, CPR, CB * 2>(lds + k % NB * C::TILE, max(0, p.len - p.t * KT),
+                                            min(KT, p.len + a.drafts - p.t * KT), col0 * 2);
             constexpr int AHEAD = CB < 4 ? CB : 4;   // operands read before their products
             Frag<T> vf[CB];
 #pragma unroll
@@ -658,7 +690,7 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
                 for (int rg = 0; rg < 4; ++rg) {
                     const int lr = 16 * rg + r16, row = rt * RT + lr;
                     const float ls = fin[(k & 1) * 128 + lr], mc = fin[(k & 1) * 128 + 64 + lr];
-                    const bool seen = ls > 0.f;
+                    const bool seen = ls != 0.f;   // a NaN shows
                     const float inv = seen ? 1.f / ls : 0.f;
                     const float lg = seen ? mc + __builtin_amdgcn_logf(ls) : -INFINITY;
                     if (row >= rows) continue;
@@ -719,18 +751,16 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentStepArgs a, int 
     float sum[PER], ls = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) sum[i] = 0.f;
-    if (top != -INFINITY) {
 #pragma unroll 4
-        for (int w = wf + w0; w <= wl; w += WPR) {
-            const float *p = piece(w);
-            const float f = exp2_hw(p[RT * R + lr] - top);
-            ls += f;
+    for (int w = wf + w0; w <= wl; w += WPR) {
+        const float *p = piece(w);
+        const float lg = p[RT * R + lr], f = lg == -INFINITY ? 0.f : exp2_hw(lg - top);
+        ls += f;
 #pragma unroll
-            for (int i = 0; i < PER; i += 4) {
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(p + (long)lr * R + i * 64 + lane * 4);
+        for (int i = 0; i < PER; i += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(p + (long)lr * R + i * 64 + lane * 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum[i + e] += f * v[e];
-            }
+            for (int e = 0; e < 4; ++e) sum[i + e] += f * v[e];
         }
     }
     if constexpr (WPR > 1) {   // one row a workgroup
@@ -751,12 +781,12 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentStepArgs a, int 
                 for (int e = 0; e < 4; ++e) sum[i + e] += v[e];
             }
     }
-    const float inv = ls > 0.f ? 1.f / ls : 0.f;
+    const float inv = ls != 0.f ? 1.f / ls : 0.f;
     T *o = (T *)a.o + at * R;
 #pragma unroll
     for (int i = 0; i < PER; i += 4)
         store4(o + i * 64 + lane * 4, f32x4{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]} * inv);
-    if (a.lse && lane == 0) a.lse[at] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+    if (a.lse && lane == 0) a.lse[at] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
 }
 
 template <typename T, int R, typename K>

@@ -399,7 +399,7 @@ GDN_API gdn_status gdn_recurrent_step_prologue(const void *q_raw, const void *k_
  * Outputs and the workspace overlap neither inputs nor each other.  scale: finite
  * and > 0.  Results are the same on every call with the same arguments.
  * NOT checked: live inputs are finite (what lies behind a sequence's live length,
- * or in cache slots behind it, may hold anything).
+ * or in cache slots behind it, and drafts that a row does not see, may hold anything).
  *
  * Expanded causal forward.
  *
@@ -413,8 +413,8 @@ GDN_API gdn_status gdn_recurrent_step_prologue(const void *q_raw, const void *k_
  * Tq <= Tk.  Query i has position p = Tk - Tq + i (Tq = Tk: a whole sequence,
  * Tq < Tk: its last rows over all keys) and sees the keys j <= p, j < lens[b].  A
  * row at p >= lens[b] is padding: o = 0, lse = -inf.  dn and dv: 64 or 128, dr: 64
- * (GDN_ENOTSUP otherwise, and for B * H * Tq >= 2^28 or B * H * ceil(Tk / 64) >=
- * 2^24).  Any size may be 0.  Long rows with few workgroups are split over the
+ * (GDN_ENOTSUP otherwise, and for H > 2^15, B * H * Tq >= 2^28, B * Tk >= 2^27 or
+ * B * H * ceil(Tk / 64) >= 2^24).  Any size may be 0.  Long rows with few workgroups are split over the
  * keys; the pieces stand in the workspace (at least
  * gdn_latent_fwd_workspace_size bytes; NULL when that is 0).
  */
@@ -454,7 +454,8 @@ GDN_API gdn_status gdn_latent_bwd(const void *q, const void *kv, const void *k_r
  * A table entry outside 0 .. pages - 1 holds no tokens (they are not seen); entries
  * behind a sequence's last page are not read.  A sequence with no token gives
  * o = 0, lse = -inf.  r: 256 or 512, dr: 64, any page >= 1 (GDN_ENOTSUP otherwise,
- * and where pages * page, N * width or the call's tiles or rows pass 32 bits).
+ * and where M * H > 2^20, N * M * H >= 2^24, width * page > 2^30, or pages * page,
+ * N * width or the call's tiles pass 31 bits).
  */
 GDN_API gdn_status gdn_latent_step(const void *q, const void *cache, const int *table, const int *lens,
                                    void *o, float *lse, void *workspace, size_t workspace_bytes,

@@ -393,6 +393,39 @@ def test_steps_ignore_bits_from_m_on():
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,M,r", [(1, 6, 512), (4, 6, 256), (16, 6, 512), (16, 6, 256), (3, 64, 512)])
+def test_unused_drafts_may_hold_anything(H, M, r, dt):
+    """A batch of chains padded to M drafts: what the rows of the used drafts do not see
+    (NaN, infinities) leaves no trace in them, and a row that sees it is a NaN."""
+    lens, used = [61, 0, 130], [4, M - 1, 1]
+    d = _paged(lens, H, r, 16, dt, M=M, seed=17)
+    d["tree"] = None
+    want, wl = _run(_dev(d), 0.1)
+    for n, k in enumerate(used):
+        d["draft"][n, k:] = float("nan")
+        if n:
+            d["draft"][n, k] = 0
+            d["draft"][n, k, 3] = float("inf")
+    got, gl = _run(_dev(d), 0.1)
+    for n, k in enumerate(used):
+        assert torch.equal(got[n, :k], want[n, :k]) and torch.equal(gl[n, :k], wl[n, :k])
+        assert torch.isnan(got[n, k + 1:]).all()
+
+
+def test_a_nan_in_a_live_token_shows():
+    """In the step, and in the forward in pieces: NaN, never the zeros of an empty row."""
+    for lens in ([5], [3000]):
+        d = _paged(lens, 4, 512, 16, "bf16", seed=18)
+        d["cache"][d["table"][0, 0], 2] = float("nan")
+        o, lse = _run(_dev(d), 0.1)
+        assert torch.isnan(o).all() and torch.isnan(lse).all()
+    d = _dev(_expanded(1, 5, 3001, 2, 128, 128, "bf16", seed=18))
+    d["q"].fill_(float("nan"))
+    o, lse = gdn.latent_fwd(d["q"], d["kv"], d["k_rope"])
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
+
+
 def test_a_long_cache_passes_32_bit_offsets():
     """Rows beyond 2^31 bytes and 2^31 elements into the cache."""
     page, D = 64, 576
