@@ -335,6 +335,16 @@ def test_many_ragged_sequences(dt):
     _check_absorbed(_paged(lens, 2, 256, 16, dt, seed=4, width=188), dt)
 
 
+@pytest.mark.parametrize("r", [512, 256])
+def test_many_ragged_trees(r):
+    """The same for 64 rows a workgroup, with drafts on their own in empty sequences."""
+    g = torch.Generator().manual_seed(23)
+    lens = [int(x) for x in torch.randint(0, 70, (300,), generator=g)]
+    lens[0], lens[5], lens[299] = 0, 2000, 0
+    _check_absorbed(_paged(lens, 5, r, 16, "bf16", M=7, seed=24, width=125), "bf16")
+    _check_absorbed(_paged(lens, 70, r, 16, "bf16", seed=25, width=125), "bf16")
+
+
 def test_one_long_sequence_among_empty_ones():
     _check_absorbed(_paged([0] * 40 + [9000] + [0] * 40, 16, 512, 64, "bf16", seed=5, width=141), "bf16")
 
@@ -486,11 +496,13 @@ def test_prefill_then_steps_then_a_tree():
         torch.testing.assert_close(one, t[:, m], rtol=1e-5, atol=1e-5)
 
 
+@pytest.mark.parametrize("T", [200, 1000])   # 1000: in pieces, forward and backward
 @pytest.mark.parametrize("other", ["object", "handle"])
-def test_another_stream(other):
+def test_another_stream(other, T):
     s = torch.cuda.Stream(DEV)
     d = _dev(_paged([700, 20], 16, 512, 16, "bf16", seed=12))
-    e = _dev(_expanded(1, 200, 200, 4, 64, 64, "bf16", seed=12))
+    e = _dev(_expanded(1, T, T, 4, 64, 64, "bf16", seed=12))
+    assert (gdn.gdn_latent_fwd_workspace_size(1, T, T, 4, 64, 64, 64, torch.bfloat16) > 0) == (T == 1000)
     want = _run(d, 0.1)
     ow = gdn.latent_fwd(e["q"], e["kv"], e["k_rope"])
     gw = gdn.latent_bwd(e["q"], e["kv"], e["k_rope"], *ow, e["d_o"])
@@ -516,14 +528,16 @@ def test_two_calls_at_once_with_their_own_workspaces():
             assert torch.equal(a, b)
 
 
-def test_captured_and_replayed():
-    """The calls in a graph, replayed with new inputs in place and eager work between."""
-    d = _dev(_paged([400, 33], 16, 512, 16, "bf16", M=4, seed=15))
-    e = _dev(_expanded(1, 150, 150, 3, 64, 64, "bf16", seed=15))
+@pytest.mark.parametrize("T,M,dt", [(150, 4, "bf16"), (700, 8, "bf16"), (300, 2, "fp32")])   # from 300 on in pieces
+def test_captured_and_replayed(T, M, dt):
+    """The calls in a graph, replayed with new inputs and lengths in place and eager work
+    between."""
+    d = _dev(_paged([400, 33], 16, 512, 16, dt, M=M, seed=15))
+    e = _dev(_expanded(2, T, T, 3, 64, 64, dt, lens=[T, T], seed=15))
 
     def work():
-        o, lse = gdn.latent_fwd(e["q"], e["kv"], e["k_rope"])
-        g = gdn.latent_bwd(e["q"], e["kv"], e["k_rope"], o, lse, e["d_o"])
+        o, lse = gdn.latent_fwd(e["q"], e["kv"], e["k_rope"], lens=e["lens"])
+        g = gdn.latent_bwd(e["q"], e["kv"], e["k_rope"], o, lse, e["d_o"], lens=e["lens"])
         return [*_run(d, 0.1), gdn.latent_step(d["q"][:, 0].contiguous(), d["cache"], d["table"], d["lens"], 0.1), o, lse, *g.values()]
 
     s = torch.cuda.Stream(DEV)
@@ -539,6 +553,7 @@ def test_captured_and_replayed():
         for x in (d["q"], d["cache"], d["draft"], e["q"], e["kv"], e["d_o"]):
             x.copy_(torch.randn(x.shape, generator=g).to(x.dtype))
         d["lens"].copy_(torch.tensor([400 - 50 * i, 33 + i], dtype=torch.int32))
+        e["lens"].copy_(torch.tensor([T - 70 * i % T, i * T // 3], dtype=torch.int32))
         want = [x.clone() for x in work()]
         graph.replay()
         torch.cuda.synchronize()
@@ -555,6 +570,15 @@ def test_outputs_stay_inside_their_buffers():
     ob = torch.full((2 * 3 * 512 + 512,), 5.0, dtype=torch.bfloat16, device=DEV)
     gdn.gdn_latent_step(d["q"], d["cache"], d["table"], d["lens"], ob[256:-256].view(2, 3, 512), None, big[4096:-4096], 0.1)
     assert (ob[:256] == 5).all() and (ob[-256:] == 5).all() and (big[:4096] == 77).all() and (big[-4096:] == 77).all()
+    f = _dev(_expanded(1, 70, 1000, 3, 64, 64, "bf16", seed=16))   # in pieces
+    n = gdn.gdn_latent_fwd_workspace_size(1, 70, 1000, 3, 64, 64, 64, torch.bfloat16)
+    big, ob = torch.full((n + 8192,), 77, dtype=torch.uint8, device=DEV), torch.full((70 * 3 * 64 + 512,), 5.0, dtype=torch.bfloat16, device=DEV)
+    lb = torch.full((70 * 3 + 64,), 5.0, device=DEV)
+    gdn.gdn_latent_fwd(f["q"], f["kv"], f["k_rope"], None, ob[256:-256].view(1, 70, 3, 64), lb[32:-32].view(1, 70, 3), big[4096:-4096], 0.1)
+    want = gdn.latent_fwd(f["q"], f["kv"], f["k_rope"], scale=0.1)
+    assert n > 0 and torch.equal(ob[256:-256].view(1, 70, 3, 64), want[0]) and torch.equal(lb[32:-32].view(1, 70, 3), want[1])
+    assert (ob[:256] == 5).all() and (ob[-256:] == 5).all() and (big[:4096] == 77).all() and (big[-4096:] == 77).all()
+    assert (lb[:32] == 5).all() and (lb[-32:] == 5).all()
     o, lse = gdn.latent_fwd(e["q"], e["kv"], e["k_rope"])
     n = gdn.gdn_latent_bwd_workspace_size(1, 70, 70, 3, 64, 64, 64, torch.bfloat16)
     big = torch.full((n + 8192,), 77, dtype=torch.uint8, device=DEV)
