@@ -31,11 +31,15 @@ struct FwdPlan {
 // Rows: two groups a wave (each key operand serves two products) once that gives
 // every compute unit a workgroup; below that, one (333 rows, 16 heads: 13.5 us from
 // 14.4).  Keys: where there is less than two workgroups a unit and a row has eight
-// tiles or more, in pieces of four tiles or more, enough to fill the units twice (four
-// where there is a workgroup a unit already: causal rows differ); the longest row of a
-// causal call is otherwise its time (bf16, one row of 16 heads over 8192 keys 246 us,
-// in pieces 36; 64 rows of 8 heads over 4096: 111, 25; fp32, 4 heads of 2048: 211, 101;
-// from 512 workgroups on pieces cost more than they give: 2 x 16 heads of 2048 64, 70).
+// tiles or more, in pieces of four tiles or more; the longest row of a causal call is
+// otherwise its time (bf16, one row of 16 heads over 8192 keys 246 us, in pieces 36; 64
+// rows of 8 heads over 4096: 111, 25; fp32, 4 heads of 2048: 211, 77; from 512
+// workgroups on pieces cost more than they give: 2 x 16 heads of 2048 64, 70).  Pieces
+// to fill the units twice, of bf16 four where there is a workgroup a unit already
+// (causal rows differ).  fp32 has tiles of half the keys and four times the time: half
+// as many again, as half the pieces of causal rows are empty (4 heads of 2048 77 us,
+// 97 without), and from a workgroup a unit on about 16 tiles a piece (8 heads of 3000
+// 223 us, in four pieces 293; 16 of 1021 in three 48, in four 52).
 inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
 {
     const long bh = (long)B * H;
@@ -43,7 +47,8 @@ inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
     FwdPlan p = {bf16 && bh * ((Tq + 127) / 128) >= 256 ? 2 : 1, 1, nt * kt};
     const long wgs = bh * ((Tq + 64 * p.nr - 1) / (64 * p.nr));
     if (wgs > 0 && wgs < 512 && nt >= 8) {
-        long n = wgs < 256 ? (512 + wgs - 1) / wgs : 4;
+        const long fill = bf16 ? 512 : 768, many = bf16 ? 4 : nt < 52 ? 3 : (nt + 12) / 16;
+        long n = wgs < 256 ? (fill + wgs - 1) / wgs : many;
         if (n > nt / 4) n = nt / 4;
         if (n > 32) n = 32;
         const int each = (int)((nt + n - 1) / n);
