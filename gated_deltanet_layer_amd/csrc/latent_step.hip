@@ -4,16 +4,28 @@
 //   row_j = [c_j (r) | k_j^rope (64)], j over the len_n cached tokens, then the drafts
 //   s_ij = scale q_i . row_j,   o_i = sum_j softmax_j(s_ij) c_j
 //
-// All M * H query rows of a sequence read the same cache rows.  A workgroup
-// takes RT of the rows and a run of key tiles; each tile is copied once into LDS and serves as keys (all columns) and as values (the first r).
-// In the first product the waves split the tile's keys, in the second the r
-// output columns, so the tile is read from LDS twice (three times at RT = 64, where two waves share
-// each slab of keys: the queries of 64 rows do not fit one wave's registers).
+// All M * H query rows of a sequence read the same cache rows.  A workgroup takes RT
+// of the rows and a run of key tiles; each tile is copied once into LDS and serves as
+// keys (all columns) and as values (the first r).  Two kernels, by the rows:
+//
+//   up to 32 (fp32: tiles of 16)  latent_step_kernel.  Four waves; in the first product
+//       they split the tile's keys, in the second the r output columns.  Bound by the
+//       cache's bytes: 64 sequences of 4100 tokens, 16 heads, r = 512 (229 MB live) 48 us
+//       in the kernel, the rate of a plain copy of such a cache; with join and launches
+//       52-62 us.  One sequence of 300: 10 us, a chain of latencies (lengths, page,
+//       tile, two products), and 4 us of the join.
+//   more (bf16)  latent_step_wide_kernel, 64 rows.  At 64 rows a byte of the cache is
+//       worth 122 operations, so the matrix cores, LDS and the copies all near their
+//       limits: 16 sequences of 4096 x 32 drafts x 32 heads 150 us (0.75 PFLOP/s, matrix
+//       cores 36 % busy), 128 of up to 8192 with 128 heads 310 us (3.0 TB/s; a tile is
+//       taken from HBM once and from L2 by the second row tile).  The four waves of the
+//       second product set the pace, about 2700 cycles for 32 keys.
 //
 // The runs are equal shares of all key tiles of the batch, whatever the lengths:
 // the workgroups add up the tiles of all sequences on their own and each takes
 // its share, which may begin and end inside a sequence.  Such pieces go to the
-// workspace (normalised, with their log-sum-exp) and a second kernel joins them.
+// workspace (normalised, with their log-sum-exp) and a second kernel joins them (4-5 us;
+// 12-16 where there are thousands of rows).
 #include "latent.h"
 
 namespace gdn {
@@ -21,7 +33,11 @@ namespace gdn {
 constexpr int STEP_CUS = 256;   // one workgroup a compute unit: two tiles fill its LDS
 
 // Up to 32 rows: four waves divide each tile's keys for the scores and the output
-// columns for the second product, every wave for all 16 G rows.
+// columns for the second product, every wave for all 16 G rows.  Two tiles of 64 keys
+// (72 KB each at r = 512) leave room for one workgroup a unit: one is in use while the
+// other arrives, which keeps 72 KB a unit in flight, more than the latency of HBM asks
+// for.  fp32: 32 keys, and two of the waves have no slab in the first product (8 x 2000
+// tokens, r = 256: 17 us).
 template <typename T, int R, int G> struct StepCfg {
     static constexpr int NW = 4, D = R + LATENT_ROPE, RT = 16 * G;
     static constexpr int KT = sizeof(T) == 2 ? 64 : 32;
@@ -463,7 +479,9 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
 // of the output columns and multiply the weights with the values, a tile behind.  So
 // neither needs more registers than two waves a SIMD have, and the matrix cores of
 // each SIMD get the products of one kind while the other's wave works on its softmax
-// or, the second kind, on the copies of the tiles to come.  Weights change hands as whole operands, a lane's own eight values.
+// or, the second kind, on the copies of the tiles to come.  Weights change hands as
+// whole operands, a lane's own eight values.  With waves that did both products for
+// 16 rows each the trees above took 209 us, with the copies before the products 186.
 template <int R>
 __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs a, int ntile, int max_shares)
 {
