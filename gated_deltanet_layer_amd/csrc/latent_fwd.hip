@@ -31,223 +31,394 @@ template <typename T, int DN, int DV, int NR> struct FwdCfg {   // NR: 16-row gr
     static constexpr int OFF_R = KT * NCPR * 16, OFF_V = OFF_R + KT * RCPR * 16, BUF = OFF_V + KT * VCPR * 16;
 };
 
-// How a call is cut: 16-row groups a wave, and pieces of the keys.
+// How a call is cut: 16-row groups a wave, and for small grids either pieces of every
+// row tile's keys, or the number of workgroups that share all key tiles of the call.
 struct FwdPlan {
-    int nr, pieces, keys;   // keys a piece, whole tiles
+    int nr, pieces, each;   // pieces of a row tile, `each` key tiles each (1: whole)
+    int shares;             // 0: none
 };
 
 // Rows: two groups a wave (each key operand serves two products) once that gives
 // every compute unit a workgroup; below that, one (333 rows, 16 heads: 13.5 us from
-// 14.4).  Keys: where there is less than two workgroups a unit and a row has eight
-// tiles or more, in pieces of four tiles or more; the longest row of a causal call is
-// otherwise its time (bf16, one row of 16 heads over 8192 keys 246 us, in pieces 36; 64
-// rows of 8 heads over 4096: 111, 25; fp32, 4 heads of 2048: 211, 77; from 512
-// workgroups on pieces cost more than they give: 2 x 16 heads of 2048 64, 70).  Pieces
-// to fill the units twice, of bf16 four where there is a workgroup a unit already
-// (causal rows differ).  fp32 has tiles of half the keys and four times the time: half
-// as many again, as half the pieces of causal rows are empty (4 heads of 2048 77 us,
-// 97 without), and from a workgroup a unit on about 16 tiles a piece (8 heads of 3000
-// 223 us, in four pieces 293; 16 of 1021 in three 48, in four 52).
+// 14.4).  Keys: the longest row of a causal call is otherwise its time.  Where there is
+// less than two workgroups a unit and a row has eight tiles or more (from 512 workgroups
+// on cutting costs more than it gives: 2 x 16 heads of 2048 64 us, 85):
+//
+// - Shares, where each gets eight tiles or more: 512 workgroups (two a unit) take equal
+//   runs of key tiles, whatever rows they are of, the runs of one head on one XCD (bf16,
+//   2 heads of 8192 71 us, as pieces 141; 8 of 4096 77, 89; 10 of 2048 43, 52; fp32, 8
+//   of 3000 175, 224; on any XCD 10 of 2048 47).  Two row groups from half a workgroup a
+//   unit on (2 heads of 8192: 71 from 83).
+// - Pieces of four tiles or more, a workgroup each, where a change of rows inside a share
+//   (its queries' loads and its result's stores, which nothing hides) would cost more
+//   (8 heads of 1024: 23 us, in shares 30; one row of 16 heads over 8192 keys 38, 51).
+//   Enough to fill the units twice, fp32, whose tiles have half the keys and four times
+//   the time, half as many again (2 x 8 heads of 700: 41 us, 46 without).
 inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
 {
-    const long bh = (long)B * H;
+    const long bh = (long)B * H, wide = bh * ((Tq + 127) / 128);
     const int kt = bf16 ? 64 : 32, nt = (Tk + kt - 1) / kt;
-    FwdPlan p = {bf16 && bh * ((Tq + 127) / 128) >= 256 ? 2 : 1, 1, nt * kt};
-    const long wgs = bh * ((Tq + 64 * p.nr - 1) / (64 * p.nr));
-    if (wgs > 0 && wgs < 512 && nt >= 8) {
-        const long fill = bf16 ? 512 : 768, many = bf16 ? 4 : nt < 52 ? 3 : (nt + 12) / 16;
-        long n = wgs < 256 ? (fill + wgs - 1) / wgs : many;
-        if (n > nt / 4) n = nt / 4;
-        if (n > 32) n = 32;
-        const int each = (int)((nt + n - 1) / n);
-        p.keys = each * kt;
-        p.pieces = (nt + each - 1) / each;
+    FwdPlan p = {bf16 && wide >= 256 ? 2 : 1, 1, nt, 0};
+    const long tiles = (Tq + 64 * p.nr - 1) / (64 * p.nr), wgs = bh * tiles;
+    if (wgs <= 0 || wgs >= 512 || nt < 8) return p;
+    if (wgs * nt - bh * tiles * (tiles - 1) / 2 * (64 * p.nr / kt) >= 8 * 512 && wgs * nt < (1L << 30)) {
+        p.shares = 512;
+        if (bf16 && wide >= 128) p.nr = 2;
+        return p;
+    }
+    const long fill = bf16 ? 512 : 768;
+    long n = wgs < 256 ? (fill + wgs - 1) / wgs : 4;
+    if (n > nt / 4) n = nt / 4;
+    if (n > 32) n = 32;
+    p.each = (int)((nt + n - 1) / n);
+    p.pieces = (nt + p.each - 1) / p.each;
+    return p;
+}
+
+// Workspace of a call that is cut.  Pieces: float o[pieces][B Tq H][DV], float
+// lse[pieces][B Tq H] (base 2).  Shares: int prefix[B + 1], the key tiles before each
+// sequence, then for each share its first and last piece of a row tile, float o[slot][DV],
+// and float lse[slot] of each, slot = min(RT, Tq) rows.
+struct FwdWs {
+    long o, lse, bytes, rows;
+    __host__ __device__ FwdWs(const FwdPlan &p, int B, int Tq, int H, int dv) {
+        const int rt = 64 * p.nr;
+        rows = p.shares ? (Tq < rt ? Tq : rt) : (long)B * Tq * H;
+        o = p.shares ? ((long)(B + 1) * 4 + 255) & ~255L : 0;
+        const long all = rows * (p.shares ? 2 * p.shares : p.pieces);
+        lse = o + all * dv * 4;
+        bytes = lse + all * 4;
+    }
+};
+
+// The key tiles of a causal call.  Row tile t of a sequence of n keys has those up to its
+// last row's position: ceil(off / KT) + (t + 1) RT / KT of them, the last live one up to n.
+template <int RT, int KT> struct FwdTiles {
+    static __device__ __forceinline__ int of(const LatentFwdArgs &a, int n, int t) {
+        const int off = a.Tk - a.Tq, end = off + min((t + 1) * RT, a.Tq);
+        return t * RT < a.Tq && off + t * RT < n ? (min(n, end) + KT - 1) / KT : 0;
+    }
+    static __device__ __forceinline__ int before(const LatentFwdArgs &a, int t) {   // row tile t, a live one
+        return t * ((a.Tk - a.Tq + KT - 1) / KT) + (RT / KT) * (t * (t + 1) / 2);
+    }
+    static __device__ __forceinline__ int all(const LatentFwdArgs &a, int n) {   // of one head
+        const int off = a.Tk - a.Tq;
+        if (n <= off) return 0;
+        const int t = (n - off - 1) / RT;
+        return before(a, t) + of(a, n, t);
+    }
+};
+
+// Key tile j of the nkt of row tile t, head h of sequence b, which has n keys.
+struct FwdPos {
+    int b, h, t, j, nkt, n;
+};
+
+// The tile after p; called only while one is left.
+template <int RT, int KT> __device__ __forceinline__ FwdPos fwd_after(const LatentFwdArgs &a, FwdPos p)
+{
+    if (++p.j < p.nkt) return p;
+    p.j = 0;
+    p.nkt = FwdTiles<RT, KT>::of(a, p.n, ++p.t);
+    if (p.nkt == 0) {
+        p.t = 0;
+        if (++p.h == a.H) {
+            p.h = 0;
+            do p.n = live_len(a.lens, ++p.b, a.Tk);
+            while (p.n <= a.Tk - a.Tq && p.b + 1 < a.B);
+        }
+        p.nkt = FwdTiles<RT, KT>::of(a, p.n, 0);
     }
     return p;
 }
 
-// Workspace of a call in pieces: float o[pieces][rows][DV], then float lse (base 2)
-// [pieces][rows], rows = B Tq H.
-template <typename T, int DN, int DV, int NR, bool CUT>
+// Sums of a value of each lane over the lanes up to it.
+__device__ __forceinline__ int lanes_scan(int x)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(x, d, 64);
+        if ((int)(threadIdx.x & 63) >= d) x += v;
+    }
+    return x;
+}
+
+// Tiles of a share: all of the call's over `most` shares, rounded up.
+__host__ __device__ inline int fwd_each(int total, int most) { return total < most ? 1 : (total + most - 1) / most; }
+
+// This workgroup's share, its first key tile and the number of them; 0 if it has none.
+// Every wave adds up all sequences on its own; the first share leaves the tiles before
+// each for the join.
+template <int RT, int KT> __device__ __forceinline__ int fwd_share(const LatentFwdArgs &a, int share, int most, FwdPos &cur)
+{
+    typedef FwdTiles<RT, KT> Tiles;
+    const int lane = threadIdx.x & 63;
+    int *prefix = (int *)a.ws;
+    auto of = [&](int b) { return b < a.B ? a.H * Tiles::all(a, live_len(a.lens, b, a.Tk)) : 0; };
+    int total = 0;
+    for (int b = 0; b < a.B; b += 64) {
+        const int mine = of(b + lane), incl = lanes_scan(mine);
+        if (share == 0 && b + lane < a.B) prefix[b + lane] = total + incl - mine;
+        total += __builtin_amdgcn_readlane(incl, 63);
+    }
+    if (share == 0 && lane == 0) prefix[a.B] = total;
+    const int each = fwd_each(total, most), g0 = share * each;
+    if (g0 >= total) return 0;
+    int at = 0;
+    for (int b = 0;; b += 64) {
+        const int mine = of(b + lane), incl = lanes_scan(mine), sum = __builtin_amdgcn_readlane(incl, 63);
+        if (g0 < at + sum) {
+            const int l = __builtin_ctzll(__ballot(g0 < at + incl));
+            cur.b = b + l;
+            at += __builtin_amdgcn_readlane(incl - mine, l);
+            break;
+        }
+        at += sum;
+    }
+    cur.n = __builtin_amdgcn_readfirstlane(live_len(a.lens, cur.b, a.Tk));
+    const unsigned one = Tiles::all(a, cur.n), r = g0 - at;
+    cur.h = (int)(r / one);
+    const int x = (int)(r % one);
+    // the row tile: before(t) <= x < before(t + 1)
+    const float c = (a.Tk - a.Tq + KT - 1) / KT + .5f * (RT / KT);
+    int t = max(0, (int)((sqrtf(c * c + 2.f * (RT / KT) * (float)x) - c) / (RT / KT)) - 1);
+    while (t * RT + RT < a.Tq && Tiles::before(a, t + 1) <= x) ++t;
+    while (t > 0 && Tiles::before(a, t) > x) --t;
+    cur.t = __builtin_amdgcn_readfirstlane(t);
+    cur.j = __builtin_amdgcn_readfirstlane(x - Tiles::before(a, t));
+    cur.nkt = Tiles::of(a, cur.n, cur.t);
+    return min(each, total - g0);
+}
+
+enum { WHOLE, PIECES, SHARES };   // how a call is cut
+
+template <typename T, int DN, int DV, int NR, int CUT>
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int ntiles, FwdPlan plan)
 {
     typedef FwdCfg<T, DN, DV, NR> C;
-    constexpr int KT = C::KT, DK = C::DK, NKB = DK / 32, NS = KT / 16, NCB = DV / 16;
+    constexpr int KT = C::KT, RT = C::RT, DK = C::DK, NKB = DK / 32, NS = KT / 16, NCB = DV / 16;
     extern __shared__ char lds[];
-    const int BH = a.B * a.H;
-    const int bh = blockIdx.x % BH, piece = CUT ? blockIdx.x / BH % plan.pieces : 0;
-    const int tile = ntiles - 1 - (int)(blockIdx.x / BH / (CUT ? plan.pieces : 1));   // longest rows first
-    const int b = bh / a.H, h = bh % a.H;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
-    const int off = a.Tk - a.Tq, n = live_len(a.lens, b, a.Tk);
-    const int q0 = tile * C::RT, w0 = q0 + wave * 16 * NR;   // first row of the workgroup, of the wave
+    const int off = a.Tk - a.Tq;
     const long qs = (long)a.H * DK, kvs = (long)a.H * (DN + DV), os = (long)a.H * DV;
-    const T *q = (const T *)a.q + ((long)b * a.Tq * a.H + h) * DK;
-    const T *kv = (const T *)a.kv + ((long)b * a.Tk * a.H + h) * (DN + DV);
-    const T *kr = (const T *)a.k_rope + (long)b * a.Tk * LATENT_ROPE;
     const float c = a.scale * LOG2E;
-
-    int pos[NR];   // position of this lane's rows; -1: the row sees nothing
-    Frag<T> qf[NR][NKB];
-#pragma unroll
-    for (int g = 0; g < NR; ++g) {
-        const int row = w0 + 16 * g + r16;
-        const bool live = row < a.Tq && off + row < n;
-        pos[g] = live ? off + row : -1;
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-            qf[g][kb] = live ? load_frag<T>(q + row * qs + 32 * kb + 8 * gq) : zero_frag<T>();
+    const FwdWs lay(plan, a.B, a.Tq, a.H, DV);
+    FwdPos cur, nxt;
+    int share = 0, left;   // key tiles to go
+    if constexpr (CUT == SHARES) {
+        // the shares of one head, which read the same keys, on one XCD
+        share = blockIdx.x % 8 * (plan.shares / 8) + blockIdx.x / 8;
+        left = fwd_share<RT, KT>(a, share, plan.shares, cur);
+        if (left == 0) return;
+    } else {
+        const int BH = a.B * a.H, bh = blockIdx.x % BH, piece = CUT == PIECES ? blockIdx.x / BH % plan.pieces : 0;
+        cur.b = bh / a.H;
+        cur.h = bh % a.H;
+        cur.t = ntiles - 1 - (int)(blockIdx.x / BH / (CUT == PIECES ? plan.pieces : 1));   // longest rows first
+        cur.n = live_len(a.lens, cur.b, a.Tk);
+        cur.nkt = FwdTiles<RT, KT>::of(a, cur.n, cur.t);
+        cur.j = piece * plan.each;
+        left = min(plan.each, cur.nkt - cur.j);
+        if (CUT == PIECES && left <= 0) return;   // the join knows which pieces there are
     }
-    f32x4 acc[NCB][NR];
-    float m[NR], l[NR];
-#pragma unroll
-    for (int g = 0; g < NR; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-#pragma unroll
-        for (int cb = 0; cb < NCB; ++cb) acc[cb][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-
-    // keys that any row of the workgroup, of this wave, may see
-    const int last = min(n, off + min(q0 + C::RT, a.Tq));
-    const int all = (off + q0 < n) ? (last + KT - 1) / KT : 0;
-    const int j0 = CUT ? piece * plan.keys / KT : 0, nt = CUT ? min(all, j0 + plan.keys / KT) : all;
-    const int wlast = min(n, off + min(w0 + 16 * NR, a.Tq)), wfull = off + w0 + 1;
-    auto load = [&](int j) {
-        char *buf = lds + (j & 1) * C::BUF;
-        load_rows<C::NCPR, KT>(buf, (const char *)kv, kvs * C::ES, j * KT, n);
-        load_rows<C::RCPR, KT>(buf + C::OFF_R, (const char *)kr, LATENT_ROPE * C::ES, j * KT, n);
-        load_rows<C::VCPR, KT>(buf + C::OFF_V, (const char *)(kv + DN), kvs * C::ES, j * KT, n);
+    auto load = [&](const FwdPos &p, int buffer) {
+        char *buf = lds + buffer * C::BUF;
+        const T *kv = (const T *)a.kv + ((long)p.b * a.Tk * a.H + p.h) * (DN + DV);
+        const T *kr = (const T *)a.k_rope + (long)p.b * a.Tk * LATENT_ROPE;
+        load_rows<C::NCPR, KT>(buf, (const char *)kv, kvs * C::ES, p.j * KT, p.n);
+        load_rows<C::RCPR, KT>(buf + C::OFF_R, (const char *)kr, LATENT_ROPE * C::ES, p.j * KT, p.n);
+        load_rows<C::VCPR, KT>(buf + C::OFF_V, (const char *)(kv + DN), kvs * C::ES, p.j * KT, p.n);
     };
     const int nb = row_base<T, C::NCPR>(r16), rb = row_base<T, C::RCPR>(r16), vb = col_base<T, C::VCPR>(4 * gq);
-    if (nt > j0) load(j0);
-    for (int j = j0; j < nt; ++j) {
-        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
-        const int k0 = j * KT;
-        wait_vm<0>();
-        lds_barrier();
-        if (j + 1 < nt) load(j + 1);
-        if (k0 >= wlast || off + w0 >= n) continue;   // nothing for this wave in the tile
-        f32x4 s[NS][NR];
-#pragma unroll
-        for (int t = 0; t < NS; ++t) {
-#pragma unroll
-            for (int g = 0; g < NR; ++g) s[t][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) {
-                const Frag<T> kf = kb < DN / 32
-                    ? row_frag<T>(kt + 16 * t * C::NCPR * 16, nb, kb)
-                    : row_frag<T>(kt + C::OFF_R + 16 * t * C::RCPR * 16, rb, kb - DN / 32);
-#pragma unroll
-                for (int g = 0; g < NR; ++g) s[t][g] = mma(s[t][g], kf, qf[g][kb]);
-            }
-        }
-        if (sizeof(T) == 2) pipeline<4, NS * NKB, NS * NKB * NR, 1, NR>();
-        if (k0 + KT > wfull || k0 + KT > n) {   // the tile reaches past some row's last key
-#pragma unroll
-            for (int t = 0; t < NS; ++t)
-#pragma unroll
-                for (int g = 0; g < NR; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (k0 + 16 * t + 4 * gq + e > pos[g]) s[t][g][e] = -INFINITY;
-        }
+    if (left > 0) load(cur, 0);
+    int buffer = 0;
+    for (;;) {   // one row tile, or what the share has of it
+        const int n = cur.n, w0 = cur.t * RT + wave * 16 * NR;   // first row of the wave
+        const int j0 = cur.j;
+        const T *q = (const T *)a.q + ((long)cur.b * a.Tq * a.H + cur.h) * DK;
+        int pos[NR];   // position of this lane's rows; -1: the row sees nothing
+        Frag<T> qf[NR][NKB];
 #pragma unroll
         for (int g = 0; g < NR; ++g) {
-            float mx = -INFINITY;
+            const int row = w0 + 16 * g + r16;
+            const bool live = row < a.Tq && off + row < n;
+            pos[g] = live ? off + row : -1;
 #pragma unroll
-            for (int t = 0; t < NS; ++t)
+            for (int kb = 0; kb < NKB; ++kb)
+                qf[g][kb] = live ? load_frag<T>(q + row * qs + 32 * kb + 8 * gq) : zero_frag<T>();
+        }
+        f32x4 acc[NCB][NR];
+        float m[NR], l[NR];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][g][e]);
-            mx = rows_max(mx);
-            const bool up = (mx - m[g]) * c > RAISE;   // false while both are -inf
-            if (__any(up)) {
-                const float mn = up ? mx : m[g];
-                const float al = up ? exp2_hw((m[g] - mn) * c) : 1.f;
-                m[g] = mn;
-                l[g] *= al;
+        for (int g = 0; g < NR; ++g) {
+            m[g] = -INFINITY;
+            l[g] = 0.f;
 #pragma unroll
-                for (int cb = 0; cb < NCB; ++cb) acc[cb][g] *= al;
-            }
-            const float mb = m[g] == -INFINITY ? 0.f : m[g] * c;
-#pragma unroll
-            for (int t = 0; t < NS; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = exp2_hw(__builtin_fmaf(s[t][g][e], c, -mb));
-                    s[t][g][e] = p;
-                    l[g] += p;
+            for (int cb = 0; cb < NCB; ++cb) acc[cb][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        const int wlast = min(n, off + min(w0 + 16 * NR, a.Tq)), wfull = off + w0 + 1;   // keys that some, that all of its rows see
+        bool more = left > 0;   // false: a row tile of padding
+        while (more) {
+            const char *kt = lds + buffer * C::BUF, *vt = kt + C::OFF_V;
+            const int k0 = cur.j * KT;
+            wait_vm<0>();
+            lds_barrier();
+            buffer ^= 1;
+            if (--left > 0) {
+                if constexpr (CUT == SHARES) {
+                    nxt = fwd_after<RT, KT>(a, cur);
+                } else {
+                    nxt = cur;
+                    ++nxt.j;
                 }
+                load(nxt, buffer);
+            }
+            more = left > 0 && (CUT != SHARES || cur.j + 1 < cur.nkt);
+            if (more) cur.j = nxt.j;
+            if (k0 >= wlast || off + w0 >= n) continue;   // nothing for this wave in the tile
+            f32x4 s[NS][NR];
+#pragma unroll
+            for (int t = 0; t < NS; ++t) {
+#pragma unroll
+                for (int g = 0; g < NR; ++g) s[t][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) {
+                    const Frag<T> kf = kb < DN / 32
+                        ? row_frag<T>(kt + 16 * t * C::NCPR * 16, nb, kb)
+                        : row_frag<T>(kt + C::OFF_R + 16 * t * C::RCPR * 16, rb, kb - DN / 32);
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) s[t][g] = mma(s[t][g], kf, qf[g][kb]);
+                }
+            }
+            if (sizeof(T) == 2) pipeline<4, NS * NKB, NS * NKB * NR, 1, NR>();
+            if (k0 + KT > wfull || k0 + KT > n) {   // the tile reaches past some row's last key
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                    for (int g = 0; g < NR; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (k0 + 16 * t + 4 * gq + e > pos[g]) s[t][g][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][g][e]);
+                mx = rows_max(mx);
+                const bool up = (mx - m[g]) * c > RAISE;   // false while both are -inf
+                if (__any(up)) {
+                    const float mn = up ? mx : m[g];
+                    const float al = up ? exp2_hw((m[g] - mn) * c) : 1.f;
+                    m[g] = mn;
+                    l[g] *= al;
+#pragma unroll
+                    for (int cb = 0; cb < NCB; ++cb) acc[cb][g] *= al;
+                }
+                const float mb = m[g] == -INFINITY ? 0.f : m[g] * c;
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = exp2_hw(__builtin_fmaf(s[t][g][e], c, -mb));
+                        s[t][g][e] = p;
+                        l[g] += p;
+                    }
+            }
+            // weights rounded to the storage type for the matrix cores (half a step
+            // each, as the output itself); their sum is the unrounded one
+#pragma unroll
+            for (int t = 0; t < NS; t += 2) {
+                Frag<T> pf[NR];
+#pragma unroll
+                for (int g = 0; g < NR; ++g) pf[g] = reg_frag<T>(s[t][g], s[t + 1][g]);
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb) {
+                    const Frag<T> vf = col_frag<T, C::VCPR>(vt + 16 * t * C::VCPR * 16, vb, cb);
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) acc[cb][g] = mma(acc[cb][g], vf, pf[g]);
+                }
+            }
+            if (sizeof(T) == 2) pipeline<4, NS * NCB, NS / 2 * NCB * NR, 2, NR>();
         }
-        // weights rounded to the storage type for the matrix cores (half a step
-        // each, as the output itself); their sum is the unrounded one
+        const bool whole = !CUT || (j0 == 0 && cur.j + 1 >= cur.nkt);
+        T *o = (T *)a.o + ((long)cur.b * a.Tq * a.H + cur.h) * DV;
+        // where a part of the row tile goes: its number, its first row there, the step from row to row
+        const long part = CUT == SHARES ? share * 2 + (j0 == 0) : j0 / plan.each, step = CUT == SHARES ? 1 : a.H;
+        const long r0 = part * lay.rows + (CUT == SHARES ? 0 : ((long)cur.b * a.Tq + cur.t * RT) * a.H + cur.h);
+        float *po = (float *)((char *)a.ws + lay.o) + r0 * DV, *pl = (float *)((char *)a.ws + lay.lse) + r0;
 #pragma unroll
-        for (int t = 0; t < NS; t += 2) {
-            Frag<T> pf[NR];
+        for (int g = 0; g < NR; ++g) {
+            const int row = w0 + 16 * g + r16, lr = row - cur.t * RT;
+            const float ls = rows_sum(l[g]);
+            // of part of the keys a row may see none: its sum is 0 (and a NaN where scores are)
+            const bool seen = pos[g] >= 0 && (!CUT || ls != 0.f);
+            const float inv = seen ? 1.f / ls : 0.f, lg = seen ? m[g] * c + __builtin_amdgcn_logf(ls) : -INFINITY;
+            if (row >= a.Tq) continue;
+            if (whole) {
 #pragma unroll
-            for (int g = 0; g < NR; ++g) pf[g] = reg_frag<T>(s[t][g], s[t + 1][g]);
+                for (int cb = 0; cb < NCB; ++cb)
+                    store4(o + row * os + 16 * cb + 4 * gq, seen ? acc[cb][g] * inv : f32x4{0.f, 0.f, 0.f, 0.f});
+                if (gq == 0 && a.lse) a.lse[((long)cur.b * a.Tq + row) * a.H + cur.h] = lg * LN2;
+            } else {
+                if (seen) {
 #pragma unroll
-            for (int cb = 0; cb < NCB; ++cb) {
-                const Frag<T> vf = col_frag<T, C::VCPR>(vt + 16 * t * C::VCPR * 16, vb, cb);
-#pragma unroll
-                for (int g = 0; g < NR; ++g) acc[cb][g] = mma(acc[cb][g], vf, pf[g]);
+                    for (int cb = 0; cb < NCB; ++cb) store4(po + lr * step * DV + 16 * cb + 4 * gq, acc[cb][g] * inv);
+                }
+                if (gq == 0) pl[lr * step] = lg;
             }
         }
-        if (sizeof(T) == 2) pipeline<4, NS * NCB, NS / 2 * NCB * NR, 2, NR>();
-    }
-    T *o = (T *)a.o + ((long)b * a.Tq * a.H + h) * DV;
-    const long rows = (long)a.B * a.Tq * a.H;
-    float *po = (float *)a.ws + piece * rows * DV + ((long)b * a.Tq * a.H + h) * DV;
-    float *pl = (float *)a.ws + plan.pieces * rows * DV + piece * rows;
-#pragma unroll
-    for (int g = 0; g < NR; ++g) {
-        const int row = w0 + 16 * g + r16;
-        const float ls = rows_sum(l[g]);
-        // a row of a piece may see none of its keys: its sum is 0 (and a NaN where scores are)
-        const bool seen = pos[g] >= (CUT ? j0 * KT : 0) && (!CUT || ls != 0.f);
-        const float inv = seen ? 1.f / ls : 0.f;
-        if (row >= a.Tq) continue;
-        if (seen || !CUT) {
-#pragma unroll
-            for (int cb = 0; cb < NCB; ++cb) {
-                const f32x4 v = seen ? acc[cb][g] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
-                if (CUT) store4(po + row * os + 16 * cb + 4 * gq, v);
-                else store4(o + row * os + 16 * cb + 4 * gq, v);
-            }
-        }
-        const float lg = seen ? m[g] * c + __builtin_amdgcn_logf(ls) : -INFINITY;
-        const long at = ((long)b * a.Tq + row) * a.H + h;
-        if (gq == 0) {
-            if (CUT) pl[at] = lg;
-            else if (a.lse) a.lse[at] = lg * LN2;
-        }
+        if (CUT != SHARES || left == 0) break;
+        cur = nxt;
     }
 }
 
-// Joins the pieces of every row; DV / 4 lanes a row.
-template <typename T, int DV>
-__global__ __launch_bounds__(256) void latent_fwd_join_kernel(LatentFwdArgs a, int pieces)
+// Joins the rows that several workgroups worked on and writes those of row tiles without a
+// key; DV / 4 lanes a row.
+template <typename T, int DN, int DV, int NR, int CUT>
+__global__ __launch_bounds__(256) void latent_fwd_join_kernel(LatentFwdArgs a, FwdPlan plan)
 {
+    typedef FwdCfg<T, DN, DV, NR> C;
+    typedef FwdTiles<C::RT, C::KT> Tiles;
     constexpr int LPR = DV / 4;
-    const long rows = (long)a.B * a.Tq * a.H, row = (long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const unsigned rows = a.B * a.Tq * a.H, row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;   // below 2^28
     const int at = threadIdx.x % LPR * 4;
     if (row >= rows) return;
-    const float *po = (const float *)a.ws, *pl = po + pieces * rows * DV;
+    const int h = (int)(row % a.H), i = (int)(row / a.H % a.Tq), b = (int)(row / a.H / a.Tq), t = i / C::RT, lr = i % C::RT;
+    const int n = live_len(a.lens, b, a.Tk), k = Tiles::of(a, n, t);
+    int wf = 0, wl = -1;   // shares, or pieces of the row tile
+    if (CUT == PIECES) {
+        wl = (k + plan.each - 1) / plan.each - 1;
+    } else if (k > 0) {
+        const int *prefix = (const int *)a.ws;
+        const unsigned c0 = prefix[b] + h * Tiles::all(a, n) + Tiles::before(a, t), each = fwd_each(prefix[a.B], plan.shares);
+        wf = (int)(c0 / each);
+        wl = (int)((c0 + k - 1) / each);
+    }
+    if (wf == wl) return;   // written by its one workgroup
+    const FwdWs lay(plan, a.B, a.Tq, a.H, DV);
+    const float *po = (const float *)((const char *)a.ws + lay.o), *pl = (const float *)((const char *)a.ws + lay.lse);
+    auto place = [&](int w) {   // of share wf its last part, of the others the first
+        return CUT == SHARES ? (w * 2 + (w == wf)) * lay.rows + lr : w * lay.rows + row;
+    };
     float top = -INFINITY, ls = 0.f;
-    for (int i = 0; i < pieces; ++i) top = fmaxf(top, pl[i * rows + row]);
+    for (int w = wf; w <= wl; ++w) top = fmaxf(top, pl[place(w)]);
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < pieces; ++i) {
-        const float lg = pl[i * rows + row];
+    for (int w = wf; w <= wl; ++w) {
+        const float lg = pl[place(w)];
         if (lg == -INFINITY) continue;   // nothing was written
         const float f = exp2_hw(lg - top);
         ls += f;
-        sum += f * *reinterpret_cast<const f32x4 *>(po + (i * rows + row) * DV + at);
+        sum += f * *reinterpret_cast<const f32x4 *>(po + place(w) * DV + at);
     }
-    store4((T *)a.o + row * DV + at, ls != 0.f ? sum * (1.f / ls) : sum);
+    store4((T *)a.o + (long)row * DV + at, ls != 0.f ? sum * (1.f / ls) : sum);
     if (a.lse && at == 0) a.lse[row] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
 }
 
-template <typename T, int DN, int DV, int NR, bool CUT>
+template <typename T, int DN, int DV, int NR, int CUT>
 static hipError_t fwd_enqueue(const LatentFwdArgs &a, const FwdPlan &plan, hipStream_t st)
 {
     typedef FwdCfg<T, DN, DV, NR> C;
@@ -255,12 +426,18 @@ static hipError_t fwd_enqueue(const LatentFwdArgs &a, const FwdPlan &plan, hipSt
     auto k = latent_fwd_kernel<T, DN, DV, NR, CUT>;
     const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * C::BUF);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k, dim3((unsigned)((long)ntiles * a.B * a.H * plan.pieces)), dim3(256), 2 * C::BUF, st, a, ntiles, plan);
-    if (CUT) {
+    hipLaunchKernelGGL(k, dim3((unsigned)(plan.shares ? plan.shares : (long)ntiles * a.B * a.H * plan.pieces)), dim3(256), 2 * C::BUF, st, a, ntiles, plan);
+    if constexpr (CUT != WHOLE) {
         const long rows = (long)a.B * a.Tq * a.H, per = 256 / (DV / 4);
-        hipLaunchKernelGGL((latent_fwd_join_kernel<T, DV>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a, plan.pieces);
+        hipLaunchKernelGGL((latent_fwd_join_kernel<T, DN, DV, NR, CUT>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a, plan);
     }
     return hipGetLastError();
+}
+
+template <typename T, int DN, int DV, int NR> static hipError_t fwd_cut(const LatentFwdArgs &a, const FwdPlan &plan, hipStream_t st)
+{
+    if (plan.shares > 0) return fwd_enqueue<T, DN, DV, NR, SHARES>(a, plan, st);
+    return plan.pieces > 1 ? fwd_enqueue<T, DN, DV, NR, PIECES>(a, plan, st) : fwd_enqueue<T, DN, DV, NR, WHOLE>(a, plan, st);
 }
 
 template <typename T, int DN, int DV> static hipError_t fwd_launch(const LatentFwdArgs &a, hipStream_t st)
@@ -268,10 +445,9 @@ template <typename T, int DN, int DV> static hipError_t fwd_launch(const LatentF
     constexpr bool BF = sizeof(T) == 2;
     const FwdPlan plan = fwd_plan(BF, a.B, a.Tq, a.Tk, a.H);
     if constexpr (BF) {
-        if (plan.nr == 2)
-            return plan.pieces > 1 ? fwd_enqueue<T, DN, DV, 2, true>(a, plan, st) : fwd_enqueue<T, DN, DV, 2, false>(a, plan, st);
+        if (plan.nr == 2) return fwd_cut<T, DN, DV, 2>(a, plan, st);
     }
-    return plan.pieces > 1 ? fwd_enqueue<T, DN, DV, 1, true>(a, plan, st) : fwd_enqueue<T, DN, DV, 1, false>(a, plan, st);
+    return fwd_cut<T, DN, DV, 1>(a, plan, st);
 }
 
 hipError_t latent_fwd_launch(bool bf16, int dn, int dv, const LatentFwdArgs &a, hipStream_t st)
@@ -287,7 +463,7 @@ hipError_t latent_fwd_launch(bool bf16, int dn, int dv, const LatentFwdArgs &a, 
 unsigned long long latent_fwd_workspace(bool bf16, int B, int Tq, int Tk, int H, int dv)
 {
     const FwdPlan plan = fwd_plan(bf16, B, Tq, Tk, H);
-    return plan.pieces > 1 ? (unsigned long long)plan.pieces * B * Tq * H * (dv + 1) * 4 : 0;
+    return plan.shares > 0 || plan.pieces > 1 ? (unsigned long long)FwdWs(plan, B, Tq, H, dv).bytes : 0;
 }
 
 } // namespace gdn
