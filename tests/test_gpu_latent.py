@@ -103,6 +103,21 @@ def test_forward_longer(B, Tq, Tk, H, dt):
     _check_fwd(_expanded(B, Tq, Tk, H, 128, 128, dt, seed=3), dt)
 
 
+@pytest.mark.parametrize("B,Tq,Tk,H,dn,dv,dt,lens", [
+    (1, 2048, 2048, 10, 128, 128, "bf16", [2011]), (4, 1000, 3000, 2, 64, 128, "bf16", [3000, 0, 2100, 2999]),
+    (3, 1000, 1000, 8, 64, 64, "fp32", [1000, 1, 640]), (2, 600, 1700, 4, 128, 128, "fp32", [1100, 1700]),
+    (100, 64, 1400, 2, 128, 64, "bf16", [(37 * i) % 1500 for i in range(100)])])
+def test_forward_in_shares(B, Tq, Tk, H, dn, dv, dt, lens):
+    """Grids small enough, and rows long enough, for workgroups that share all key tiles:
+    some or all sequences padded, empty ones between."""
+    _say(f"fwd shares B{B} Tq{Tq} Tk{Tk} H{H} dn{dn} dv{dv} {dt}")
+    d = _expanded(B, Tq, Tk, H, dn, dv, dt, lens=lens, seed=29)
+    o, lse = _check_fwd(d, dt)
+    x = _dev(d)
+    o2, lse2 = gdn.latent_fwd(x["q"], x["kv"], x["k_rope"], lens=x["lens"])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_forward_large_scores(dt):
     """Scores of some hundreds: one key takes nearly all of a row, and the running
@@ -496,13 +511,13 @@ def test_prefill_then_steps_then_a_tree():
         torch.testing.assert_close(one, t[:, m], rtol=1e-5, atol=1e-5)
 
 
-@pytest.mark.parametrize("T", [200, 1000])   # 1000: in pieces, forward and backward
+@pytest.mark.parametrize("T", [200, 1000, 3100])   # in pieces, 3100: the forward in shares
 @pytest.mark.parametrize("other", ["object", "handle"])
 def test_another_stream(other, T):
     s = torch.cuda.Stream(DEV)
     d = _dev(_paged([700, 20], 16, 512, 16, "bf16", seed=12))
     e = _dev(_expanded(1, T, T, 4, 64, 64, "bf16", seed=12))
-    assert (gdn.gdn_latent_fwd_workspace_size(1, T, T, 4, 64, 64, 64, torch.bfloat16) > 0) == (T == 1000)
+    assert (gdn.gdn_latent_fwd_workspace_size(1, T, T, 4, 64, 64, 64, torch.bfloat16) > 0) == (T >= 1000)
     want = _run(d, 0.1)
     ow = gdn.latent_fwd(e["q"], e["kv"], e["k_rope"])
     gw = gdn.latent_bwd(e["q"], e["kv"], e["k_rope"], *ow, e["d_o"])
@@ -528,7 +543,7 @@ def test_two_calls_at_once_with_their_own_workspaces():
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T,M,dt", [(150, 4, "bf16"), (700, 8, "bf16"), (300, 2, "fp32")])   # from 300 on in pieces
+@pytest.mark.parametrize("T,M,dt", [(150, 4, "bf16"), (700, 8, "bf16"), (300, 2, "fp32"), (2500, 3, "bf16")])   # in pieces, 2500: shares
 def test_captured_and_replayed(T, M, dt):
     """The calls in a graph, replayed with new inputs and lengths in place and eager work
     between."""
