@@ -77,6 +77,32 @@ template <typename T> __device__ __forceinline__ float frag_dot(const Frag<T> &x
     return s;
 }
 
+// P from wave to wave: fp32 as it is, beside bf16 operands as fp16 of P 2^12 (half the
+// room, which lets the waves meet once a tile of 64 rows instead of 32: 4 x 16 heads of
+// 1531, 64 / 128, 156 us from 168; at 128 / 128 the same).  P <= 1, so nothing overflows,
+// and down to P = 2^-26 it is off by 2^-11 of itself, an eighth of what dS, which it
+// becomes, is rounded by; below, by 2^-37.  The power of two comes out of dk at the end.
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+template <typename T> __device__ __forceinline__ constexpr float hand_scale() { return sizeof(T) == 2 ? 1.f / 4096.f : 1.f; }
+template <typename T> __device__ __forceinline__ void hand_over(char *to, f32x4 p) {
+    if constexpr (sizeof(T) == 2) {
+        f16x4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = (_Float16)(p[e] * 4096.f);
+        *reinterpret_cast<f16x4 *>(to) = h;
+    } else {
+        *reinterpret_cast<f32x4 *>(to) = p;
+    }
+}
+template <typename T> __device__ __forceinline__ f32x4 take_over(const char *from) {
+    if constexpr (sizeof(T) == 2) {
+        const f16x4 h = *reinterpret_cast<const f16x4 *>(from);
+        return f32x4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
+    } else {
+        return *reinterpret_cast<const f32x4 *>(from);
+    }
+}
+
 template <typename T, int DN, int DV> struct BwdCfg {
     static constexpr int NG = sizeof(T) == 2 ? 2 : 1;      // 16-row groups a wave owns
     static constexpr int OWN = 64 * NG;                    // rows a workgroup owns (keys or queries)
@@ -86,7 +112,8 @@ template <typename T, int DN, int DV> struct BwdCfg {
     // a tile: [ST][DN] and [ST][64] of the rows' two key parts, [ST][DV]
     static constexpr int OFF_R = ST * NCPR * 16, OFF_V = OFF_R + ST * RCPR * 16, BUF = OFF_V + ST * VCPR * 16;
     static constexpr int ROWS = 2 * ST * 4;                // lse and D of the tile's rows
-    static constexpr int HAND = 2 * 2 * NG * 1024;         // two blocks of P, one pair of waves
+    static constexpr int HP = 64 * 4 * (ES == 2 ? 2 : 4);  // four values of P of each lane
+    static constexpr int HAND = 2 * ST / 16 * NG * HP;     // P of two tiles, one pair of waves
     static constexpr int KV_LDS = 3 * (BUF + ROWS) + 4 * HAND;
     static_assert(KV_LDS <= 160 * 1024, "LDS");
 };
@@ -129,9 +156,9 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
     // query rows that are no padding and see the workgroup's first key (of the piece)
     const int qn = min(min(a.Tq, n - off), CUT ? (piece + 1) * plan.qstep : a.Tq);
     const int qfirst = max(CUT ? piece * plan.qstep : 0, max(0, k0 - off) / ST * ST);
-    const int nt = k0 < n && qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0, nblk = nt * BPT;
+    const int nt = k0 < n && qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0;
     auto load = [&](int j) {
-        const int r0 = qfirst + j * ST, buf = j % 3;
+        const int r0 = qfirst + j * ST, buf = __builtin_amdgcn_readfirstlane(j % 3);
         char *to = lds + buf * C::BUF;
         load_rows<C::NCPR, ST, 512>(to, (const char *)q, qs * C::ES, r0, qn);
         load_rows<C::RCPR, ST, 512>(to + C::OFF_R, (const char *)(q + DN), qs * C::ES, r0, qn);
@@ -142,15 +169,11 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
             copy4(src, (char *)(stat + (buf * 2 + wave) * ST));
         }
     };
-    // before block i: block i - 1 of P is whole, and where a tile begins it is there
-    auto sync = [&](int i) {
-        if (i < nblk && i % BPT == 0) {
-            wait_vm<0>();
-            lds_barrier();
-            if (i / BPT + 1 < nt) load(i / BPT + 1);   // over the tile before the one that block i - 1 is of
-        } else {
-            lds_barrier();
-        }
+    // before tile j: it is there, and P of tile j - 1 is whole
+    auto sync = [&](int j) {
+        if (j < nt) wait_vm<0>();
+        lds_barrier();
+        if (j + 1 < nt) load(j + 1);   // over tile j - 2
     };
     auto seen = [&](int i) {   // whether a row of block i sees a key of the wave
         return off + qfirst + i * 32 + 31 >= w0 && w0 < n;
@@ -178,55 +201,59 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
 #pragma unroll
             for (int i = 0; i < NVC; ++i) dv[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int i = 0; i <= nblk; ++i) {
-            sync(i);
-            if (i == nblk || !seen(i)) continue;
-            const char *qt = lds + i / BPT % 3 * C::BUF, *dt = qt + C::OFF_V;
-            const float *st = stat + i / BPT % 3 * 2 * ST;
-            const int t = i % BPT, r0 = qfirst + i * 32;
-            const bool part = off + r0 < w0 + 16 * NG - 1 || r0 + 32 > qn;
-            f32x4 s[2][NG];
+        for (int j = 0; j <= nt; ++j) {
+            sync(j);
+            if (j == nt) break;
+            const char *qt = lds + j % 3 * C::BUF, *dt = qt + C::OFF_V;
+            const float *st = stat + j % 3 * 2 * ST;
+            char *to = hand + (j & 1) * (C::HAND / 2) + lane * (C::HP / 64);
+#pragma unroll 1
+            for (int t = 0; t < BPT; ++t) {
+                if (!seen(j * BPT + t)) continue;
+                const int r0 = qfirst + j * ST + t * 32;
+                const bool part = off + r0 < w0 + 16 * NG - 1 || r0 + 32 > qn;
+                f32x4 s[2][NG];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    const Frag<T> f = kb < DN / 32
-                        ? row_frag<T>(qt + (32 * t + 16 * u) * C::NCPR * 16, nb, kb)
-                        : row_frag<T>(qt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rb, kb - DN / 32);
+                    for (int kb = 0; kb < NKB; ++kb) {
+                        const Frag<T> f = kb < DN / 32
+                            ? row_frag<T>(qt + (32 * t + 16 * u) * C::NCPR * 16, nb, kb)
+                            : row_frag<T>(qt + C::OFF_R + (32 * t + 16 * u) * C::RCPR * 16, rb, kb - DN / 32);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, kf[g][kb]);
-                }
-                const int row = 16 * u + 4 * gq;
-                const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 32 * t + row) * LOG2E;
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
-                if (part) {
+                        for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, kf[g][kb]);
+                    }
+                    const int row = 16 * u + 4 * gq;
+                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 32 * t + row) * LOG2E;
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const bool hide = (off + r0 + row + e < w0 + 16 * g + r16) | (r0 + row + e >= qn);
-                            s[u][g][e] = hide ? 0.f : s[u][g][e];
-                        }
+                        for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
+                    if (part) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool hide = (off + r0 + row + e < w0 + 16 * g + r16) | (r0 + row + e >= qn);
+                                s[u][g][e] = hide ? 0.f : s[u][g][e];
+                            }
+                    }
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) hand_over<T>(to + ((2 * t + u) * NG + g) * C::HP, s[u][g]);
                 }
+                // P (and below dS) rounded to the storage type for the matrix cores: half
+                // a step each, as the gradients themselves
+                Frag<T> pf[NG];
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    *reinterpret_cast<f32x4 *>(hand + (((i & 1) * 2 + u) * NG + g) * 1024 + lane * 16) = s[u][g];
-            }
-            // P (and below dS) rounded to the storage type for the matrix cores: half
-            // a step each, as the gradients themselves
-            Frag<T> pf[NG];
+                for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
+                for (int v = 0; v < NVC; ++v) {
+                    const Frag<T> f = col_frag<T, C::VCPR>(dt + 32 * t * C::VCPR * 16, vc, v);
 #pragma unroll
-            for (int v = 0; v < NVC; ++v) {
-                const Frag<T> f = col_frag<T, C::VCPR>(dt + 32 * t * C::VCPR * 16, vc, v);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) dv[v][g] = mma(dv[v][g], f, pf[g]);
+                    for (int g = 0; g < NG; ++g) dv[v][g] = mma(dv[v][g], f, pf[g]);
+                }
             }
         }
         T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV) + DN;
@@ -257,40 +284,45 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
 #pragma unroll
             for (int i = 0; i < NKC; ++i) dk[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int i = 0; i <= nblk; ++i) {
-            sync(i);
-            if (i == 0 || !seen(i - 1)) continue;
-            const int k = i - 1, t = k % BPT;
-            const char *qt = lds + k / BPT % 3 * C::BUF, *dt = qt + C::OFF_V;
-            const float *st = stat + (k / BPT % 3 * 2 + 1) * ST;
-            f32x4 dp[2][NG];
+        for (int j = 0; j <= nt; ++j) {
+            sync(j);
+            if (j == 0) continue;
+            const int k = j - 1;
+            const char *qt = lds + k % 3 * C::BUF, *dt = qt + C::OFF_V;
+            const float *st = stat + (k % 3 * 2 + 1) * ST;
+            const char *from = hand + (k & 1) * (C::HAND / 2) + lane * (C::HP / 64);
+#pragma unroll 1
+            for (int t = 0; t < BPT; ++t) {
+                if (!seen(k * BPT + t)) continue;
+                f32x4 dp[2][NG];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int v = 0; v < NVB; ++v) {
-                    const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::VCPR * 16, vb, v);
+                    for (int v = 0; v < NVB; ++v) {
+                        const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::VCPR * 16, vb, v);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, vf[g][v]);
+                        for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, vf[g][v]);
+                    }
+                    const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 32 * t + 16 * u + 4 * gq);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const f32x4 p = take_over<T>(from + ((2 * t + u) * NG + g) * C::HP);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
+                    }
                 }
-                const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 32 * t + 16 * u + 4 * gq);
+                Frag<T> sf[NG];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const f32x4 p = *reinterpret_cast<const f32x4 *>(hand + (((k & 1) * 2 + u) * NG + g) * 1024 + lane * 16);
+                for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
+                for (int v = 0; v < NKC; ++v) {
+                    const Frag<T> f = v < DN / 16 ? col_frag<T, C::NCPR>(qt + 32 * t * C::NCPR * 16, nc, v)
+                                                  : col_frag<T, C::RCPR>(qt + C::OFF_R + 32 * t * C::RCPR * 16, rc, v - DN / 16);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) dk[v][g] = mma(dk[v][g], f, sf[g]);
                 }
-            }
-            Frag<T> sf[NG];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
-#pragma unroll
-            for (int v = 0; v < NKC; ++v) {
-                const Frag<T> f = v < DN / 16 ? col_frag<T, C::NCPR>(qt + 32 * t * C::NCPR * 16, nc, v)
-                                              : col_frag<T, C::RCPR>(qt + C::OFF_R + 32 * t * C::RCPR * 16, rc, v - DN / 16);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) dk[v][g] = mma(dk[v][g], f, sf[g]);
             }
         }
         T *dkv = (T *)a.dkv + ((long)b * a.Tk * a.H + h) * (DN + DV);
@@ -302,7 +334,7 @@ __global__ __launch_bounds__(512, 1) void latent_bwd_kv_kernel(LatentBwdArgs a, 
             if (key >= a.Tk) continue;
 #pragma unroll
             for (int i = 0; i < NKC; ++i) {
-                const f32x4 v = dk[i][g] * a.scale;
+                const f32x4 v = dk[i][g] * (a.scale * hand_scale<T>());
                 if (16 * i >= DN)
                     store4(rope + (((piece * (long)a.B + b) * a.Tk + key) * a.H + h) * LATENT_ROPE + (16 * i - DN) + 4 * gq, v);
                 else if (CUT) store4(part + key * kvs + 16 * i + 4 * gq, v);

@@ -156,7 +156,8 @@ def test_what_lies_behind_a_sequence_is_not_touched(dt):
 
 def _bwd_tol(d, o, lse, scale, u):
     """Tolerances of dq, dkv, dk_rope: the terms' absolute values times what each may
-    be off.  P: 2 ds + 8 e (and the rounding u in dv); dP - D: (DV + 2) e sums of
+    be off.  P: 2 ds + 8 e (and the rounding u in dv; for bf16 in dk half a step of fp16,
+    2^-11, of 4096 P, or of its subnormals, 2^-25 / 4096); dP - D: (DV + 2) e sums of
     absolute products, and in D u |do| |o|, by which do . o of the rounded o may be off
     the sum of P dP, which the kernel takes for the first rows; dS: u."""
     Q, K, V = ref.heads(d["q"], d["kv"], d["k_rope"])
@@ -178,7 +179,8 @@ def _bwd_tol(d, o, lse, scale, u):
     S = scale * p * np.abs(dp - Dv)
     nq, nk = (Tk + 8) * E, (Tq * 1 + 8) * E
     dq = (eS + nq * S) @ np.abs(K)
-    dk = (eS + nk * S).swapaxes(2, 3) @ np.abs(Q)
+    hand = scale * np.where(see, p * 2.0 ** -11 + 2.0 ** -37, 0) * np.abs(dp - Dv) if u > E else 0
+    dk = (eS + hand + nk * S).swapaxes(2, 3) @ np.abs(Q)
     dv = (p * (u + ds + nk)).swapaxes(2, 3) @ np.abs(dO)
     dn = D - 64
     rope = (dk[..., dn:] + H * E * (S.swapaxes(2, 3) @ np.abs(Q))[..., dn:]).sum(1)
