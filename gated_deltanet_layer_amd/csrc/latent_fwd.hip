@@ -33,6 +33,7 @@ template <typename T, int DN, int DV, int NR> struct FwdCfg {   // NR: 16-row gr
 
 // How a call is cut: 16-row groups a wave, and for small grids either pieces of every
 // row tile's keys, or the number of workgroups that share all key tiles of the call.
+constexpr int FWD_SHARES = 512;   // two workgroups a compute unit
 struct FwdPlan {
     int nr, pieces, each;   // pieces of a row tile, `each` key tiles each (1: whole)
     int shares;             // 0: none
@@ -62,7 +63,7 @@ inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
     const long tiles = (Tq + 64 * p.nr - 1) / (64 * p.nr), wgs = bh * tiles;
     if (wgs <= 0 || wgs >= 512 || nt < 8) return p;
     if (wgs * nt - bh * tiles * (tiles - 1) / 2 * (64 * p.nr / kt) >= 8 * 512 && wgs * nt < (1L << 30)) {
-        p.shares = 512;
+        p.shares = FWD_SHARES;
         if (bf16 && wide >= 128) p.nr = 2;
         return p;
     }
@@ -143,13 +144,13 @@ __device__ __forceinline__ int lanes_scan(int x)
     return x;
 }
 
-// Tiles of a share: all of the call's over `most` shares, rounded up.
-__host__ __device__ inline int fwd_each(int total, int most) { return total < most ? 1 : (total + most - 1) / most; }
+// Tiles of a share: all of the call's over the shares, rounded up.
+__device__ __forceinline__ int fwd_each(int total) { return max(1, (total + FWD_SHARES - 1) / FWD_SHARES); }
 
 // This workgroup's share, its first key tile and the number of them; 0 if it has none.
 // Every wave adds up all sequences on its own; the first share leaves the tiles before
 // each for the join.
-template <int RT, int KT> __device__ __forceinline__ int fwd_share(const LatentFwdArgs &a, int share, int most, FwdPos &cur)
+template <int RT, int KT> __device__ __forceinline__ int fwd_share(const LatentFwdArgs &a, int share, FwdPos &cur)
 {
     typedef FwdTiles<RT, KT> Tiles;
     const int lane = threadIdx.x & 63;
@@ -162,7 +163,7 @@ template <int RT, int KT> __device__ __forceinline__ int fwd_share(const LatentF
         total += __builtin_amdgcn_readlane(incl, 63);
     }
     if (share == 0 && lane == 0) prefix[a.B] = total;
-    const int each = fwd_each(total, most), g0 = share * each;
+    const int each = fwd_each(total), g0 = share * each;
     if (g0 >= total) return 0;
     int at = 0;
     for (int b = 0;; b += 64) {
@@ -207,8 +208,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentFwdArgs a, int
     int share = 0, left;   // key tiles to go
     if constexpr (CUT == SHARES) {
         // the shares of one head, which read the same keys, on one XCD
-        share = blockIdx.x % 8 * (plan.shares / 8) + blockIdx.x / 8;
-        left = fwd_share<RT, KT>(a, share, plan.shares, cur);
+        share = blockIdx.x % 8 * (FWD_SHARES / 8) + blockIdx.x / 8;
+        left = fwd_share<RT, KT>(a, share, cur);
         if (left == 0) return;
     } else {
         const int BH = a.B * a.H, bh = blockIdx.x % BH, piece = CUT == PIECES ? blockIdx.x / BH % plan.pieces : 0;
@@ -384,19 +385,25 @@ __global__ __launch_bounds__(256) void latent_fwd_join_kernel(LatentFwdArgs a, F
     typedef FwdCfg<T, DN, DV, NR> C;
     typedef FwdTiles<C::RT, C::KT> Tiles;
     constexpr int LPR = DV / 4;
-    const unsigned rows = a.B * a.Tq * a.H, row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;   // below 2^28
-    const int at = threadIdx.x % LPR * 4;
-    if (row >= rows) return;
-    const int h = (int)(row % a.H), i = (int)(row / a.H % a.Tq), b = (int)(row / a.H / a.Tq), t = i / C::RT, lr = i % C::RT;
+    const unsigned of = a.Tq * a.H, r = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;   // the rows of sequence b
+    const int at = threadIdx.x % LPR * 4, b = blockIdx.y;
+    if (r >= of) return;
+    const int i = (int)(r / a.H), h = (int)(r - i * a.H), t = i / C::RT, lr = i % C::RT;
+    const long row = (long)b * of + r;
     const int n = live_len(a.lens, b, a.Tk), k = Tiles::of(a, n, t);
     int wf = 0, wl = -1;   // shares, or pieces of the row tile
     if (CUT == PIECES) {
         wl = (k + plan.each - 1) / plan.each - 1;
     } else if (k > 0) {
         const int *prefix = (const int *)a.ws;
-        const unsigned c0 = prefix[b] + h * Tiles::all(a, n) + Tiles::before(a, t), each = fwd_each(prefix[a.B], plan.shares);
-        wf = (int)(c0 / each);
-        wl = (int)((c0 + k - 1) / each);
+        const int c0 = prefix[b] + h * Tiles::all(a, n) + Tiles::before(a, t), each = fwd_each(prefix[a.B]);
+        const float inv = 1.f / (float)each;
+        auto share = [&](int c) {   // c / each, below FWD_SHARES: the product is off by less than 1
+            const int q = (int)((float)c * inv), left = c - q * each;
+            return q + (left >= each) - (left < 0);
+        };
+        wf = share(c0);
+        wl = share(c0 + k - 1);
     }
     if (wf == wl) return;   // written by its one workgroup
     const FwdWs lay(plan, a.B, a.Tq, a.H, DV);
@@ -407,14 +414,16 @@ __global__ __launch_bounds__(256) void latent_fwd_join_kernel(LatentFwdArgs a, F
     float top = -INFINITY, ls = 0.f;
     for (int w = wf; w <= wl; ++w) top = fmaxf(top, pl[place(w)]);
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
     for (int w = wf; w <= wl; ++w) {
         const float lg = pl[place(w)];
-        if (lg == -INFINITY) continue;   // nothing was written
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(po + place(w) * DV + at);
         const float f = exp2_hw(lg - top);
+        if (lg == -INFINITY) continue;   // v was never written
         ls += f;
-        sum += f * *reinterpret_cast<const f32x4 *>(po + place(w) * DV + at);
+        sum += f * v;
     }
-    store4((T *)a.o + (long)row * DV + at, ls != 0.f ? sum * (1.f / ls) : sum);
+    store4((T *)a.o + row * DV + at, ls != 0.f ? sum * (1.f / ls) : sum);
     if (a.lse && at == 0) a.lse[row] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
 }
 
@@ -428,8 +437,8 @@ static hipError_t fwd_enqueue(const LatentFwdArgs &a, const FwdPlan &plan, hipSt
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k, dim3((unsigned)(plan.shares ? plan.shares : (long)ntiles * a.B * a.H * plan.pieces)), dim3(256), 2 * C::BUF, st, a, ntiles, plan);
     if constexpr (CUT != WHOLE) {
-        const long rows = (long)a.B * a.Tq * a.H, per = 256 / (DV / 4);
-        hipLaunchKernelGGL((latent_fwd_join_kernel<T, DN, DV, NR, CUT>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a, plan);
+        const long rows = (long)a.Tq * a.H, per = 256 / (DV / 4);
+        hipLaunchKernelGGL((latent_fwd_join_kernel<T, DN, DV, NR, CUT>), dim3((unsigned)((rows + per - 1) / per), a.B), dim3(256), 0, st, a, plan);
     }
     return hipGetLastError();
 }
