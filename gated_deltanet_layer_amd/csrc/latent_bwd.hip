@@ -14,7 +14,7 @@
 // rows of 16 heads, bf16, dn = dv = 128 in 1155-1270 us (dq 480-520, dk and dv 640-700),
 // 1.0 PFLOP/s over the seven, about a library product's rate on the same card (1.11;
 // matrix cores 51 and 42 % busy).  Padded batches of some 1500 rows (4 x 16 heads, 70 +
-// 98 us) are bound by each workgroup's own chain (loads of its operands, blocks one
+// 100 us) are bound by each workgroup's own chain (loads of its operands, blocks one
 // after the other, its stores), which at one workgroup a unit nothing hides.
 #include "latent.h"
 

@@ -47,14 +47,14 @@ struct FwdPlan {
 //
 // - Shares, where each gets eight tiles or more: 512 workgroups (two a unit) take equal
 //   runs of key tiles, whatever rows they are of, the runs of one head on one XCD (bf16,
-//   2 heads of 8192 71 us, as pieces 141; 8 of 4096 77, 89; 10 of 2048 43, 52; fp32, 8
-//   of 3000 175, 224; on any XCD 10 of 2048 47).  Two row groups from half a workgroup a
-//   unit on (2 heads of 8192: 71 from 83).
+//   2 heads of 8192 68 us, as pieces 141; 8 of 4096 75, 88; 10 of 2048 41, 51; fp32, 8
+//   of 3000 173, 223, 2 x 8 of 1021 42, 48; 10 of 2048 on any XCD 3 us more).  Two row
+//   groups from half a workgroup a unit on (2 heads of 8192: 12 us).
 // - Pieces of four tiles or more, a workgroup each, where a change of rows inside a share
 //   (its queries' loads and its result's stores, which nothing hides) would cost more
-//   (8 heads of 1024: 23 us, in shares 30; one row of 16 heads over 8192 keys 38, 51).
-//   Enough to fill the units twice, fp32, whose tiles have half the keys and four times
-//   the time, half as many again (2 x 8 heads of 700: 41 us, 46 without).
+//   (8 heads of 1024: 21 us, in shares 5 more; one row of 16 heads over 8192 keys 30, 8
+//   more).  Enough to fill the units twice, fp32, whose tiles have half the keys and four
+//   times the time, half as many again (2 x 8 heads of 700: 39 us, 5 more without).
 inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
 {
     const long bh = (long)B * H, wide = bh * ((Tq + 127) / 128);
