@@ -165,8 +165,8 @@ template <int RT, int KT> __device__ __forceinline__ int fwd_share(const LatentF
     if (share == 0 && lane == 0) prefix[a.B] = total;
     const int each = fwd_each(total), g0 = share * each;
     if (g0 >= total) return 0;
-    int at = 0;
-    for (int b = 0;; b += 64) {
+    int at = cur.b = 0;
+    for (int b = 0; b < a.B; b += 64) {
         const int mine = of(b + lane), incl = lanes_scan(mine), sum = __builtin_amdgcn_readlane(incl, 63);
         if (g0 < at + sum) {
             const int l = __builtin_ctzll(__ballot(g0 < at + incl));
