@@ -142,13 +142,13 @@ __device__ __forceinline__ unsigned lds_at(const char *lds) {   // uniform
     return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)lds;
 }
 __device__ __forceinline__ void copy16(const void *src, const char *lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");
 }
 __device__ __forceinline__ void copy16s(const void *base, unsigned off, const char *lds) {   // base: uniform
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_at(lds)) : "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_at(lds)) : "m0");
 }
 __device__ __forceinline__ void copy4(const void *src, const char *lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");
 }
 
 // Enqueue the copy of rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes

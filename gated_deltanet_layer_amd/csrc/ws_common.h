@@ -50,13 +50,14 @@ template <int CPR> __device__ __forceinline__ Frag<__bf16> qk_frag(const char *M
 // that the compiler's own wait-count tracking, which would otherwise wait for
 // every copy in flight before any LDS access, leaves them alone: the kernel
 // waits for them explicitly (wait_vm) before their data is read.  They have no
-// register results.
+// register results.  The compiler does not see the load inside either, so the wait
+// state that it needs behind a scalar write of M0 is written out (s_nop 0).
 __device__ __forceinline__ unsigned lds_addr(const char *lds) {
     return (unsigned)__builtin_amdgcn_readfirstlane(
         (int)(uintptr_t)(__attribute__((address_space(3))) const char *)lds);
 }
 __device__ __forceinline__ void g2lds16(const void *src, char *lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                  ::"v"(src), "s"(lds_addr(lds)) : "memory", "m0");
 }
 // Same, from a wave-uniform base (held in SGPRs) plus a 32-bit per-lane byte
@@ -67,11 +68,11 @@ __device__ __forceinline__ void g2lds16s(const void *base, unsigned off, char *l
     const unsigned lo = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)b);
     const unsigned hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(b >> 32));
     const void *sb = (const void *)(uintptr_t)(((unsigned long long)hi << 32) | lo);
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  ::"v"(off), "s"(sb), "s"(lds_addr(lds)) : "memory", "m0");
 }
 __device__ __forceinline__ void g2lds4(const void *src, char *lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                  ::"v"(src), "s"(lds_addr(lds)) : "memory", "m0");
 }
 
