@@ -144,8 +144,21 @@ __device__ __forceinline__ unsigned lds_at(const char *lds) {   // uniform
 __device__ __forceinline__ void copy16(const void *src, const char *lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");
 }
-__device__ __forceinline__ void copy16s(const void *base, unsigned off, const char *lds) {   // base: uniform
+// base: uniform, and from scalar instructions or settled (below).
+__device__ __forceinline__ void copy16s(const void *base, unsigned off, const char *lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_at(lds)) : "m0");
+}
+// Address that lane `lane` holds, in scalar registers, and the wait for a group of them:
+// a memory instruction reads a scalar register that a vector instruction wrote five wait
+// states later at the soonest, and the compiler does not see the loads in the copies.  The
+// operands tie it between the lane reads and the copies.
+__device__ __forceinline__ unsigned long long lane_address(const char *p, int lane) {
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(uintptr_t)p, lane);
+    const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)((uintptr_t)p >> 32), lane);
+    return (unsigned long long)hi << 32 | lo;
+}
+__device__ __forceinline__ void settle(unsigned long long (&b)[8]) {
+    asm volatile("s_nop 4" : "+s"(b[0]), "+s"(b[1]), "+s"(b[2]), "+s"(b[3]), "+s"(b[4]), "+s"(b[5]), "+s"(b[6]), "+s"(b[7]));
 }
 __device__ __forceinline__ void copy4(const void *src, const char *lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_at(lds)) : "m0");

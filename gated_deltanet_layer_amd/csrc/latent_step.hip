@@ -285,13 +285,19 @@ __global__ __launch_bounds__(256, 1) void latent_step_kernel(LatentStepArgs a, i
         };
         char *dst = lds + buf * C::TILE + wave * WR * CPR * 16;
         if constexpr (CPR >= 64) {   // a row is whole instructions: its address is uniform
+            static_assert(WR % 8 == 0, "");
 #pragma unroll
-            for (int i = 0; i < WR; ++i) {
-                const unsigned rlo = (unsigned)__builtin_amdgcn_readlane(lo, i), rhi = (unsigned)__builtin_amdgcn_readlane(hi, i);
-                const char *q = (const char *)(((uintptr_t)rhi << 32) | rlo);
+            for (int i0 = 0; i0 < WR; i0 += 8) {
+                unsigned long long q[8];
 #pragma unroll
-                for (int k = 0; k < CPR / 64; ++k)
-                    g2lds16s(q, (unsigned)((k * 64 + (lane ^ swz<CPR>(wave * WR + i))) * 16), dst + (i * CPR / 64 + k) * 1024);
+                for (int i = 0; i < 8; ++i) q[i] = lane_address(src, i0 + i);
+                settle(q);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int k = 0; k < CPR / 64; ++k)
+                        copy16s((const char *)(uintptr_t)q[i], (unsigned)((k * 64 + (lane ^ swz<CPR>(wave * WR + i0 + i))) * 16),
+                                dst + ((i0 + i) * CPR / 64 + k) * 1024);
             }
         } else {
 #pragma unroll
@@ -596,15 +602,22 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
             const int lo = (int)(uintptr_t)p, hi = (int)((uintptr_t)p >> 32);
             return (const char *)(((uintptr_t)(unsigned)__shfl(hi, r, 64) << 32) | (unsigned)__shfl(lo, r, 64));
         };
-        auto load_row = [&](const char *p, int i, int k) {   // k < CB: as many as the wave has column blocks
-            char *dst = lds + i % NB * C::TILE + w * WR * CPR * 16 + k * 1024;
+        auto load_latents = [&](const char *p, int i) {   // as many copies as the wave has column blocks
+            char *dst = lds + i % NB * C::TILE + w * WR * CPR * 16;
             if constexpr (WHOLE) {
-                const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(uintptr_t)p, k);
-                const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)((uintptr_t)p >> 32), k);
-                copy16s((const char *)(((uintptr_t)hi << 32) | lo), (unsigned)((lane ^ swz<CPR>(w * WR + k)) * 16), dst);
+                unsigned long long b[CB];
+#pragma unroll
+                for (int k = 0; k < CB; ++k) b[k] = lane_address(p, k);
+                settle(b);
+#pragma unroll
+                for (int k = 0; k < CB; ++k)
+                    copy16s((const char *)(uintptr_t)b[k], (unsigned)((lane ^ swz<CPR>(w * WR + k)) * 16), dst + k * 1024);
             } else {
-                const int r = k * (64 / CPR) + lane / CPR;
-                copy16(of_row(p, r) + ((lane % CPR) ^ swz<CPR>(w * WR + r)) * 16, dst);
+#pragma unroll
+                for (int k = 0; k < CB; ++k) {
+                    const int r = k * (64 / CPR) + lane / CPR;
+                    copy16(of_row(p, r) + ((lane % CPR) ^ swz<CPR>(w * WR + r)) * 16, dst + k * 1024);
+                }
             }
         };
         const int rrow = lane / C::RCPR, rch = ((lane % C::RCPR) ^ swz<C::RCPR>(w * WR + rrow)) * 16 + R * 2;
@@ -626,8 +639,7 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
         wait_vm<0>();
         for (int k = 0; k < 2; ++k) {
             const char *r = address(pa, page_id(k));
-#pragma unroll
-            for (int b = 0; b < CB; ++b) load_row(r, k, b);
+            load_latents(r, k);
             load_rope(r, of_row(r, rrow), k);
             advance(pa, na);
         }
@@ -647,8 +659,7 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
         StepPos p = pos;   // of the tile before
         int kt0 = pos.t;
         lds_barrier();   // step 0
-#pragma unroll
-        for (int k = 0; k < CB; ++k) load_row(row, 2, k);
+        load_latents(row, 2);
         load_rope(row, of_row(row, rrow), 2);
         load_ids(pi, 5);
         advance(pi, ni);
@@ -659,8 +670,7 @@ __global__ __launch_bounds__(512, 1) void latent_step_wide_kernel(LatentStepArgs
             wait_vm<NV>();
             lds_barrier();
             const int k = i - 1;
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) load_row(row, i + 2, cb);   // at once: their latency is what a step waits for
+            load_latents(row, i + 2);   // at once: their latency is what a step waits for
             GDN_SCHED_FENCE();
             Frag<T> pf[4];
             float al[4];

@@ -1,10 +1,14 @@
 """Wait states in the compiled gfx950 code (CPU: only the library's own machine code is
 read, nothing runs).
 
-On this architecture the program keeps one wait state from a scalar instruction that
-writes M0 to a copy from global memory into LDS.  The compiler does so for the instructions
-that it knows; copies written as inline assembly are its blind spot, so every kernel of the
-library is checked here as built.
+Two distances between instructions are the program's to keep on this architecture:
+
+ * five wait states from a vector instruction that writes a scalar register to a memory
+   instruction that reads it (its address);
+ * one from a scalar instruction that writes M0 to a copy from global memory into LDS.
+
+The compiler keeps them for the instructions that it knows; copies written as inline
+assembly are its blind spot, so every kernel of the library is checked here as built.
 """
 import os
 import re
@@ -18,6 +22,7 @@ import gated_deltanet_layer_amd as gdn
 
 OBJDUMP = shutil.which("llvm-objdump") or "/opt/rocm/llvm/bin/llvm-objdump"
 MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
+SGPR = re.compile(r"\bs(?:(\d+)|\[(\d+):(\d+)\])(?![\w:])")
 
 
 def code_objects(path):
@@ -54,6 +59,26 @@ def functions(text):
             code.append((int(m[3], 16), op, m[2], to))
     if code:
         yield name, code
+
+
+def scalars(operands):
+    """Scalar registers named in operands; vcc and m0 by name."""
+    out = set()
+    for a, lo, hi in SGPR.findall(operands):
+        out.update(range(int(a), int(a) + 1) if a else range(int(lo), int(hi) + 1))
+    out.update(x for x in ("vcc", "m0") if re.search(rf"\b{x}(_lo|_hi)?\b", operands))
+    return out
+
+
+def vector_writes(op, operands):
+    """Scalar registers that a vector instruction writes."""
+    if not op.startswith("v_"):
+        return set()
+    args = re.split(r",\s*(?![^\[]*\])", operands)
+    out = scalars(args[0])
+    if "_co_" in op or "div_scale" in op:   # the carry is the second operand
+        out |= scalars(args[1])
+    return out
 
 
 def is_memory(op):
@@ -94,6 +119,9 @@ def hazards(code):
     for i, (a, op, args, _) in enumerate(code):
         if not is_memory(op):
             continue
+        if regs := scalars(args):
+            if hit := find(i, vector_writes, regs, 5):
+                yield a, f"{op} {args}", " ".join(code[hit[0]][1:3]), hit[1]
         if "_load_lds_" in op or re.search(r"\blds\b", args):
             if hit := find(i, m0_writes, {"m0"}, 1):
                 yield a, f"{op} {args}", " ".join(code[hit[0]][1:3]), hit[1]
@@ -106,21 +134,34 @@ def listing(obj, tmp):
     return subprocess.run([OBJDUMP, "-d", path], capture_output=True, text=True, check=True).stdout
 
 
-def test_the_search_itself():
+SHORT = """
+0000000000001000 <k>:
+\tv_readlane_b32 s4, v1, 3                                   // 000000001000: D2890004 00010701
+\tv_readlane_b32 s5, v2, 3                                   // 000000001008: D2890005 00010702
+\ts_mov_b32 m0, s9                                           // 000000001010: BEFC0009
+{nop}\tglobal_load_lds_dwordx4 v3, s[4:5]                         // 000000001018: DDF48000 00040003
+\ts_endpgm                                                   // 000000001020: BF810000
+"""
+NOP = "\ts_nop {n}                                                    // 000000001014: BF80000{n}\n"
+
+
+@pytest.mark.parametrize("nop,found", [("", {1, 0}), (NOP.format(n=0), {2}), (NOP.format(n=2), {4}), (NOP.format(n=3), set())])
+def test_the_search_itself(nop, found):
+    (_, code), = functions(SHORT.format(nop=nop))
+    assert {h[3] for h in hazards(code)} == found
+
+
+def test_the_search_follows_branches():
     text = """
 0000000000001000 <k>:
-\tglobal_load_lds_dwordx4 v3, s[4:5]                         // 000000001000: DDF48000 00040003
-\ts_nop 0                                                    // 000000001008: BF800000
-\ts_mov_b32 m0, s9                                           // 00000000100C: BEFC0009
+\tglobal_load_dword v1, v2, s[4:5]                           // 000000001000: DC508000 01040002
+\ts_nop 1                                                    // 000000001008: BF800001
+\tv_readfirstlane_b32 s5, v1                                 // 00000000100C: 7E0A0501
 \ts_cbranch_scc0 65531                                       // 000000001010: BF84FFFB <k>
-\tglobal_load_lds_dwordx4 v3, s[4:5]                         // 000000001014: DDF48000 00040003
-\ts_mov_b32 m0, s9                                           // 00000000101C: BEFC0009
-\tglobal_load_lds_dwordx4 v3, s[4:5]                         // 000000001020: DDF48000 00040003
-\ts_mov_b32 m0, s9                                           // 000000001028: BEFC0009
-\ts_branch 65523                                             // 00000000102C: BF82FFF3 <k>
+\ts_endpgm                                                   // 000000001014: BF810000
 """
     (_, code), = functions(text)
-    assert [h[0] for h in hazards(code)] == [0x1020]
+    assert [h[3] for h in hazards(code)] == [1]
 
 
 @pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
