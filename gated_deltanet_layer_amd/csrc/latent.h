@@ -8,6 +8,7 @@
 // for bf16), and hold scores so that an accumulator tile feeds the next product
 // as its B operand without leaving the registers (reg_frag).
 #pragma once
+#include "latent_plan.h"
 #include "ws_common.h"
 #include <stddef.h>
 

@@ -20,37 +20,6 @@
 
 namespace gdn {
 
-// How a call is cut.  Where the workgroups that own rows are too few for the device,
-// the rows that walk by are cut into pieces, one workgroup each; the pieces' sums
-// stand in the workspace and the last kernel adds them up in order.  The longest walk
-// of a causal call is otherwise its time.
-struct BwdPlan {
-    int kp, qp;        // pieces of the keys (dq), of the query rows (dk, dv)
-    int kstep, qstep;  // rows of a piece, whole tiles
-};
-
-inline int bwd_pieces(long wgs, long fill, int tiles, int least) {   // of `least` tiles or more
-    if (wgs <= 0 || wgs >= fill || tiles < 2 * least) return 1;
-    const long n = (fill + wgs - 1) / wgs;
-    return (int)(n > tiles / least ? tiles / least : n > 16 ? 16 : n);
-}
-
-inline BwdPlan bwd_plan(bool bf16, int B, int Tq, int Tk, int H)
-{
-    const int own = bf16 ? 128 : 64, st = bf16 ? 64 : 32;
-    const long bh = (long)B * H;
-    const int nk = (Tk + st - 1) / st, nq = (Tq + st - 1) / st;
-    const int least = bf16 ? 2 : 1;   // 500 rows of 16 heads: 48 us (55 with four); fp32, 257 of 4: 27 us (34 with two)
-    const int kp = bwd_pieces(bh * ((Tq + own - 1) / own), 512, nk, least);
-    const int qp = bwd_pieces(bh * ((Tk + own - 1) / own), 256, nq, least);
-    BwdPlan p;
-    p.kstep = (nk + kp - 1) / kp * st;
-    p.qstep = (nq + qp - 1) / qp * st;
-    p.kp = kp > 1 ? (Tk + p.kstep - 1) / p.kstep : 1;
-    p.qp = qp > 1 ? (Tq + p.qstep - 1) / p.qstep : 1;
-    return p;
-}
-
 // Workspace, all float: D[B][Tq][H]; dk_rope[qp][B][Tk][H][64]; where there are pieces,
 // dq[kp][B][Tq][H][DK] and dkv[qp][B][Tk][H][DN + DV].
 struct BwdWs {

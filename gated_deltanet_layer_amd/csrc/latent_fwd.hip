@@ -31,51 +31,6 @@ template <typename T, int DN, int DV, int NR> struct FwdCfg {   // NR: 16-row gr
     static constexpr int OFF_R = KT * NCPR * 16, OFF_V = OFF_R + KT * RCPR * 16, BUF = OFF_V + KT * VCPR * 16;
 };
 
-// How a call is cut: 16-row groups a wave, and for small grids either pieces of every
-// row tile's keys, or the number of workgroups that share all key tiles of the call.
-constexpr int FWD_SHARES = 512;   // two workgroups a compute unit
-struct FwdPlan {
-    int nr, pieces, each;   // pieces of a row tile, `each` key tiles each (1: whole)
-    int shares;             // 0: none
-};
-
-// Rows: two groups a wave (each key operand serves two products) once that gives
-// every compute unit a workgroup; below that, one (333 rows, 16 heads: 13.5 us from
-// 14.4).  Keys: the longest row of a causal call is otherwise its time.  Where there is
-// less than two workgroups a unit and a row has eight tiles or more (from 512 workgroups
-// on cutting costs more than it gives: 2 x 16 heads of 2048 64 us, 85):
-//
-// - Shares, where each gets eight tiles or more: 512 workgroups (two a unit) take equal
-//   runs of key tiles, whatever rows they are of, the runs of one head on one XCD (bf16,
-//   2 heads of 8192 68 us, as pieces 141; 8 of 4096 75, 88; 10 of 2048 41, 51; fp32, 8
-//   of 3000 173, 223, 2 x 8 of 1021 42, 48; 10 of 2048 on any XCD 3 us more).  Two row
-//   groups from half a workgroup a unit on (2 heads of 8192: 12 us).
-// - Pieces of four tiles or more, a workgroup each, where a change of rows inside a share
-//   (its queries' loads and its result's stores, which nothing hides) would cost more
-//   (8 heads of 1024: 21 us, in shares 5 more; one row of 16 heads over 8192 keys 30, 8
-//   more).  Enough to fill the units twice, fp32, whose tiles have half the keys and four
-//   times the time, half as many again (2 x 8 heads of 700: 39 us, 5 more without).
-inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
-{
-    const long bh = (long)B * H, wide = bh * ((Tq + 127) / 128);
-    const int kt = bf16 ? 64 : 32, nt = (Tk + kt - 1) / kt;
-    FwdPlan p = {bf16 && wide >= 256 ? 2 : 1, 1, nt, 0};
-    const long tiles = (Tq + 64 * p.nr - 1) / (64 * p.nr), wgs = bh * tiles;
-    if (wgs <= 0 || wgs >= 512 || nt < 8) return p;
-    if (wgs * nt - bh * tiles * (tiles - 1) / 2 * (64 * p.nr / kt) >= 8 * 512 && wgs * nt < (1L << 30)) {
-        p.shares = FWD_SHARES;
-        if (bf16 && wide >= 128) p.nr = 2;
-        return p;
-    }
-    const long fill = bf16 ? 512 : 768;
-    long n = wgs < 256 ? (fill + wgs - 1) / wgs : 4;
-    if (n > nt / 4) n = nt / 4;
-    if (n > 32) n = 32;
-    p.each = (int)((nt + n - 1) / n);
-    p.pieces = (nt + p.each - 1) / p.each;
-    return p;
-}
-
 // Workspace of a call that is cut.  Pieces: float o[pieces][B Tq H][DV], float
 // lse[pieces][B Tq H] (base 2).  Shares: int prefix[B + 1], the key tiles before each
 // sequence, then for each share its first and last piece of a row tile, float o[slot][DV],

@@ -30,8 +30,6 @@
 
 namespace gdn {
 
-constexpr int STEP_CUS = 256;   // one workgroup a compute unit: two tiles fill its LDS
-
 // Up to 32 rows: four waves divide each tile's keys for the scores and the output
 // columns for the second product, every wave for all 16 G rows.  Two tiles of 64 keys
 // (72 KB each at r = 512) leave room for one workgroup a unit: one is in use while the
@@ -71,19 +69,6 @@ template <int R> struct WideCfg {
     static constexpr int BYTES = OFF_SCAN + 10 * 4;
     static_assert(BYTES <= 160 * 1024, "");
 };
-
-// Rows of a workgroup.  fp32 has registers for 16.
-__host__ __device__ inline int step_rt(bool bf16, int rows)
-{
-    return !bf16 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
-
-// Workgroups that may share the key tiles of one row tile.
-__host__ __device__ inline int step_shares(int ntile) {
-    int g = STEP_CUS / (ntile < 1 ? 1 : ntile);
-    if (g >= 8) g &= ~7;   // the row tiles of one share land on one XCD
-    return g < 1 ? 1 : g;
-}
 
 // Workspace: int prefix[N + 1] tiles before each sequence, then for each share, its
 // first and last piece and each row tile: float o[RT][R], float lse[RT] (base 2).
