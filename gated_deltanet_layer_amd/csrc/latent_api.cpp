@@ -43,6 +43,15 @@ gdn_status expanded_sizes(int B, int Tq, int Tk, int H, int dn, int dr, int dv, 
     return GDN_OK;
 }
 
+// The same for the backward, whose key-owning kernel has 512 threads a workgroup.
+gdn_status backward_sizes(int B, int Tq, int Tk, int H, int dn, int dr, int dv, gdn_dtype dtype)
+{
+    const gdn_status st = expanded_sizes(B, Tq, Tk, H, dn, dr, dv, dtype);
+    if (st != GDN_OK) return st;
+    const long long own = dtype == GDN_BF16 ? 128 : 64;
+    return prod(B, H, (Tk + own - 1) / own) < (1LL << 23) ? GDN_OK : GDN_ENOTSUP;
+}
+
 gdn_status absorbed_sizes(int N, int M, int H, int r, int dr, gdn_dtype dtype)
 {
     if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_EINVAL;
@@ -145,7 +154,7 @@ gdn_status gdn_latent_bwd_workspace_size(int B, int Tq, int Tk, int H, int dn, i
                                          size_t *bytes)
 {
     if (!bytes) return GDN_EINVAL;
-    const gdn_status st = expanded_sizes(B, Tq, Tk, H, dn, dr, dv, dtype);
+    const gdn_status st = backward_sizes(B, Tq, Tk, H, dn, dr, dv, dtype);
     if (st != GDN_OK) return st;
     *bytes = (size_t)gdn::latent_bwd_workspace(dtype == GDN_BF16, B, Tq, Tk, H, dn, dv);
     return GDN_OK;
@@ -156,7 +165,7 @@ gdn_status gdn_latent_bwd(const void *q, const void *kv, const void *k_rope, con
                           size_t workspace_bytes, int B, int Tq, int Tk, int H, int dn, int dr, int dv, float scale,
                           gdn_dtype dtype, void *stream)
 {
-    const gdn_status st = expanded_sizes(B, Tq, Tk, H, dn, dr, dv, dtype);
+    const gdn_status st = backward_sizes(B, Tq, Tk, H, dn, dr, dv, dtype);
     if (st == GDN_EINVAL) return st;
     if (!scale_ok(scale)) return GDN_EINVAL;
     const long long es = dtype == GDN_BF16 ? 2 : 4, qrows = prod(B, Tq, H), krows = prod(B, Tk, H), ks = prod(B, Tk);

@@ -570,7 +570,9 @@ static hipError_t bwd_launch(const LatentBwdArgs &a, hipStream_t st)
     if (e == hipSuccess) e = allow_lds((const void *)kq, 2 * C::BUF);
     if (e != hipSuccess) return e;
     if (BH * nq > 0) hipLaunchKernelGGL(kq, dim3((unsigned)(BH * nq * plan.kp)), dim3(256), 2 * C::BUF, st, a, nq, plan);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     if (BH * nk > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)(BH * nk * plan.qp)), dim3(512), C::KV_LDS, st, a, plan);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     auto groups = [](long values) { return (int)((values + 1023) / 1024); };
     const int nr = (int)((krows + 15) / 16), ndq = plan.kp > 1 ? groups(BH * a.Tq * C::DK) : 0;
     const int ndkv = plan.qp > 1 ? groups(BH * a.Tk * (DN + DV)) : 0;

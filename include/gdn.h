@@ -429,7 +429,8 @@ GDN_API gdn_status gdn_latent_fwd(const void *q, const void *kv, const void *k_r
  * Gradients of gdn_latent_fwd.  q .. lse as given to and written by the forward
  * (lse is required), d_o [B, Tq, H, dv] dtype; writes dq, dkv and dk_rope in the
  * layouts of q, kv and k_rope (dk_rope is the sum over the heads).  Gradients of
- * padding rows and keys are 0.  Deterministic: no atomics.
+ * padding rows and keys are 0.  Deterministic: no atomics.  GDN_ENOTSUP also from
+ * B * H * ceil(Tk / 128) = 2^23 on (GDN_F32: Tk / 64).
  */
 GDN_API gdn_status gdn_latent_bwd_workspace_size(int B, int Tq, int Tk, int H, int dn, int dr, int dv,
                                                  gdn_dtype dtype, size_t *bytes);

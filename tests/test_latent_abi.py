@@ -136,6 +136,18 @@ def test_rows_too_wide_for_32_bit_offsets_are_refused(L):
     assert _bwd(L, B=1, Tq=1, Tk=1, H=(1 << 15) + 1) == gdn.GDN_ENOTSUP
 
 
+@pytest.mark.parametrize("dtype,keys", [(0, 64), (1, 128)])
+def test_bwd_grid_of_512_threads(L, dtype, keys):
+    """The key-owning kernel's workgroups times 512 threads stay below 2^32."""
+    n = ctypes.c_size_t(0)
+    ask = lambda **a: L.gdn_latent_bwd_workspace_size(a["B"], 1, a["Tk"], a["H"], 64, 64, 64, dtype, ctypes.byref(n))  # noqa: E731
+    for Tk, H in ((1, 1 << 15), (keys, 1 << 15), (keys + 1, 1 << 14)):
+        assert ask(B=256, Tk=Tk, H=H) == gdn.GDN_ENOTSUP
+        assert _bwd(L, B=256, Tq=1, Tk=Tk, H=H, dn=64, dv=64, dtype=dtype) == gdn.GDN_ENOTSUP
+        assert ask(B=255, Tk=Tk, H=H) == gdn.GDN_OK
+    assert L.gdn_latent_fwd_workspace_size(256, 1, 1, 1 << 15, 64, 64, 64, dtype, ctypes.byref(n)) == gdn.GDN_OK
+
+
 def test_steps_takes_at_most_64_drafts(L):
     assert _steps(L, M=65) == gdn.GDN_ENOTSUP
 
