@@ -68,10 +68,19 @@ struct BwdPlan {
     int kstep, qstep;  // rows of a piece, whole tiles
 };
 
-inline int bwd_pieces(long wgs, long fill, int tiles, int least) {   // of `least` tiles or more
+// Pieces of `tiles` walked tiles, `least` tiles each or more, to give `fill` workgroups:
+// at most 16, and 32 where more than that are asked for, as each adds to what the last
+// kernel reads.  One row over 65,408 keys 128 us, with 16 207, with as many as there are
+// (511) 173; 64 rows of 4 heads over 8192 46 us, 50, 52.  Where fewer are asked for, up to
+// 32 are no better: fp32, one head of 1200 54 us with 16, 60; 2 heads of 1000 rows over
+// 8000 keys 69, 72.
+inline int bwd_pieces(long wgs, long fill, int tiles, int least)
+{
     if (wgs <= 0 || wgs >= fill || tiles < 2 * least) return 1;
-    const long n = (fill + wgs - 1) / wgs;
-    return (int)(n > tiles / least ? tiles / least : n > 16 ? 16 : n);
+    long n = (fill + wgs - 1) / wgs;
+    const long most = n > 32 ? 32 : 16;
+    if (n > tiles / least) n = tiles / least;
+    return (int)(n > most ? most : n);
 }
 
 inline BwdPlan bwd_plan(bool bf16, int B, int Tq, int Tk, int H)

@@ -119,6 +119,14 @@ def test_backward_in_long_pieces(B, T, H, dn, dv, lens, keys, rows, seqs):
     _bwd_parts(_expanded(B, T, T, H, dn, dv, "bf16", seed=36, lens=lens), "bf16", seqs)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,Tq,Tk,H,lens", [(1, 1, 5000, 1, None), (2, 7, 4200, 2, [4200, 4194])])
+def test_backward_of_few_rows_over_many_keys(B, Tq, Tk, H, lens, dt):
+    (kp, _), (qp, _) = plans.bwd(dt, B, Tq, Tk, H)
+    assert 20 <= kp <= 32 and qp == 1
+    _bwd_parts(_expanded(B, Tq, Tk, H, 128, 64, dt, seed=41, lens=lens), dt, list(range(B)))
+
+
 def _tiles_a_share(dt, lens, rows, drafts):
     rt, shares = plans.step(dt, rows)
     kt = 64 if dt == "bf16" and rt <= 32 else 32
