@@ -25,7 +25,8 @@ template <int NO, int NI> bool outputs_clear(const Range (&out)[NO], const Range
     return true;
 }
 
-bool scale_ok(float s) { return isfinite(s) && s > 0.f; }
+// The kernels take exponentials to the base 2, of scores times scale log2(e).
+bool scale_ok(float s) { return s > 0.f && isfinite(s * gdn::LOG2E); }
 
 // Sizes of the expanded form: EINVAL for negative or overflowing ones, ENOTSUP for
 // those without a kernel.

@@ -396,8 +396,8 @@ GDN_API gdn_status gdn_recurrent_step_prologue(const void *q_raw, const void *k_
  * from lens, lse, table (4 bytes) and tree (8 bytes) needs 16-byte alignment, a
  * workspace 256 bytes; a workspace's contents on entry do not matter, on return
  * they are unspecified, and calls that share one must not run concurrently.
- * Outputs and the workspace overlap neither inputs nor each other.  scale: finite
- * and > 0.  Results are the same on every call with the same arguments.
+ * Outputs and the workspace overlap neither inputs nor each other.  scale: > 0,
+ * with scale / ln 2 finite.  Results are the same on every call with the same arguments.
  * NOT checked: live inputs are finite (what lies behind a sequence's live length,
  * or in cache slots behind it, and drafts that a row does not see, may hold anything).
  *

@@ -136,6 +136,18 @@ def test_rows_too_wide_for_32_bit_offsets_are_refused(L):
     assert _bwd(L, B=1, Tq=1, Tk=1, H=(1 << 15) + 1) == gdn.GDN_ENOTSUP
 
 
+@pytest.mark.parametrize("call", [_fwd, _bwd, _step, _steps])
+def test_scale_beyond_base_two_is_refused(L, call):
+    """scale log2(e) must be a number: a score of 0 would otherwise be 0 times infinity."""
+    top = 3.4028234663852886e38   # the largest float
+    for scale in (top, top * 0.7):
+        assert call(L, scale=scale) == gdn.GDN_EINVAL
+    if call is _fwd:
+        assert call(L, scale=top * 0.69, B=0) == gdn.GDN_OK
+    elif call is not _bwd:
+        assert call(L, scale=top * 0.69, N=0) == gdn.GDN_OK
+
+
 @pytest.mark.parametrize("dtype,keys", [(0, 64), (1, 128)])
 def test_bwd_grid_of_512_threads(L, dtype, keys):
     """The key-owning kernel's workgroups times 512 threads stay below 2^32."""
