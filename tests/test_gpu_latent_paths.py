@@ -120,6 +120,22 @@ def test_backward_in_long_pieces(B, T, H, dn, dv, lens, keys, rows, seqs):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_backward_of_peaked_rows(dt):
+    """Scores of a standard deviation of 8: most rows give nearly all their weight to one key,
+    and D, by the stored o, carries that key's rounding.  Also says how far the gradients
+    are from those of the forward in 64 bits, whose o is not rounded."""
+    B, T, H = 2, 400, 5
+    scale = 1 / math.sqrt(192)
+    d = _expanded(B, T, T, H, 128, 128, dt, seed=42)
+    d["q"] = (d["q"].float() * 8).to(DT[dt])
+    g = _bwd_parts(d, dt, [0, 1])
+    o, lse = ref.forward(d["q"], d["kv"], d["k_rope"], None, scale)
+    want = ref.backward(d["q"], d["kv"], d["k_rope"], None, o, lse, d["d_o"], scale)
+    for name, w in zip(("dq", "dkv", "dk_rope"), want):
+        _say(f"{name} {dt}: off by {np.linalg.norm(ref.f64(g[name]) - w) / np.linalg.norm(w):.2e} of its norm")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("B,Tq,Tk,H,lens", [(1, 1, 5000, 1, None), (2, 7, 4200, 2, [4200, 4194])])
 def test_backward_of_few_rows_over_many_keys(B, Tq, Tk, H, lens, dt):
     (kp, _), (qp, _) = plans.bwd(dt, B, Tq, Tk, H)
