@@ -35,7 +35,12 @@ struct FwdPlan {
 //   (its queries' loads and its result's stores, which nothing hides) would cost more
 //   (8 heads of 1024: 21 us, in shares 5 more; one row of 16 heads over 8192 keys 30, 8
 //   more).  Enough to fill the units twice, fp32, whose tiles have half the keys and four
-//   times the time, half as many again (2 x 8 heads of 700: 39 us, 5 more without).
+//   times the time, half as many again (2 x 8 heads of 700: 39 us, 5 more without), and 32
+//   at most, for the join's sake (one row over 32,768 keys 37 us, with up to 16 59, 64 31,
+//   128 40; of 4 heads over 16,384 29, 39, 31, 31; 100 rows over 30,000 44, 62, 46, 56).
+//
+// Rows of less than eight tiles have neither two pieces of four nor, in less than 512
+// workgroups, eight tiles for each of 512 shares.
 inline FwdPlan fwd_plan(bool bf16, int B, int Tq, int Tk, int H)
 {
     const long bh = (long)B * H, wide = bh * ((Tq + 127) / 128);
@@ -88,6 +93,10 @@ inline BwdPlan bwd_plan(bool bf16, int B, int Tq, int Tk, int H)
     const int own = bf16 ? 128 : 64, st = bf16 ? 64 : 32;
     const long bh = (long)B * H;
     const int nk = (Tk + st - 1) / st, nq = (Tq + st - 1) / st;
+    // dq (two workgroups a unit) is cut below 512 workgroups, dk and dv (one) below 256:
+    // 8 heads of 2048 101 us; dq below 256 or 1024 112, 116; dk and dv below 128 or 512 131,
+    // 112.  Just below a bound cutting can lose (16 heads of 1920, 240 workgroups: 156 us,
+    // dk and dv uncut 140), just above it it would (16 of 2048 163 uncut, 181).
     const int least = bf16 ? 2 : 1;   // 500 rows of 16 heads: 48 us (55 with four); fp32, 257 of 4: 27 us (34 with two)
     const int kp = bwd_pieces(bh * ((Tq + own - 1) / own), 512, nk, least);
     const int qp = bwd_pieces(bh * ((Tk + own - 1) / own), 256, nq, least);
@@ -103,16 +112,23 @@ inline BwdPlan bwd_plan(bool bf16, int B, int Tq, int Tk, int H)
 
 constexpr int STEP_CUS = 256;   // one workgroup a compute unit: two tiles fill its LDS
 
-// Rows of a workgroup.  fp32 has registers for 16.
+// Rows of a workgroup.  fp32 has registers for 16.  bf16: 17 to 32 rows by 32 stand between
+// two tiles of 16 and one of 64, never the slowest for long (32 heads, r = 512: 32 sequences
+// of 4000 tokens 47 us, by 16 51, by 64 42; 4 of 2000 20, 17, 22; 128 of 2000, r = 256, 45,
+// 62, 46); beyond, 64 (64 heads, 64 of 2000: 47 us, two tiles of 32 69; 8 of 2000 27, 26).
 GDN_PLAN_FN int step_rt(bool bf16, int rows)
 {
     return !bf16 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-// Workgroups that may share the key tiles of one row tile.
+// Workgroups that may share the key tiles of one row tile: with a multiple of eight the row
+// tiles of one share, which read the same keys, land on one XCD.  r = 512, 8 sequences of
+// 2000: 5 row tiles 35.5 us, without rounding down 45; 10 tiles 47, 56; 15 tiles 59, 66; 28
+// tiles 88, 98.  Where it costs nearly half of the workgroups it loses: 17 tiles (8 for 15)
+// 85 us, 72; 20 (8 for 12) 86, 79; fp32, r = 256, 17 tiles 61, 42.
 GDN_PLAN_FN int step_shares(int ntile) {
     int g = STEP_CUS / (ntile < 1 ? 1 : ntile);
-    if (g >= 8) g &= ~7;   // the row tiles of one share land on one XCD
+    if (g >= 8) g &= ~7;
     return g < 1 ? 1 : g;
 }
 

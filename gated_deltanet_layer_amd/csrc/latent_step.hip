@@ -12,14 +12,15 @@
 //       they split the tile's keys, in the second the r output columns.  Bound by the
 //       cache's bytes: 64 sequences of 4100 tokens, 16 heads, r = 512 (229 MB live) 48 us
 //       in the kernel, the rate of a plain copy of such a cache; with join and launches
-//       52-62 us.  One sequence of 300: 10 us, a chain of latencies (lengths, page,
+//       52-63 us.  One sequence of 300: 10 us, a chain of latencies (lengths, page,
 //       tile, two products), and 4 us of the join.
 //   more (bf16)  latent_step_wide_kernel, 64 rows.  At 64 rows a byte of the cache is
 //       worth 122 operations, so the matrix cores, LDS and the copies all near their
-//       limits: 16 sequences of 4096 x 32 drafts x 32 heads 150 us (0.75 PFLOP/s, matrix
-//       cores 36 % busy), 128 of up to 8192 with 128 heads 310 us (3.0 TB/s; a tile is
-//       taken from HBM once and from L2 by the second row tile).  The four waves of the
-//       second product set the pace, about 2700 cycles for 32 keys.
+//       limits: 16 sequences of 4096 x 32 drafts x 32 heads 147-168 us (0.67-0.77 PFLOP/s,
+//       matrix cores 35 % busy), 128 of up to 8192 with 128 heads 310-332 us (2.8-3.0 TB/s; a tile is
+//       taken from HBM once and from L2 by the second row tile).  A tile of 32
+//       keys takes 3,200 cycles, in which the matrix cores work for 1,100 and the LDS,
+//       whose score waves read the whole tile each, for some 1,850 (236 KB).
 //
 // The runs are equal shares of all key tiles of the batch, whatever the lengths:
 // the workgroups add up the tiles of all sequences on their own and each takes
@@ -809,7 +810,9 @@ static hipError_t step_enqueue(K k, int rt, int threads, int lds, const LatentSt
     const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k, dim3(ntile * shares), dim3(threads), lds, st, a, ntile, shares);
-    // pieces a sequence: about shares / N
+    // Pieces a sequence: about shares / N.  r = 512, 16 heads: 4 sequences of 2000 tokens
+    // 14.9 us with four waves a row, 17.3 with one; 48 of 2000 33.1, 33.4; 64 of 2000 35.5,
+    // 35.3; 128 of 2000 63.5, 62.2.
     if (shares > 4 * a.N)
         hipLaunchKernelGGL((latent_join_kernel<T, R, 4>), dim3(a.N * rows), dim3(256), 0, st, a, ntile, shares, rt);
     else

@@ -52,6 +52,8 @@
 extern "C" {
 #endif
 
+/* Raised when an entry point of an earlier version changes.  New entry points may come
+ * without a new version: a program that binds at run time finds out by the symbol. */
 #define GDN_ABI_VERSION 7
 
 #if defined(__GNUC__)
@@ -429,7 +431,13 @@ GDN_API gdn_status gdn_latent_fwd(const void *q, const void *kv, const void *k_r
  * Gradients of gdn_latent_fwd.  q .. lse as given to and written by the forward
  * (lse is required), d_o [B, Tq, H, dv] dtype; writes dq, dkv and dk_rope in the
  * layouts of q, kv and k_rope (dk_rope is the sum over the heads).  Gradients of
- * padding rows and keys are 0.  Deterministic: no atomics.  GDN_ENOTSUP also from
+ * padding rows and keys are 0.  Deterministic: no atomics.
+ *
+ * With D_i = d_o_i . o_i (fp32, of o as stored) and dS = P (dP - D): for GDN_BF16, P is
+ * rounded to bf16 for dv and dS for dq and dk, and the P in dk's dS to fp16 of 4096 P.
+ * o as stored is off by its rounding, which reaches the gradients of a row whose weights
+ * sit on one key undiminished; a run of 128 query rows (from row 0 on) that all see at
+ * most 128 keys has D from P and dP instead.  GDN_F32 rounds nothing to fewer bits.  GDN_ENOTSUP also from
  * B * H * ceil(Tk / 128) = 2^23 on (GDN_F32: Tk / 64).
  */
 GDN_API gdn_status gdn_latent_bwd_workspace_size(int B, int Tq, int Tk, int H, int dn, int dr, int dv,
