@@ -55,10 +55,10 @@ FLUSH_BYTES = 512 << 20        # twice the 256 MB last-level cache
 MEASURED_TRAFFIC = {
     "chunk_fwd_ws_kernel<128>": (("chunk_fwd_ws.hip", "ws_common.h", "gdn_common.h",
                                   "mfma_frag.h"),
-                                 "5df1a38c069ce213", 862547296),
+                                 "2e52f8a616c0bc9f", 862494003),
     "chunk_fwd_wsc_kernel<128>": (("chunk_fwd_wsc.hip", "ws_common.h", "gdn_common.h",
                                    "mfma_frag.h"),
-                                  "919f74973a0c28f3", 420173184),
+                                  "b690bd72f47f9c61", 420173619),
     "recurrent_step_kernel<bf16,128,128,channel>": (("recurrent_step.hip", "gdn_common.h"),
                                                     "6075e5972b67aade", 1642950528),
     "recurrent_multi_kernel<bf16,128,128,channel>/final": (("recurrent_multi.hip", "gdn_common.h"),
@@ -71,12 +71,12 @@ MEASURED_TRAFFIC = {
                                                                   "prologue_ops.h", "gdn_common.h"),
                                                                  "672309d493c963a2", 1719409472),
     "chunk_fwd_seg/channel_long": (("chunk_fwd_seg.hip", "ws_common.h", "gdn_common.h",
-                                    "mfma_frag.h"), "db896b910e4d7fd9", 13454399872),
+                                    "mfma_frag.h"), "c87089ab789465f7", 13447411098),
     "chunk_fwd_seg/channel_long/o": (("chunk_fwd_seg.hip", "chunk_fwd_wsc.hip", "ws_common.h",
-                                      "gdn_common.h", "mfma_frag.h"), "0980df048bf9396b", 33386495168),
+                                      "gdn_common.h", "mfma_frag.h"), "b1137063a3e86b4c", 33385523200),
     # the whole backward call (prep, sweeps, grad) at B4 H6 T4096, per-channel gate, bf16
     "chunk_bwd/channel_bf16": (("chunk_bwd.hip", "chunk_bwd.h", "ws_common.h", "gdn_common.h",
-                                "mfma_frag.h"), "909863fa64a1af75", 1350448320),
+                                "mfma_frag.h"), "f9abfea51d20aa4e", 1350927053),
 }
 
 # bf16 matrix-core work per launch (SQ_INSTS_VALU_MFMA_MOPS_BF16, units of 512
@@ -84,7 +84,7 @@ MEASURED_TRAFFIC = {
 MEASURED_MFMA_MOPS = {
     "chunk_fwd_ws_kernel<128>": (("chunk_fwd_ws.hip", "ws_common.h", "gdn_common.h",
                                   "mfma_frag.h"),
-                                 "5df1a38c069ce213", 257949696),
+                                 "2e52f8a616c0bc9f", 257949696),
 }
 
 
