@@ -143,6 +143,15 @@ def test_backward_of_few_rows_over_many_keys(B, Tq, Tk, H, lens, dt):
     _bwd_parts(_expanded(B, Tq, Tk, H, 128, 64, dt, seed=41, lens=lens), dt, list(range(B)))
 
 
+def test_backward_without_heads_writes_zeros():
+    """No head, but keys: the rotary gradient, a sum over no heads, is written."""
+    x = [torch.randn(s, device="cuda") for s in ((2, 5, 0, 128), (2, 5, 0, 128), (2, 5, 64))]
+    o, lse = gdn.latent_fwd(*x)
+    g = gdn.latent_bwd(*x, o, lse, torch.empty_like(o))
+    assert o.shape == (2, 5, 0, 64) and g["dq"].numel() == 0 and g["dkv"].numel() == 0
+    assert g["dk_rope"].shape == (2, 5, 64) and (g["dk_rope"] == 0).all()
+
+
 def _tiles_a_share(dt, lens, rows, drafts):
     rt, shares = plans.step(dt, rows)
     kt = 64 if dt == "bf16" and rt <= 32 else 32
