@@ -152,6 +152,27 @@ def test_backward_without_heads_writes_zeros():
     assert g["dk_rope"].shape == (2, 5, 64) and (g["dk_rope"] == 0).all()
 
 
+def test_keys_beyond_32_bit_offsets():
+    """kv and its gradient of more than 2^31 values: the first and the last head."""
+    Tq, Tk, H, heads = 64, 66000, 256, [0, 255]
+    assert Tk * H * 128 > 1 << 31
+    gen = torch.Generator("cuda").manual_seed(43)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    x = dict(q=r(1, Tq, H, 128), kv=r(1, Tk, H, 128), k_rope=r(1, Tk, 64), d_o=r(1, Tq, H, 64))
+    o, lse = gdn.latent_fwd(x["q"], x["kv"], x["k_rope"])
+    g = gdn.latent_bwd(x["q"], x["kv"], x["k_rope"], o, lse, x["d_o"])
+    p = {k: v.cpu() for k, v in _part({**x, "o": o, "lse": lse}, [0], heads).items() if v is not None}
+    scale = 1 / math.sqrt(128)
+    ro, rl = ref.forward(p["q"], p["kv"], p["k_rope"], None, scale)
+    to, tl = _fwd_tol({**p, "lens": None}, scale, U["bf16"])
+    _close("o", p["o"], ro, to + U["bf16"] * np.abs(ro) + 1e-37)
+    _close("lse", p["lse"], rl, tl + 4 * E * np.abs(rl))
+    want = ref.backward(p["q"], p["kv"], p["k_rope"], None, p["o"], p["lse"], p["d_o"], scale)
+    tol = _bwd_tol({**p, "lens": None}, p["o"], p["lse"], scale, U["bf16"])
+    for name, w, t in list(zip(("dq", "dkv"), want, tol)):
+        _close(name, g[name][:, :, heads], w, t + U["bf16"] * np.abs(w) + 1e-37)
+
+
 def _tiles_a_share(dt, lens, rows, drafts):
     rt, shares = plans.step(dt, rows)
     kt = 64 if dt == "bf16" and rt <= 32 else 32
