@@ -37,6 +37,16 @@ Latent attention, for the attention layers between such mixers (latent.py):
     latent_step(q, cache, table, lens, scale) -> o
     latent_steps(q, draft, tree, cache, table, lens, scale) -> o
     and the C ABI's own gdn_latent_fwd, _bwd, _step, _steps with their workspace queries
+Attention of grouped heads, for hybrids whose attention has ordinary keys (attention.py):
+    attn_prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, eps=1e-6) -> (q, k)
+    attn_prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, eps=1e-6)
+        -> dict of dq_raw, dk_raw, dw_q, dw_k
+    attn_fwd(q, k, v, cu_q, cu_k=None, scale=None) -> (o, lse)
+    attn_bwd(q, k, v, o, lse, d_o, cu_q, cu_k=None, scale=None) -> dict of dq, dk, dv
+    attn_append_(k, v, k_cache, v_cache, k_scale, v_scale, table, lens, cu=None)   (in place)
+    attn_step(q, k_cache, v_cache, k_scale, v_scale, table, lens, scale=None) -> o
+    and the C ABI's own gdn_attn_prologue, _prologue_bwd, _fwd, _bwd, _append, _step with
+    their workspace queries
 """
 from __future__ import annotations
 
@@ -59,7 +69,10 @@ SYMBOLS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_ws",
            "gdn_recurrent_step_decoupled", "gdn_chunk_fwd_prologue",
            "gdn_latent_fwd_workspace_size", "gdn_latent_fwd", "gdn_latent_bwd_workspace_size",
            "gdn_latent_bwd", "gdn_latent_steps_workspace_size", "gdn_latent_step",
-           "gdn_latent_steps", "gdn_status_str", "gdn_abi_version")
+           "gdn_latent_steps", "gdn_attn_prologue", "gdn_attn_prologue_bwd_workspace_size",
+           "gdn_attn_prologue_bwd", "gdn_attn_fwd_workspace_size", "gdn_attn_fwd",
+           "gdn_attn_bwd_workspace_size", "gdn_attn_bwd", "gdn_attn_append",
+           "gdn_attn_step_workspace_size", "gdn_attn_step", "gdn_status_str", "gdn_abi_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -136,6 +149,20 @@ def lib() -> ctypes.CDLL:
         L.gdn_latent_step.restype = i
         L.gdn_latent_steps.argtypes = [vp, vp, vp, vp, vp, vp, vp, fp, vp, sz] + [i] * 8 + [f, i, vp]
         L.gdn_latent_steps.restype = i
+        ll, szp = ctypes.c_longlong, ctypes.POINTER(sz)
+        L.gdn_attn_prologue.argtypes = [vp] * 8 + [i] * 5 + [ll] * 2 + [f, i, vp]
+        L.gdn_attn_prologue_bwd_workspace_size.argtypes = [i] * 6 + [szp]
+        L.gdn_attn_prologue_bwd.argtypes = [vp] * 13 + [sz] + [i] * 5 + [ll] * 4 + [f, i, vp]
+        L.gdn_attn_fwd_workspace_size.argtypes = [i] * 7 + [szp]
+        L.gdn_attn_fwd.argtypes = [vp] * 8 + [sz] + [i] * 6 + [ll] * 3 + [f, i, vp]
+        L.gdn_attn_bwd_workspace_size.argtypes = [i] * 7 + [szp]
+        L.gdn_attn_bwd.argtypes = [vp] * 12 + [sz] + [i] * 6 + [ll] * 6 + [f, i, vp]
+        L.gdn_attn_append.argtypes = [vp] * 9 + [i] * 7 + [ll] * 2 + [i, vp]
+        L.gdn_attn_step_workspace_size.argtypes = [i] * 6 + [szp]
+        L.gdn_attn_step.argtypes = [vp] * 10 + [sz] + [i] * 7 + [f, i, vp]
+        for name in SYMBOLS:
+            if name.startswith("gdn_attn_"):
+                getattr(L, name).restype = i
         L.gdn_status_str.argtypes = [i]
         L.gdn_status_str.restype = ctypes.c_char_p
         L.gdn_abi_version.argtypes = []
@@ -655,3 +682,8 @@ from .latent import (  # noqa: E402  (needs the names above)
     gdn_latent_bwd, gdn_latent_bwd_workspace_size, gdn_latent_fwd, gdn_latent_fwd_workspace_size,
     gdn_latent_step, gdn_latent_steps, gdn_latent_steps_workspace_size, latent_bwd, latent_fwd,
     latent_step, latent_steps)
+from .attention import (  # noqa: E402
+    attn_append_, attn_bwd, attn_fwd, attn_prologue, attn_prologue_bwd, attn_step, gdn_attn_append,
+    gdn_attn_bwd, gdn_attn_bwd_workspace_size, gdn_attn_fwd, gdn_attn_fwd_workspace_size,
+    gdn_attn_prologue, gdn_attn_prologue_bwd, gdn_attn_prologue_bwd_workspace_size, gdn_attn_step,
+    gdn_attn_step_workspace_size)

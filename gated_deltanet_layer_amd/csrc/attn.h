@@ -1,0 +1,237 @@
+// attn.h -- arguments and shared device helpers of the grouped-attention kernels
+// (gfx950): attn_prologue.hip, attn_fwd.hip, attn_bwd.hip, attn_cache.hip.
+#pragma once
+#include "attn_plan.h"
+#include "latent.h"
+
+namespace gdn {
+
+struct AttnPrologueArgs {
+    const void *q_raw, *k_raw;
+    const float *w_q, *w_k, *inv_freq;
+    const int *pos;
+    void *q, *k;                 // forward: outputs; backward: gradients of them (inputs)
+    void *dq_raw, *dk_raw;
+    float *dw_q, *dw_k;
+    float *ws;
+    long q_stride, k_stride;     // elements from token to token
+    long dq_stride, dk_stride;
+    float eps;
+    int T, Hq, Hk, R;
+};
+
+struct AttnArgs {
+    const void *q, *k, *v;
+    const int *cu_q, *cu_k;
+    void *o;
+    float *lse;
+    const void *d_o;
+    void *dq, *dk, *dv;
+    void *ws;
+    long qs, ks, vs;             // elements from token to token
+    long dqs, dks, dvs;
+    float scale;
+    int B, Tq, Tk, Hk, G;
+    unsigned g_mul;              // r / G = r g_mul >> g_shift for r < 2^30 (set by the launcher)
+    int g_shift;
+};
+
+struct AttnCacheArgs {
+    const void *q, *k, *v;
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    const int *table, *lens, *cu;
+    void *o;
+    float *lse;
+    void *ws;
+    long qs, ks, vs;             // elements from token to token
+    float scale;
+    int N, T, Hk, G;
+    int pages, page, width;
+    unsigned bpp_mul;            // block / (page / 16) (set by the launcher)
+    int bpp_shift;
+};
+
+hipError_t attn_prologue_launch(bool bf16, int D, const AttnPrologueArgs &a, hipStream_t st);
+hipError_t attn_prologue_bwd_launch(bool bf16, int D, const AttnPrologueArgs &a, hipStream_t st);
+unsigned long long attn_prologue_bwd_workspace(int T, int D);
+hipError_t attn_fwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st);
+unsigned long long attn_fwd_workspace(bool bf16, int B, int Tq, int Tk, int Hk, int G, int D);
+hipError_t attn_bwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st);
+unsigned long long attn_bwd_workspace(bool bf16, int B, int Tq, int Tk, int Hk, int G, int D);
+hipError_t attn_append_launch(bool bf16, int D, const AttnCacheArgs &a, hipStream_t st);
+hipError_t attn_step_launch(bool bf16, int D, const AttnCacheArgs &a, hipStream_t st);
+unsigned long long attn_step_workspace(int N, int Hk, int G, int D, int page, int width);
+
+// x / d = x mul >> shift for 0 <= x < 2^30, 1 <= d < 2^15: with shift = 30 + s, 2^s >= d
+// the smallest, the error x (mul d - 2^shift) / (d 2^shift) is below 1 / d.
+inline void divisor(int d, unsigned &mul, int &shift) {
+    int s = 0;
+    while ((1 << s) < d) ++s;
+    shift = 30 + s;
+    mul = (unsigned)(((1ULL << shift) + d - 1) / d);
+}
+
+#ifdef __HIPCC__
+__device__ __forceinline__ int quotient(int x, unsigned mul, int shift) {
+    return (int)((unsigned long long)(unsigned)x * mul >> shift);
+}
+
+// Where sequence b stands in the packed rows, in scalar registers.  Offsets that are no
+// rising numbers within the tensor give wrong lengths but never rows outside of it.
+struct Seq {
+    int q0, lq, k0, lk;
+};
+__device__ __forceinline__ int within(int x, int n) { return x < 0 ? 0 : x > n ? n : x; }
+__device__ __forceinline__ Seq seq_lane(const AttnArgs &a, int b) {   // b may differ by lane
+    Seq s;
+    s.q0 = within(a.cu_q[b], a.Tq);
+    s.lq = max(0, within(a.cu_q[b + 1], a.Tq) - s.q0);
+    if (a.cu_k) {
+        s.k0 = within(a.cu_k[b], a.Tk);
+        s.lk = max(0, within(a.cu_k[b + 1], a.Tk) - s.k0);
+    } else {   // Tk = Tq
+        s.k0 = s.q0;
+        s.lk = s.lq;
+    }
+    return s;
+}
+__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b) {
+    Seq s = seq_lane(a, b);
+    s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
+    s.lq = __builtin_amdgcn_readfirstlane(s.lq);
+    s.k0 = __builtin_amdgcn_readfirstlane(s.k0);
+    s.lk = __builtin_amdgcn_readfirstlane(s.lk);
+    return s;
+}
+
+// Over the lanes of a wave, by shifts within rows of 16 lanes: the sums up to each lane,
+// the sum, and the maximum of values that are not negative.
+template <int CTRL> __device__ __forceinline__ int row_shift(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, 0xf, 0xf, true);   // zeros from outside
+}
+__device__ __forceinline__ int row_scan(int x) {
+    x += row_shift<0x111>(x);
+    x += row_shift<0x112>(x);
+    x += row_shift<0x114>(x);
+    return x + row_shift<0x118>(x);
+}
+__device__ __forceinline__ int scan_lanes(int x) {
+    x = row_scan(x);
+    const int a = __builtin_amdgcn_readlane(x, 15), b = a + __builtin_amdgcn_readlane(x, 31);
+    const int c = b + __builtin_amdgcn_readlane(x, 47), row = (threadIdx.x & 63) >> 4;
+    return x + (row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c);
+}
+__device__ __forceinline__ int sum_lanes(int x) {
+    x = row_scan(x);
+    return __builtin_amdgcn_readlane(x, 15) + __builtin_amdgcn_readlane(x, 31) + __builtin_amdgcn_readlane(x, 47) + __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ int max_lanes(int x) {
+    x = max(x, row_shift<0x111>(x));
+    x = max(x, row_shift<0x112>(x));
+    x = max(x, row_shift<0x114>(x));
+    x = max(x, row_shift<0x118>(x));
+    return max(max(__builtin_amdgcn_readlane(x, 15), __builtin_amdgcn_readlane(x, 31)),
+               max(__builtin_amdgcn_readlane(x, 47), __builtin_amdgcn_readlane(x, 63)));
+}
+
+// Item w of a list to which sequence b gives count(b) items: the sequence and the item's
+// number within it; -1 where the list is shorter.  Every lane of the wave calls it.
+struct Item {
+    int b, i;
+};
+template <typename F> __device__ __forceinline__ Item find_item(int B, int w, F count)
+{
+    const int lane = threadIdx.x & 63;
+    int at = 0;
+    for (int b = 0; b < B; b += 64) {
+        const int mine = b + lane < B ? count(b + lane) : 0, incl = scan_lanes(mine);
+        const int sum = __builtin_amdgcn_readlane(incl, 63);
+        if (w < at + sum) {
+            const int l = (int)__builtin_ctzll(__ballot(w < at + incl));
+            return {b + l, w - at - __builtin_amdgcn_readlane(incl - mine, l)};
+        }
+        at += sum;
+    }
+    return {-1, 0};
+}
+
+// The same list with the last items of all sequences first: item i of every sequence
+// stands behind items i + 1 of all of them.  Rows further down a causal sequence have more
+// keys, so that the longest work begins first.
+template <typename F> __device__ __forceinline__ Item find_last(int B, int w, F count)
+{
+    const int lane = threadIdx.x & 63;
+    const int first = lane < B ? count(lane) : 0;
+    auto from = [&](int i) {   // items i and on
+        int sum = max(0, first - i);
+        for (int b = 64 + lane; b < B; b += 64) sum += max(0, count(b) - i);
+        return sum_lanes(sum);
+    };
+    if (w >= from(0)) return {-1, 0};
+    int most = first;
+    for (int b = 64 + lane; b < B; b += 64) most = max(most, count(b));
+    int lo = 0, hi = max_lanes(most);   // from(lo) > w >= from(hi)
+    int behind = 0;                     // from(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1, n = from(mid);
+        if (n > w) lo = mid;
+        else hi = mid, behind = n;
+    }
+    const Item found = find_item(B, w - behind, [&](int b) { return (b < 64 ? first : count(b)) > lo ? 1 : 0; });
+    return {found.b, lo};
+}
+
+// Row tiles of a sequence: tile t has the tokens from t `per` on.
+struct AttnTiles {
+    int per, off, lq, lk;
+    __device__ __forceinline__ AttnTiles(int per, const Seq &s) : per(per), off(s.lk - s.lq), lq(s.lq), lk(s.lk) {}
+    __device__ __forceinline__ int count() const { return (lq + per - 1) / per; }
+    // keys that the last row of tile t sees
+    __device__ __forceinline__ int keys(int t) const { return max(0, off + min((t + 1) * per, lq)); }
+    __device__ __forceinline__ int first() const { return off < 0 ? min(-off / per, count()) : 0; }   // tile that sees any
+    // keys of the row tiles before t (a tile with keys, or count())
+    __device__ __forceinline__ long before(int t) const {
+        const int f = first();
+        const long n = t - f;
+        return n <= 0 ? 0 : n * off + (long)per * ((long)t * (t + 1) - (long)f * (f + 1)) / 2;
+    }
+    __device__ __forceinline__ long all() const {
+        const int n = count();
+        return n > first() ? before(n - 1) + keys(n - 1) : 0;
+    }
+};
+
+// x, which every lane of the wave has, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// The same of an address that memory instructions in inline assembly read: five wait states
+// after the vector instructions that wrote it.
+__device__ __forceinline__ const char *uniform(const void *p) {
+    unsigned long long b = (unsigned)uniform((int)(uintptr_t)p) | (unsigned long long)(unsigned)uniform((int)((uintptr_t)p >> 32)) << 32;
+    asm volatile("s_nop 4" : "+s"(b));
+    return (const char *)b;
+}
+
+// Enqueue the copy of packed rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes apart,
+// x: row 0) into an LDS tile, as load_rows does; the row and the address may be in vector
+// registers, but are the same in every lane.  Rows from n on read as zeros.
+template <int CPR, int ROWS> __device__ __forceinline__ void load_tile(char *tile, const char *x, long stride, int r0, int n)
+{
+    const char *p = uniform(x + r0 * stride);
+    load_rows<CPR, ROWS>(tile, p, stride, 0, uniform(n - r0));
+}
+
+// The sequence of a packed query (or key) row: the last one that begins at or before it,
+// which the row is behind if it is of none.
+__device__ __forceinline__ int seq_at(const int *cu, int B, int T, int row) {
+    int b = 0, hi = B;
+    while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (within(cu[mid], T) <= row) b = mid;
+        else hi = mid;
+    }
+    return b;
+}
+#endif
+
+} // namespace gdn

@@ -1,0 +1,535 @@
+// attn_bwd.hip -- gradients of the packed grouped attention (gfx950).
+//
+//   P_ij = exp(s_ij - lse_i),  D_i = do_i . o_i,  dS_ij = scale P_ij (do_i . v_j - D_i)
+//   dv_j = sum_i P_ij do_i,  dk_j = sum_i dS_ij q_i,  dq_i = sum_j dS_ij k_j
+//
+// The sums of dk and dv run over the rows of all G query heads that share the key head: rows
+// (token, head) in one run, as in the forward's tiles.  No atomics, so results do not depend
+// on the order in which workgroups run: one kernel owns query rows and walks their keys (dq),
+// one owns keys and walks the rows that see them (dk, dv); the scores are computed in both.
+// Where the owners are too few for the device, what walks by is cut into pieces, whose sums a
+// third kernel adds up in order.
+#include "attn.h"
+
+namespace gdn {
+
+// Workspace, all float: D[Tq][Hq]; where there are pieces, dq[kp][Tq][Hq][D] and
+// dkv[qp][Tk][Hk][2 D].
+struct AttnBwdWs {
+    long dq, dkv, bytes;
+    __host__ __device__ AttnBwdWs(const AttnBwdPlan &p, int Tq, int Tk, int Hk, int G, int d) {
+        const long qr = (long)Tq * Hk * G, kr = (long)Tk * Hk;
+        dq = (qr * 4 + 255) & ~255L;
+        dkv = dq + (p.kp > 1 ? p.kp * qr * d * 4 : 0);
+        bytes = dkv + (p.qp > 1 ? p.qp * kr * 2 * d * 4 : 0);
+    }
+};
+
+// This lane's share of a row's do . o (the four 16-lane rows hold its columns).
+template <typename T> __device__ __forceinline__ float frag_dot(const Frag<T> &x, const Frag<T> &y) {
+    float s = 0.f;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += (float)x.v[e] * (float)y.v[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += x.lo[e] * y.lo[e] + x.hi[e] * y.hi[e];
+    }
+    return s;
+}
+
+// P from wave to wave: fp32 as it is, beside bf16 operands as fp16 of P 2^12 (half the
+// room).  P <= 1, so nothing overflows, and down to P = 2^-26 it is off by 2^-11 of itself,
+// an eighth of what dS, which it becomes, is rounded by; below, by 2^-37.  The power of two
+// comes out of dk at the end.
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+template <typename T> __device__ __forceinline__ constexpr float hand_scale() { return sizeof(T) == 2 ? 1.f / 4096.f : 1.f; }
+template <typename T> __device__ __forceinline__ void hand_over(char *to, f32x4 p) {
+    if constexpr (sizeof(T) == 2) {
+        f16x4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = (_Float16)(p[e] * 4096.f);
+        *reinterpret_cast<f16x4 *>(to) = h;
+    } else {
+        *reinterpret_cast<f32x4 *>(to) = p;
+    }
+}
+template <typename T> __device__ __forceinline__ f32x4 take_over(const char *from) {
+    if constexpr (sizeof(T) == 2) {
+        const f16x4 h = *reinterpret_cast<const f16x4 *>(from);
+        return f32x4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
+    } else {
+        return *reinterpret_cast<const f32x4 *>(from);
+    }
+}
+
+template <typename T, int D> struct AttnBwdCfg {
+    static constexpr int OWN = attn_own(sizeof(T) == 2), ST = attn_walk(sizeof(T) == 2), NG = OWN / 64;
+    static constexpr int ES = (int)sizeof(T), CPR = D * ES / 16;
+    static constexpr int OFF_V = ST * CPR * 16, BUF = 2 * OFF_V;   // a tile: [ST][D] of k or q, [ST][D] of v or do
+    static constexpr int ROWS = 2 * ST * 4;                        // lse and D of the tile's rows
+    static constexpr int HP = 64 * 4 * (ES == 2 ? 2 : 4);          // four values of P of each lane
+    static constexpr int HAND = 2 * ST / 16 * NG * HP;             // P of two tiles, one pair of waves
+    static constexpr int KV_LDS = 3 * (BUF + ROWS) + 4 * HAND;
+    static_assert(KV_LDS <= 160 * 1024, "LDS");
+};
+
+// The rows that walk by an owner of keys from k0 on: all that see one of them.  Row r of a
+// key head: token r / G, head r % G.
+struct Walk {
+    int first, end;   // rows, first a multiple of the tile's
+    __device__ __forceinline__ Walk(const AttnArgs &a, const Seq &s, int k0, int st) {
+        first = max(0, k0 - (s.lk - s.lq)) * a.G / st * st;
+        end = k0 < s.lk ? s.lq * a.G : 0;
+    }
+};
+
+// dk and dv.  Four pairs of waves; a pair owns 16 NG keys.  The first of the pair
+// computes the scores and P and adds up dv^T (k and dv in its registers), the second
+// takes P over, computes dP and dS and adds up dk^T (v and dk in its registers): the
+// same number of products for both, and of q and do each reads from LDS one along
+// the rows and the other across them, where one wave for both would not have the
+// registers for 32 keys, and with 16 keys would read twice as much.  The second is
+// one tile of query rows behind, so neither waits for the other inside a tile.
+// Scores have query rows on the accumulator's rows: P and dS feed the gradient
+// products as B operands straight from the registers, and P changes hands between
+// equal lanes.
+template <typename T, int D, bool CUT>
+__global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwdPlan plan)
+{
+    typedef AttnBwdCfg<T, D> C;
+    constexpr int NG = C::NG, ST = C::ST, NKB = D / 32, NC = D / 16, OWN = C::OWN;
+    constexpr int BPT = ST / 32;   // blocks a tile
+    extern __shared__ char lds[];
+    const int h = blockIdx.x % a.Hk, piece = CUT ? blockIdx.x / a.Hk % plan.qp : 0;
+    auto owners = [&](int b) { return (seq_lane(a, b).lk + OWN - 1) / OWN; };
+    // the first keys are seen by most rows: the longest walks begin first
+    const Item it = find_last(a.B, blockIdx.x / a.Hk / (CUT ? plan.qp : 1), owners);
+    if (it.b < 0) return;
+    const Seq sq = seq_of(a, it.b);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int pair = wave & 3, lane = threadIdx.x & 63, Hq = a.Hk * a.G;
+    const int off = sq.lk - sq.lq, n = sq.lk;
+    const int k0 = ((n + OWN - 1) / OWN - 1 - uniform(it.i)) * OWN, w0 = k0 + pair * 16 * NG;
+    const T *q = (const T *)a.q + sq.q0 * a.qs + h * a.G * D;
+    const T *d_o = (const T *)a.d_o + ((long)sq.q0 * Hq + h * a.G) * D;
+    const float *lse = a.lse + (long)sq.q0 * Hq + h * a.G, *Dw = (const float *)a.ws + (long)sq.q0 * Hq + h * a.G;
+    const float c = a.scale * LOG2E;
+    float *stat = (float *)(lds + 3 * C::BUF);                  // [3][2][ST]: lse and D of the rows
+    char *hand = lds + 3 * (C::BUF + C::ROWS) + pair * C::HAND; // [2][ST / 16 NG][64 lanes]: P of a tile, four values a lane
+
+    const Walk walk(a, sq, k0, ST);
+    const int qn = CUT ? (int)min((long)walk.end, (piece + 1L) * plan.qstep) : walk.end;
+    const int qfirst = CUT ? (int)max((long)walk.first, (long)piece * plan.qstep) : walk.first;
+    const int nt = qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0;
+    auto load = [&](int j) {
+        const int r0 = qfirst + j * ST, buf = __builtin_amdgcn_readfirstlane(j % 3);
+        constexpr int RP = 512 / C::CPR;
+        static_assert(ST % RP == 0 && RP % 16 == 0, "");
+        const int row = threadIdx.x / C::CPR, ch = ((threadIdx.x % C::CPR) ^ swz<C::CPR>(row)) * 16;
+        const char *to = lds + buf * C::BUF + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < ST / RP; ++i) {
+            const int r = r0 + i * RP + row, t = quotient(r, a.g_mul, a.g_shift), g = r - t * a.G;
+            const char *sq_ = r < qn ? (const char *)(q + t * a.qs + g * D) + ch : (const char *)latent_zero;
+            const char *sd = r < qn ? (const char *)(d_o + ((long)t * Hq + g) * D) + ch : (const char *)latent_zero;
+            copy16(sq_, to + i * 512 * 16);
+            copy16(sd, to + C::OFF_V + i * 512 * 16);
+        }
+        if (wave < 2 && lane < ST) {   // lse by the first wave, D by the second
+            const int r = r0 + lane, t = quotient(r, a.g_mul, a.g_shift);
+            const void *src = r >= qn ? (const void *)latent_zero : (wave ? Dw : lse) + (long)t * Hq + (r - t * a.G);
+            copy4(src, (char *)(stat + (buf * 2 + wave) * ST));
+        }
+    };
+    // before tile j: it is there, and P of tile j - 1 is whole
+    auto sync = [&](int j) {
+        if (j < nt) wait_vm<0>();
+        lds_barrier();
+        if (j + 1 < nt) load(j + 1);   // over tile j - 2
+    };
+    // first row that sees key j: its token is j - off
+    auto sees = [&](int j) { return (j - off) * a.G; };
+    auto seen = [&](int i) {   // whether a row of block i sees a key of the wave
+        return qfirst + i * 32 + 31 >= sees(w0) && w0 < n;
+    };
+    const AttnBwdWs lay(plan, a.Tq, a.Tk, a.Hk, a.G, D);
+    if (CUT && nt == 0) return;   // the last kernel knows which pieces there are
+    if (nt > 0) load(0);
+    const T *x = wave < 4 ? (const T *)a.k + sq.k0 * a.ks + h * D : (const T *)a.v + sq.k0 * a.vs + h * D;
+    const long xs = wave < 4 ? a.ks : a.vs;
+    Frag<T> xf[NG][NKB];   // k for the first of the pair, v for the second
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int key = w0 + 16 * g + r16;
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) xf[g][kb] = key < n ? load_frag<T>(x + key * xs + 32 * kb + 8 * gq) : zero_frag<T>();
+    }
+    f32x4 acc[NC][NG];   // dv^T, dk^T
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) acc[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int rb = row_base<T, C::CPR>(r16), cb = col_base<T, C::CPR>(4 * gq);
+
+    if (wave < 4) {
+#pragma unroll 1
+        for (int j = 0; j <= nt; ++j) {
+            sync(j);
+            if (j == nt) break;
+            const char *qt = lds + j % 3 * C::BUF, *dt = qt + C::OFF_V;
+            const float *st = stat + j % 3 * 2 * ST;
+            char *to = hand + (j & 1) * (C::HAND / 2) + lane * (C::HP / 64);
+#pragma unroll 1
+            for (int t = 0; t < BPT; ++t) {
+                if (!seen(j * BPT + t)) continue;
+                const int r0 = qfirst + j * ST + t * 32;
+                const bool part = r0 < sees(w0 + 16 * NG - 1) || r0 + 32 > qn;
+                f32x4 s[2][NG];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int kb = 0; kb < NKB; ++kb) {
+                        const Frag<T> f = row_frag<T>(qt + (32 * t + 16 * u) * C::CPR * 16, rb, kb);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, xf[g][kb]);
+                    }
+                    const int row = 16 * u + 4 * gq;
+                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 32 * t + row) * LOG2E;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
+                    if (part) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const int lim = sees(w0 + 16 * g + r16);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool hide = (r0 + row + e < lim) | (r0 + row + e >= qn);
+                                s[u][g][e] = hide ? 0.f : s[u][g][e];
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) hand_over<T>(to + ((2 * t + u) * NG + g) * C::HP, s[u][g]);
+                }
+                // P (and below dS) rounded to the storage type for the matrix cores: half
+                // a step each, as the gradients themselves
+                Frag<T> pf[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
+#pragma unroll
+                for (int v = 0; v < NC; ++v) {
+                    const Frag<T> f = col_frag<T, C::CPR>(dt + 32 * t * C::CPR * 16, cb, v);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, pf[g]);
+                }
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j <= nt; ++j) {
+            sync(j);
+            if (j == 0) continue;
+            const int k = j - 1;
+            const char *qt = lds + k % 3 * C::BUF, *dt = qt + C::OFF_V;
+            const float *st = stat + (k % 3 * 2 + 1) * ST;
+            const char *from = hand + (k & 1) * (C::HAND / 2) + lane * (C::HP / 64);
+#pragma unroll 1
+            for (int t = 0; t < BPT; ++t) {
+                if (!seen(k * BPT + t)) continue;
+                f32x4 dp[2][NG];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int v = 0; v < NKB; ++v) {
+                        const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::CPR * 16, rb, v);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, xf[g][v]);
+                    }
+                    const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 32 * t + 16 * u + 4 * gq);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const f32x4 p = take_over<T>(from + ((2 * t + u) * NG + g) * C::HP);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
+                    }
+                }
+                Frag<T> sf[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+#pragma unroll
+                for (int v = 0; v < NC; ++v) {
+                    const Frag<T> f = col_frag<T, C::CPR>(qt + 32 * t * C::CPR * 16, cb, v);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, sf[g]);
+                }
+            }
+        }
+    }
+    const bool isv = wave < 4;
+    const float by = isv ? 1.f : a.scale * hand_scale<T>();
+    T *out = isv ? (T *)a.dv + sq.k0 * a.dvs + h * D : (T *)a.dk + sq.k0 * a.dks + h * D;
+    const long outs = isv ? a.dvs : a.dks;
+    float *sum = (float *)((char *)a.ws + lay.dkv) + (((long)piece * a.Tk + sq.k0) * a.Hk + h) * 2 * D + (isv ? D : 0);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int key = w0 + 16 * g + r16;
+        if (key >= n) continue;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const f32x4 v = acc[i][g] * by;
+            if (CUT) store4(sum + (long)key * a.Hk * 2 * D + 16 * i + 4 * gq, v);
+            else store4(out + key * outs + 16 * i + 4 * gq, v);
+        }
+    }
+}
+
+// dq, and D for the kernel above, which is launched after this one.  A wave owns 16
+// NG rows, q and do of them in registers; scores are transposed as in the forward pass,
+// and dS^T feeds dq^T = K^T dS^T from the registers.
+template <typename T, int D, bool CUT>
+__global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdPlan plan)
+{
+    typedef AttnBwdCfg<T, D> C;
+    constexpr int NG = C::NG, ST = C::ST, NKB = D / 32, NC = D / 16;
+    constexpr bool BF = sizeof(T) == 2;
+    extern __shared__ char lds[];
+    const int h = blockIdx.x % a.Hk, piece = CUT ? blockIdx.x / a.Hk % plan.kp : 0, per = plan.tokens;
+    const Item it = find_last(a.B, blockIdx.x / a.Hk / (CUT ? plan.kp : 1), [&](int b) { return AttnTiles(per, seq_lane(a, b)).count(); });
+    if (it.b < 0) return;
+    const Seq sq = seq_of(a, it.b);
+    const AttnTiles tl(per, sq);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    const int off = tl.off, n = sq.lk, Hq = a.Hk * a.G, t0 = uniform(it.i) * per, lr0 = wave * 16 * NG;
+    const int nlive = min(per, sq.lq - t0) * a.G;
+    const T *k = (const T *)a.k + sq.k0 * a.ks + h * D, *v = (const T *)a.v + sq.k0 * a.vs + h * D;
+    const float c = a.scale * LOG2E;
+
+    int pos[NG];
+    long row[NG];   // of [Tq Hq]
+    float ls[NG], dd[NG];
+    Frag<T> qf[NG][NKB], of[NG][NKB];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int lr = lr0 + 16 * g + r16, i = quotient(lr, a.g_mul, a.g_shift), tok = t0 + i, head = h * a.G + lr - i * a.G;
+        const bool live = lr < nlive && off + tok >= 0;
+        pos[g] = live ? off + tok : -1;
+        row[g] = (sq.q0 + (long)tok) * Hq + head;
+        const T *q = (const T *)a.q + (sq.q0 + (long)tok) * a.qs + head * D;
+        const T *d_o = (const T *)a.d_o + row[g] * D, *o = (const T *)a.o + row[g] * D;
+        ls[g] = live ? a.lse[row[g]] * LOG2E : 0.f;
+        float dot = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+            qf[g][kb] = live ? load_frag<T>(q + 32 * kb + 8 * gq) : zero_frag<T>();
+            of[g][kb] = live ? load_frag<T>(d_o + 32 * kb + 8 * gq) : zero_frag<T>();
+            if (live) dot += frag_dot<T>(of[g][kb], load_frag<T>(o + 32 * kb + 8 * gq));
+        }
+        dd[g] = rows_sum(dot);
+    }
+    f32x4 dq[NC][NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) dq[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int all = uniform((tl.keys(it.i) + ST - 1) / ST);
+    const int j0 = CUT ? piece * (plan.kstep / ST) : 0, nt = CUT ? min(all, j0 + plan.kstep / ST) : all;
+    if (CUT && piece > 0 && nt <= j0) return;   // the last kernel knows which pieces there are
+    // keys that some, that all of the wave's rows see
+    const int wend = min(lr0 + 16 * NG, nlive) - 1;
+    const int wlast = wend < lr0 ? 0 : off + t0 + quotient(max(wend, 0), a.g_mul, a.g_shift) + 1;
+    const int wfull = off + t0 + quotient(lr0, a.g_mul, a.g_shift) + 1;
+    auto load = [&](int j) {
+        char *to = lds + (j & 1) * C::BUF;
+        load_tile<C::CPR, ST>(to, (const char *)k, a.ks * C::ES, j * ST, n);
+        load_tile<C::CPR, ST>(to + C::OFF_V, (const char *)v, a.vs * C::ES, j * ST, n);
+    };
+    const int rb = row_base<T, C::CPR>(r16), cb = col_base<T, C::CPR>(4 * gq);
+    // of 32 keys (block t of tile j): P, and dP in the same layout
+    auto products = [&](int j, int t, f32x4 (&s)[2][NG], f32x4 (&dp)[2][NG]) {
+        const char *kt = lds + (j & 1) * C::BUF, *vt = kt + C::OFF_V;
+        const int k0 = j * ST, rbl = pin(rb);
+        const bool part = k0 + ST > wfull;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                dp[u][g] = s[u][g];
+            }
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const Frag<T> f = row_frag<T>(kt + (32 * t + 16 * u) * C::CPR * 16, rbl, kb);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, qf[g][kb]);
+            }
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const Frag<T> f = row_frag<T>(vt + (32 * t + 16 * u) * C::CPR * 16, rbl, kb);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, of[g][kb]);
+            }
+            if (BF) pipeline<4, 2 * NKB, 2 * NKB * NG, 1, NG>();
+            GDN_SCHED_FENCE();
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[g]));
+            if (part) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[u][g][e] = k0 + 32 * t + 16 * u + 4 * gq + e > pos[g] ? 0.f : s[u][g][e];
+            }
+        }
+    };
+    if (BF && all <= 2) {
+        // The first rows, of few keys: o, rounded to bf16, is as large as v there, and the
+        // error that its rounding leaves in D, the same for all keys of a row, would be as
+        // large as the rounding of dS.  They have D from P and dP themselves.  The others
+        // have do . o, where that error is small as long as a row's weights are spread over
+        // its n keys (1 / sqrt(n) as large), and is not where one key takes most of them.
+        float sum[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+        for (int j = 0; j < all; ++j) {
+            if (j == 0) load(0);
+            wait_vm<0>();
+            lds_barrier();
+            if (j + 1 < all) load(j + 1);
+#pragma unroll 1
+            for (int t = 0; t < ST / 32; ++t) {
+                f32x4 s[2][NG], dp[2][NG];
+                products(j, t, s, dp);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[g] += s[u][g][e] * dp[u][g][e];
+            }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int g = 0; g < NG; ++g) dd[g] = rows_sum(sum[g]);
+    }
+    if (piece == 0 && gq == 0) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)   // also of rows that see nothing: they stand in walked tiles
+            if (lr0 + 16 * g + r16 < nlive) ((float *)a.ws)[row[g]] = dd[g];
+    }
+    if (nt > j0) load(j0);
+    for (int j = j0; j < nt; ++j) {
+        const char *kt = lds + (j & 1) * C::BUF;
+        wait_vm<0>();
+        lds_barrier();
+        if (j + 1 < nt) load(j + 1);
+        if (j * ST >= wlast) continue;
+#pragma unroll 1
+        for (int t = 0; t < ST / 32; ++t) {
+            f32x4 s[2][NG], dp[2][NG];
+            products(j, t, s, dp);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dp[u][g] = s[u][g] * (dp[u][g] - dd[g]);
+            const int cbl = pin(cb);
+            Frag<T> sf[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const Frag<T> f = col_frag<T, C::CPR>(kt + 32 * t * C::CPR * 16, cbl, i);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) dq[i][g] = mma(dq[i][g], f, sf[g]);
+            }
+            if (BF) pipeline<4, 2 * NC, NC * NG, 2, NG>();
+        }
+    }
+    float *sum = (float *)((char *)a.ws + AttnBwdWs(plan, a.Tq, a.Tk, a.Hk, a.G, D).dq) + (long)piece * a.Tq * Hq * D;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int lr = lr0 + 16 * g + r16, i = quotient(lr, a.g_mul, a.g_shift);
+        if (lr >= nlive) continue;
+        T *out = (T *)a.dq + (sq.q0 + (long)(t0 + i)) * a.dqs + (h * a.G + lr - i * a.G) * D;
+#pragma unroll
+        for (int e = 0; e < NC; ++e) {
+            const f32x4 x = pos[g] >= 0 ? dq[e][g] * a.scale : f32x4{0.f, 0.f, 0.f, 0.f};
+            if (CUT) store4(sum + row[g] * D + 16 * e + 4 * gq, x);
+            else store4(out + 16 * e + 4 * gq, x);
+        }
+    }
+}
+
+// The sums over the pieces, in order: of dq by the first ndq workgroups (D / 4 lanes a row),
+// of dk and dv by the others (2 D / 4 lanes a key).  A piece counts for the rows that its
+// workgroup has worked on.
+template <typename T, int D> __global__ __launch_bounds__(256) void attn_bwd_sum_kernel(AttnArgs a, AttnBwdPlan plan, int ndq)
+{
+    typedef AttnBwdCfg<T, D> C;
+    const AttnBwdWs lay(plan, a.Tq, a.Tk, a.Hk, a.G, D);
+    const bool isq = (int)blockIdx.x < ndq;
+    const int W = isq ? D : 2 * D, H = isq ? a.Hk * a.G : a.Hk, T_ = isq ? a.Tq : a.Tk;
+    const long at = ((long)(blockIdx.x - (isq ? 0 : ndq)) * 256 + threadIdx.x) * 4, size = (long)T_ * H * W;
+    if (at >= size) return;
+    const int token = (int)(at / W / H), col = (int)(at % W), head = (int)(at / W % H);
+    const int b = seq_at(isq || !a.cu_k ? a.cu_q : a.cu_k, a.B, T_, token);
+    const Seq s = seq_lane(a, b);
+    const int i = token - (isq ? s.q0 : s.k0);
+    if (i < 0 || i >= (isq ? s.lq : s.lk)) return;   // of no sequence
+    int first = 0, end;
+    if (isq) {   // the owner of the row walks the keys up to its last row's position; piece 0 always writes
+        end = max(1, (AttnTiles(plan.tokens, s).keys(i / plan.tokens) + plan.kstep - 1) / plan.kstep);
+    } else {
+        const Walk w(a, s, i / C::OWN * C::OWN, C::ST);
+        first = w.first / plan.qstep;
+        end = w.first < w.end ? (w.end - 1) / plan.qstep + 1 : first;
+    }
+    const float *part = (const float *)((const char *)a.ws + (isq ? lay.dq : lay.dkv)) + at;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int p = first; p < end; ++p) x += *reinterpret_cast<const f32x4 *>(part + p * size);
+    T *out = isq ? (T *)a.dq + token * a.dqs + head * D + col
+                 : col < D ? (T *)a.dk + token * a.dks + head * D + col : (T *)a.dv + token * a.dvs + head * D + col - D;
+    store4(out, x);
+}
+
+template <typename T, int D> static hipError_t bwd_launch(AttnArgs a, hipStream_t st)
+{
+    typedef AttnBwdCfg<T, D> C;
+    const AttnBwdPlan plan = attn_bwd_plan(sizeof(T) == 2, a.B, a.Tq, a.Tk, a.Hk, a.G);
+    divisor(a.G, a.g_mul, a.g_shift);
+    auto kkv = plan.qp > 1 ? attn_bwd_kv_kernel<T, D, true> : attn_bwd_kv_kernel<T, D, false>;
+    auto kq = plan.kp > 1 ? attn_bwd_q_kernel<T, D, true> : attn_bwd_q_kernel<T, D, false>;
+    hipError_t e = hipFuncSetAttribute((const void *)kkv, hipFuncAttributeMaxDynamicSharedMemorySize, C::KV_LDS);
+    if (e != hipSuccess) return e;
+    static_assert(2 * C::BUF <= 64 * 1024, "more dynamic LDS has to be asked for");
+    if (plan.qtiles > 0) hipLaunchKernelGGL(kq, dim3((unsigned)(plan.qtiles * a.Hk * plan.kp)), dim3(256), 2 * C::BUF, st, a, plan);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (plan.ktiles > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)(plan.ktiles * a.Hk * plan.qp)), dim3(512), C::KV_LDS, st, a, plan);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    auto groups = [](long values) { return (int)((values + 1023) / 1024); };
+    const int ndq = plan.kp > 1 ? groups((long)a.Tq * a.Hk * a.G * D) : 0, ndkv = plan.qp > 1 ? groups((long)a.Tk * a.Hk * 2 * D) : 0;
+    if (ndq + ndkv > 0) hipLaunchKernelGGL((attn_bwd_sum_kernel<T, D>), dim3(ndq + ndkv), dim3(256), 0, st, a, plan, ndq);
+    return hipGetLastError();
+}
+
+hipError_t attn_bwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st)
+{
+    if (bf16) return D == 128 ? bwd_launch<__bf16, 128>(a, st) : bwd_launch<__bf16, 64>(a, st);
+    return D == 128 ? bwd_launch<float, 128>(a, st) : bwd_launch<float, 64>(a, st);
+}
+
+unsigned long long attn_bwd_workspace(bool bf16, int B, int Tq, int Tk, int Hk, int G, int D)
+{
+    return (unsigned long long)AttnBwdWs(attn_bwd_plan(bf16, B, Tq, Tk, Hk, G), Tq, Tk, Hk, G, D).bytes;
+}
+
+} // namespace gdn

@@ -1,0 +1,406 @@
+// attn_fwd.hip -- causal attention of grouped heads over packed sequences (gfx950).
+//
+//   s_ij = scale q_i . k_j,  j <= p_i = lk - lq + i        (within one sequence)
+//   o_i = sum_j softmax_j(s_ij) v_j,   lse_i = log sum_j exp s_ij
+//
+// The G query heads that share a key head are rows of one tile (row r: token r / G, head
+// r % G), so a tile of 64 or 128 rows covers few tokens: keys are read once for all heads,
+// little of the diagonal's tiles is masked, and short sequences still fill a tile.
+//
+// A workgroup of four waves owns a row tile of one key head and walks the key tiles once,
+// keeping the running maximum and sum of every row.  Scores are computed transposed (keys
+// on the accumulator's rows, query rows on its lanes): a lane holds four consecutive keys of
+// one row, the softmax needs two cross-lane steps a tile, and the weights feed the second
+// product (o^T = V^T P^T) as its B operand straight from the registers.
+#include "attn.h"
+
+namespace gdn {
+
+template <typename T, int D, int NR> struct AttnFwdCfg {   // NR: 16-row groups a wave
+    static constexpr int RT = 64 * NR;                     // rows a workgroup
+    static constexpr int KT = sizeof(T) == 2 ? 64 : 32;    // keys a tile
+    static constexpr int ES = (int)sizeof(T), CPR = D * ES / 16;
+    static constexpr int OFF_V = KT * CPR * 16, BUF = 2 * OFF_V;   // a tile: [KT][D] keys, [KT][D] values
+};
+
+// Workspace of a call in shares: long prefix[B + 1], the keys (of row tiles) before each
+// sequence, then for each share its first and last piece of a row tile, float o[slot][D],
+// and float lse[slot] of each, slot = RT rows.
+struct AttnFwdWs {
+    long o, lse, bytes;
+    __host__ __device__ AttnFwdWs(int B, int rt, int d) {
+        o = ((long)(B + 1) * 8 + 255) & ~255L;
+        lse = o + 2L * ATTN_SHARES * rt * d * 4;
+        bytes = lse + 2L * ATTN_SHARES * rt * 4;
+    }
+};
+
+__device__ __forceinline__ long scan_lanes64(long x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const long v = __shfl_up(x, d, 64);
+        if ((int)(threadIdx.x & 63) >= d) x += v;
+    }
+    return x;
+}
+__device__ __forceinline__ long lane_of(long x, int l) {
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)x, l), hi = (unsigned)__builtin_amdgcn_readlane((int)(x >> 32), l);
+    return (long)((unsigned long long)hi << 32 | lo);
+}
+
+// Keys of a share: all of the call's over the shares, rounded up; four tiles at least.
+template <int KT> __device__ __forceinline__ long attn_each(long total) { return max(4L * KT, (total + ATTN_SHARES - 1) / ATTN_SHARES); }
+
+// What a workgroup works on at a time: key tiles j .. end of the nkt of row tile t.
+struct Run {
+    int b, h, t, j, end, nkt;
+    Seq s;
+};
+
+// A share: a run of the keys of all row tiles (sequence by sequence, head by head), from
+// which follow whole key tiles: those that begin in it.
+template <int KT> struct Share {
+    Run r;
+    long left;   // keys of the share behind r
+    int x;       // first key of row tile r.t behind r
+    // the next run that has a key tile; false: none
+    __device__ __forceinline__ bool next(const AttnArgs &a, int per) {
+        for (;;) {
+            if (left <= 0) return false;
+            const AttnTiles tl(per, r.s);
+            const int keys = r.t < tl.count() ? tl.keys(r.t) : 0;
+            if (x < keys) {
+                const int n = (int)min(left, (long)(keys - x));
+                r.nkt = (keys + KT - 1) / KT;
+                r.j = (x + KT - 1) / KT;
+                r.end = (x + n + KT - 1) / KT;
+                x += n;
+                left -= n;
+                if (r.j < r.end) {
+                    r.t = uniform(r.t);
+                    r.j = uniform(r.j);
+                    r.end = uniform(r.end);
+                    r.nkt = uniform(r.nkt);
+                    return true;
+                }
+            } else {
+                x = 0;
+                if (r.t + 1 < tl.count()) {
+                    ++r.t;
+                } else if (r.h + 1 < a.Hk && tl.all() > 0) {
+                    ++r.h;
+                    r.t = tl.first();
+                } else {
+                    if (r.b + 1 >= a.B) return false;
+                    r.s = seq_of(a, ++r.b);
+                    r.h = 0;
+                    r.t = AttnTiles(per, r.s).first();
+                }
+            }
+        }
+    }
+};
+
+// The share's begin; false: it has none.  Every wave adds up all sequences on its own; the
+// first share leaves the keys before each for the join.
+template <int KT> __device__ __forceinline__ bool share_begin(const AttnArgs &a, int per, int share, Share<KT> &sh)
+{
+    const int lane = threadIdx.x & 63;
+    long *prefix = (long *)a.ws;
+    auto of = [&](int b) { return b < a.B ? a.Hk * AttnTiles(per, seq_lane(a, b)).all() : 0L; };
+    long total = 0;
+    for (int b = 0; b < a.B; b += 64) {
+        const long mine = of(b + lane), incl = scan_lanes64(mine);
+        if (share == 0 && b + lane < a.B) prefix[b + lane] = total + incl - mine;
+        total += lane_of(incl, 63);
+    }
+    if (share == 0 && lane == 0) prefix[a.B] = total;
+    const long each = attn_each<KT>(total), g0 = share * each;
+    if (g0 >= total) return false;
+    long at = 0;
+    sh.r.b = 0;
+    for (int b = 0; b < a.B; b += 64) {
+        const long mine = of(b + lane), incl = scan_lanes64(mine), sum = lane_of(incl, 63);
+        if (g0 < at + sum) {
+            const int l = (int)__builtin_ctzll(__ballot(g0 < at + incl));
+            sh.r.b = b + l;
+            at += lane_of(incl - mine, l);
+            break;
+        }
+        at += sum;
+    }
+    sh.r.s = seq_of(a, sh.r.b);
+    const AttnTiles tl(per, sh.r.s);
+    const long one = tl.all(), r = g0 - at;
+    sh.r.h = __builtin_amdgcn_readfirstlane((int)(r / one));
+    const long x = r - sh.r.h * one;
+    // the row tile: before(t) <= x < before(t + 1)
+    int lo = tl.first(), hi = tl.count();
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tl.before(mid) <= x) lo = mid;
+        else hi = mid;
+    }
+    sh.r.t = __builtin_amdgcn_readfirstlane(lo);
+    sh.x = __builtin_amdgcn_readfirstlane((int)(x - tl.before(lo)));
+    const long left = min(each, total - g0);
+    sh.left = lane_of(left, 0);
+    return true;
+}
+
+template <typename T, int D, int NR, bool SHARES>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
+{
+    typedef AttnFwdCfg<T, D, NR> C;
+    constexpr int KT = C::KT, RT = C::RT, NKB = D / 32, NS = KT / 16, NCB = D / 16;
+    extern __shared__ char lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    const float c = a.scale * LOG2E;
+    const int share = SHARES ? blockIdx.x % 8 * (ATTN_SHARES / 8) + blockIdx.x / 8 : 0;   // a head's on one XCD
+    Share<KT> sh;
+    Run cur;
+    bool any = true;
+    if constexpr (SHARES) {
+        if (!share_begin<KT>(a, per, share, sh) || !sh.next(a, per)) return;
+        cur = sh.r;
+    } else {
+        cur.h = blockIdx.x % a.Hk;
+        const Item it = find_last(a.B, blockIdx.x / a.Hk, [&](int b) { return AttnTiles(per, seq_lane(a, b)).count(); });
+        if (it.b < 0) return;
+        cur.b = it.b;
+        cur.t = uniform(it.i);
+        cur.s = seq_of(a, it.b);
+        cur.j = 0;
+        cur.nkt = cur.end = uniform((AttnTiles(per, cur.s).keys(cur.t) + KT - 1) / KT);
+        any = cur.end > 0;
+    }
+    auto load = [&](const Run &r, int j, int buffer) {
+        char *buf = lds + buffer * C::BUF;
+        const T *k = (const T *)a.k + r.s.k0 * a.ks + r.h * D, *v = (const T *)a.v + r.s.k0 * a.vs + r.h * D;
+        load_tile<C::CPR, KT>(buf, (const char *)k, a.ks * C::ES, j * KT, r.s.lk);
+        load_tile<C::CPR, KT>(buf + C::OFF_V, (const char *)v, a.vs * C::ES, j * KT, r.s.lk);
+    };
+    const int kb0 = row_base<T, C::CPR>(r16), vb = col_base<T, C::CPR>(4 * gq);
+    if (any) load(cur, cur.j, 0);
+    int buffer = 0;
+    bool more = false;
+    for (;;) {   // one row tile, or what the share has of it
+        const int off = cur.s.lk - cur.s.lq, lr0 = wave * 16 * NR;   // first row of the wave
+        const int nlive = min(per, cur.s.lq - cur.t * per) * a.G;    // rows of the tile
+        int pos[NR];   // position of this lane's rows; -1: the row sees nothing, or is none
+        int tok[NR], head[NR];
+        Frag<T> qf[NR][NKB];
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+            const int lr = lr0 + 16 * g + r16, i = quotient(lr, a.g_mul, a.g_shift);
+            tok[g] = cur.t * per + i;
+            head[g] = cur.h * a.G + lr - i * a.G;
+            const bool live = lr < nlive && off + tok[g] >= 0;
+            pos[g] = live ? off + tok[g] : -1;
+            const T *q = (const T *)a.q + (cur.s.q0 + (long)tok[g]) * a.qs + head[g] * D;
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) qf[g][kb] = live ? load_frag<T>(q + 32 * kb + 8 * gq) : zero_frag<T>();
+        }
+        f32x4 acc[NCB][NR];
+        float m[NR], l[NR];
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+            m[g] = -INFINITY;
+            l[g] = 0.f;
+#pragma unroll
+            for (int cb = 0; cb < NCB; ++cb) acc[cb][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        // keys that some, that all of the wave's rows see
+        const int wend = min(lr0 + 16 * NR, nlive) - 1;
+        const int wlast = wend < lr0 ? 0 : off + cur.t * per + quotient(max(wend, 0), a.g_mul, a.g_shift) + 1;
+        const int wfull = off + cur.t * per + quotient(lr0, a.g_mul, a.g_shift) + 1;
+        for (int j = cur.j; j < cur.end; ++j) {
+            const char *kt = lds + buffer * C::BUF, *vt = kt + C::OFF_V;
+            const int k0 = j * KT;
+            wait_vm<0>();
+            lds_barrier();
+            buffer ^= 1;
+            if (j + 1 < cur.end) {
+                load(cur, j + 1, buffer);
+            } else if (SHARES) {
+                more = sh.next(a, per);
+                if (more) load(sh.r, sh.r.j, buffer);
+            }
+            if (k0 >= wlast) continue;   // nothing for this wave in the tile
+            f32x4 s[NS][NR];
+#pragma unroll
+            for (int t = 0; t < NS; ++t) {
+#pragma unroll
+                for (int g = 0; g < NR; ++g) s[t][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) {
+                    const Frag<T> kf = row_frag<T>(kt + 16 * t * C::CPR * 16, kb0, kb);
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) s[t][g] = mma(s[t][g], kf, qf[g][kb]);
+                }
+            }
+            if (sizeof(T) == 2) pipeline<4, NS * NKB, NS * NKB * NR, 1, NR>();
+            if (k0 + KT > wfull) {   // the tile reaches past some row's last key
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                    for (int g = 0; g < NR; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (k0 + 16 * t + 4 * gq + e > pos[g]) s[t][g][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][g][e]);
+                mx = rows_max(mx);
+                const bool up = (mx - m[g]) * c > RAISE;   // false while both are -inf
+                if (__any(up)) {
+                    const float mn = up ? mx : m[g];
+                    const float al = up ? exp2_hw((m[g] - mn) * c) : 1.f;
+                    m[g] = mn;
+                    l[g] *= al;
+#pragma unroll
+                    for (int cb = 0; cb < NCB; ++cb) acc[cb][g] *= al;
+                }
+                const float mb = m[g] == -INFINITY ? 0.f : m[g] * c;
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = exp2_hw(__builtin_fmaf(s[t][g][e], c, -mb));
+                        s[t][g][e] = p;
+                        l[g] += p;
+                    }
+            }
+            // weights rounded to the storage type for the matrix cores (half a step each,
+            // as the output itself); their sum is the unrounded one
+#pragma unroll
+            for (int t = 0; t < NS; t += 2) {
+                Frag<T> pf[NR];
+#pragma unroll
+                for (int g = 0; g < NR; ++g) pf[g] = reg_frag<T>(s[t][g], s[t + 1][g]);
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb) {
+                    const Frag<T> vf = col_frag<T, C::CPR>(vt + 16 * t * C::CPR * 16, vb, cb);
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) acc[cb][g] = mma(acc[cb][g], vf, pf[g]);
+                }
+            }
+            if (sizeof(T) == 2) pipeline<4, NS * NCB, NS / 2 * NCB * NR, 2, NR>();
+        }
+        const bool whole = !SHARES || (cur.j == 0 && cur.end == cur.nkt);
+        const AttnFwdWs lay(a.B, RT, D);
+        const long slot = (share * 2 + (cur.j == 0)) * (long)RT;
+        float *po = (float *)((char *)a.ws + lay.o) + slot * D, *pl = (float *)((char *)a.ws + lay.lse) + slot;
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+            const int lr = lr0 + 16 * g + r16;
+            const float ls = rows_sum(l[g]);
+            // of part of the keys a row may see none: its sum is 0 (and a NaN where scores are)
+            const bool seen = pos[g] >= 0 && (!SHARES || ls != 0.f);
+            const float inv = seen ? 1.f / ls : 0.f, lg = seen ? m[g] * c + __builtin_amdgcn_logf(ls) : -INFINITY;
+            if (lr >= nlive) continue;
+            if (whole) {
+                const long row = (cur.s.q0 + (long)tok[g]) * (a.Hk * a.G) + head[g];
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb)
+                    store4((T *)a.o + row * D + 16 * cb + 4 * gq, seen ? acc[cb][g] * inv : f32x4{0.f, 0.f, 0.f, 0.f});
+                if (gq == 0 && a.lse) a.lse[row] = lg * LN2;
+            } else {
+                if (seen) {
+#pragma unroll
+                    for (int cb = 0; cb < NCB; ++cb) store4(po + lr * D + 16 * cb + 4 * gq, acc[cb][g] * inv);
+                }
+                if (gq == 0) pl[lr] = lg;
+            }
+        }
+        if (!SHARES || !more) break;
+        cur = sh.r;
+    }
+}
+
+// Joins the rows that several shares worked on and writes those that see no key; D / 4
+// lanes a row.
+template <typename T, int D, int NR> __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int per)
+{
+    typedef AttnFwdCfg<T, D, NR> C;
+    constexpr int LPR = D / 4, KT = C::KT;
+    const int Hq = a.Hk * a.G, at = threadIdx.x % LPR * 4;
+    const long row = (long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    if (row >= (long)a.Tq * Hq) return;
+    const int token = (int)(row / Hq), head = (int)(row - (long)token * Hq);
+    const int b = seq_at(a.cu_q, a.B, a.Tq, token);
+    const Seq s = seq_lane(a, b);
+    const int i = token - s.q0;
+    if (i < 0 || i >= s.lq) return;   // of no sequence
+    const AttnTiles tl(per, s);
+    const int t = i / per, lr = (i - t * per) * a.G + head % a.G, keys = tl.keys(t);
+    int wf = 0, wl = -1;
+    if (keys > 0) {
+        const long *prefix = (const long *)a.ws;
+        const long each = attn_each<KT>(prefix[a.B]), c0 = prefix[b] + head / a.G * tl.all() + tl.before(t);
+        wf = (int)(c0 / each);
+        wl = (int)((c0 + keys - 1) / each);
+        // the last share has no key tile if none begins in it
+        if (wl > wf && (wl * each - c0 + KT - 1) / KT >= (keys + KT - 1) / KT) --wl;
+    }
+    if (wf == wl) return;   // written by its one workgroup
+    const AttnFwdWs lay(a.B, C::RT, D);
+    const float *po = (const float *)((const char *)a.ws + lay.o), *pl = (const float *)((const char *)a.ws + lay.lse);
+    auto place = [&](int w) { return (w * 2 + (w == wf)) * (long)C::RT + lr; };   // of share wf its last part
+    float top = -INFINITY, ls = 0.f;
+    for (int w = wf; w <= wl; ++w) top = fmaxf(top, pl[place(w)]);
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int w = wf; w <= wl; ++w) {
+        const float lg = pl[place(w)];
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(po + place(w) * D + at);
+        const float f = exp2_hw(lg - top);
+        if (lg == -INFINITY) continue;   // v was never written
+        ls += f;
+        sum += f * v;
+    }
+    store4((T *)a.o + row * D + at, ls != 0.f ? sum * (1.f / ls) : sum);
+    if (a.lse && at == 0) a.lse[row] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+}
+
+template <typename T, int D, int NR> static hipError_t fwd_enqueue(const AttnArgs &a, const AttnFwdPlan &plan, hipStream_t st)
+{
+    typedef AttnFwdCfg<T, D, NR> C;
+    auto k = plan.shares ? attn_fwd_kernel<T, D, NR, true> : attn_fwd_kernel<T, D, NR, false>;
+    static_assert(2 * C::BUF <= 64 * 1024, "more dynamic LDS has to be asked for");
+    hipLaunchKernelGGL(k, dim3((unsigned)(plan.shares ? plan.shares : plan.tiles * a.Hk)), dim3(256), 2 * C::BUF, st, a, plan.tokens);
+    if (plan.shares) {
+        const long rows = (long)a.Tq * a.Hk * a.G, each = 256 / (D / 4);
+        hipLaunchKernelGGL((attn_fwd_join_kernel<T, D, NR>), dim3((unsigned)((rows + each - 1) / each)), dim3(256), 0, st, a, plan.tokens);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int D> static hipError_t fwd_launch(AttnArgs a, hipStream_t st)
+{
+    const AttnFwdPlan plan = attn_fwd_plan(sizeof(T) == 2, a.B, a.Tq, a.Tk, a.Hk, a.G);
+    divisor(a.G, a.g_mul, a.g_shift);
+    if constexpr (sizeof(T) == 2) {
+        if (plan.nr == 2) return fwd_enqueue<T, D, 2>(a, plan, st);
+    }
+    return fwd_enqueue<T, D, 1>(a, plan, st);
+}
+
+hipError_t attn_fwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st)
+{
+    if (bf16) return D == 128 ? fwd_launch<__bf16, 128>(a, st) : fwd_launch<__bf16, 64>(a, st);
+    return D == 128 ? fwd_launch<float, 128>(a, st) : fwd_launch<float, 64>(a, st);
+}
+
+unsigned long long attn_fwd_workspace(bool bf16, int B, int Tq, int Tk, int Hk, int G, int D)
+{
+    const AttnFwdPlan plan = attn_fwd_plan(bf16, B, Tq, Tk, Hk, G);
+    return plan.shares ? (unsigned long long)AttnFwdWs(B, 64 * plan.nr, D).bytes : 0;
+}
+
+} // namespace gdn

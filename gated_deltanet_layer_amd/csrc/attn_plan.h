@@ -1,0 +1,76 @@
+// attn_plan.h -- how calls of the grouped-attention kernels are cut over workgroups.
+// Rules on sizes and type alone, without a HIP header: launchers, kernels and host
+// programs read the same ones.  What depends on the sequences' lengths, which only the
+// device knows, is worked out there.
+#pragma once
+
+namespace gdn {
+
+// --- packed forward -------------------------------------------------------------
+
+// The G query heads that share a key head stand side by side in a row tile: row r of a
+// tile is token r / G of it, head r % G, and a tile has as many whole tokens as fit.
+constexpr int ATTN_SHARES = 512;   // two workgroups a compute unit
+struct AttnFwdPlan {
+    int nr;        // 16-row groups a wave: a row tile has 64 nr rows
+    int tokens;    // of a row tile
+    int shares;    // 0: a workgroup for every row tile
+    long tiles;    // row tiles of one key head, at most
+};
+
+inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G)
+{
+    AttnFwdPlan p;
+    const long wide = (long)Tq * G / 128 * Hk;
+    p.nr = bf16 && wide >= 256 ? 2 : 1;
+    p.tokens = 64 * p.nr / G;
+    p.tiles = Tq / p.tokens + (B < Tq ? B : Tq);
+    // key tiles that the call has if it is one sequence: the most that it may have
+    const int kt = bf16 ? 64 : 32;
+    const long wgs = ((Tq + p.tokens - 1) / p.tokens) * (long)Hk, keys = Tk - Tq / 2 > 0 ? Tk - Tq / 2 : Tk / 2;
+    p.shares = wgs > 0 && wgs < ATTN_SHARES && wgs * (keys / kt) >= 8 * ATTN_SHARES ? ATTN_SHARES : 0;
+    return p;
+}
+
+// --- packed backward ------------------------------------------------------------
+
+// Rows (of queries, or keys) that a workgroup owns, and that walk by in a tile.
+constexpr int attn_own(bool bf16) { return bf16 ? 128 : 64; }
+constexpr int attn_walk(bool bf16) { return bf16 ? 64 : 32; }
+
+struct AttnBwdPlan {
+    int tokens;          // of a query tile, which has 128 (64) rows
+    int kp, qp;          // pieces of the walked keys (dq), of the walked query rows (dk, dv)
+    int kstep, qstep;    // walked rows of a piece
+    long qtiles, ktiles; // owners of one key head, at most
+};
+
+// Pieces of `tiles` walked tiles, `least` tiles each or more, to give `fill` workgroups.
+inline int attn_pieces(long wgs, long fill, long tiles, int least)
+{
+    if (wgs <= 0 || wgs >= fill || tiles < 2 * least) return 1;
+    long n = (fill + wgs - 1) / wgs;
+    const long most = n > 32 ? 32 : 16;
+    if (n > tiles / least) n = tiles / least;
+    return (int)(n > most ? most : n);
+}
+
+// The walk of one sequence that has all rows is the longest that a call may have.
+inline AttnBwdPlan attn_bwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G)
+{
+    AttnBwdPlan p;
+    const int own = attn_own(bf16), st = attn_walk(bf16), least = bf16 ? 2 : 1;
+    const long rows = (long)Tq * G, nk = (Tk + st - 1) / st, nq = (rows + st - 1) / st;
+    p.tokens = own / G;
+    p.qtiles = Tq / p.tokens + (B < Tq ? B : Tq);
+    p.ktiles = Tk / own + (B < Tk ? B : Tk);
+    const int kp = attn_pieces(Hk * ((long)(Tq + p.tokens - 1) / p.tokens), 512, nk, least);
+    const int qp = attn_pieces(Hk * ((long)(Tk + own - 1) / own), 256, nq, least);
+    p.kstep = (int)((nk + kp - 1) / kp * st);
+    p.qstep = (int)((nq + qp - 1) / qp * st);
+    p.kp = kp > 1 ? (Tk + p.kstep - 1) / p.kstep : 1;
+    p.qp = qp > 1 ? (int)((rows + p.qstep - 1) / p.qstep) : 1;
+    return p;
+}
+
+} // namespace gdn

@@ -1,7 +1,7 @@
 /*
  * gdn.h -- C ABI of the MI355X (gfx950) Gated DeltaNet mixer: prologue, forward,
- * decode, verify and backward; and of the latent attention that a hybrid stack puts
- * between such layers (gdn_latent_*).
+ * decode, verify and backward; and of the attention that a hybrid stack puts between
+ * such layers: latent (gdn_latent_*) or with grouped heads (gdn_attn_*).
  *
  * The operation (Atomic-GDN2 model card, section 2.1 "Gated DeltaNet-2"), for
  * every batch row b and head h independently, token by token:
@@ -494,6 +494,148 @@ GDN_API gdn_status gdn_latent_steps(const void *q, const void *draft, const long
                                     void *o, float *lse, void *workspace, size_t workspace_bytes,
                                     int N, int M, int H, int r, int dr, int pages, int page, int width,
                                     float scale, gdn_dtype dtype, void *stream);
+
+/*
+ * Grouped attention: the softmax attention layer of a hybrid whose attention has ordinary
+ * keys and values ("Hybrid layouts": three DeltaNet layers, one attention layer), Hq query
+ * heads over Hk heads of keys and values; query head h belongs to key head h / (Hq / Hk).
+ * Its modes are the mixer's: a prologue between the projections and the attention, forward
+ * and backward over whole sequences, and one token at a time, over a paged cache in 8 bits.
+ *
+ * Storage types are those of gdn_dtype; norms, angles' cosines, scores, softmax statistics,
+ * sums and lse are fp32; for GDN_BF16 the softmax weights are rounded to bf16 for the matrix
+ * cores.  Tokens of all sequences stand packed one behind the other, [tokens, heads, D].
+ * q_stride and the like are the elements from one token to the next, at least heads * D and a
+ * multiple of 16 bytes (GDN_EINVAL), at most 2^22 (GDN_ENOTSUP): q, k and v may be slices of
+ * one projection's output, and gradients of one gradient.  Other tensors are contiguous.
+ * Pointers need 16-byte alignment, those of int and of float other than the norm weights
+ * 4 bytes, a workspace 256; a workspace's contents on entry do not matter, on return they are
+ * unspecified, and calls that share one must not run concurrently.  Outputs and the workspace
+ * overlap neither inputs nor each other (slices of one tensor with equal strides do not).
+ * D: 64 or 128, Hq / Hk: at most 64 (GDN_ENOTSUP otherwise).  scale: > 0, with scale / ln 2
+ * finite.  Results are the same on every call with the same arguments.  NOT checked: live
+ * inputs are finite; offsets rise within the tensor (others give unspecified results, within
+ * the outputs).
+ *
+ * The prologue: RMS norm of every query and key head and the rotation by its position.
+ *
+ *   x' = w x / sqrt(mean x^2 + eps)                              (over the D channels of a head)
+ *   y_i = x'_i cos a_i - x'_{i+R/2} sin a_i,  y_{i+R/2} = x'_{i+R/2} cos a_i + x'_i sin a_i,
+ *   a_i = pos inv_freq_i  (i < R/2);  y_c = x'_c from channel R on
+ *
+ *   q_raw [T, Hq, D], k_raw [T, Hk, D] dtype (strided);  w_q, w_k [D] fp32
+ *   inv_freq [R / 2] fp32, pos [T] int32 (any value: the angle is taken in 64 bits)
+ *   q [T, Hq, D], k [T, Hk, D] dtype
+ *
+ * R: a multiple of 16 (GDN_ENOTSUP otherwise), 0 .. D; 0: no rotation (pos and inv_freq may
+ * be NULL).  Hq or Hk may be 0 here.  eps: >= 0 (a head of zeros with eps = 0 gives NaN).
+ */
+GDN_API gdn_status gdn_attn_prologue(const void *q_raw, const void *k_raw, const float *w_q, const float *w_k,
+                                     const float *inv_freq, const int *pos, void *q, void *k, int T, int Hq, int Hk,
+                                     int D, int R, long long q_stride, long long k_stride, float eps,
+                                     gdn_dtype dtype, void *stream);
+
+/*
+ * Gradients of gdn_attn_prologue: d_q [T, Hq, D] and d_k [T, Hk, D] dtype in; writes dq_raw
+ * and dk_raw (strided) and dw_q, dw_k [D] fp32, the sums over tokens and heads.
+ */
+GDN_API gdn_status gdn_attn_prologue_bwd_workspace_size(int T, int Hq, int Hk, int D, int R, gdn_dtype dtype,
+                                                        size_t *bytes);
+GDN_API gdn_status gdn_attn_prologue_bwd(const void *q_raw, const void *k_raw, const float *w_q, const float *w_k,
+                                         const float *inv_freq, const int *pos, const void *d_q, const void *d_k,
+                                         void *dq_raw, void *dk_raw, float *dw_q, float *dw_k, void *workspace,
+                                         size_t workspace_bytes, int T, int Hq, int Hk, int D, int R,
+                                         long long q_stride, long long k_stride, long long dq_stride,
+                                         long long dk_stride, float eps, gdn_dtype dtype, void *stream);
+
+/*
+ * Causal forward over B packed sequences.
+ *
+ *   q [Tq, Hq, D], k, v [Tk, Hk, D] dtype (strided)
+ *   cu_q [B + 1] int32: sequence b has the query rows cu_q[b] .. cu_q[b + 1] - 1
+ *   cu_k [B + 1] int32: and the keys cu_k[b] .. cu_k[b + 1] - 1; NULL: as cu_q (Tk = Tq)
+ *   o [Tq, Hq, D] dtype, lse [Tq, Hq] fp32 or NULL
+ *
+ * Row i of a sequence of lq rows and lk keys has position p = lk - lq + i and sees the keys
+ * j <= p: a whole prompt (lq = lk), or the last rows of a longer sequence.  A row that sees
+ * none (p < 0) gives o = 0, lse = -inf.  Rows of no sequence are left as they were.  Any
+ * length may be 0.  GDN_ENOTSUP from Hq > 2^15, Tq Hq or Tk Hk >= 2^28, B >= 2^24, (Tq + Tk)
+ * Hq / Hk >= 2^30 and 2^24 row tiles on.  Long rows of few heads are split over the keys; the pieces stand in the
+ * workspace (at least gdn_attn_fwd_workspace_size bytes; NULL when that is 0).
+ */
+GDN_API gdn_status gdn_attn_fwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int D, gdn_dtype dtype,
+                                               size_t *bytes);
+GDN_API gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,
+                                void *o, float *lse, void *workspace, size_t workspace_bytes, int B, int Tq, int Tk,
+                                int Hq, int Hk, int D, long long q_stride, long long k_stride, long long v_stride,
+                                float scale, gdn_dtype dtype, void *stream);
+
+/*
+ * Gradients of gdn_attn_fwd.  q .. lse as given to and written by the forward (lse is
+ * required), d_o [Tq, Hq, D] dtype; writes dq, dk and dv (strided; dk and dv are the sums over
+ * the query heads that share them).  Gradients of rows that see nothing and of keys that no
+ * row sees are 0; rows of no sequence are left as they were.  No atomics.
+ *
+ * For GDN_BF16, P is rounded to bf16 for dv and dS for dq and dk, the P in dk's dS to fp16 of
+ * 4096 P, and D = d_o . o is of o as stored, whose rounding reaches the gradients of a row
+ * with nearly all weight on one key undiminished; tiles of query rows that see at most 128
+ * keys have D from P and dP instead.  GDN_F32 rounds nothing to fewer bits.
+ */
+GDN_API gdn_status gdn_attn_bwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int D, gdn_dtype dtype,
+                                               size_t *bytes);
+GDN_API gdn_status gdn_attn_bwd(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,
+                                const void *o, const float *lse, const void *d_o, void *dq, void *dk, void *dv,
+                                void *workspace, size_t workspace_bytes, int B, int Tq, int Tk, int Hq, int Hk, int D,
+                                long long q_stride, long long k_stride, long long v_stride, long long dq_stride,
+                                long long dk_stride, long long dv_stride, float scale, gdn_dtype dtype, void *stream);
+
+/*
+ * New tokens into a paged cache of 8-bit keys and values.
+ *
+ *   k_cache [pages, Hk, page, D]          e4m3 (OCP, finite only), one byte each
+ *   v_cache [pages, Hk, page / 16, D, 16] e4m3: the 16 tokens of a block stand together
+ *   k_scale, v_scale [pages, Hk, page / 16] fp32: a value is its byte's times its block's scale
+ *   table [N, width] int32   token t of sequence n is slot t % page of page table[n, t / page]
+ *   lens [N] int32           tokens of each sequence, the new ones among them
+ *   k, v [T, Hk, D] dtype (strided): the new tokens, those of sequence n in rows cu[n] ..
+ *                            cu[n + 1] - 1, for its last positions
+ *   cu [N + 1] int32, or NULL: one token each (T = N)
+ *
+ * A block's scale is the smallest power of two, 2^-126 or more, that takes the largest
+ * magnitude in it to 448 or less; values are rounded to nearest, ties to even.  Where a new
+ * token joins older ones, the scale is the larger of theirs and its own; if it grows, the
+ * older values move to it, exactly but for those that fall below e4m3's smallest normal (2^-6
+ * of the scale).  A value that is not finite is stored as NaN and does not count for the
+ * scale.  Other slots keep their bytes.  Tokens at positions below 0 or from width * page on,
+ * and tokens whose table entry is outside 0 .. pages - 1, are not stored.  Two sequences must
+ * not append to the same block (results are unspecified, within the cache).
+ *
+ * page: a multiple of 16 (GDN_ENOTSUP otherwise, from page 2^19, pages * page / 16 * Hk or N *
+ * width past 31 bits, width * page > 2^30, N >= 2^22 and T / 16 + 2 N >= 2^24 on).
+ */
+GDN_API gdn_status gdn_attn_append(const void *k, const void *v, const int *cu, void *k_cache, void *v_cache,
+                                   float *k_scale, float *v_scale, const int *table, const int *lens, int N, int T,
+                                   int Hk, int D, int pages, int page, int width, long long k_stride,
+                                   long long v_stride, gdn_dtype dtype, void *stream);
+
+/*
+ * One token of N sequences over such a cache.
+ *
+ *   q [N, Hq, D] dtype, o [N, Hq, D] dtype, lse [N, Hq] fp32 or NULL
+ *   the cache, table and lens as above (lens clamped to 0 .. width * page); scales may be any
+ *   positive numbers
+ *
+ * Every head sees all lens[n] tokens.  A table entry outside 0 .. pages - 1 holds no tokens;
+ * entries behind a sequence's last page are not read, and slots and scales behind its last
+ * token may hold anything.  A sequence with no token gives o = 0, lse = -inf.  For GDN_BF16
+ * the softmax weights, times the values' scale, are rounded to bf16 for the matrix cores;
+ * GDN_F32 rounds nothing to fewer bits.  GDN_ENOTSUP also from N * Hq >= 2^24 on.
+ */
+GDN_API gdn_status gdn_attn_step_workspace_size(int N, int Hq, int Hk, int D, int page, int width, size_t *bytes);
+GDN_API gdn_status gdn_attn_step(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                 const float *v_scale, const int *table, const int *lens, void *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, int N, int Hq, int Hk, int D, int pages,
+                                 int page, int width, float scale, gdn_dtype dtype, void *stream);
 
 /* Static English text for a status code (never NULL). */
 GDN_API const char *gdn_status_str(gdn_status s);
