@@ -188,7 +188,7 @@ struct AttnTiles {
     __device__ __forceinline__ AttnTiles(int per, const Seq &s) : per(per), off(s.lk - s.lq), lq(s.lq), lk(s.lk) {}
     __device__ __forceinline__ int count() const { return (lq + per - 1) / per; }
     // keys that the last row of tile t sees
-    __device__ __forceinline__ int keys(int t) const { return max(0, off + min((t + 1) * per, lq)); }
+    __device__ __forceinline__ int size(int t) const { return max(0, off + min((t + 1) * per, lq)); }
     __device__ __forceinline__ int first() const { return off < 0 ? min(-off / per, count()) : 0; }   // tile that sees any
     // keys of the row tiles before t (a tile with keys, or count())
     __device__ __forceinline__ long before(int t) const {
@@ -198,7 +198,7 @@ struct AttnTiles {
     }
     __device__ __forceinline__ long all() const {
         const int n = count();
-        return n > first() ? before(n - 1) + keys(n - 1) : 0;
+        return n > first() ? before(n - 1) + size(n - 1) : 0;
     }
 };
 
@@ -219,6 +219,126 @@ template <int CPR, int ROWS> __device__ __forceinline__ void load_tile(char *til
 {
     const char *p = uniform(x + r0 * stride);
     load_rows<CPR, ROWS>(tile, p, stride, 0, uniform(n - r0));
+}
+
+// Shares: calls of few owners (row tiles, key tiles) with long walks are cut over a fixed
+// number of workgroups, each of which takes an equal run of all that the owners walk by
+// (sequence by sequence, head by head, owner by owner), in units of keys or rows.  From that
+// follow whole tiles of UT units: those that begin in the run.  `make(seq)` gives a sequence's
+// owners of one key head: count(), first() with any work, size(i), before(i), all().
+struct Run {   // what a workgroup works on at a time: tiles j .. end of the n of owner t
+    int b, h, t, j, end, n;
+    Seq s;
+};
+struct Share {
+    Run r;
+    long left;   // units of the share behind r
+    int x;       // first unit of owner r.t behind r
+};
+__device__ __forceinline__ long scan_lanes(long x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const long v = __shfl_up(x, d, 64);
+        if ((int)(threadIdx.x & 63) >= d) x += v;
+    }
+    return x;
+}
+__device__ __forceinline__ long lane_of(long x, int l) {
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)x, l), hi = (unsigned)__builtin_amdgcn_readlane((int)(x >> 32), l);
+    return (long)((unsigned long long)hi << 32 | lo);
+}
+
+// Units of a share: all of the call's over the shares, rounded up; `least` tiles or more.
+template <int UT> __device__ __forceinline__ long share_each(long total, int shares, int least) {
+    return max((long)least * UT, (total + shares - 1) / shares);
+}
+
+// The next run that has a tile; false: none.
+template <int UT, typename M> __device__ __forceinline__ bool share_next(const AttnArgs &a, M make, Share &sh)
+{
+    Run &r = sh.r;
+    for (;;) {
+        if (sh.left <= 0) return false;
+        const auto owners = make(r.s);
+        const int size = r.t < owners.count() ? owners.size(r.t) : 0;
+        if (sh.x < size) {
+            const int n = (int)min(sh.left, (long)(size - sh.x));
+            r.n = uniform((size + UT - 1) / UT);
+            r.j = uniform((sh.x + UT - 1) / UT);
+            r.end = uniform((sh.x + n + UT - 1) / UT);
+            sh.x += n;
+            sh.left -= n;
+            if (r.j < r.end) {
+                r.t = uniform(r.t);
+                return true;
+            }
+        } else {
+            sh.x = 0;
+            if (r.t + 1 < owners.count()) {
+                ++r.t;
+            } else if (r.h + 1 < a.Hk && owners.all() > 0) {
+                ++r.h;
+                r.t = owners.first();
+            } else {
+                if (r.b + 1 >= a.B) return false;
+                r.s = seq_of(a, ++r.b);
+                r.h = 0;
+                r.t = make(r.s).first();
+            }
+        }
+    }
+}
+
+// A share's begin; false: it has none.  Every wave adds up all sequences on its own; the
+// first share leaves the units before each, and all of them, in prefix[B + 1] for the join.
+template <int UT, typename M> __device__ __forceinline__ bool share_begin(const AttnArgs &a, M make, int share, int shares, int least, long *prefix, Share &sh)
+{
+    const int lane = threadIdx.x & 63;
+    auto of = [&](int b) { return b < a.B ? a.Hk * make(seq_lane(a, b)).all() : 0L; };
+    long total = 0;
+    for (int b = 0; b < a.B; b += 64) {
+        const long mine = of(b + lane), incl = scan_lanes(mine);
+        if (share == 0 && b + lane < a.B) prefix[b + lane] = total + incl - mine;
+        total += lane_of(incl, 63);
+    }
+    if (share == 0 && lane == 0) prefix[a.B] = total;
+    const long each = share_each<UT>(total, shares, least), g0 = share * each;
+    if (g0 >= total) return false;
+    long at = 0;
+    sh.r.b = 0;
+    for (int b = 0; b < a.B; b += 64) {
+        const long mine = of(b + lane), incl = scan_lanes(mine), sum = lane_of(incl, 63);
+        if (g0 < at + sum) {
+            const int l = (int)__builtin_ctzll(__ballot(g0 < at + incl));
+            sh.r.b = b + l;
+            at += lane_of(incl - mine, l);
+            break;
+        }
+        at += sum;
+    }
+    sh.r.s = seq_of(a, sh.r.b);
+    const auto owners = make(sh.r.s);
+    const long one = owners.all(), r = g0 - at;
+    sh.r.h = uniform((int)(r / one));
+    const long x = r - sh.r.h * one;
+    int lo = owners.first(), hi = owners.count();   // the owner: before(t) <= x < before(t + 1)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (owners.before(mid) <= x) lo = mid;
+        else hi = mid;
+    }
+    sh.r.t = uniform(lo);
+    sh.x = uniform((int)(x - owners.before(lo)));
+    sh.left = lane_of(min(each, total - g0), 0);
+    return true;
+}
+
+// The shares that worked on an owner of `size` units, the first of them unit c0 of the call:
+// the first, and the last that a tile begins in.
+template <int UT> __device__ __forceinline__ void share_range(long c0, int size, long each, int &first, int &last) {
+    first = (int)(c0 / each);
+    last = (int)((c0 + size - 1) / each);
+    if (last > first && (last * each - c0 + UT - 1) / UT >= (size + UT - 1) / UT) --last;
 }
 
 // The sequence of a packed query (or key) row: the last one that begins at or before it,

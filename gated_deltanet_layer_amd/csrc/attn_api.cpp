@@ -76,7 +76,7 @@ gdn_status attn_sizes(int B, int Tq, int Tk, int Hq, int Hk, int D, gdn_dtype dt
     if (B >= (1 << 24)) return GDN_ENOTSUP;
     const gdn::AttnFwdPlan f = gdn::attn_fwd_plan(bf16, B, Tq, Tk, Hk, G);
     const gdn::AttnBwdPlan b = gdn::attn_bwd_plan(bf16, B, Tq, Tk, Hk, G);
-    if (f.tiles * Hk >= (1LL << 24) || b.qtiles * Hk * b.kp >= (1LL << 24) || b.ktiles * Hk * b.qp >= (1LL << 23)) return GDN_ENOTSUP;
+    if (f.tiles * Hk >= (1LL << 24) || b.qtiles * Hk * b.kp >= (1LL << 24)) return GDN_ENOTSUP;
     return GDN_OK;
 }
 

@@ -13,15 +13,19 @@
 
 namespace gdn {
 
-// Workspace, all float: D[Tq][Hq]; where there are pieces, dq[kp][Tq][Hq][D] and
-// dkv[qp][Tk][Hk][2 D].
+// Workspace: float D[Tq][Hq]; where dq is cut, float dq[kp][Tq][Hq][D]; long prefix[B + 1],
+// the rows that the owners of keys walk by before each sequence, then for each share of them
+// its first and last piece, float dkv[slot][2 D] (dk, then dv), slot = min(OWN, Tk) keys.
 struct AttnBwdWs {
-    long dq, dkv, bytes;
-    __host__ __device__ AttnBwdWs(const AttnBwdPlan &p, int Tq, int Tk, int Hk, int G, int d) {
-        const long qr = (long)Tq * Hk * G, kr = (long)Tk * Hk;
+    long dq, prefix, dkv, bytes;
+    int rows;
+    __host__ __device__ AttnBwdWs(const AttnBwdPlan &p, int B, int Tq, int Tk, int Hk, int G, int d, int own) {
+        const long qr = (long)Tq * Hk * G;
+        rows = Tk < own ? Tk : own;
         dq = (qr * 4 + 255) & ~255L;
-        dkv = dq + (p.kp > 1 ? p.kp * qr * d * 4 : 0);
-        bytes = dkv + (p.qp > 1 ? p.qp * kr * 2 * d * 4 : 0);
+        prefix = dq + (p.kp > 1 ? p.kp * qr * d * 4 : 0);
+        dkv = prefix + (((long)(B + 1) * 8 + 255) & ~255L);
+        bytes = dkv + 2L * p.shares * rows * 2 * d * 4;
     }
 };
 
@@ -74,15 +78,22 @@ template <typename T, int D> struct AttnBwdCfg {
     static_assert(KV_LDS <= 160 * 1024, "LDS");
 };
 
-// The rows that walk by an owner of keys from k0 on: all that see one of them.  Row r of a
-// key head: token r / G, head r % G.
-struct Walk {
-    int first, end;   // rows, first a multiple of the tile's
-    __device__ __forceinline__ Walk(const AttnArgs &a, const Seq &s, int k0, int st) {
-        first = max(0, k0 - (s.lk - s.lq)) * a.G / st * st;
-        end = k0 < s.lk ? s.lq * a.G : 0;
+// Owners of OWN keys of a sequence, and the rows that walk by: all that see one of the keys.
+// Those are the last of the sequence: row r of a key head is token r / G, head r % G.
+template <int OWN> struct KeyTiles {
+    int lq, lk, g;
+    __device__ __forceinline__ KeyTiles(const Seq &s, int g) : lq(s.lq), lk(s.lk), g(g) {}
+    __device__ __forceinline__ int count() const { return (lk + OWN - 1) / OWN; }
+    __device__ __forceinline__ int first() const { return 0; }
+    __device__ __forceinline__ int size(int i) const { return min(lq, lk - i * OWN) * g; }
+    __device__ __forceinline__ long before(int i) const {
+        const int f = lq > lk ? 0 : min(i, (lk - lq) / OWN + 1);   // owners that all rows see
+        return ((long)f * lq + (long)(i - f) * lk - OWN * ((long)i * (i - 1) - (long)f * (f - 1)) / 2) * g;
     }
+    __device__ __forceinline__ long all() const { return before(count()); }
 };
+
+constexpr int BWD_LEAST = 2;   // tiles of a share
 
 // dk and dv.  Four pairs of waves; a pair owns 16 NG keys.  The first of the pair
 // computes the scores and P and adds up dv^T (k and dv in its registers), the second
@@ -94,198 +105,200 @@ struct Walk {
 // Scores have query rows on the accumulator's rows: P and dS feed the gradient
 // products as B operands straight from the registers, and P changes hands between
 // equal lanes.
-template <typename T, int D, bool CUT>
+template <typename T, int D>
 __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwdPlan plan)
 {
     typedef AttnBwdCfg<T, D> C;
     constexpr int NG = C::NG, ST = C::ST, NKB = D / 32, NC = D / 16, OWN = C::OWN;
     constexpr int BPT = ST / 32;   // blocks a tile
     extern __shared__ char lds[];
-    const int h = blockIdx.x % a.Hk, piece = CUT ? blockIdx.x / a.Hk % plan.qp : 0;
-    auto owners = [&](int b) { return (seq_lane(a, b).lk + OWN - 1) / OWN; };
-    // the first keys are seen by most rows: the longest walks begin first
-    const Item it = find_last(a.B, blockIdx.x / a.Hk / (CUT ? plan.qp : 1), owners);
-    if (it.b < 0) return;
-    const Seq sq = seq_of(a, it.b);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
     const int pair = wave & 3, lane = threadIdx.x & 63, Hq = a.Hk * a.G;
-    const int off = sq.lk - sq.lq, n = sq.lk;
-    const int k0 = ((n + OWN - 1) / OWN - 1 - uniform(it.i)) * OWN, w0 = k0 + pair * 16 * NG;
-    const T *q = (const T *)a.q + sq.q0 * a.qs + h * a.G * D;
-    const T *d_o = (const T *)a.d_o + ((long)sq.q0 * Hq + h * a.G) * D;
-    const float *lse = a.lse + (long)sq.q0 * Hq + h * a.G, *Dw = (const float *)a.ws + (long)sq.q0 * Hq + h * a.G;
+    const bool isv = wave < 4;   // the first of the pair
+    const AttnBwdWs lay(plan, a.B, a.Tq, a.Tk, a.Hk, a.G, D, OWN);
+    // shares of one head, which walk by the same rows, on one XCD
+    const int share = blockIdx.x % 8 * (plan.shares / 8) + blockIdx.x / 8;
+    auto make = [&](const Seq &s) { return KeyTiles<OWN>(s, a.G); };
+    Share sh;
+    if (!share_begin<ST>(a, make, share, plan.shares, BWD_LEAST, (long *)((char *)a.ws + lay.prefix), sh) || !share_next<ST>(a, make, sh)) return;
     const float c = a.scale * LOG2E;
     float *stat = (float *)(lds + 3 * C::BUF);                  // [3][2][ST]: lse and D of the rows
     char *hand = lds + 3 * (C::BUF + C::ROWS) + pair * C::HAND; // [2][ST / 16 NG][64 lanes]: P of a tile, four values a lane
-
-    const Walk walk(a, sq, k0, ST);
-    const int qn = CUT ? (int)min((long)walk.end, (piece + 1L) * plan.qstep) : walk.end;
-    const int qfirst = CUT ? (int)max((long)walk.first, (long)piece * plan.qstep) : walk.first;
-    const int nt = qfirst < qn ? (qn - qfirst + ST - 1) / ST : 0;
-    auto load = [&](int j) {
-        const int r0 = qfirst + j * ST, buf = __builtin_amdgcn_readfirstlane(j % 3);
-        constexpr int RP = 512 / C::CPR;
-        static_assert(ST % RP == 0 && RP % 16 == 0, "");
-        const int row = threadIdx.x / C::CPR, ch = ((threadIdx.x % C::CPR) ^ swz<C::CPR>(row)) * 16;
-        const char *to = lds + buf * C::BUF + wave * 1024;
-#pragma unroll
-        for (int i = 0; i < ST / RP; ++i) {
-            const int r = r0 + i * RP + row, t = quotient(r, a.g_mul, a.g_shift), g = r - t * a.G;
-            const char *sq_ = r < qn ? (const char *)(q + t * a.qs + g * D) + ch : (const char *)latent_zero;
-            const char *sd = r < qn ? (const char *)(d_o + ((long)t * Hq + g) * D) + ch : (const char *)latent_zero;
-            copy16(sq_, to + i * 512 * 16);
-            copy16(sd, to + C::OFF_V + i * 512 * 16);
-        }
-        if (wave < 2 && lane < ST) {   // lse by the first wave, D by the second
-            const int r = r0 + lane, t = quotient(r, a.g_mul, a.g_shift);
-            const void *src = r >= qn ? (const void *)latent_zero : (wave ? Dw : lse) + (long)t * Hq + (r - t * a.G);
-            copy4(src, (char *)(stat + (buf * 2 + wave) * ST));
-        }
-    };
-    // before tile j: it is there, and P of tile j - 1 is whole
-    auto sync = [&](int j) {
-        if (j < nt) wait_vm<0>();
-        lds_barrier();
-        if (j + 1 < nt) load(j + 1);   // over tile j - 2
-    };
-    // first row that sees key j: its token is j - off
-    auto sees = [&](int j) { return (j - off) * a.G; };
-    auto seen = [&](int i) {   // whether a row of block i sees a key of the wave
-        return qfirst + i * 32 + 31 >= sees(w0) && w0 < n;
-    };
-    const AttnBwdWs lay(plan, a.Tq, a.Tk, a.Hk, a.G, D);
-    if (CUT && nt == 0) return;   // the last kernel knows which pieces there are
-    if (nt > 0) load(0);
-    const T *x = wave < 4 ? (const T *)a.k + sq.k0 * a.ks + h * D : (const T *)a.v + sq.k0 * a.vs + h * D;
-    const long xs = wave < 4 ? a.ks : a.vs;
-    Frag<T> xf[NG][NKB];   // k for the first of the pair, v for the second
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const int key = w0 + 16 * g + r16;
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) xf[g][kb] = key < n ? load_frag<T>(x + key * xs + 32 * kb + 8 * gq) : zero_frag<T>();
-    }
-    f32x4 acc[NC][NG];   // dv^T, dk^T
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int i = 0; i < NC; ++i) acc[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int rb = row_base<T, C::CPR>(r16), cb = col_base<T, C::CPR>(4 * gq);
+    int count = 0;   // tiles so far: which of three buffers, and of two places for P
 
-    if (wave < 4) {
+    for (bool more = true; more;) {   // one owner, or what the share has of its walk
+        const Run cur = sh.r;
+        const Seq sq = cur.s;
+        const int off = sq.lk - sq.lq, n = sq.lk, h = cur.h;
+        const int k0 = cur.t * OWN, w0 = k0 + pair * 16 * NG;
+        const T *q = (const T *)a.q + sq.q0 * a.qs + h * a.G * D;
+        const T *d_o = (const T *)a.d_o + ((long)sq.q0 * Hq + h * a.G) * D;
+        const float *lse = a.lse + (long)sq.q0 * Hq + h * a.G, *Dw = (const float *)a.ws + (long)sq.q0 * Hq + h * a.G;
+        const int qfirst = max(0, k0 - off) * a.G + cur.j * ST, qn = min(sq.lq * a.G, qfirst + (cur.end - cur.j) * ST);
+        const int nt = cur.end - cur.j;
+        auto load = [&](int j) {
+            const int r0 = qfirst + j * ST, buf = uniform((count + j) % 3);
+            constexpr int RP = 512 / C::CPR;
+            static_assert(ST % RP == 0 && RP % 16 == 0, "");
+            const int row = threadIdx.x / C::CPR, ch = ((threadIdx.x % C::CPR) ^ swz<C::CPR>(row)) * 16;
+            const char *to = lds + buf * C::BUF + wave * 1024;
+#pragma unroll
+            for (int i = 0; i < ST / RP; ++i) {
+                const int r = r0 + i * RP + row, t = quotient(r, a.g_mul, a.g_shift), g = r - t * a.G;
+                const char *from_q = r < qn ? (const char *)(q + t * a.qs + g * D) + ch : (const char *)latent_zero;
+                const char *from_do = r < qn ? (const char *)(d_o + ((long)t * Hq + g) * D) + ch : (const char *)latent_zero;
+                copy16(from_q, to + i * 512 * 16);
+                copy16(from_do, to + C::OFF_V + i * 512 * 16);
+            }
+            if (wave < 2 && lane < ST) {   // lse by the first wave, D by the second
+                const int r = r0 + lane, t = quotient(r, a.g_mul, a.g_shift);
+                const void *src = r >= qn ? (const void *)latent_zero : (wave ? Dw : lse) + (long)t * Hq + (r - t * a.G);
+                copy4(src, (char *)(stat + (buf * 2 + wave) * ST));
+            }
+        };
+        // before tile j: it is there, and P of tile j - 1 is whole
+        auto sync = [&](int j) {
+            if (j < nt) wait_vm<0>();
+            lds_barrier();
+            if (j + 1 < nt) load(j + 1);   // over tile j - 2
+        };
+        // first row that sees key j: its token is j - off
+        auto sees = [&](int j) { return (j - off) * a.G; };
+        auto seen = [&](int r) { return r + 31 >= sees(w0) && w0 < n; };   // whether one of 32 rows sees a key of the wave
+        load(0);
+        const T *x = isv ? (const T *)a.k + sq.k0 * a.ks + h * D : (const T *)a.v + sq.k0 * a.vs + h * D;
+        const long xs = isv ? a.ks : a.vs;
+        Frag<T> xf[NG][NKB];   // k for the first of the pair, v for the second
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int key = w0 + 16 * g + r16;
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) xf[g][kb] = key < n ? load_frag<T>(x + key * xs + 32 * kb + 8 * gq) : zero_frag<T>();
+        }
+        f32x4 acc[NC][NG];   // dv^T, dk^T
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < NC; ++i) acc[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+        if (isv) {
 #pragma unroll 1
-        for (int j = 0; j <= nt; ++j) {
-            sync(j);
-            if (j == nt) break;
-            const char *qt = lds + j % 3 * C::BUF, *dt = qt + C::OFF_V;
-            const float *st = stat + j % 3 * 2 * ST;
-            char *to = hand + (j & 1) * (C::HAND / 2) + lane * (C::HP / 64);
+            for (int j = 0; j <= nt; ++j) {
+                sync(j);
+                if (j == nt) break;
+                const char *qt = lds + (count + j) % 3 * C::BUF, *dt = qt + C::OFF_V;
+                const float *st = stat + (count + j) % 3 * 2 * ST;
+                char *to = hand + ((count + j) & 1) * (C::HAND / 2) + lane * (C::HP / 64);
 #pragma unroll 1
-            for (int t = 0; t < BPT; ++t) {
-                if (!seen(j * BPT + t)) continue;
-                const int r0 = qfirst + j * ST + t * 32;
-                const bool part = r0 < sees(w0 + 16 * NG - 1) || r0 + 32 > qn;
-                f32x4 s[2][NG];
+                for (int t = 0; t < BPT; ++t) {
+                    const int r0 = qfirst + j * ST + t * 32;
+                    if (!seen(r0)) continue;
+                    const bool part = r0 < sees(w0 + 16 * NG - 1) || r0 + 32 > qn;
+                    f32x4 s[2][NG];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int kb = 0; kb < NKB; ++kb) {
-                        const Frag<T> f = row_frag<T>(qt + (32 * t + 16 * u) * C::CPR * 16, rb, kb);
+                        for (int kb = 0; kb < NKB; ++kb) {
+                            const Frag<T> f = row_frag<T>(qt + (32 * t + 16 * u) * C::CPR * 16, rb, kb);
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, xf[g][kb]);
-                    }
-                    const int row = 16 * u + 4 * gq;
-                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 32 * t + row) * LOG2E;
+                            for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, xf[g][kb]);
+                        }
+                        const int row = 16 * u + 4 * gq;
+                        const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 32 * t + row) * LOG2E;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g)
+                        for (int g = 0; g < NG; ++g)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
-                    if (part) {
+                            for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
+                        if (part) {
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            const int lim = sees(w0 + 16 * g + r16);
+                            for (int g = 0; g < NG; ++g) {
+                                const int lim = sees(w0 + 16 * g + r16);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const bool hide = (r0 + row + e < lim) | (r0 + row + e >= qn);
-                                s[u][g][e] = hide ? 0.f : s[u][g][e];
+                                for (int e = 0; e < 4; ++e) {
+                                    const bool hide = (r0 + row + e < lim) | (r0 + row + e >= qn);
+                                    s[u][g][e] = hide ? 0.f : s[u][g][e];
+                                }
                             }
                         }
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) hand_over<T>(to + ((2 * t + u) * NG + g) * C::HP, s[u][g]);
                     }
+                    // P (and below dS) rounded to the storage type for the matrix cores: half
+                    // a step each, as the gradients themselves
+                    Frag<T> pf[NG];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) hand_over<T>(to + ((2 * t + u) * NG + g) * C::HP, s[u][g]);
+                    for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
+#pragma unroll
+                    for (int v = 0; v < NC; ++v) {
+                        const Frag<T> f = col_frag<T, C::CPR>(dt + 32 * t * C::CPR * 16, cb, v);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, pf[g]);
+                    }
                 }
-                // P (and below dS) rounded to the storage type for the matrix cores: half
-                // a step each, as the gradients themselves
-                Frag<T> pf[NG];
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j <= nt; ++j) {
+                sync(j);
+                if (j == 0) continue;
+                const int k = count + j - 1;
+                const char *qt = lds + k % 3 * C::BUF, *dt = qt + C::OFF_V;
+                const float *st = stat + (k % 3 * 2 + 1) * ST;
+                const char *from = hand + (k & 1) * (C::HAND / 2) + lane * (C::HP / 64);
+#pragma unroll 1
+                for (int t = 0; t < BPT; ++t) {
+                    if (!seen(qfirst + (j - 1) * ST + t * 32)) continue;
+                    f32x4 dp[2][NG];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
+                    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int v = 0; v < NC; ++v) {
-                    const Frag<T> f = col_frag<T, C::CPR>(dt + 32 * t * C::CPR * 16, cb, v);
+                        for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, pf[g]);
+                        for (int v = 0; v < NKB; ++v) {
+                            const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::CPR * 16, rb, v);
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, xf[g][v]);
+                        }
+                        const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 32 * t + 16 * u + 4 * gq);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const f32x4 p = take_over<T>(from + ((2 * t + u) * NG + g) * C::HP);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
+                        }
+                    }
+                    Frag<T> sf[NG];
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+#pragma unroll
+                    for (int v = 0; v < NC; ++v) {
+                        const Frag<T> f = col_frag<T, C::CPR>(qt + 32 * t * C::CPR * 16, cb, v);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, sf[g]);
+                    }
                 }
             }
         }
-    } else {
-#pragma unroll 1
-        for (int j = 0; j <= nt; ++j) {
-            sync(j);
-            if (j == 0) continue;
-            const int k = j - 1;
-            const char *qt = lds + k % 3 * C::BUF, *dt = qt + C::OFF_V;
-            const float *st = stat + (k % 3 * 2 + 1) * ST;
-            const char *from = hand + (k & 1) * (C::HAND / 2) + lane * (C::HP / 64);
-#pragma unroll 1
-            for (int t = 0; t < BPT; ++t) {
-                if (!seen(k * BPT + t)) continue;
-                f32x4 dp[2][NG];
+        count += nt;
+        more = share_next<ST>(a, make, sh);
+        const bool whole = cur.j == 0 && cur.end == cur.n;
+        const float by = isv ? 1.f : a.scale * hand_scale<T>();
+        T *out = isv ? (T *)a.dv + sq.k0 * a.dvs + h * D : (T *)a.dk + sq.k0 * a.dks + h * D;
+        const long outs = isv ? a.dvs : a.dks;
+        float *sum = (float *)((char *)a.ws + lay.dkv) + (share * 2 + (cur.j == 0)) * (long)lay.rows * 2 * D + (isv ? D : 0);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+        for (int g = 0; g < NG; ++g) {
+            const int key = w0 + 16 * g + r16;
+            if (key >= n) continue;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int v = 0; v < NKB; ++v) {
-                        const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::CPR * 16, rb, v);
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, xf[g][v]);
-                    }
-                    const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 32 * t + 16 * u + 4 * gq);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const f32x4 p = take_over<T>(from + ((2 * t + u) * NG + g) * C::HP);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
-                    }
-                }
-                Frag<T> sf[NG];
-#pragma unroll
-                for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
-#pragma unroll
-                for (int v = 0; v < NC; ++v) {
-                    const Frag<T> f = col_frag<T, C::CPR>(qt + 32 * t * C::CPR * 16, cb, v);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, sf[g]);
-                }
+            for (int i = 0; i < NC; ++i) {
+                const f32x4 v = acc[i][g] * by;
+                if (whole) store4(out + key * outs + 16 * i + 4 * gq, v);
+                else store4(sum + (key - k0) * 2 * D + 16 * i + 4 * gq, v);
             }
-        }
-    }
-    const bool isv = wave < 4;
-    const float by = isv ? 1.f : a.scale * hand_scale<T>();
-    T *out = isv ? (T *)a.dv + sq.k0 * a.dvs + h * D : (T *)a.dk + sq.k0 * a.dks + h * D;
-    const long outs = isv ? a.dvs : a.dks;
-    float *sum = (float *)((char *)a.ws + lay.dkv) + (((long)piece * a.Tk + sq.k0) * a.Hk + h) * 2 * D + (isv ? D : 0);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const int key = w0 + 16 * g + r16;
-        if (key >= n) continue;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const f32x4 v = acc[i][g] * by;
-            if (CUT) store4(sum + (long)key * a.Hk * 2 * D + 16 * i + 4 * gq, v);
-            else store4(out + key * outs + 16 * i + 4 * gq, v);
         }
     }
 }
@@ -339,7 +352,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
 #pragma unroll
         for (int i = 0; i < NC; ++i) dq[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int all = uniform((tl.keys(it.i) + ST - 1) / ST);
+    const int all = uniform((tl.size(it.i) + ST - 1) / ST);
     const int j0 = CUT ? piece * (plan.kstep / ST) : 0, nt = CUT ? min(all, j0 + plan.kstep / ST) : all;
     if (CUT && piece > 0 && nt <= j0) return;   // the last kernel knows which pieces there are
     // keys that some, that all of the wave's rows see
@@ -454,7 +467,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
             if (BF) pipeline<4, 2 * NC, NC * NG, 2, NG>();
         }
     }
-    float *sum = (float *)((char *)a.ws + AttnBwdWs(plan, a.Tq, a.Tk, a.Hk, a.G, D).dq) + (long)piece * a.Tq * Hq * D;
+    float *sum = (float *)((char *)a.ws + AttnBwdWs(plan, a.B, a.Tq, a.Tk, a.Hk, a.G, D, C::OWN).dq) + (long)piece * a.Tq * Hq * D;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         const int lr = lr0 + 16 * g + r16, i = quotient(lr, a.g_mul, a.g_shift);
@@ -469,36 +482,44 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
     }
 }
 
-// The sums over the pieces, in order: of dq by the first ndq workgroups (D / 4 lanes a row),
-// of dk and dv by the others (2 D / 4 lanes a key).  A piece counts for the rows that its
-// workgroup has worked on.
+// The sums over pieces and shares, in order: of dq by the first ndq workgroups (D / 4 lanes a
+// row), of dk and dv by the others (2 D / 4 lanes a key), which also write the keys that no
+// row sees.  A piece counts for the rows that its workgroup has worked on.
 template <typename T, int D> __global__ __launch_bounds__(256) void attn_bwd_sum_kernel(AttnArgs a, AttnBwdPlan plan, int ndq)
 {
     typedef AttnBwdCfg<T, D> C;
-    const AttnBwdWs lay(plan, a.Tq, a.Tk, a.Hk, a.G, D);
+    const AttnBwdWs lay(plan, a.B, a.Tq, a.Tk, a.Hk, a.G, D, C::OWN);
     const bool isq = (int)blockIdx.x < ndq;
     const int W = isq ? D : 2 * D, H = isq ? a.Hk * a.G : a.Hk, T_ = isq ? a.Tq : a.Tk;
-    const long at = ((long)(blockIdx.x - (isq ? 0 : ndq)) * 256 + threadIdx.x) * 4, size = (long)T_ * H * W;
-    if (at >= size) return;
-    const int token = (int)(at / W / H), col = (int)(at % W), head = (int)(at / W % H);
+    const long at = ((long)(blockIdx.x - (isq ? 0 : ndq)) * 256 + threadIdx.x) * 4;
+    const int col = (int)(at % W);
+    const long row = at / W;
+    if (row >= (long)T_ * H) return;
+    const int token = (int)(row / H), head = (int)(row - (long)token * H);
     const int b = seq_at(isq || !a.cu_k ? a.cu_q : a.cu_k, a.B, T_, token);
     const Seq s = seq_lane(a, b);
     const int i = token - (isq ? s.q0 : s.k0);
     if (i < 0 || i >= (isq ? s.lq : s.lk)) return;   // of no sequence
-    int first = 0, end;
-    if (isq) {   // the owner of the row walks the keys up to its last row's position; piece 0 always writes
-        end = max(1, (AttnTiles(plan.tokens, s).keys(i / plan.tokens) + plan.kstep - 1) / plan.kstep);
-    } else {
-        const Walk w(a, s, i / C::OWN * C::OWN, C::ST);
-        first = w.first / plan.qstep;
-        end = w.first < w.end ? (w.end - 1) / plan.qstep + 1 : first;
-    }
-    const float *part = (const float *)((const char *)a.ws + (isq ? lay.dq : lay.dkv)) + at;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int p = first; p < end; ++p) x += *reinterpret_cast<const f32x4 *>(part + p * size);
-    T *out = isq ? (T *)a.dq + token * a.dqs + head * D + col
-                 : col < D ? (T *)a.dk + token * a.dks + head * D + col : (T *)a.dv + token * a.dvs + head * D + col - D;
-    store4(out, x);
+    if (isq) {   // the owner of the row walks the keys up to its last row's position; piece 0 always writes
+        const int end = max(1, (AttnTiles(plan.tokens, s).size(i / plan.tokens) + plan.kstep - 1) / plan.kstep);
+        const float *part = (const float *)((const char *)a.ws + lay.dq) + at;
+        for (int p = 0; p < end; ++p) x += *reinterpret_cast<const f32x4 *>(part + p * (long)T_ * H * W);
+        store4((T *)a.dq + token * a.dqs + head * D + col, x);
+        return;
+    }
+    const KeyTiles<C::OWN> owners(s, a.G);
+    const int t = i / C::OWN, size = owners.size(t);
+    if (size > 0) {
+        const long *prefix = (const long *)((const char *)a.ws + lay.prefix);
+        int wf, wl;
+        share_range<C::ST>(prefix[b] + head * owners.all() + owners.before(t), size, share_each<C::ST>(prefix[a.B], plan.shares, BWD_LEAST), wf, wl);
+        if (wf == wl) return;   // written by its one workgroup
+        const float *part = (const float *)((const char *)a.ws + lay.dkv) + (i - t * C::OWN) * 2 * D + col;
+#pragma unroll 4
+        for (int w = wf; w <= wl; ++w) x += *reinterpret_cast<const f32x4 *>(part + (w * 2 + (w == wf)) * (long)lay.rows * 2 * D);
+    }
+    store4(col < D ? (T *)a.dk + token * a.dks + head * D + col : (T *)a.dv + token * a.dvs + head * D + col - D, x);
 }
 
 template <typename T, int D> static hipError_t bwd_launch(AttnArgs a, hipStream_t st)
@@ -506,17 +527,17 @@ template <typename T, int D> static hipError_t bwd_launch(AttnArgs a, hipStream_
     typedef AttnBwdCfg<T, D> C;
     const AttnBwdPlan plan = attn_bwd_plan(sizeof(T) == 2, a.B, a.Tq, a.Tk, a.Hk, a.G);
     divisor(a.G, a.g_mul, a.g_shift);
-    auto kkv = plan.qp > 1 ? attn_bwd_kv_kernel<T, D, true> : attn_bwd_kv_kernel<T, D, false>;
+    auto kkv = attn_bwd_kv_kernel<T, D>;
     auto kq = plan.kp > 1 ? attn_bwd_q_kernel<T, D, true> : attn_bwd_q_kernel<T, D, false>;
     hipError_t e = hipFuncSetAttribute((const void *)kkv, hipFuncAttributeMaxDynamicSharedMemorySize, C::KV_LDS);
     if (e != hipSuccess) return e;
     static_assert(2 * C::BUF <= 64 * 1024, "more dynamic LDS has to be asked for");
     if (plan.qtiles > 0) hipLaunchKernelGGL(kq, dim3((unsigned)(plan.qtiles * a.Hk * plan.kp)), dim3(256), 2 * C::BUF, st, a, plan);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (plan.ktiles > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)(plan.ktiles * a.Hk * plan.qp)), dim3(512), C::KV_LDS, st, a, plan);
+    if (a.Tk > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)plan.shares), dim3(512), C::KV_LDS, st, a, plan);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     auto groups = [](long values) { return (int)((values + 1023) / 1024); };
-    const int ndq = plan.kp > 1 ? groups((long)a.Tq * a.Hk * a.G * D) : 0, ndkv = plan.qp > 1 ? groups((long)a.Tk * a.Hk * 2 * D) : 0;
+    const int ndq = plan.kp > 1 ? groups((long)a.Tq * a.Hk * a.G * D) : 0, ndkv = groups((long)a.Tk * a.Hk * 2 * D);
     if (ndq + ndkv > 0) hipLaunchKernelGGL((attn_bwd_sum_kernel<T, D>), dim3(ndq + ndkv), dim3(256), 0, st, a, plan, ndq);
     return hipGetLastError();
 }
@@ -529,7 +550,7 @@ hipError_t attn_bwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st)
 
 unsigned long long attn_bwd_workspace(bool bf16, int B, int Tq, int Tk, int Hk, int G, int D)
 {
-    return (unsigned long long)AttnBwdWs(attn_bwd_plan(bf16, B, Tq, Tk, Hk, G), Tq, Tk, Hk, G, D).bytes;
+    return (unsigned long long)AttnBwdWs(attn_bwd_plan(bf16, B, Tq, Tk, Hk, G), B, Tq, Tk, Hk, G, D, attn_own(bf16)).bytes;
 }
 
 } // namespace gdn

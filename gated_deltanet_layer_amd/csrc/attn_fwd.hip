@@ -35,118 +35,7 @@ struct AttnFwdWs {
     }
 };
 
-__device__ __forceinline__ long scan_lanes64(long x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const long v = __shfl_up(x, d, 64);
-        if ((int)(threadIdx.x & 63) >= d) x += v;
-    }
-    return x;
-}
-__device__ __forceinline__ long lane_of(long x, int l) {
-    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)x, l), hi = (unsigned)__builtin_amdgcn_readlane((int)(x >> 32), l);
-    return (long)((unsigned long long)hi << 32 | lo);
-}
-
-// Keys of a share: all of the call's over the shares, rounded up; four tiles at least.
-template <int KT> __device__ __forceinline__ long attn_each(long total) { return max(4L * KT, (total + ATTN_SHARES - 1) / ATTN_SHARES); }
-
-// What a workgroup works on at a time: key tiles j .. end of the nkt of row tile t.
-struct Run {
-    int b, h, t, j, end, nkt;
-    Seq s;
-};
-
-// A share: a run of the keys of all row tiles (sequence by sequence, head by head), from
-// which follow whole key tiles: those that begin in it.
-template <int KT> struct Share {
-    Run r;
-    long left;   // keys of the share behind r
-    int x;       // first key of row tile r.t behind r
-    // the next run that has a key tile; false: none
-    __device__ __forceinline__ bool next(const AttnArgs &a, int per) {
-        for (;;) {
-            if (left <= 0) return false;
-            const AttnTiles tl(per, r.s);
-            const int keys = r.t < tl.count() ? tl.keys(r.t) : 0;
-            if (x < keys) {
-                const int n = (int)min(left, (long)(keys - x));
-                r.nkt = (keys + KT - 1) / KT;
-                r.j = (x + KT - 1) / KT;
-                r.end = (x + n + KT - 1) / KT;
-                x += n;
-                left -= n;
-                if (r.j < r.end) {
-                    r.t = uniform(r.t);
-                    r.j = uniform(r.j);
-                    r.end = uniform(r.end);
-                    r.nkt = uniform(r.nkt);
-                    return true;
-                }
-            } else {
-                x = 0;
-                if (r.t + 1 < tl.count()) {
-                    ++r.t;
-                } else if (r.h + 1 < a.Hk && tl.all() > 0) {
-                    ++r.h;
-                    r.t = tl.first();
-                } else {
-                    if (r.b + 1 >= a.B) return false;
-                    r.s = seq_of(a, ++r.b);
-                    r.h = 0;
-                    r.t = AttnTiles(per, r.s).first();
-                }
-            }
-        }
-    }
-};
-
-// The share's begin; false: it has none.  Every wave adds up all sequences on its own; the
-// first share leaves the keys before each for the join.
-template <int KT> __device__ __forceinline__ bool share_begin(const AttnArgs &a, int per, int share, Share<KT> &sh)
-{
-    const int lane = threadIdx.x & 63;
-    long *prefix = (long *)a.ws;
-    auto of = [&](int b) { return b < a.B ? a.Hk * AttnTiles(per, seq_lane(a, b)).all() : 0L; };
-    long total = 0;
-    for (int b = 0; b < a.B; b += 64) {
-        const long mine = of(b + lane), incl = scan_lanes64(mine);
-        if (share == 0 && b + lane < a.B) prefix[b + lane] = total + incl - mine;
-        total += lane_of(incl, 63);
-    }
-    if (share == 0 && lane == 0) prefix[a.B] = total;
-    const long each = attn_each<KT>(total), g0 = share * each;
-    if (g0 >= total) return false;
-    long at = 0;
-    sh.r.b = 0;
-    for (int b = 0; b < a.B; b += 64) {
-        const long mine = of(b + lane), incl = scan_lanes64(mine), sum = lane_of(incl, 63);
-        if (g0 < at + sum) {
-            const int l = (int)__builtin_ctzll(__ballot(g0 < at + incl));
-            sh.r.b = b + l;
-            at += lane_of(incl - mine, l);
-            break;
-        }
-        at += sum;
-    }
-    sh.r.s = seq_of(a, sh.r.b);
-    const AttnTiles tl(per, sh.r.s);
-    const long one = tl.all(), r = g0 - at;
-    sh.r.h = __builtin_amdgcn_readfirstlane((int)(r / one));
-    const long x = r - sh.r.h * one;
-    // the row tile: before(t) <= x < before(t + 1)
-    int lo = tl.first(), hi = tl.count();
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tl.before(mid) <= x) lo = mid;
-        else hi = mid;
-    }
-    sh.r.t = __builtin_amdgcn_readfirstlane(lo);
-    sh.x = __builtin_amdgcn_readfirstlane((int)(x - tl.before(lo)));
-    const long left = min(each, total - g0);
-    sh.left = lane_of(left, 0);
-    return true;
-}
+constexpr int FWD_LEAST = 4;   // key tiles of a share
 
 template <typename T, int D, int NR, bool SHARES>
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
@@ -157,21 +46,22 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
     const float c = a.scale * LOG2E;
     const int share = SHARES ? blockIdx.x % 8 * (ATTN_SHARES / 8) + blockIdx.x / 8 : 0;   // a head's on one XCD
-    Share<KT> sh;
+    auto make = [&](const Seq &s) { return AttnTiles(per, s); };
+    Share sh;
     Run cur;
     bool any = true;
     if constexpr (SHARES) {
-        if (!share_begin<KT>(a, per, share, sh) || !sh.next(a, per)) return;
+        if (!share_begin<KT>(a, make, share, ATTN_SHARES, FWD_LEAST, (long *)a.ws, sh) || !share_next<KT>(a, make, sh)) return;
         cur = sh.r;
     } else {
         cur.h = blockIdx.x % a.Hk;
-        const Item it = find_last(a.B, blockIdx.x / a.Hk, [&](int b) { return AttnTiles(per, seq_lane(a, b)).count(); });
+        const Item it = find_last(a.B, blockIdx.x / a.Hk, [&](int b) { return make(seq_lane(a, b)).count(); });
         if (it.b < 0) return;
         cur.b = it.b;
         cur.t = uniform(it.i);
         cur.s = seq_of(a, it.b);
         cur.j = 0;
-        cur.nkt = cur.end = uniform((AttnTiles(per, cur.s).keys(cur.t) + KT - 1) / KT);
+        cur.n = cur.end = uniform((make(cur.s).size(cur.t) + KT - 1) / KT);
         any = cur.end > 0;
     }
     auto load = [&](const Run &r, int j, int buffer) {
@@ -223,7 +113,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
             if (j + 1 < cur.end) {
                 load(cur, j + 1, buffer);
             } else if (SHARES) {
-                more = sh.next(a, per);
+                more = share_next<KT>(a, make, sh);
                 if (more) load(sh.r, sh.r.j, buffer);
             }
             if (k0 >= wlast) continue;   // nothing for this wave in the tile
@@ -292,7 +182,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
             }
             if (sizeof(T) == 2) pipeline<4, NS * NCB, NS / 2 * NCB * NR, 2, NR>();
         }
-        const bool whole = !SHARES || (cur.j == 0 && cur.end == cur.nkt);
+        const bool whole = !SHARES || (cur.j == 0 && cur.end == cur.n);
         const AttnFwdWs lay(a.B, RT, D);
         const long slot = (share * 2 + (cur.j == 0)) * (long)RT;
         float *po = (float *)((char *)a.ws + lay.o) + slot * D, *pl = (float *)((char *)a.ws + lay.lse) + slot;
@@ -338,15 +228,11 @@ template <typename T, int D, int NR> __global__ __launch_bounds__(256) void attn
     const int i = token - s.q0;
     if (i < 0 || i >= s.lq) return;   // of no sequence
     const AttnTiles tl(per, s);
-    const int t = i / per, lr = (i - t * per) * a.G + head % a.G, keys = tl.keys(t);
+    const int t = i / per, lr = (i - t * per) * a.G + head % a.G, keys = tl.size(t);
     int wf = 0, wl = -1;
     if (keys > 0) {
         const long *prefix = (const long *)a.ws;
-        const long each = attn_each<KT>(prefix[a.B]), c0 = prefix[b] + head / a.G * tl.all() + tl.before(t);
-        wf = (int)(c0 / each);
-        wl = (int)((c0 + keys - 1) / each);
-        // the last share has no key tile if none begins in it
-        if (wl > wf && (wl * each - c0 + KT - 1) / KT >= (keys + KT - 1) / KT) --wl;
+        share_range<KT>(prefix[b] + head / a.G * tl.all() + tl.before(t), keys, share_each<KT>(prefix[a.B], ATTN_SHARES, FWD_LEAST), wf, wl);
     }
     if (wf == wl) return;   // written by its one workgroup
     const AttnFwdWs lay(a.B, C::RT, D);

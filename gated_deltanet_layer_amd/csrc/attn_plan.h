@@ -40,9 +40,9 @@ constexpr int attn_walk(bool bf16) { return bf16 ? 64 : 32; }
 
 struct AttnBwdPlan {
     int tokens;          // of a query tile, which has 128 (64) rows
-    int kp, qp;          // pieces of the walked keys (dq), of the walked query rows (dk, dv)
-    int kstep, qstep;    // walked rows of a piece
-    long qtiles, ktiles; // owners of one key head, at most
+    int kp, kstep;       // pieces of the walked keys (dq), and the keys of one
+    int shares;          // workgroups that share the walked rows of all keys (dk, dv)
+    long qtiles;         // query tiles of one key head, at most
 };
 
 // Pieces of `tiles` walked tiles, `least` tiles each or more, to give `fill` workgroups.
@@ -60,16 +60,16 @@ inline AttnBwdPlan attn_bwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G
 {
     AttnBwdPlan p;
     const int own = attn_own(bf16), st = attn_walk(bf16), least = bf16 ? 2 : 1;
-    const long rows = (long)Tq * G, nk = (Tk + st - 1) / st, nq = (rows + st - 1) / st;
+    const long rows = (long)Tq * G, nk = (Tk + st - 1) / st;
     p.tokens = own / G;
     p.qtiles = Tq / p.tokens + (B < Tq ? B : Tq);
-    p.ktiles = Tk / own + (B < Tk ? B : Tk);
     const int kp = attn_pieces(Hk * ((long)(Tq + p.tokens - 1) / p.tokens), 512, nk, least);
-    const int qp = attn_pieces(Hk * ((long)(Tk + own - 1) / own), 256, nq, least);
     p.kstep = (int)((nk + kp - 1) / kp * st);
-    p.qstep = (int)((nq + qp - 1) / qp * st);
     p.kp = kp > 1 ? (Tk + p.kstep - 1) / p.kstep : 1;
-    p.qp = qp > 1 ? (int)((rows + p.qstep - 1) / p.qstep) : 1;
+    // one workgroup a compute unit (two do not fit its LDS), and eight at a time, as there are
+    // XCDs; fewer where the call cannot have two tiles for each
+    const long tiles = Hk * ((long)(Tk + own - 1) / own + (B < Tk ? B : Tk)) * ((rows + st - 1) / st);
+    p.shares = tiles >= 2 * 256 ? 256 : (int)((tiles / 2 + 8) & ~7L);
     return p;
 }
 
