@@ -212,6 +212,14 @@ __device__ __forceinline__ const char *uniform(const void *p) {
     return (const char *)b;
 }
 
+// Operands that a loop holds in registers, there before it begins: the compiler waits for a
+// load where its value is first used, and inside of a loop with copies into LDS under way that
+// would be a wait for all of them, every time around.
+template <typename T> __device__ __forceinline__ void landed(Frag<T> &f) {
+    if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(f.v));
+    else asm volatile("" : "+v"(f.lo), "+v"(f.hi));
+}
+
 // Enqueue the copy of packed rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes apart,
 // x: row 0) into an LDS tile, as load_rows does; the row and the address may be in vector
 // registers, but are the same in every lane.  Rows from n on read as zeros.

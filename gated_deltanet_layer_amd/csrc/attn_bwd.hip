@@ -110,7 +110,7 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
 {
     typedef AttnBwdCfg<T, D> C;
     constexpr int NG = C::NG, ST = C::ST, NKB = D / 32, NC = D / 16, OWN = C::OWN;
-    constexpr int BPT = ST / 32;   // blocks a tile
+    constexpr int NS = ST / 16;
     extern __shared__ char lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
     const int pair = wave & 3, lane = threadIdx.x & 63, Hq = a.Hk * a.G;
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
         };
         // first row that sees key j: its token is j - off
         auto sees = [&](int j) { return (j - off) * a.G; };
-        auto seen = [&](int r) { return r + 31 >= sees(w0) && w0 < n; };   // whether one of 32 rows sees a key of the wave
+        auto seen = [&](int r) { return r + ST - 1 >= sees(w0) && w0 < n; };   // whether a row of the tile sees a key of the wave
         load(0);
         const T *x = isv ? (const T *)a.k + sq.k0 * a.ks + h * D : (const T *)a.v + sq.k0 * a.vs + h * D;
         const long xs = isv ? a.ks : a.vs;
@@ -176,6 +176,10 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb) xf[g][kb] = key < n ? load_frag<T>(x + key * xs + 32 * kb + 8 * gq) : zero_frag<T>();
         }
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) landed<T>(xf[g][kb]);
         f32x4 acc[NC][NG];   // dv^T, dk^T
 #pragma unroll
         for (int g = 0; g < NG; ++g)
@@ -190,50 +194,52 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
                 const char *qt = lds + (count + j) % 3 * C::BUF, *dt = qt + C::OFF_V;
                 const float *st = stat + (count + j) % 3 * 2 * ST;
                 char *to = hand + ((count + j) & 1) * (C::HAND / 2) + lane * (C::HP / 64);
-#pragma unroll 1
-                for (int t = 0; t < BPT; ++t) {
-                    const int r0 = qfirst + j * ST + t * 32;
-                    if (!seen(r0)) continue;
-                    const bool part = r0 < sees(w0 + 16 * NG - 1) || r0 + 32 > qn;
-                    f32x4 s[2][NG];
+                const int r0 = qfirst + j * ST;
+                if (!seen(r0)) continue;
+                f32x4 s[NS][NG];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < NS; ++u) {
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int g = 0; g < NG; ++g) s[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int kb = 0; kb < NKB; ++kb) {
-                            const Frag<T> f = row_frag<T>(qt + (32 * t + 16 * u) * C::CPR * 16, rb, kb);
+                    for (int kb = 0; kb < NKB; ++kb) {
+                        const Frag<T> f = row_frag<T>(qt + 16 * u * C::CPR * 16, rb, kb);
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, xf[g][kb]);
-                        }
-                        const int row = 16 * u + 4 * gq;
-                        const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 32 * t + row) * LOG2E;
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
-                        if (part) {
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                const int lim = sees(w0 + 16 * g + r16);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const bool hide = (r0 + row + e < lim) | (r0 + row + e >= qn);
-                                    s[u][g][e] = hide ? 0.f : s[u][g][e];
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) hand_over<T>(to + ((2 * t + u) * NG + g) * C::HP, s[u][g]);
+                        for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, xf[g][kb]);
                     }
-                    // P (and below dS) rounded to the storage type for the matrix cores: half
-                    // a step each, as the gradients themselves
+                }
+#pragma unroll
+                for (int u = 0; u < NS; ++u) {
+                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 16 * u + 4 * gq) * LOG2E;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[u][g][e] = exp2_hw(__builtin_fmaf(s[u][g][e], c, -ls[e]));
+                }
+                if (r0 < sees(w0 + 16 * NG - 1) || r0 + ST > qn) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const int lim = sees(w0 + 16 * g + r16) - r0 - 4 * gq, end = qn - r0 - 4 * gq;
+#pragma unroll
+                        for (int u = 0; u < NS; ++u)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[u][g][e] = (16 * u + e < lim) | (16 * u + e >= end) ? 0.f : s[u][g][e];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < NS; ++u)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) hand_over<T>(to + (u * NG + g) * C::HP, s[u][g]);
+                // P (and below dS) rounded to the storage type for the matrix cores: half
+                // a step each, as the gradients themselves
+#pragma unroll
+                for (int u = 0; u < NS; u += 2) {
                     Frag<T> pf[NG];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[0][g], s[1][g]);
+                    for (int g = 0; g < NG; ++g) pf[g] = reg_frag<T>(s[u][g], s[u + 1][g]);
 #pragma unroll
                     for (int v = 0; v < NC; ++v) {
-                        const Frag<T> f = col_frag<T, C::CPR>(dt + 32 * t * C::CPR * 16, cb, v);
+                        const Frag<T> f = col_frag<T, C::CPR>(dt + 16 * u * C::CPR * 16, cb, v);
 #pragma unroll
                         for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, pf[g]);
                     }
@@ -248,34 +254,37 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
                 const char *qt = lds + k % 3 * C::BUF, *dt = qt + C::OFF_V;
                 const float *st = stat + (k % 3 * 2 + 1) * ST;
                 const char *from = hand + (k & 1) * (C::HAND / 2) + lane * (C::HP / 64);
-#pragma unroll 1
-                for (int t = 0; t < BPT; ++t) {
-                    if (!seen(qfirst + (j - 1) * ST + t * 32)) continue;
-                    f32x4 dp[2][NG];
+                if (!seen(qfirst + (j - 1) * ST)) continue;
+                f32x4 dp[NS][NG];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < NS; ++u) {
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int v = 0; v < NKB; ++v) {
-                            const Frag<T> f = row_frag<T>(dt + (32 * t + 16 * u) * C::CPR * 16, rb, v);
+                    for (int v = 0; v < NKB; ++v) {
+                        const Frag<T> f = row_frag<T>(dt + 16 * u * C::CPR * 16, rb, v);
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, xf[g][v]);
-                        }
-                        const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 32 * t + 16 * u + 4 * gq);
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            const f32x4 p = take_over<T>(from + ((2 * t + u) * NG + g) * C::HP);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
-                        }
+                        for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, xf[g][v]);
                     }
+                }
+#pragma unroll
+                for (int u = 0; u < NS; ++u) {
+                    const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 16 * u + 4 * gq);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const f32x4 p = take_over<T>(from + (u * NG + g) * C::HP);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < NS; u += 2) {
                     Frag<T> sf[NG];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[0][g], dp[1][g]);
+                    for (int g = 0; g < NG; ++g) sf[g] = reg_frag<T>(dp[u][g], dp[u + 1][g]);
 #pragma unroll
                     for (int v = 0; v < NC; ++v) {
-                        const Frag<T> f = col_frag<T, C::CPR>(qt + 32 * t * C::CPR * 16, cb, v);
+                        const Frag<T> f = col_frag<T, C::CPR>(qt + 16 * u * C::CPR * 16, cb, v);
 #pragma unroll
                         for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, sf[g]);
                     }
@@ -345,6 +354,15 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
             if (live) dot += frag_dot<T>(of[g][kb], load_frag<T>(o + 32 * kb + 8 * gq));
         }
         dd[g] = rows_sum(dot);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        asm volatile("" : "+v"(ls[g]));
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+            landed<T>(qf[g][kb]);
+            landed<T>(of[g][kb]);
+        }
     }
     f32x4 dq[NC][NG];
 #pragma unroll

@@ -91,6 +91,10 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb) qf[g][kb] = live ? load_frag<T>(q + 32 * kb + 8 * gq) : zero_frag<T>();
         }
+#pragma unroll
+        for (int g = 0; g < NR; ++g)
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) landed<T>(qf[g][kb]);
         f32x4 acc[NCB][NR];
         float m[NR], l[NR];
 #pragma unroll
