@@ -34,6 +34,7 @@ struct AttnArgs {
     int B, Tq, Tk, Hk, G;
     unsigned g_mul;              // r / G = r g_mul >> g_shift for r < 2^30 (set by the launcher)
     int g_shift;
+    unsigned g_mul16;            // r / G = r g_mul16 >> 16 for r < 256
 };
 
 struct AttnCacheArgs {
@@ -184,21 +185,22 @@ template <typename F> __device__ __forceinline__ Item find_last(int B, int w, F 
 
 // Row tiles of a sequence: tile t has the tokens from t `per` on.
 struct AttnTiles {
+    static constexpr int extra = 128;
     int per, off, lq, lk;
     __device__ __forceinline__ AttnTiles(int per, const Seq &s) : per(per), off(s.lk - s.lq), lq(s.lq), lk(s.lk) {}
     __device__ __forceinline__ int count() const { return (lq + per - 1) / per; }
     // keys that the last row of tile t sees
-    __device__ __forceinline__ int size(int t) const { return max(0, off + min((t + 1) * per, lq)); }
+    __device__ __forceinline__ int walk(int t) const { return max(0, off + min((t + 1) * per, lq)); }
     __device__ __forceinline__ int first() const { return off < 0 ? min(-off / per, count()) : 0; }   // tile that sees any
     // keys of the row tiles before t (a tile with keys, or count())
     __device__ __forceinline__ long before(int t) const {
         const int f = first();
         const long n = t - f;
-        return n <= 0 ? 0 : n * off + (long)per * ((long)t * (t + 1) - (long)f * (f + 1)) / 2;
+        return n <= 0 ? 0 : n * (off + extra) + (long)per * ((long)t * (t + 1) - (long)f * (f + 1)) / 2;
     }
     __device__ __forceinline__ long all() const {
         const int n = count();
-        return n > first() ? before(n - 1) + size(n - 1) : 0;
+        return n > first() && walk(n - 1) > 0 ? before(n - 1) + walk(n - 1) + extra : 0;
     }
 };
 
@@ -233,7 +235,10 @@ template <int CPR, int ROWS> __device__ __forceinline__ void load_tile(char *til
 // number of workgroups, each of which takes an equal run of all that the owners walk by
 // (sequence by sequence, head by head, owner by owner), in units of keys or rows.  From that
 // follow whole tiles of UT units: those that begin in the run.  `make(seq)` gives a sequence's
-// owners of one key head: count(), first() with any work, size(i), before(i), all().
+// owners of one key head: count(), first() with any work, walk(i), before(i), all().  To the
+// walk of an owner belong `extra` units without a tile, as long as a change of owners takes
+// (its operands' loads, its results' stores): shares of many short walks would else take
+// longer than those of one long walk.
 struct Run {   // what a workgroup works on at a time: tiles j .. end of the n of owner t
     int b, h, t, j, end, n;
     Seq s;
@@ -268,12 +273,12 @@ template <int UT, typename M> __device__ __forceinline__ bool share_next(const A
     for (;;) {
         if (sh.left <= 0) return false;
         const auto owners = make(r.s);
-        const int size = r.t < owners.count() ? owners.size(r.t) : 0;
+        const int walk = r.t < owners.count() ? owners.walk(r.t) : 0, size = walk > 0 ? walk + owners.extra : 0;
         if (sh.x < size) {
             const int n = (int)min(sh.left, (long)(size - sh.x));
-            r.n = uniform((size + UT - 1) / UT);
+            r.n = uniform((walk + UT - 1) / UT);
             r.j = uniform((sh.x + UT - 1) / UT);
-            r.end = uniform((sh.x + n + UT - 1) / UT);
+            r.end = uniform(min((sh.x + n + UT - 1) / UT, r.n));
             sh.x += n;
             sh.left -= n;
             if (r.j < r.end) {
@@ -341,12 +346,13 @@ template <int UT, typename M> __device__ __forceinline__ bool share_begin(const 
     return true;
 }
 
-// The shares that worked on an owner of `size` units, the first of them unit c0 of the call:
-// the first, and the last that a tile begins in.
-template <int UT> __device__ __forceinline__ void share_range(long c0, int size, long each, int &first, int &last) {
+// The shares that worked on owner i, whose first unit is unit c0 of the call: the first, and
+// the last that a tile begins in.
+template <int UT, typename O> __device__ __forceinline__ void share_range(long c0, const O &owners, int i, long each, int &first, int &last) {
+    const int walk = owners.walk(i), tiles = (walk + UT - 1) / UT;
     first = (int)(c0 / each);
-    last = (int)((c0 + size - 1) / each);
-    if (last > first && (last * each - c0 + UT - 1) / UT >= (size + UT - 1) / UT) --last;
+    last = (int)((c0 + walk + owners.extra - 1) / each);
+    while (last > first && (last * each - c0 + UT - 1) / UT >= tiles) --last;
 }
 
 // The sequence of a packed query (or key) row: the last one that begins at or before it,

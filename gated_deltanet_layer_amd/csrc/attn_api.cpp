@@ -53,7 +53,7 @@ bool scale_ok(float s) { return s > 0.f && isfinite(s * gdn::LOG2E); }
 
 // Elements from token to token: the heads of a token at least, and whole 16-byte pieces.
 bool stride_ok(long long s, int H, int D, long long es) { return s >= (long long)H * D && s * es % 16 == 0; }
-constexpr long long STRIDES = 1LL << 22;   // and at most so many (GDN_ENOTSUP beyond)
+constexpr long long STRIDES = 1LL << 21;   // and at most so many (GDN_ENOTSUP beyond): 24 bits of bytes
 
 gdn_status prologue_sizes(int T, int Hq, int Hk, int D, int R, gdn_dtype dtype)
 {
@@ -68,7 +68,7 @@ gdn_status attn_sizes(int B, int Tq, int Tk, int Hq, int Hk, int D, gdn_dtype dt
 {
     if (!dtype_ok(dtype) || B < 0 || Tq < 0 || Tk < 0 || Hq <= 0 || Hk <= 0 || D <= 0 || Hq % Hk != 0) return GDN_EINVAL;
     if (prod(Tq, Hq, D, 4) < 0 || prod(Tk, Hk, D, 4) < 0) return GDN_EINVAL;
-    if ((D != 64 && D != 128) || Hq / Hk > 64 || Hq > (1 << 15)) return GDN_ENOTSUP;
+    if ((D != 64 && D != 128) || Hq / Hk > 64 || Hq > (1 << 14)) return GDN_ENOTSUP;
     // rows of a key head (token, head) in 30 bits, those of all heads in 28; grids: workgroups * threads < 2^32
     const bool bf16 = dtype == GDN_BF16;
     const int G = Hq / Hk;

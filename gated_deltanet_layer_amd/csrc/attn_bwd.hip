@@ -44,15 +44,15 @@ template <typename T> __device__ __forceinline__ float frag_dot(const Frag<T> &x
 
 // P from wave to wave: fp32 as it is, beside bf16 operands as fp16 of P 2^12 (half the
 // room).  P <= 1, so nothing overflows, and down to P = 2^-26 it is off by 2^-11 of itself,
-// an eighth of what dS, which it becomes, is rounded by; below, by 2^-37.  The power of two
-// comes out of dk at the end.
+// an eighth of what dS, which it becomes, is rounded by; below, by 2^-37.  The exponential
+// gives the power of two along, which comes out of dk and dv at the end.
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-template <typename T> __device__ __forceinline__ constexpr float hand_scale() { return sizeof(T) == 2 ? 1.f / 4096.f : 1.f; }
+template <typename T> __device__ __forceinline__ constexpr float hand_bits() { return sizeof(T) == 2 ? 12.f : 0.f; }
 template <typename T> __device__ __forceinline__ void hand_over(char *to, f32x4 p) {
     if constexpr (sizeof(T) == 2) {
         f16x4 h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = (_Float16)(p[e] * 4096.f);
+        for (int e = 0; e < 4; ++e) h[e] = (_Float16)p[e];
         *reinterpret_cast<f16x4 *>(to) = h;
     } else {
         *reinterpret_cast<f32x4 *>(to) = p;
@@ -78,17 +78,20 @@ template <typename T, int D> struct AttnBwdCfg {
     static_assert(KV_LDS <= 160 * 1024, "LDS");
 };
 
+constexpr int OWN_COST = 2;   // what a change of owners takes, in rows for each of its keys (see Share)
+
 // Owners of OWN keys of a sequence, and the rows that walk by: all that see one of the keys.
 // Those are the last of the sequence: row r of a key head is token r / G, head r % G.
 template <int OWN> struct KeyTiles {
+    static constexpr int extra = OWN_COST * OWN;
     int lq, lk, g;
     __device__ __forceinline__ KeyTiles(const Seq &s, int g) : lq(s.lq), lk(s.lk), g(g) {}
     __device__ __forceinline__ int count() const { return (lk + OWN - 1) / OWN; }
     __device__ __forceinline__ int first() const { return 0; }
-    __device__ __forceinline__ int size(int i) const { return min(lq, lk - i * OWN) * g; }
+    __device__ __forceinline__ int walk(int i) const { return min(lq, lk - i * OWN) * g; }
     __device__ __forceinline__ long before(int i) const {
         const int f = lq > lk ? 0 : min(i, (lk - lq) / OWN + 1);   // owners that all rows see
-        return ((long)f * lq + (long)(i - f) * lk - OWN * ((long)i * (i - 1) - (long)f * (f - 1)) / 2) * g;
+        return ((long)f * lq + (long)(i - f) * lk - OWN * ((long)i * (i - 1) - (long)f * (f - 1)) / 2) * g + (lq > 0 ? (long)i * extra : 0);
     }
     __device__ __forceinline__ long all() const { return before(count()); }
 };
@@ -127,46 +130,56 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
     const int rb = row_base<T, C::CPR>(r16), cb = col_base<T, C::CPR>(4 * gq);
     int count = 0;   // tiles so far: which of three buffers, and of two places for P
 
+    // Copies of tile j of a run into its buffer: rows r0 .. of the packed (token, head) rows
+    // that see the owner's keys, r0 in token t0 of the sequence at head g0.  A row is at
+    // token (g0 + row) / G behind t0: all offsets of a tile in 24-bit products from scalar
+    // addresses (64-bit ones a lane took as long as the tile's scores).
+    auto first_row = [&](const Run &r) { return max(0, r.t * OWN - (r.s.lk - r.s.lq)) * a.G; };
+    auto load = [&](const Run &r, int j, int buf) {
+        const int r0 = first_row(r) + (r.j + j) * ST, left = min(r.s.lq * a.G, first_row(r) + r.end * ST) - r0;
+        const int t0 = uniform(quotient(r0, a.g_mul, a.g_shift)), g0 = r0 - t0 * a.G;
+        constexpr int RP = 512 / C::CPR;
+        static_assert(ST % RP == 0 && RP % 16 == 0, "");
+        const int row = threadIdx.x / C::CPR, ch = ((threadIdx.x % C::CPR) ^ swz<C::CPR>(row)) * 16;
+        const char *to = lds + uniform(buf * C::BUF + wave * 1024);
+        const long tok = (long)r.s.q0 + t0, head = (long)tok * Hq + r.h * a.G;
+        const char *q = uniform((const T *)a.q + tok * a.qs + r.h * a.G * D), *d_o = uniform((const T *)a.d_o + head * D);
+        const unsigned qst = (unsigned)a.qs * C::ES, ost = Hq * D * C::ES;
+#pragma unroll
+        for (int i = 0; i < ST / RP; ++i) {
+            const int x = g0 + i * RP + row, t = (int)(__umul24(x, a.g_mul16) >> 16), g = x - t * a.G;
+            const unsigned in = g * (D * C::ES) + ch, oq = __umul24(t, qst) + in, od = __umul24(t, ost) + in;
+            if (left >= ST) {
+                copy16s(q, oq, to + i * 512 * 16);
+                copy16s(d_o, od, to + C::OFF_V + i * 512 * 16);
+            } else {
+                const bool is = i * RP + row < left;
+                copy16(is ? q + oq : (const char *)latent_zero, to + i * 512 * 16);
+                copy16(is ? d_o + od : (const char *)latent_zero, to + C::OFF_V + i * 512 * 16);
+            }
+        }
+        if (wave < 2 && lane < ST) {   // lse by the first wave, D by the second
+            const int x = g0 + lane, t = (int)(__umul24(x, a.g_mul16) >> 16);
+            const float *src = (wave ? (const float *)a.ws : a.lse) + head + t * Hq + (x - t * a.G);
+            copy4(lane < left ? (const void *)src : (const void *)latent_zero, (char *)(stat + uniform((buf * 2 + wave) * ST)));
+        }
+    };
+    load(sh.r, 0, 0);
     for (bool more = true; more;) {   // one owner, or what the share has of its walk
         const Run cur = sh.r;
         const Seq sq = cur.s;
         const int off = sq.lk - sq.lq, n = sq.lk, h = cur.h;
         const int k0 = cur.t * OWN, w0 = k0 + pair * 16 * NG;
-        const T *q = (const T *)a.q + sq.q0 * a.qs + h * a.G * D;
-        const T *d_o = (const T *)a.d_o + ((long)sq.q0 * Hq + h * a.G) * D;
-        const float *lse = a.lse + (long)sq.q0 * Hq + h * a.G, *Dw = (const float *)a.ws + (long)sq.q0 * Hq + h * a.G;
-        const int qfirst = max(0, k0 - off) * a.G + cur.j * ST, qn = min(sq.lq * a.G, qfirst + (cur.end - cur.j) * ST);
-        const int nt = cur.end - cur.j;
-        auto load = [&](int j) {
-            const int r0 = qfirst + j * ST, buf = uniform((count + j) % 3);
-            constexpr int RP = 512 / C::CPR;
-            static_assert(ST % RP == 0 && RP % 16 == 0, "");
-            const int row = threadIdx.x / C::CPR, ch = ((threadIdx.x % C::CPR) ^ swz<C::CPR>(row)) * 16;
-            const char *to = lds + buf * C::BUF + wave * 1024;
-#pragma unroll
-            for (int i = 0; i < ST / RP; ++i) {
-                const int r = r0 + i * RP + row, t = quotient(r, a.g_mul, a.g_shift), g = r - t * a.G;
-                const char *from_q = r < qn ? (const char *)(q + t * a.qs + g * D) + ch : (const char *)latent_zero;
-                const char *from_do = r < qn ? (const char *)(d_o + ((long)t * Hq + g) * D) + ch : (const char *)latent_zero;
-                copy16(from_q, to + i * 512 * 16);
-                copy16(from_do, to + C::OFF_V + i * 512 * 16);
-            }
-            if (wave < 2 && lane < ST) {   // lse by the first wave, D by the second
-                const int r = r0 + lane, t = quotient(r, a.g_mul, a.g_shift);
-                const void *src = r >= qn ? (const void *)latent_zero : (wave ? Dw : lse) + (long)t * Hq + (r - t * a.G);
-                copy4(src, (char *)(stat + (buf * 2 + wave) * ST));
-            }
-        };
+        const int qfirst = first_row(cur) + cur.j * ST, nt = cur.end - cur.j, qn = min(sq.lq * a.G, qfirst + nt * ST);
         // before tile j: it is there, and P of tile j - 1 is whole
         auto sync = [&](int j) {
             if (j < nt) wait_vm<0>();
             lds_barrier();
-            if (j + 1 < nt) load(j + 1);   // over tile j - 2
+            if (j + 1 < nt) load(cur, j + 1, uniform((count + j + 1) % 3));   // over tile j - 2
         };
         // first row that sees key j: its token is j - off
         auto sees = [&](int j) { return (j - off) * a.G; };
         auto seen = [&](int r) { return r + ST - 1 >= sees(w0) && w0 < n; };   // whether a row of the tile sees a key of the wave
-        load(0);
         const T *x = isv ? (const T *)a.k + sq.k0 * a.ks + h * D : (const T *)a.v + sq.k0 * a.vs + h * D;
         const long xs = isv ? a.ks : a.vs;
         Frag<T> xf[NG][NKB];   // k for the first of the pair, v for the second
@@ -208,9 +221,11 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
                         for (int g = 0; g < NG; ++g) s[u][g] = mma(s[u][g], f, xf[g][kb]);
                     }
                 }
+                if (sizeof(T) == 2) pipeline<6, NS * NKB, NS * NKB * NG, 1, NG>();
+                GDN_SCHED_FENCE();
 #pragma unroll
                 for (int u = 0; u < NS; ++u) {
-                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 16 * u + 4 * gq) * LOG2E;
+                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(st + 16 * u + 4 * gq) * LOG2E - hand_bits<T>();
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -223,7 +238,7 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
 #pragma unroll
                         for (int u = 0; u < NS; ++u)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) s[u][g][e] = (16 * u + e < lim) | (16 * u + e >= end) ? 0.f : s[u][g][e];
+                            for (int e = 0; e < 4; ++e) s[u][g][e] = ((16 * u + e < lim) | (16 * u + e >= end)) ? 0.f : s[u][g][e];
                     }
                 }
 #pragma unroll
@@ -244,6 +259,7 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
                         for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, pf[g]);
                     }
                 }
+                if (sizeof(T) == 2) pipeline<6, NS * NC, NS / 2 * NC * NG, 2, NG>();
             }
         } else {
 #pragma unroll 1
@@ -259,7 +275,7 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
 #pragma unroll
                 for (int u = 0; u < NS; ++u) {
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) dp[u][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int g = 0; g < NG; ++g) dp[u][g] = -*reinterpret_cast<const f32x4 *>(st + 16 * u + 4 * gq);   // D
 #pragma unroll
                     for (int v = 0; v < NKB; ++v) {
                         const Frag<T> f = row_frag<T>(dt + 16 * u * C::CPR * 16, rb, v);
@@ -267,15 +283,12 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
                         for (int g = 0; g < NG; ++g) dp[u][g] = mma(dp[u][g], f, xf[g][v]);
                     }
                 }
+                if (sizeof(T) == 2) pipeline<6, NS * NKB, NS * NKB * NG, 1, NG>();
+                GDN_SCHED_FENCE();
 #pragma unroll
                 for (int u = 0; u < NS; ++u) {
-                    const f32x4 dd = *reinterpret_cast<const f32x4 *>(st + 16 * u + 4 * gq);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const f32x4 p = take_over<T>(from + (u * NG + g) * C::HP);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dp[u][g][e] = p[e] * (dp[u][g][e] - dd[e]);
-                    }
+                    for (int g = 0; g < NG; ++g) dp[u][g] *= take_over<T>(from + (u * NG + g) * C::HP);
                 }
 #pragma unroll
                 for (int u = 0; u < NS; u += 2) {
@@ -289,12 +302,14 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
                         for (int g = 0; g < NG; ++g) acc[v][g] = mma(acc[v][g], f, sf[g]);
                     }
                 }
+                if (sizeof(T) == 2) pipeline<6, NS * NC, NS / 2 * NC * NG, 2, NG>();
             }
         }
-        count += nt;
+        count = uniform(count + nt);
         more = share_next<ST>(a, make, sh);
+        if (more) load(sh.r, 0, uniform(count % 3));   // over the tile before the last
         const bool whole = cur.j == 0 && cur.end == cur.n;
-        const float by = isv ? 1.f : a.scale * hand_scale<T>();
+        const float by = (isv ? 1.f : a.scale) * exp2_hw(-hand_bits<T>());
         T *out = isv ? (T *)a.dv + sq.k0 * a.dvs + h * D : (T *)a.dk + sq.k0 * a.dks + h * D;
         const long outs = isv ? a.dvs : a.dks;
         float *sum = (float *)((char *)a.ws + lay.dkv) + (share * 2 + (cur.j == 0)) * (long)lay.rows * 2 * D + (isv ? D : 0);
@@ -370,7 +385,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
 #pragma unroll
         for (int i = 0; i < NC; ++i) dq[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int all = uniform((tl.size(it.i) + ST - 1) / ST);
+    const int all = uniform((tl.walk(it.i) + ST - 1) / ST);
     const int j0 = CUT ? piece * (plan.kstep / ST) : 0, nt = CUT ? min(all, j0 + plan.kstep / ST) : all;
     if (CUT && piece > 0 && nt <= j0) return;   // the last kernel knows which pieces there are
     // keys that some, that all of the wave's rows see
@@ -520,18 +535,18 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_bwd_sum
     if (i < 0 || i >= (isq ? s.lq : s.lk)) return;   // of no sequence
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if (isq) {   // the owner of the row walks the keys up to its last row's position; piece 0 always writes
-        const int end = max(1, (AttnTiles(plan.tokens, s).size(i / plan.tokens) + plan.kstep - 1) / plan.kstep);
+        const int end = max(1, (AttnTiles(plan.tokens, s).walk(i / plan.tokens) + plan.kstep - 1) / plan.kstep);
         const float *part = (const float *)((const char *)a.ws + lay.dq) + at;
         for (int p = 0; p < end; ++p) x += *reinterpret_cast<const f32x4 *>(part + p * (long)T_ * H * W);
         store4((T *)a.dq + token * a.dqs + head * D + col, x);
         return;
     }
     const KeyTiles<C::OWN> owners(s, a.G);
-    const int t = i / C::OWN, size = owners.size(t);
-    if (size > 0) {
+    const int t = i / C::OWN;
+    if (s.lq > 0) {
         const long *prefix = (const long *)((const char *)a.ws + lay.prefix);
         int wf, wl;
-        share_range<C::ST>(prefix[b] + head * owners.all() + owners.before(t), size, share_each<C::ST>(prefix[a.B], plan.shares, BWD_LEAST), wf, wl);
+        share_range<C::ST>(prefix[b] + head * owners.all() + owners.before(t), owners, t, share_each<C::ST>(prefix[a.B], plan.shares, BWD_LEAST), wf, wl);
         if (wf == wl) return;   // written by its one workgroup
         const float *part = (const float *)((const char *)a.ws + lay.dkv) + (i - t * C::OWN) * 2 * D + col;
 #pragma unroll 4
@@ -545,6 +560,7 @@ template <typename T, int D> static hipError_t bwd_launch(AttnArgs a, hipStream_
     typedef AttnBwdCfg<T, D> C;
     const AttnBwdPlan plan = attn_bwd_plan(sizeof(T) == 2, a.B, a.Tq, a.Tk, a.Hk, a.G);
     divisor(a.G, a.g_mul, a.g_shift);
+    a.g_mul16 = (65536 + a.G - 1) / a.G;
     auto kkv = attn_bwd_kv_kernel<T, D>;
     auto kq = plan.kp > 1 ? attn_bwd_q_kernel<T, D, true> : attn_bwd_q_kernel<T, D, false>;
     hipError_t e = hipFuncSetAttribute((const void *)kkv, hipFuncAttributeMaxDynamicSharedMemorySize, C::KV_LDS);

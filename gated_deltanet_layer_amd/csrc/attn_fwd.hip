@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
         cur.t = uniform(it.i);
         cur.s = seq_of(a, it.b);
         cur.j = 0;
-        cur.n = cur.end = uniform((make(cur.s).size(cur.t) + KT - 1) / KT);
+        cur.n = cur.end = uniform((make(cur.s).walk(cur.t) + KT - 1) / KT);
         any = cur.end > 0;
     }
     auto load = [&](const Run &r, int j, int buffer) {
@@ -232,11 +232,11 @@ template <typename T, int D, int NR> __global__ __launch_bounds__(256) void attn
     const int i = token - s.q0;
     if (i < 0 || i >= s.lq) return;   // of no sequence
     const AttnTiles tl(per, s);
-    const int t = i / per, lr = (i - t * per) * a.G + head % a.G, keys = tl.size(t);
+    const int t = i / per, lr = (i - t * per) * a.G + head % a.G, keys = tl.walk(t);
     int wf = 0, wl = -1;
     if (keys > 0) {
         const long *prefix = (const long *)a.ws;
-        share_range<KT>(prefix[b] + head / a.G * tl.all() + tl.before(t), keys, share_each<KT>(prefix[a.B], ATTN_SHARES, FWD_LEAST), wf, wl);
+        share_range<KT>(prefix[b] + head / a.G * tl.all() + tl.before(t), tl, t, share_each<KT>(prefix[a.B], ATTN_SHARES, FWD_LEAST), wf, wl);
     }
     if (wf == wl) return;   // written by its one workgroup
     const AttnFwdWs lay(a.B, C::RT, D);

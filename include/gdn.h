@@ -506,7 +506,7 @@ GDN_API gdn_status gdn_latent_steps(const void *q, const void *draft, const long
  * sums and lse are fp32; for GDN_BF16 the softmax weights are rounded to bf16 for the matrix
  * cores.  Tokens of all sequences stand packed one behind the other, [tokens, heads, D].
  * q_stride and the like are the elements from one token to the next, at least heads * D and a
- * multiple of 16 bytes (GDN_EINVAL), at most 2^22 (GDN_ENOTSUP): q, k and v may be slices of
+ * multiple of 16 bytes (GDN_EINVAL), at most 2^21 (GDN_ENOTSUP): q, k and v may be slices of
  * one projection's output, and gradients of one gradient.  Other tensors are contiguous.
  * Pointers need 16-byte alignment, those of int and of float other than the norm weights
  * 4 bytes, a workspace 256; a workspace's contents on entry do not matter, on return they are
@@ -559,7 +559,7 @@ GDN_API gdn_status gdn_attn_prologue_bwd(const void *q_raw, const void *k_raw, c
  * Row i of a sequence of lq rows and lk keys has position p = lk - lq + i and sees the keys
  * j <= p: a whole prompt (lq = lk), or the last rows of a longer sequence.  A row that sees
  * none (p < 0) gives o = 0, lse = -inf.  Rows of no sequence are left as they were.  Any
- * length may be 0.  GDN_ENOTSUP from Hq > 2^15, Tq Hq or Tk Hk >= 2^28, B >= 2^24, (Tq + Tk)
+ * length may be 0.  GDN_ENOTSUP from Hq > 2^14, Tq Hq or Tk Hk >= 2^28, B >= 2^24, (Tq + Tk)
  * Hq / Hk >= 2^30 and 2^24 row tiles on.  Long rows of few heads are split over the keys; the pieces stand in the
  * workspace (at least gdn_attn_fwd_workspace_size bytes; NULL when that is 0).
  */
