@@ -23,8 +23,12 @@ the stream that the call runs on.
 """
 from __future__ import annotations
 
-from . import _check, lib
-from .latent import _bytes, _done, _dtype, _gpu, _need, _on, _ptr, _query, _scale, _workspace
+import functools
+
+import torch
+
+from . import GDN_BF16, GDN_F32, _check, lib
+from .latent import _bytes, _done, _dtype, _gpu, _on as _on_slow, _ptr, _query, _scale, _workspace
 
 __all__ = ["gdn_attn_prologue", "gdn_attn_prologue_bwd", "gdn_attn_prologue_bwd_workspace_size",
            "gdn_attn_fwd", "gdn_attn_fwd_workspace_size", "gdn_attn_bwd", "gdn_attn_bwd_workspace_size",
@@ -34,15 +38,42 @@ __all__ = ["gdn_attn_prologue", "gdn_attn_prologue_bwd", "gdn_attn_prologue_bwd_
 BLOCK = 16  # tokens that share a scale
 
 
-def _step_of(t, name, T, H, D, dtype, device) -> int:
-    """Check a packed tensor [T, H, D] that may be a slice along the heads; returns the
-    elements from token to token."""
+@functools.lru_cache(maxsize=None)   # the loaded library keeps its entry points
+def _entry(name):
+    return getattr(lib(), name)
+
+
+# Small calls take as long as their host side, so the checks below look at what must hold
+# first, in as few steps as it takes, and say what does not hold only then.
+
+_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+
+
+def _code(t) -> int:
+    """The dtype code of a tensor on a GPU."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        code = _dtype(t.dtype)
+    if not t.is_cuda:
+        _gpu(t)
+    return code
+
+
+def _need(t, name, shape, dtype, dev):
+    """Check a contiguous tensor on GPU `dev`."""
+    if not (t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _check(t, name, shape, dtype, torch.device("cuda", dev))
+
+
+def _step_of(t, name, T, H, D, dtype, dev) -> int:
+    """Check a packed tensor [T, H, D] on GPU `dev` that may be a slice along the heads;
+    returns the elements from token to token."""
     if t.shape != (T, H, D):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, D)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     s0, s1, s2 = t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
@@ -55,16 +86,28 @@ def _packed(t, name):
     return t.shape
 
 
+def _space(workspace, dev):
+    if workspace is not None:
+        _check(workspace, "workspace", device=torch.device("cuda", dev))
+
+
+def _on(t, stream, call):
+    """``call(handle)`` with t's GPU current, and the stream that the work goes to."""
+    if stream is None:
+        i = t.get_device()
+        if i == torch._C._cuda_getDevice():
+            return call(torch._C._cuda_getCurrentRawStream(i))
+    return _on_slow(t, stream, call)
+
+
 # --- prologue -------------------------------------------------------------------
 
 def _prologue_args(q_raw, k_raw, w_q, w_k, inv_freq, pos):
     """Check the inputs; returns (T, Hq, Hk, D, R), the strides and the dtype code."""
-    import torch
     T, Hq, D = _packed(q_raw, "q_raw")
     Hk = _packed(k_raw, "k_raw")[1]
-    dt, dev = q_raw.dtype, q_raw.device
-    code = _dtype(dt)
-    _gpu(q_raw)
+    code = _code(q_raw)
+    dt, dev = q_raw.dtype, q_raw.get_device()
     qs = _step_of(q_raw, "q_raw", T, Hq, D, dt, dev)
     ks = _step_of(k_raw, "k_raw", T, Hk, D, dt, dev)
     _need(w_q, "w_q", (D,), torch.float32, dev)
@@ -82,7 +125,7 @@ def _prologue_args(q_raw, k_raw, w_q, w_k, inv_freq, pos):
 
 
 def _prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, q, k, eps, sizes, steps, code, handle):
-    _done(lib().gdn_attn_prologue(q_raw.data_ptr(), k_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), _ptr(inv_freq),
+    _done(_entry("gdn_attn_prologue")(q_raw.data_ptr(), k_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), _ptr(inv_freq),
                                   _ptr(pos), q.data_ptr(), k.data_ptr(), *sizes, *steps, eps, code, handle),
           "gdn_attn_prologue")
 
@@ -95,19 +138,17 @@ def gdn_attn_prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, q, k, eps, stream=N
     (no rotation); pos [T] int32.
     """
     sizes, steps, code = _prologue_args(q_raw, k_raw, w_q, w_k, inv_freq, pos)
-    _need(q, "q", q_raw.shape, q_raw.dtype, q_raw.device)
-    _need(k, "k", k_raw.shape, q_raw.dtype, q_raw.device)
+    _need(q, "q", q_raw.shape, q_raw.dtype, q_raw.get_device())
+    _need(k, "k", k_raw.shape, q_raw.dtype, q_raw.get_device())
     _on(q_raw, stream, lambda handle: _prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, q, k, eps, sizes, steps, code, handle))
 
 
 def attn_prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, eps=1e-6, stream=None):
     """Allocate q and k, run gdn_attn_prologue, return (q, k)."""
-    import torch
     sizes, steps, code = _prologue_args(q_raw, k_raw, w_q, w_k, inv_freq, pos)
 
     def call(handle):
-        q = torch.empty(q_raw.shape, dtype=q_raw.dtype, device=q_raw.device)
-        k = torch.empty(k_raw.shape, dtype=q_raw.dtype, device=q_raw.device)
+        q, k = q_raw.new_empty(q_raw.shape), q_raw.new_empty(k_raw.shape)
         _prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, q, k, eps, sizes, steps, code, handle)
         return q, k
 
@@ -121,14 +162,14 @@ def gdn_attn_prologue_bwd_workspace_size(T, Hq, Hk, D, R, dtype) -> int:
 
 def _prologue_bwd_args(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k):
     args = _prologue_args(q_raw, k_raw, w_q, w_k, inv_freq, pos)
-    _need(d_q, "d_q", q_raw.shape, q_raw.dtype, q_raw.device)
-    _need(d_k, "d_k", k_raw.shape, q_raw.dtype, q_raw.device)
+    _need(d_q, "d_q", q_raw.shape, q_raw.dtype, q_raw.get_device())
+    _need(d_k, "d_k", k_raw.shape, q_raw.dtype, q_raw.get_device())
     return args
 
 
 def _prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, dq_raw, dk_raw, dw_q, dw_k, workspace, eps, sizes, steps,
                   code, handle):
-    _done(lib().gdn_attn_prologue_bwd(q_raw.data_ptr(), k_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), _ptr(inv_freq),
+    _done(_entry("gdn_attn_prologue_bwd")(q_raw.data_ptr(), k_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), _ptr(inv_freq),
                                       _ptr(pos), d_q.data_ptr(), d_k.data_ptr(), dq_raw.data_ptr(), dk_raw.data_ptr(),
                                       dw_q.data_ptr(), dw_k.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, *steps,
                                       eps, code, handle), "gdn_attn_prologue_bwd")
@@ -138,14 +179,13 @@ def gdn_attn_prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, dq_ra
                           stream=None) -> None:
     """Gradients of gdn_attn_prologue: writes dq_raw, dk_raw in the shapes of q_raw, k_raw
     and dw_q, dw_k [D] fp32, from d_q and d_k, the gradients of its outputs."""
-    import torch
     sizes, steps, code = _prologue_bwd_args(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k)
     T, Hq, Hk, D, _ = sizes
-    dt, dev = q_raw.dtype, q_raw.device
+    dt, dev = q_raw.dtype, q_raw.get_device()
     steps += (_step_of(dq_raw, "dq_raw", T, Hq, D, dt, dev), _step_of(dk_raw, "dk_raw", T, Hk, D, dt, dev))
     _need(dw_q, "dw_q", (D,), torch.float32, dev)
     _need(dw_k, "dw_k", (D,), torch.float32, dev)
-    _check(workspace, "workspace", device=dev)
+    _space(workspace, dev)
     _on(q_raw, stream, lambda handle: _prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, dq_raw, dk_raw, dw_q,
                                                     dw_k, workspace, eps, sizes, steps, code, handle))
 
@@ -153,19 +193,15 @@ def gdn_attn_prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, dq_ra
 def attn_prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, eps=1e-6, workspace=None, stream=None):
     """Allocate the gradients (and the workspace unless one is given), run
     gdn_attn_prologue_bwd, return a dict with dq_raw, dk_raw, dw_q, dw_k."""
-    import torch
     sizes, steps, code = _prologue_bwd_args(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k)
     T, Hq, Hk, D, _ = sizes
-    dev = q_raw.device
-    _check(workspace, "workspace", device=dev)
+    _space(workspace, q_raw.get_device())
     steps += (max(Hq, 1) * D, max(Hk, 1) * D)
 
     def call(handle):
-        g = dict(dq_raw=torch.empty(q_raw.shape, dtype=q_raw.dtype, device=dev),
-                 dk_raw=torch.empty(k_raw.shape, dtype=q_raw.dtype, device=dev),
-                 dw_q=torch.empty(D, dtype=torch.float32, device=dev), dw_k=torch.empty(D, dtype=torch.float32, device=dev))
+        g = dict(dq_raw=q_raw.new_empty(q_raw.shape), dk_raw=q_raw.new_empty(k_raw.shape), dw_q=w_q.new_empty(D), dw_k=w_q.new_empty(D))
         ws = workspace if workspace is not None else \
-            _workspace(_query("gdn_attn_prologue_bwd_workspace_size", *sizes, code), dev)
+            _workspace(_query("gdn_attn_prologue_bwd_workspace_size", *sizes, code), q_raw.device)
         _prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, g["dq_raw"], g["dk_raw"], g["dw_q"], g["dw_k"], ws,
                       eps, sizes, steps, code, handle)
         return g
@@ -177,12 +213,10 @@ def attn_prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, eps=1e-6,
 
 def _attn_args(q, k, v, cu_q, cu_k):
     """Check the inputs; returns (B, Tq, Tk, Hq, Hk, D), the strides and the dtype code."""
-    import torch
     Tq, Hq, D = _packed(q, "q")
     Tk, Hk, _ = _packed(k, "k")
-    dt, dev = q.dtype, q.device
-    code = _dtype(dt)
-    _gpu(q)
+    code = _code(q)
+    dt, dev = q.dtype, q.get_device()
     steps = (_step_of(q, "q", Tq, Hq, D, dt, dev), _step_of(k, "k", Tk, Hk, D, dt, dev), _step_of(v, "v", Tk, Hk, D, dt, dev))
     if cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError("cu_q must be [B + 1]")
@@ -205,7 +239,7 @@ def gdn_attn_bwd_workspace_size(B, Tq, Tk, Hq, Hk, D, dtype) -> int:
 
 
 def _fwd(q, k, v, cu_q, cu_k, o, lse, workspace, scale, sizes, steps, code, handle):
-    _done(lib().gdn_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), _ptr(cu_k), o.data_ptr(), _ptr(lse),
+    _done(_entry("gdn_attn_fwd")(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), _ptr(cu_k), o.data_ptr(), _ptr(lse),
                              _ptr(workspace), _bytes(workspace), *sizes, *steps, scale, code, handle), "gdn_attn_fwd")
 
 
@@ -217,11 +251,10 @@ def gdn_attn_fwd(q, k, v, cu_q, cu_k, o, lse, workspace, scale, stream=None) -> 
     sequence of lq rows and lk keys sees the keys up to lk - lq + i; a row that sees none has
     o = 0, lse = -inf.  Rows of no sequence are left as they were.
     """
-    import torch
     sizes, steps, code = _attn_args(q, k, v, cu_q, cu_k)
-    _need(o, "o", q.shape, q.dtype, q.device)
+    _need(o, "o", q.shape, q.dtype, q.get_device())
     _check(lse, "lse", q.shape[:2], torch.float32, q.device)
-    _check(workspace, "workspace", device=q.device)
+    _space(workspace, q.get_device())
     _on(q, stream, lambda handle: _fwd(q, k, v, cu_q, cu_k, o, lse, workspace, scale, sizes, steps, code, handle))
 
 
@@ -229,13 +262,11 @@ def attn_fwd(q, k, v, cu_q, cu_k=None, scale=None, workspace=None, stream=None):
     """Allocate o and lse (and the workspace, if one is needed and none is given), run
     gdn_attn_fwd, return (o, lse).  scale: 1 / sqrt(D) unless given.  Rows of no sequence
     hold whatever the memory held."""
-    import torch
     sizes, steps, code = _attn_args(q, k, v, cu_q, cu_k)
-    _check(workspace, "workspace", device=q.device)
+    _space(workspace, q.get_device())
 
     def call(handle):
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        o, lse = q.new_empty(q.shape), q.new_empty(q.shape[:2], dtype=torch.float32)
         ws = workspace if workspace is not None else _workspace(_query("gdn_attn_fwd_workspace_size", *sizes, code), q.device)
         _fwd(q, k, v, cu_q, cu_k, o, lse, ws, _scale(scale, sizes[5]), sizes, steps, code, handle)
         return o, lse
@@ -244,16 +275,16 @@ def attn_fwd(q, k, v, cu_q, cu_k=None, scale=None, workspace=None, stream=None):
 
 
 def _bwd_args(q, k, v, o, lse, d_o, cu_q, cu_k):
-    import torch
     args = _attn_args(q, k, v, cu_q, cu_k)
-    _need(o, "o", q.shape, q.dtype, q.device)
-    _need(d_o, "d_o", q.shape, q.dtype, q.device)
-    _need(lse, "lse", q.shape[:2], torch.float32, q.device)
+    dev = q.get_device()
+    _need(o, "o", q.shape, q.dtype, dev)
+    _need(d_o, "d_o", q.shape, q.dtype, dev)
+    _need(lse, "lse", q.shape[:2], torch.float32, dev)
     return args
 
 
 def _bwd(q, k, v, cu_q, cu_k, o, lse, d_o, dq, dk, dv, workspace, scale, sizes, steps, code, handle):
-    _done(lib().gdn_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), _ptr(cu_k), o.data_ptr(),
+    _done(_entry("gdn_attn_bwd")(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), _ptr(cu_k), o.data_ptr(),
                              lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(workspace),
                              _bytes(workspace), *sizes, *steps, scale, code, handle), "gdn_attn_bwd")
 
@@ -263,10 +294,10 @@ def gdn_attn_bwd(q, k, v, cu_q, cu_k, o, lse, d_o, dq, dk, dv, workspace, scale,
     lse are the forward's outputs.  Rows of no sequence are left as they were."""
     sizes, steps, code = _bwd_args(q, k, v, o, lse, d_o, cu_q, cu_k)
     _, Tq, Tk, Hq, Hk, D = sizes
-    dt, dev = q.dtype, q.device
+    dt, dev = q.dtype, q.get_device()
     steps += (_step_of(dq, "dq", Tq, Hq, D, dt, dev), _step_of(dk, "dk", Tk, Hk, D, dt, dev),
               _step_of(dv, "dv", Tk, Hk, D, dt, dev))
-    _check(workspace, "workspace", device=dev)
+    _space(workspace, dev)
     _on(q, stream, lambda handle: _bwd(q, k, v, cu_q, cu_k, o, lse, d_o, dq, dk, dv, workspace, scale, sizes, steps, code, handle))
 
 
@@ -274,14 +305,13 @@ def attn_bwd(q, k, v, o, lse, d_o, cu_q, cu_k=None, scale=None, workspace=None, 
     """Allocate the gradients (and the workspace unless one is given), run gdn_attn_bwd,
     return a dict with dq, dk, dv.  cu_q, cu_k and scale as given to the forward.  Rows of
     no sequence hold whatever the memory held."""
-    import torch
     sizes, steps, code = _bwd_args(q, k, v, o, lse, d_o, cu_q, cu_k)
-    _check(workspace, "workspace", device=q.device)
+    _space(workspace, q.get_device())
     _, _, _, Hq, Hk, D = sizes
     steps += (Hq * D, Hk * D, Hk * D)
 
     def call(handle):
-        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
+        dq, dk, dv = q.new_empty(q.shape), q.new_empty(k.shape), q.new_empty(k.shape)
         ws = workspace if workspace is not None else _workspace(_query("gdn_attn_bwd_workspace_size", *sizes, code), q.device)
         _bwd(q, k, v, cu_q, cu_k, o, lse, d_o, dq, dk, dv, ws, _scale(scale, D), sizes, steps, code, handle)
         return dict(dq=dq, dk=dk, dv=dv)
@@ -291,9 +321,8 @@ def attn_bwd(q, k, v, o, lse, d_o, cu_q, cu_k=None, scale=None, workspace=None, 
 
 # --- the cache ------------------------------------------------------------------
 
-def _cache_args(k_cache, v_cache, k_scale, v_scale, table, lens, device):
+def _cache_args(k_cache, v_cache, k_scale, v_scale, table, lens, dev):
     """Check a cache; returns (N, Hk, D, pages, page, width)."""
-    import torch
     if k_cache.dim() != 4 or table.dim() != 2:
         raise ValueError("k_cache must be [pages, Hk, page, D], table [N, width]")
     pages, Hk, page, D = k_cache.shape
@@ -303,12 +332,12 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, table, lens, device):
     dt = k_cache.dtype
     if dt is not torch.float8_e4m3fn and dt is not torch.uint8:
         raise TypeError(f"k_cache must be float8_e4m3fn or uint8, got {dt}")
-    _need(k_cache, "k_cache", k_cache.shape, dt, device)
-    _need(v_cache, "v_cache", (pages, Hk, page // BLOCK, D, BLOCK), dt, device)
-    _need(k_scale, "k_scale", (pages, Hk, page // BLOCK), torch.float32, device)
-    _need(v_scale, "v_scale", (pages, Hk, page // BLOCK), torch.float32, device)
-    _need(table, "table", (N, width), torch.int32, device)
-    _need(lens, "lens", (N,), torch.int32, device)
+    _need(k_cache, "k_cache", k_cache.shape, dt, dev)
+    _need(v_cache, "v_cache", (pages, Hk, page // BLOCK, D, BLOCK), dt, dev)
+    _need(k_scale, "k_scale", (pages, Hk, page // BLOCK), torch.float32, dev)
+    _need(v_scale, "v_scale", (pages, Hk, page // BLOCK), torch.float32, dev)
+    _need(table, "table", (N, width), torch.int32, dev)
+    _need(lens, "lens", (N,), torch.int32, dev)
     return N, Hk, D, pages, page, width
 
 
@@ -320,11 +349,9 @@ def gdn_attn_append(k, v, cu, k_cache, v_cache, k_scale, v_scale, table, lens, s
     power of two as its scale that brings its largest magnitude to 448 or less; a block that
     older tokens share keeps theirs unless it has to grow.
     """
-    import torch
     T = _packed(k, "k")[0]
-    dt, dev = k.dtype, k.device
-    code = _dtype(dt)
-    _gpu(k)
+    code = _code(k)
+    dt, dev = k.dtype, k.get_device()
     N, Hk, D, pages, page, width = _cache_args(k_cache, v_cache, k_scale, v_scale, table, lens, dev)
     ks, vs = _step_of(k, "k", T, Hk, D, dt, dev), _step_of(v, "v", T, Hk, D, dt, dev)
     if cu is not None:
@@ -332,7 +359,7 @@ def gdn_attn_append(k, v, cu, k_cache, v_cache, k_scale, v_scale, table, lens, s
     elif T != N:
         raise ValueError(f"{T} tokens for {N} sequences: cu is required")
     _on(k, stream, lambda handle: _done(
-        lib().gdn_attn_append(k.data_ptr(), v.data_ptr(), _ptr(cu), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        _entry("gdn_attn_append")(k.data_ptr(), v.data_ptr(), _ptr(cu), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                               v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), N, T, Hk, D, pages, page, width, ks, vs,
                               code, handle), "gdn_attn_append"))
 
@@ -350,15 +377,14 @@ def gdn_attn_step_workspace_size(N, Hq, Hk, D, page, width) -> int:
 def _step_args(q, k_cache, v_cache, k_scale, v_scale, table, lens):
     """Check the inputs; returns (N, Hq, Hk, D, pages, page, width) and the dtype code."""
     N, Hq, D = _packed(q, "q")
-    code = _dtype(q.dtype)
-    _gpu(q)
-    _, Hk, _, pages, page, width = _cache_args(k_cache, v_cache, k_scale, v_scale, table, lens, q.device)
-    _need(q, "q", (table.shape[0], Hq, k_cache.shape[3]), q.dtype, q.device)
+    code, dev = _code(q), q.get_device()
+    n, Hk, d, pages, page, width = _cache_args(k_cache, v_cache, k_scale, v_scale, table, lens, dev)
+    _need(q, "q", (n, Hq, d), q.dtype, dev)
     return (N, Hq, Hk, D, pages, page, width), code
 
 
 def _step(q, k_cache, v_cache, k_scale, v_scale, table, lens, o, lse, workspace, scale, sizes, code, handle):
-    _done(lib().gdn_attn_step(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+    _done(_entry("gdn_attn_step")(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                               table.data_ptr(), lens.data_ptr(), o.data_ptr(), _ptr(lse), _ptr(workspace), _bytes(workspace),
                               *sizes, scale, code, handle), "gdn_attn_step")
 
@@ -367,11 +393,10 @@ def gdn_attn_step(q, k_cache, v_cache, k_scale, v_scale, table, lens, o, lse, wo
     """One token a sequence: q [N,Hq,D] over the cache by table [N,width] int32 and lens [N]
     int32; writes o [N,Hq,D] and lse [N,Hq] fp32 (or None).  Pages outside the cache hold no
     tokens; a sequence with no token has o = 0, lse = -inf."""
-    import torch
     sizes, code = _step_args(q, k_cache, v_cache, k_scale, v_scale, table, lens)
-    _need(o, "o", q.shape, q.dtype, q.device)
+    _need(o, "o", q.shape, q.dtype, q.get_device())
     _check(lse, "lse", q.shape[:2], torch.float32, q.device)
-    _check(workspace, "workspace", device=q.device)
+    _space(workspace, q.get_device())
     _on(q, stream, lambda handle: _step(q, k_cache, v_cache, k_scale, v_scale, table, lens, o, lse, workspace, scale, sizes,
                                         code, handle))
 
@@ -379,13 +404,12 @@ def gdn_attn_step(q, k_cache, v_cache, k_scale, v_scale, table, lens, o, lse, wo
 def attn_step(q, k_cache, v_cache, k_scale, v_scale, table, lens, scale=None, want_lse=False, workspace=None, stream=None):
     """Allocate o (and the workspace, if one is needed and none is given), run gdn_attn_step,
     return o, or (o, lse).  scale: 1 / sqrt(D) unless given."""
-    import torch
     sizes, code = _step_args(q, k_cache, v_cache, k_scale, v_scale, table, lens)
-    _check(workspace, "workspace", device=q.device)
+    _space(workspace, q.get_device())
 
     def call(handle):
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
+        o = q.new_empty(q.shape)
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32) if want_lse else None
         N, Hq, Hk, D, _, page, width = sizes
         ws = workspace if workspace is not None else \
             _workspace(_query("gdn_attn_step_workspace_size", N, Hq, Hk, D, page, width), q.device)
