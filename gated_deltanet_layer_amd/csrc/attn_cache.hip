@@ -52,10 +52,38 @@ __device__ __forceinline__ int fp8_moved(int bytes, float by)   // four values, 
     return __builtin_amdgcn_cvt_pk_fp8_f32(b[0] * by, b[1] * by, __builtin_amdgcn_cvt_pk_fp8_f32(a[0] * by, a[1] * by, 0, false), true);
 }
 
-// One wave a block, head and kind (keys or values): D / 64 channels a lane, all 16 tokens.
+// A value as it is stored: what is not finite becomes NaN.
+__device__ __forceinline__ float stored(float x, float inv)
+{
+    return (__float_as_int(x) & 0x7fffffff) < 0x7f800000 ? x * inv : __int_as_float(0x7fc00000);
+}
+__device__ __forceinline__ int magnitude(float x)   // the bits of |x|; 0 where it is not finite
+{
+    const int bits = __float_as_int(x) & 0x7fffffff;
+    return bits < 0x7f800000 ? bits : 0;
+}
+__device__ __forceinline__ int fp8_four(float a, float b, float c, float d)
+{
+    return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+}
+
+// The scale of a block for new values of magnitude `most` (bits), where older ones may stand
+// in front; `moved`: what those are multiplied by.
+struct BlockScale {
+    float scale, inv, moved;
+    __device__ __forceinline__ BlockScale(int most, bool older, const float *held) {
+        scale = pow2_scale(most);
+        const float before = older ? *held : scale;
+        if (older) scale = fmaxf(before, scale);
+        inv = 1.f / scale;
+        moved = before * inv;
+    }
+};
+
+// One wave a block, head and kind.  Keys: 16 channels of a token a lane, 16 bytes as they are
+// stored.  Values: D / 64 channels of all 16 tokens a lane, the 16 bytes of each channel.
 template <typename T, int D> __global__ __launch_bounds__(256) void attn_append_kernel(AttnCacheArgs a)
 {
-    constexpr int CH = D / 64;
     const int unit = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (unit >= 2 * a.Hk) return;
     const int h = unit >> 1;
@@ -69,82 +97,105 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_append_
     const int lo = max(f.lo - base, 0), hi = min(f.hi - base, CACHE_BLOCK);   // slots of new tokens
     const int gb = cache_block(a, it.b, h, blk);
     if (gb < 0) return;
-    const T *x = (isv ? (const T *)a.v : (const T *)a.k) + h * D + lane * CH;
-    const long stride = isv ? a.vs : a.ks, row = f.row + (base + lo - f.lo);
-    float v[16][CH];
-    int amax = 0;
-#pragma unroll
-    for (int t = 0; t < 16; ++t) {
-        const bool mine = t >= lo && t < hi;
-#pragma unroll
-        for (int e = 0; e < CH; ++e) v[t][e] = 0.f;
-        if (mine) {
-            if constexpr (CH == 2) {
-                typedef T Pair __attribute__((ext_vector_type(2)));
-                const Pair p = *reinterpret_cast<const Pair *>(x + (row + (t - lo)) * stride);
-                v[t][0] = to_f32(p[0]);
-                v[t][1] = to_f32(p[1]);
-            } else {
-                v[t][0] = to_f32(x[(row + (t - lo)) * stride]);
-            }
-        }
-    }
-    constexpr int INF = 0x7f800000;
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-#pragma unroll
-        for (int e = 0; e < CH; ++e) {
-            const int bits = __float_as_int(v[t][e]) & 0x7fffffff;
-            amax = max(amax, bits < INF ? bits : 0);
-        }
+    const long row = f.row + (base - f.lo);   // of slot 0, which may be none
     float *sp = (isv ? a.v_scale : a.k_scale) + gb;
-    float scale = pow2_scale(max_lanes(amax)), before = scale;
-    if (lo > 0) {   // older tokens in front
-        before = *sp;
-        scale = fmaxf(before, scale);
-    }
-    const float inv = 1.f / scale, moved = before * inv;
-    const bool grown = lo > 0 && scale != before;
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-#pragma unroll
-        for (int e = 0; e < CH; ++e)   // what is not finite is stored as NaN
-            v[t][e] = (__float_as_int(v[t][e]) & 0x7fffffff) < INF ? v[t][e] * inv : __int_as_float(0x7fc00000);
     char *cache = (char *)(isv ? a.v_cache : a.k_cache) + (long)gb * CACHE_BLOCK * D;
     if (isv) {
-        const unsigned slots = (0xffffu >> (16 - hi)) & (0xffffu << lo), old = (1u << lo) - 1;
-        u32x4 *p = (u32x4 *)(cache + lane * CH * CACHE_BLOCK);
-        u32x4 w[CH];
-        if (hi - lo < CACHE_BLOCK) {
+        constexpr int CH = D / 64;
+        const T *x = (const T *)a.v + h * D + lane * CH;
+        const unsigned slots = (0xffffu >> (16 - hi)) & (0xffffu << lo), older = (1u << lo) - 1;
+        const bool part = hi - lo < CACHE_BLOCK;
+        u32x4 *p = (u32x4 *)(cache + lane * CH * CACHE_BLOCK), w[CH];
+        if (part) {
 #pragma unroll
             for (int e = 0; e < CH; ++e) w[e] = p[e];
         }
+        float v[16][CH];
+        int most = 0;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+#pragma unroll
+            for (int e = 0; e < CH; ++e) v[t][e] = 0.f;
+            if (t >= lo && t < hi) {
+                if constexpr (CH == 2) {
+                    typedef T Pair __attribute__((ext_vector_type(2)));
+                    const Pair y = *reinterpret_cast<const Pair *>(x + (row + t) * a.vs);
+                    v[t][0] = to_f32(y[0]);
+                    v[t][1] = to_f32(y[1]);
+                } else {
+                    v[t][0] = to_f32(x[(row + t) * a.vs]);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+#pragma unroll
+            for (int e = 0; e < CH; ++e) most = max(most, magnitude(v[t][e]));
+        const BlockScale s(max_lanes(most), lo > 0, sp);
 #pragma unroll
         for (int e = 0; e < CH; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 auto bytes = [&](unsigned m) { return (((m >> (4 * i)) & 15u) * 0x00204081u & 0x01010101u) * 0xffu; };
-                int nw = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i][e], v[4 * i + 1][e], 0, false);
-                nw = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2][e], v[4 * i + 3][e], nw, true);
-                if (hi - lo < CACHE_BLOCK) {
+                unsigned nw = fp8_four(stored(v[4 * i][e], s.inv), stored(v[4 * i + 1][e], s.inv), stored(v[4 * i + 2][e], s.inv),
+                                       stored(v[4 * i + 3][e], s.inv));
+                if (part) {
                     unsigned held = w[e][i];
-                    if (grown) held = (held & ~bytes(old)) | ((unsigned)fp8_moved((int)held, moved) & bytes(old));
-                    nw = (int)((held & ~bytes(slots)) | ((unsigned)nw & bytes(slots)));
+                    if (s.moved != 1.f) held = (held & ~bytes(older)) | ((unsigned)fp8_moved((int)held, s.moved) & bytes(older));
+                    nw = (held & ~bytes(slots)) | (nw & bytes(slots));
                 }
-                w[e][i] = (unsigned)nw;
+                w[e][i] = nw;
             }
 #pragma unroll
         for (int e = 0; e < CH; ++e) p[e] = w[e];
+        if (lane == 0) *sp = s.scale;
     } else {
-        typedef typename std::conditional<CH == 2, unsigned short, unsigned char>::type Bytes;
-        Bytes *p = (Bytes *)cache + lane;
-        if (grown)
-            for (int t = 0; t < lo; ++t) p[t * 64] = (Bytes)fp8_moved(p[t * 64], moved);
+        constexpr int LPR = D / 16, RP = 64 / LPR, NP = 16 / RP;   // lanes a token, tokens at a time, times
+        const int t0 = lane / LPR, ch = lane % LPR * 16;
+        const T *x = (const T *)a.k + h * D + ch;
+        float k[NP][16];
+        int most = 0;
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
-            if (t >= lo && t < hi) p[t * 64] = (Bytes)__builtin_amdgcn_cvt_pk_fp8_f32(v[t][0], v[t][CH - 1], 0, false);
+        for (int i = 0; i < NP; ++i) {
+            const int t = i * RP + t0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) k[i][e] = 0.f;
+            if (t >= lo && t < hi) {
+#pragma unroll
+                for (int c = 0; c < 16; c += 8) {
+                    const Frag<T> y = load_frag<T>(x + (row + t) * a.ks + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if constexpr (sizeof(T) == 2) k[i][c + e] = (float)y.v[e];
+                        else k[i][c + e] = e < 4 ? y.lo[e] : y.hi[e - 4];
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) most = max(most, magnitude(k[i][e]));
+        const BlockScale s(max_lanes(most), lo > 0, sp);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int t = i * RP + t0;
+            u32x4 *p = (u32x4 *)(cache + t * D + ch);
+            if (t >= lo && t < hi) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = fp8_four(stored(k[i][4 * e], s.inv), stored(k[i][4 * e + 1], s.inv), stored(k[i][4 * e + 2], s.inv), stored(k[i][4 * e + 3], s.inv));
+                *p = w;
+            } else if (t < lo && s.moved != 1.f) {
+                u32x4 w = *p;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = fp8_moved((int)w[e], s.moved);
+                *p = w;
+            }
+        }
+        if (lane == 0) *sp = s.scale;
     }
-    if (lane == 0) *sp = scale;
 }
 
 // --- one token ------------------------------------------------------------------

@@ -18,6 +18,15 @@ struct AttnFwdPlan {
     long tiles;    // row tiles of one key head, at most
 };
 
+// Rows: two groups a wave (each key operand serves two products) once that gives every
+// compute unit a workgroup.
+//
+// Shares: with fewer row tiles than two a unit, the longest row is the call's time unless all
+// rows' key tiles are shared equally; but a share begins, changes rows and is joined for
+// some 12 us.  Lengths are on the device, so the rule takes the call for up to four sequences
+// of equal length, and shares from 20 key tiles a sequence on (8 over 2 heads of 128 in bf16:
+// one sequence of 1000 25.7 us, whole 25.6; of 2048 36, 46; of 4096 64, 81; four of 1000 41,
+// 29; fp32, D = 64: one of 1000 31, 49; three of 1000 53, 57).
 inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G)
 {
     AttnFwdPlan p;
@@ -25,10 +34,8 @@ inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G
     p.nr = bf16 && wide >= 256 ? 2 : 1;
     p.tokens = 64 * p.nr / G;
     p.tiles = Tq / p.tokens + (B < Tq ? B : Tq);
-    // key tiles that the call has if it is one sequence: the most that it may have
-    const int kt = bf16 ? 64 : 32;
-    const long wgs = ((Tq + p.tokens - 1) / p.tokens) * (long)Hk, keys = Tk - Tq / 2 > 0 ? Tk - Tq / 2 : Tk / 2;
-    p.shares = wgs > 0 && wgs < ATTN_SHARES && wgs * (keys / kt) >= 8 * ATTN_SHARES ? ATTN_SHARES : 0;
+    const long wgs = ((Tq + p.tokens - 1) / p.tokens) * (long)Hk, each = B > 0 ? Tk / (B < 4 ? B : 4) : 0;
+    p.shares = wgs > 0 && wgs < ATTN_SHARES && each >= 20 * (bf16 ? 64 : 32) ? ATTN_SHARES : 0;
     return p;
 }
 

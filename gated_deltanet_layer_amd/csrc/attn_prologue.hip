@@ -181,21 +181,21 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_prologu
     }
 }
 
-// dw_q and dw_k from the workgroups' sums: a workgroup for 16 channels, 16 runs of the sums.
-template <int D> __global__ __launch_bounds__(256) void attn_prologue_dw_kernel(AttnPrologueArgs a, int wgs)
+// dw_q and dw_k from the workgroups' sums: a workgroup for 16 channels, 64 runs of the sums.
+template <int D> __global__ __launch_bounds__(1024) void attn_prologue_dw_kernel(AttnPrologueArgs a, int wgs)
 {
-    __shared__ float sums[16][16];
+    __shared__ float sums[64][16];
     const int c = threadIdx.x & 15, run = threadIdx.x >> 4, col = blockIdx.x * 16 + c;   // of 2 D columns
-    const int per = (wgs + 15) / 16, end = min(wgs, (run + 1) * per);
+    const int per = (wgs + 63) / 64, end = min(wgs, (run + 1) * per);
     float s = 0.f;
-#pragma unroll 4
+#pragma unroll 16
     for (int i = run * per; i < end; ++i) s += a.ws[(long)i * 2 * D + col];
     sums[run][c] = s;
     __syncthreads();
     if (run > 0) return;
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += sums[i][c];
+    for (int i = 0; i < 64; ++i) s += sums[i][c];
     (col < D ? a.dw_q : a.dw_k)[col % D] = s;
 }
 
@@ -212,7 +212,7 @@ template <typename T, int D> static hipError_t prologue_bwd(const AttnPrologueAr
     if (wgs > 0) hipLaunchKernelGGL((attn_prologue_bwd_kernel<T, D>), dim3(wgs), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_prologue_dw_kernel<D>), dim3(2 * D / 16), dim3(256), 0, st, a, wgs);
+    hipLaunchKernelGGL((attn_prologue_dw_kernel<D>), dim3(2 * D / 16), dim3(1024), 0, st, a, wgs);
     return hipGetLastError();
 }
 
