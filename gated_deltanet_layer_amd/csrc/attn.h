@@ -206,12 +206,14 @@ struct AttnTiles {
 
 // x, which every lane of the wave has, in a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-// The same of an address that memory instructions in inline assembly read: five wait states
-// after the vector instructions that wrote it.
 __device__ __forceinline__ const char *uniform(const void *p) {
-    unsigned long long b = (unsigned)uniform((int)(uintptr_t)p) | (unsigned long long)(unsigned)uniform((int)((uintptr_t)p >> 32)) << 32;
-    asm volatile("s_nop 4" : "+s"(b));
-    return (const char *)b;
+    return (const char *)((unsigned)uniform((int)(uintptr_t)p) | (unsigned long long)(unsigned)uniform((int)((uintptr_t)p >> 32)) << 32);
+}
+// copy16s from an address that a vector instruction may have written last (a readfirstlane,
+// or a scalar register that the compiler kept in a vector register's lane): the load reads it
+// five wait states after the asm begins.
+__device__ __forceinline__ void copy16u(const void *base, unsigned off, const char *lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_at(lds)) : "m0");
 }
 
 // Operands that a loop holds in registers, there before it begins: the compiler waits for a
@@ -223,12 +225,20 @@ template <typename T> __device__ __forceinline__ void landed(Frag<T> &f) {
 }
 
 // Enqueue the copy of packed rows r0 .. r0 + ROWS - 1 (CPR chunks each, `stride` bytes apart,
-// x: row 0) into an LDS tile, as load_rows does; the row and the address may be in vector
-// registers, but are the same in every lane.  Rows from n on read as zeros.
-template <int CPR, int ROWS> __device__ __forceinline__ void load_tile(char *tile, const char *x, long stride, int r0, int n)
+// x: row 0) into an LDS tile by 256 threads, tid 0 .. 255; the row and the address may be in
+// vector registers, but are the same in every lane.  Rows from n on read as zeros.
+template <int CPR, int ROWS> __device__ __forceinline__ void load_tile(char *tile, const char *x, long stride, int r0, int n, int tid)
 {
-    const char *p = uniform(x + r0 * stride);
-    load_rows<CPR, ROWS>(tile, p, stride, 0, uniform(n - r0));
+    constexpr int RP = 256 / CPR;
+    static_assert(RP % 8 == 0 && ROWS % RP == 0, "");
+    const char *p = uniform(x + r0 * stride), *dst = tile + uniform(tid >> 6) * 1024;
+    const int row = tid / CPR, left = uniform(n - r0);
+#pragma unroll
+    for (int i = 0; i < ROWS / RP; ++i) {
+        const int ch = ((tid % CPR) ^ swz<CPR>(i * RP + row)) * 16;   // the same for all i, but for row bit 3 where RP is 8
+        if (left >= ROWS) copy16u(p + i * RP * stride, (unsigned)(row * (int)stride + ch), dst + i * 4096);
+        else copy16(i * RP + row < left ? p + (i * RP + row) * stride + ch : (const char *)latent_zero, dst + i * 4096);
+    }
 }
 
 // Shares: calls of few owners (row tiles, key tiles) with long walks are cut over a fixed

@@ -150,8 +150,8 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
             const int x = g0 + i * RP + row, t = (int)(__umul24(x, a.g_mul16) >> 16), g = x - t * a.G;
             const unsigned in = g * (D * C::ES) + ch, oq = __umul24(t, qst) + in, od = __umul24(t, ost) + in;
             if (left >= ST) {
-                copy16s(q, oq, to + i * 512 * 16);
-                copy16s(d_o, od, to + C::OFF_V + i * 512 * 16);
+                copy16u(q, oq, to + i * 512 * 16);
+                copy16u(d_o, od, to + C::OFF_V + i * 512 * 16);
             } else {
                 const bool is = i * RP + row < left;
                 copy16(is ? q + oq : (const char *)latent_zero, to + i * 512 * 16);
@@ -394,8 +394,8 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
     const int wfull = off + t0 + quotient(lr0, a.g_mul, a.g_shift) + 1;
     auto load = [&](int j) {
         char *to = lds + (j & 1) * C::BUF;
-        load_tile<C::CPR, ST>(to, (const char *)k, a.ks * C::ES, j * ST, n);
-        load_tile<C::CPR, ST>(to + C::OFF_V, (const char *)v, a.vs * C::ES, j * ST, n);
+        load_tile<C::CPR, ST>(to, (const char *)k, a.ks * C::ES, j * ST, n, threadIdx.x);
+        load_tile<C::CPR, ST>(to + C::OFF_V, (const char *)v, a.vs * C::ES, j * ST, n, threadIdx.x);
     };
     const int rb = row_base<T, C::CPR>(r16), cb = col_base<T, C::CPR>(4 * gq);
     // of 32 keys (block t of tile j): P, and dP in the same layout

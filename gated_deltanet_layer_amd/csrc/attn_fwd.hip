@@ -37,13 +37,19 @@ struct AttnFwdWs {
 
 constexpr int FWD_LEAST = 4;   // key tiles of a share
 
-template <typename T, int D, int NR, bool SHARES>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
+// KS: groups of four waves that take the key tiles of a row tile in turn, each with buffers of
+// its own, and put their sums together at the end: two for calls that leave compute units idle.
+enum { WHOLE, HALVES, SHARED };
+template <typename T, int D, int NR, int FORM>
+__global__ __launch_bounds__(FORM == HALVES ? 512 : 256, FORM == HALVES ? 1 : 2) void attn_fwd_kernel(AttnArgs a, int per)
 {
     typedef AttnFwdCfg<T, D, NR> C;
-    constexpr int KT = C::KT, RT = C::RT, NKB = D / 32, NS = KT / 16, NCB = D / 16;
-    extern __shared__ char lds[];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane_r16(), gq = lane_gq();
+    constexpr int KT = C::KT, RT = C::RT, NKB = D / 32, NS = KT / 16, NCB = D / 16, KS = FORM == HALVES ? 2 : 1;
+    constexpr bool SHARES = FORM == SHARED;
+    extern __shared__ char all_lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3, r16 = lane_r16(), gq = lane_gq();
+    const int half = KS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0, tid = threadIdx.x & 255;
+    char *lds = all_lds + half * 2 * C::BUF;
     const float c = a.scale * LOG2E;
     const int share = SHARES ? blockIdx.x % 8 * (ATTN_SHARES / 8) + blockIdx.x / 8 : 0;   // a head's on one XCD
     auto make = [&](const Seq &s) { return AttnTiles(per, s); };
@@ -62,16 +68,17 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
         cur.s = seq_of(a, it.b);
         cur.j = 0;
         cur.n = cur.end = uniform((make(cur.s).walk(cur.t) + KT - 1) / KT);
-        any = cur.end > 0;
+        if (half > 0 && cur.end < 2) return;   // nothing to take
+        any = cur.end > half;
     }
     auto load = [&](const Run &r, int j, int buffer) {
         char *buf = lds + buffer * C::BUF;
         const T *k = (const T *)a.k + r.s.k0 * a.ks + r.h * D, *v = (const T *)a.v + r.s.k0 * a.vs + r.h * D;
-        load_tile<C::CPR, KT>(buf, (const char *)k, a.ks * C::ES, j * KT, r.s.lk);
-        load_tile<C::CPR, KT>(buf + C::OFF_V, (const char *)v, a.vs * C::ES, j * KT, r.s.lk);
+        load_tile<C::CPR, KT>(buf, (const char *)k, a.ks * C::ES, j * KT, r.s.lk, tid);
+        load_tile<C::CPR, KT>(buf + C::OFF_V, (const char *)v, a.vs * C::ES, j * KT, r.s.lk, tid);
     };
     const int kb0 = row_base<T, C::CPR>(r16), vb = col_base<T, C::CPR>(4 * gq);
-    if (any) load(cur, cur.j, 0);
+    if (any) load(cur, cur.j + half, 0);
     int buffer = 0;
     bool more = false;
     for (;;) {   // one row tile, or what the share has of it
@@ -108,19 +115,19 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
         const int wend = min(lr0 + 16 * NR, nlive) - 1;
         const int wlast = wend < lr0 ? 0 : off + cur.t * per + quotient(max(wend, 0), a.g_mul, a.g_shift) + 1;
         const int wfull = off + cur.t * per + quotient(lr0, a.g_mul, a.g_shift) + 1;
-        for (int j = cur.j; j < cur.end; ++j) {
+        for (int j = cur.j + half; j < cur.end + half; j += KS) {   // as many times in both halves
             const char *kt = lds + buffer * C::BUF, *vt = kt + C::OFF_V;
             const int k0 = j * KT;
             wait_vm<0>();
             lds_barrier();
             buffer ^= 1;
-            if (j + 1 < cur.end) {
-                load(cur, j + 1, buffer);
+            if (j + KS < cur.end) {
+                load(cur, j + KS, buffer);
             } else if (SHARES) {
                 more = share_next<KT>(a, make, sh);
                 if (more) load(sh.r, sh.r.j, buffer);
             }
-            if (k0 >= wlast) continue;   // nothing for this wave in the tile
+            if (k0 >= wlast || (KS > 1 && j >= cur.end)) continue;   // nothing for this wave in the tile
             f32x4 s[NS][NR];
 #pragma unroll
             for (int t = 0; t < NS; ++t) {
@@ -185,6 +192,31 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a, int per)
                 }
             }
             if (sizeof(T) == 2) pipeline<4, NS * NCB, NS / 2 * NCB * NR, 2, NR>();
+        }
+        if (KS > 1 && cur.end > 1) {   // the second half's maxima and sums, through LDS, to the first
+            lds_barrier();
+            f32x4 *to = (f32x4 *)all_lds + wave * (NCB * NR + 1) * 64 + (threadIdx.x & 63);
+            static_assert(4 * (NCB * NR + 1) * 64 * 16 <= 4 * C::BUF && NR <= 2, "");
+            if (half > 0) {
+                f32x4 ml = {m[0], l[0], m[NR - 1], l[NR - 1]};
+                to[0] = ml;
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) to[(1 + cb * NR + g) * 64] = acc[cb][g];
+            }
+            lds_barrier();
+            if (half > 0) return;
+            const f32x4 ml = to[0];
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+                const float m1 = ml[2 * g], mn = fmaxf(m[g], m1);
+                const float f0 = m[g] == -INFINITY ? 0.f : exp2_hw((m[g] - mn) * c), f1 = m1 == -INFINITY ? 0.f : exp2_hw((m1 - mn) * c);
+                m[g] = mn;
+                l[g] = l[g] * f0 + ml[2 * g + 1] * f1;
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb) acc[cb][g] = acc[cb][g] * f0 + to[(1 + cb * NR + g) * 64] * f1;
+            }
         }
         const bool whole = !SHARES || (cur.j == 0 && cur.end == cur.n);
         const AttnFwdWs lay(a.B, RT, D);
@@ -258,13 +290,17 @@ template <typename T, int D, int NR> __global__ __launch_bounds__(256) void attn
     if (a.lse && at == 0) a.lse[row] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
 }
 
-template <typename T, int D, int NR> static hipError_t fwd_enqueue(const AttnArgs &a, const AttnFwdPlan &plan, hipStream_t st)
+template <typename T, int D, int NR, int FORM> static hipError_t fwd_enqueue(const AttnArgs &a, const AttnFwdPlan &plan, hipStream_t st)
 {
     typedef AttnFwdCfg<T, D, NR> C;
-    auto k = plan.shares ? attn_fwd_kernel<T, D, NR, true> : attn_fwd_kernel<T, D, NR, false>;
-    static_assert(2 * C::BUF <= 64 * 1024, "more dynamic LDS has to be asked for");
-    hipLaunchKernelGGL(k, dim3((unsigned)(plan.shares ? plan.shares : plan.tiles * a.Hk)), dim3(256), 2 * C::BUF, st, a, plan.tokens);
-    if (plan.shares) {
+    constexpr int KS = FORM == HALVES ? 2 : 1, BYTES = KS * 2 * C::BUF;
+    auto k = attn_fwd_kernel<T, D, NR, FORM>;
+    if (BYTES > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(k, dim3((unsigned)(FORM == SHARED ? plan.shares : plan.tiles * a.Hk)), dim3(KS * 256), BYTES, st, a, plan.tokens);
+    if (FORM == SHARED) {
         const long rows = (long)a.Tq * a.Hk * a.G, each = 256 / (D / 4);
         hipLaunchKernelGGL((attn_fwd_join_kernel<T, D, NR>), dim3((unsigned)((rows + each - 1) / each)), dim3(256), 0, st, a, plan.tokens);
     }
@@ -276,9 +312,10 @@ template <typename T, int D> static hipError_t fwd_launch(AttnArgs a, hipStream_
     const AttnFwdPlan plan = attn_fwd_plan(sizeof(T) == 2, a.B, a.Tq, a.Tk, a.Hk, a.G);
     divisor(a.G, a.g_mul, a.g_shift);
     if constexpr (sizeof(T) == 2) {
-        if (plan.nr == 2) return fwd_enqueue<T, D, 2>(a, plan, st);
+        if (plan.nr == 2) return plan.shares ? fwd_enqueue<T, D, 2, SHARED>(a, plan, st) : fwd_enqueue<T, D, 2, WHOLE>(a, plan, st);
     }
-    return fwd_enqueue<T, D, 1>(a, plan, st);
+    if (plan.shares) return fwd_enqueue<T, D, 1, SHARED>(a, plan, st);
+    return plan.halves ? fwd_enqueue<T, D, 1, HALVES>(a, plan, st) : fwd_enqueue<T, D, 1, WHOLE>(a, plan, st);
 }
 
 hipError_t attn_fwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st)

@@ -15,18 +15,24 @@ struct AttnFwdPlan {
     int nr;        // 16-row groups a wave: a row tile has 64 nr rows
     int tokens;    // of a row tile
     int shares;    // 0: a workgroup for every row tile
+    bool halves;   // whose waves take the key tiles in two groups
     long tiles;    // row tiles of one key head, at most
 };
 
 // Rows: two groups a wave (each key operand serves two products) once that gives every
 // compute unit a workgroup.
 //
+// Halves: with a workgroup a unit or fewer, and one row group a wave, four more waves take
+// every other key tile (32 over 8 heads of 128, 333 rows 11.4 us from 12.8; 8 over 2, 1000
+// rows 20 from 26).
+//
 // Shares: with fewer row tiles than two a unit, the longest row is the call's time unless all
 // rows' key tiles are shared equally; but a share begins, changes rows and is joined for
 // some 12 us.  Lengths are on the device, so the rule takes the call for up to four sequences
-// of equal length, and shares from 20 key tiles a sequence on (8 over 2 heads of 128 in bf16:
-// one sequence of 1000 25.7 us, whole 25.6; of 2048 36, 46; of 4096 64, 81; four of 1000 41,
-// 29; fp32, D = 64: one of 1000 31, 49; three of 1000 53, 57).
+// of equal length, and shares from 20 key tiles a sequence on, or 36 where halves would do in
+// bf16 (8 over 2 heads of 128: one sequence of 1000 26 us, in halves 21; of 2048 36, 35; 4
+// over 1, of 4096 48, 62; whole, four of 1000 41, 29, one of 4096 64, 81; fp32, D = 64: one of
+// 1000 31, 44; three of 1000 53, 57).
 inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G)
 {
     AttnFwdPlan p;
@@ -35,7 +41,9 @@ inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G
     p.tokens = 64 * p.nr / G;
     p.tiles = Tq / p.tokens + (B < Tq ? B : Tq);
     const long wgs = ((Tq + p.tokens - 1) / p.tokens) * (long)Hk, each = B > 0 ? Tk / (B < 4 ? B : 4) : 0;
-    p.shares = wgs > 0 && wgs < ATTN_SHARES && each >= 20 * (bf16 ? 64 : 32) ? ATTN_SHARES : 0;
+    const long least = !bf16 ? 20 * 32 : p.nr == 1 && wgs <= 256 ? 36 * 64 : 20 * 64;
+    p.shares = wgs > 0 && wgs < ATTN_SHARES && each >= least ? ATTN_SHARES : 0;
+    p.halves = !p.shares && p.nr == 1 && wgs <= 256;
     return p;
 }
 
