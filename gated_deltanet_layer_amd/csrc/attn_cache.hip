@@ -80,8 +80,52 @@ struct BlockScale {
     }
 };
 
-// One wave a block, head and kind.  Keys: 16 channels of a token a lane, 16 bytes as they are
-// stored.  Values: D / 64 channels of all 16 tokens a lane, the 16 bytes of each channel.
+// Values of 16 tokens from lanes that hold four tokens (4 q .. 4 q + 3 in 16-lane row q) of NC
+// channels each, as one dword a channel, to lanes that hold all 16 tokens of NC / 4 channels:
+// row q then has channels NC / 4 q and on.  Two rounds of swaps between rows.
+template <int NC> __device__ __forceinline__ void turn_tokens(const unsigned (&x)[NC], u32x4 (&w)[NC / 4])
+{
+    unsigned lo[NC / 2], hi[NC / 2];   // tokens 0-7, tokens 8-15
+#pragma unroll
+    for (int e = 0; e < NC / 2; ++e) {
+        const auto s = __builtin_amdgcn_permlane32_swap(x[e], x[e + NC / 2], false, false);
+        lo[e] = s[0];
+        hi[e] = s[1];
+    }
+#pragma unroll
+    for (int e = 0; e < NC / 4; ++e) {
+        const auto a = __builtin_amdgcn_permlane16_swap(lo[e], lo[e + NC / 4], false, false);
+        const auto b = __builtin_amdgcn_permlane16_swap(hi[e], hi[e + NC / 4], false, false);
+        w[e] = u32x4{(unsigned)a[0], (unsigned)a[1], (unsigned)b[0], (unsigned)b[1]};
+    }
+}
+
+// N consecutive values, 4 or a multiple of 8.
+template <int N, typename T> __device__ __forceinline__ void load_values(const T *p, float *v)
+{
+    if constexpr (N == 4 && sizeof(T) == 2) {
+        const bf16x4 y = *reinterpret_cast<const bf16x4 *>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)y[e];
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int c = 0; c < N; c += 8) {
+            const bf16x8 y = *reinterpret_cast<const bf16x8 *>(p + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[c + e] = (float)y[e];
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+            const f32x4 y = *reinterpret_cast<const f32x4 *>(p + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[c + e] = y[e];
+        }
+    }
+}
+
+// One wave a block, head and kind, 16 bytes a lane to the cache.  Keys: a lane has 16 channels
+// of a token.  Values: D / 16 channels of four tokens, turned to D / 64 channels of all.
 template <typename T, int D> __global__ __launch_bounds__(256) void attn_append_kernel(AttnCacheArgs a)
 {
     const int unit = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -101,51 +145,46 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_append_
     float *sp = (isv ? a.v_scale : a.k_scale) + gb;
     char *cache = (char *)(isv ? a.v_cache : a.k_cache) + (long)gb * CACHE_BLOCK * D;
     if (isv) {
-        constexpr int CH = D / 64;
-        const T *x = (const T *)a.v + h * D + lane * CH;
+        constexpr int NC = D / 16, CH = D / 64;
+        const int q = lane >> 4, ch = (lane & 15) * NC;
+        const T *x = (const T *)a.v + h * D + ch;
         const unsigned slots = (0xffffu >> (16 - hi)) & (0xffffu << lo), older = (1u << lo) - 1;
         const bool part = hi - lo < CACHE_BLOCK;
-        u32x4 *p = (u32x4 *)(cache + lane * CH * CACHE_BLOCK), w[CH];
+        u32x4 *p = (u32x4 *)(cache + (ch + q * CH) * CACHE_BLOCK), w[CH], old[CH];
         if (part) {
 #pragma unroll
-            for (int e = 0; e < CH; ++e) w[e] = p[e];
+            for (int e = 0; e < CH; ++e) old[e] = p[e];
         }
-        float v[16][CH];
+        float v[4][NC];
         int most = 0;
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
+        for (int i = 0; i < 4; ++i) {
+            const int t = 4 * q + i;
 #pragma unroll
-            for (int e = 0; e < CH; ++e) v[t][e] = 0.f;
-            if (t >= lo && t < hi) {
-                if constexpr (CH == 2) {
-                    typedef T Pair __attribute__((ext_vector_type(2)));
-                    const Pair y = *reinterpret_cast<const Pair *>(x + (row + t) * a.vs);
-                    v[t][0] = to_f32(y[0]);
-                    v[t][1] = to_f32(y[1]);
-                } else {
-                    v[t][0] = to_f32(x[(row + t) * a.vs]);
-                }
-            }
+            for (int e = 0; e < NC; ++e) v[i][e] = 0.f;
+            if (t >= lo && t < hi) load_values<NC>(x + (row + t) * a.vs, v[i]);
         }
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < CH; ++e) most = max(most, magnitude(v[t][e]));
+            for (int e = 0; e < NC; ++e) most = max(most, magnitude(v[i][e]));
         const BlockScale s(max_lanes(most), lo > 0, sp);
+        unsigned four[NC];
 #pragma unroll
-        for (int e = 0; e < CH; ++e)
+        for (int e = 0; e < NC; ++e)
+            four[e] = fp8_four(stored(v[0][e], s.inv), stored(v[1][e], s.inv), stored(v[2][e], s.inv), stored(v[3][e], s.inv));
+        turn_tokens<NC>(four, w);
+        if (part) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                auto bytes = [&](unsigned m) { return (((m >> (4 * i)) & 15u) * 0x00204081u & 0x01010101u) * 0xffu; };
-                unsigned nw = fp8_four(stored(v[4 * i][e], s.inv), stored(v[4 * i + 1][e], s.inv), stored(v[4 * i + 2][e], s.inv),
-                                       stored(v[4 * i + 3][e], s.inv));
-                if (part) {
-                    unsigned held = w[e][i];
+            for (int e = 0; e < CH; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    auto bytes = [&](unsigned m) { return (((m >> (4 * i)) & 15u) * 0x00204081u & 0x01010101u) * 0xffu; };
+                    unsigned held = old[e][i];
                     if (s.moved != 1.f) held = (held & ~bytes(older)) | ((unsigned)fp8_moved((int)held, s.moved) & bytes(older));
-                    nw = (held & ~bytes(slots)) | (nw & bytes(slots));
+                    w[e][i] = (held & ~bytes(slots)) | (w[e][i] & bytes(slots));
                 }
-                w[e][i] = nw;
-            }
+        }
 #pragma unroll
         for (int e = 0; e < CH; ++e) p[e] = w[e];
         if (lane == 0) *sp = s.scale;
@@ -160,17 +199,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_append_
             const int t = i * RP + t0;
 #pragma unroll
             for (int e = 0; e < 16; ++e) k[i][e] = 0.f;
-            if (t >= lo && t < hi) {
-#pragma unroll
-                for (int c = 0; c < 16; c += 8) {
-                    const Frag<T> y = load_frag<T>(x + (row + t) * a.ks + c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if constexpr (sizeof(T) == 2) k[i][c + e] = (float)y.v[e];
-                        else k[i][c + e] = e < 4 ? y.lo[e] : y.hi[e - 4];
-                    }
-                }
-            }
+            if (t >= lo && t < hi) load_values<16>(x + (row + t) * a.ks, k[i]);
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i)
