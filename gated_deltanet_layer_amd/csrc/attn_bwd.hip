@@ -7,8 +7,8 @@
 // (token, head) in one run, as in the forward's tiles.  No atomics, so results do not depend
 // on the order in which workgroups run: one kernel owns query rows and walks their keys (dq),
 // one owns keys and walks the rows that see them (dk, dv); the scores are computed in both.
-// Where the owners are too few for the device, what walks by is cut into pieces, whose sums a
-// third kernel adds up in order.
+// What walks by keys is shared by a fixed number of workgroups, what walks by few query rows is
+// cut into pieces; the sums of what is cut a third kernel adds up in order.
 #include "attn.h"
 
 namespace gdn {
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
         for (int i = 0; i < NC; ++i) dq[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int all = uniform((tl.walk(it.i) + ST - 1) / ST);
-    const int j0 = CUT ? piece * (plan.kstep / ST) : 0, nt = CUT ? min(all, j0 + plan.kstep / ST) : all;
+    const int j0 = CUT ? piece * (plan.kstep / ST) : 0, nt = CUT && piece + 1 < plan.kp ? min(all, j0 + plan.kstep / ST) : all;
     if (CUT && piece > 0 && nt <= j0) return;   // the last kernel knows which pieces there are
     // keys that some, that all of the wave's rows see
     const int wend = min(lr0 + 16 * NG, nlive) - 1;
@@ -535,7 +535,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_bwd_sum
     if (i < 0 || i >= (isq ? s.lq : s.lk)) return;   // of no sequence
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if (isq) {   // the owner of the row walks the keys up to its last row's position; piece 0 always writes
-        const int end = max(1, (AttnTiles(plan.tokens, s).walk(i / plan.tokens) + plan.kstep - 1) / plan.kstep);
+        const int end = min(plan.kp, max(1, (AttnTiles(plan.tokens, s).walk(i / plan.tokens) + plan.kstep - 1) / plan.kstep));
         const float *part = (const float *)((const char *)a.ws + lay.dq) + at;
         for (int p = 0; p < end; ++p) x += *reinterpret_cast<const f32x4 *>(part + p * (long)T_ * H * W);
         store4((T *)a.dq + token * a.dqs + head * D + col, x);

@@ -54,10 +54,10 @@ constexpr int attn_own(bool bf16) { return bf16 ? 128 : 64; }
 constexpr int attn_walk(bool bf16) { return bf16 ? 64 : 32; }
 
 struct AttnBwdPlan {
-    int tokens;          // of a query tile, which has 128 (64) rows
-    int kp, kstep;       // pieces of the walked keys (dq), and the keys of one
-    int shares;          // workgroups that share the walked rows of all keys (dk, dv)
-    long qtiles;         // query tiles of one key head, at most
+    int tokens;      // of a query tile, which has attn_own() rows
+    long qtiles;     // query tiles of one key head, at most
+    int kp, kstep;   // pieces of the keys that walk by them (dq), and the keys of one
+    int shares;      // workgroups that share the rows that walk by all keys (dk, dv)
 };
 
 // Pieces of `tiles` walked tiles, `least` tiles each or more, to give `fill` workgroups.
@@ -70,20 +70,24 @@ inline int attn_pieces(long wgs, long fill, long tiles, int least)
     return (int)(n > most ? most : n);
 }
 
-// The walk of one sequence that has all rows is the longest that a call may have.
 inline AttnBwdPlan attn_bwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G)
 {
     AttnBwdPlan p;
-    const int own = attn_own(bf16), st = attn_walk(bf16), least = bf16 ? 2 : 1;
-    const long rows = (long)Tq * G, nk = (Tk + st - 1) / st;
+    const int own = attn_own(bf16), st = attn_walk(bf16), least = bf16 ? 4 : 1;
     p.tokens = own / G;
     p.qtiles = Tq / p.tokens + (B < Tq ? B : Tq);
-    const int kp = attn_pieces(Hk * ((long)(Tq + p.tokens - 1) / p.tokens), 512, nk, least);
-    p.kstep = (int)((nk + kp - 1) / kp * st);
-    p.kp = kp > 1 ? (Tk + p.kstep - 1) / p.kstep : 1;
-    // one workgroup a compute unit (two do not fit its LDS), and eight at a time, as there are
+    // dq, below two workgroups a unit: pieces for up to eight sequences of equal length (the
+    // lengths are on the device), the last with what a longer one has more, of four tiles (fp32
+    // one) or more.  8 over 2 heads of 128: eight sequences of 300 65 us cut, 45 whole; one of
+    // 700 43, 55; of 1000 48, 65; of 2048 80, 106; 16 over 4, one of 333 41 both; fp32, D = 64,
+    // 4 heads of 300 25 (26 with two), 41.
+    const long walk = B > 0 ? (Tk / (B < 8 ? B : 8) + st - 1) / st : 0;
+    const int kp = attn_pieces(Hk * ((long)(Tq + p.tokens - 1) / p.tokens), 512, walk, least);
+    p.kp = kp;
+    p.kstep = (int)(kp > 1 ? (walk + kp - 1) / kp * st : 0);
+    // dk and dv: one workgroup a unit (two do not fit its LDS), eight at a time, as there are
     // XCDs; fewer where the call cannot have two tiles for each
-    const long tiles = Hk * ((long)(Tk + own - 1) / own + (B < Tk ? B : Tk)) * ((rows + st - 1) / st);
+    const long tiles = Hk * (Tk / own + (long)(B < Tk ? B : Tk)) * (((long)Tq * G + st - 1) / st);
     p.shares = tiles >= 2 * 256 ? 256 : (int)((tiles / 2 + 8) & ~7L);
     return p;
 }
