@@ -136,6 +136,9 @@ __device__ __forceinline__ int max_lanes(int x) {
                max(__builtin_amdgcn_readlane(x, 47), __builtin_amdgcn_readlane(x, 63)));
 }
 
+// x, which every lane of the wave has, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // Item w of a list to which sequence b gives count(b) items: the sequence and the item's
 // number within it; -1 where the list is shorter.  Every lane of the wave calls it.
 struct Item {
@@ -157,7 +160,23 @@ template <typename F> __device__ __forceinline__ Item find_item(int B, int w, F 
     return {-1, 0};
 }
 
-// The same list with the last items of all sequences first: item i of every sequence
+// The last of B sequences with from(b) <= w, for numbers that rise from from(0) <= w on, by
+// 64 probes at a time.
+template <typename F> __device__ __forceinline__ int find_slot(int B, int w, F from)
+{
+    const int lane = threadIdx.x & 63;
+    int at = 0;
+    while (B > 1) {
+        const int step = (B + 63) >> 6, b = lane * step;
+        const unsigned long long ok = __ballot(b < B && from(at + b) <= w);
+        const int l = ok ? 63 - (int)__builtin_clzll(ok) : 0;
+        at += l * step;
+        B = min(step, B - l * step);
+    }
+    return uniform(at);
+}
+
+// The list of find_item with the last items of all sequences first: item i of every sequence
 // stands behind items i + 1 of all of them.  Rows further down a causal sequence have more
 // keys, so that the longest work begins first.
 template <typename F> __device__ __forceinline__ Item find_last(int B, int w, F count)
@@ -204,8 +223,7 @@ struct AttnTiles {
     }
 };
 
-// x, which every lane of the wave has, in a scalar register.
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// The same of an address.
 __device__ __forceinline__ const char *uniform(const void *p) {
     return (const char *)((unsigned)uniform((int)(uintptr_t)p) | (unsigned long long)(unsigned)uniform((int)((uintptr_t)p >> 32)) << 32);
 }
@@ -239,6 +257,17 @@ template <int CPR, int ROWS> __device__ __forceinline__ void load_tile(char *til
         if (left >= ROWS) copy16u(p + i * RP * stride, (unsigned)(row * (int)stride + ch), dst + i * 4096);
         else copy16(i * RP + row < left ? p + (i * RP + row) * stride + ch : (const char *)latent_zero, dst + i * 4096);
     }
+}
+
+// Row tile w of a call's `most`, -1 where there are fewer.  Up to 64 sequences, the tiles with
+// the most keys first.  Beyond, where that search would take longer than the tile: tile t of
+// sequence b is number cu_q[b] / per + b + t, which leaves gaps, from the last one down.
+__device__ __forceinline__ Item find_tile(const AttnArgs &a, int per, int w, int most)
+{
+    if (a.B <= 64) return find_last(a.B, w, [&](int b) { return AttnTiles(per, seq_lane(a, b)).count(); });
+    auto from = [&](int b) { return within(a.cu_q[b], a.Tq) / per + b; };
+    const int b = find_slot(a.B, most - 1 - w, from), t = most - 1 - w - from(b);
+    return {t >= 0 && t < AttnTiles(per, seq_lane(a, b)).count() ? b : -1, t};
 }
 
 // Shares: calls of few owners (row tiles, key tiles) with long walks are cut over a fixed

@@ -70,9 +70,10 @@ gdn_status attn_sizes(int B, int Tq, int Tk, int Hq, int Hk, int D, gdn_dtype dt
     if (prod(Tq, Hq, D, 4) < 0 || prod(Tk, Hk, D, 4) < 0) return GDN_EINVAL;
     if ((D != 64 && D != 128) || Hq / Hk > 64 || Hq > (1 << 14)) return GDN_ENOTSUP;
     // rows of a key head (token, head) in 30 bits, those of all heads in 28; grids: workgroups * threads < 2^32
+    // (64 threads a key where dk and dv are added up)
     const bool bf16 = dtype == GDN_BF16;
     const int G = Hq / Hk;
-    if (((long long)Tq + Tk) * G >= (1LL << 30) || prod(Tq, Hq) >= (1LL << 28) || prod(Tk, Hk) >= (1LL << 28)) return GDN_ENOTSUP;
+    if (((long long)Tq + Tk) * G >= (1LL << 30) || prod(Tq, Hq) >= (1LL << 28) || prod(Tk, Hk) >= (1LL << 26)) return GDN_ENOTSUP;
     if (B >= (1 << 24)) return GDN_ENOTSUP;
     const gdn::AttnFwdPlan f = gdn::attn_fwd_plan(bf16, B, Tq, Tk, Hk, G);
     const gdn::AttnBwdPlan b = gdn::attn_bwd_plan(bf16, B, Tq, Tk, Hk, G);
@@ -298,7 +299,7 @@ gdn_status gdn_attn_step_workspace_size(int N, int Hq, int Hk, int D, int page, 
     if (!bytes || Hq <= 0 || Hk <= 0 || Hq % Hk != 0) return GDN_EINVAL;
     const gdn_status st = cache_sizes(N, Hk, D, 0, page, width);
     if (st != GDN_OK) return st;
-    if (Hq / Hk > 64 || prod(N, Hq) >= (1LL << 24)) return GDN_ENOTSUP;
+    if (Hq / Hk > 64 || prod(N, Hq) >= (1LL << 23)) return GDN_ENOTSUP;
     *bytes = (size_t)gdn::attn_step_workspace(N, Hk, Hq / Hk, D, page, width);
     return GDN_OK;
 }
@@ -311,8 +312,8 @@ gdn_status gdn_attn_step(const void *q, const void *k_cache, const void *v_cache
     if (!dtype_ok(dtype) || Hq <= 0 || !scale_ok(scale)) return GDN_EINVAL;
     gdn_status st = cache_sizes(N, Hk, D, pages, page, width);
     if (st == GDN_EINVAL || Hq % Hk != 0) return GDN_EINVAL;
-    // the join's grid: a workgroup of 256 threads for eight or sixteen rows
-    if (Hq / Hk > 64 || prod(N, Hq) >= (1LL << 24)) st = GDN_ENOTSUP;
+    // the grid: a workgroup of 256 threads for each 16 heads, and those that share the tiles
+    if (Hq / Hk > 64 || prod(N, Hq) >= (1LL << 23)) st = GDN_ENOTSUP;
     const long long es = dtype == GDN_BF16 ? 2 : 4, bytes = prod(N, Hq, D, es);
     if (bytes < 0) return GDN_EINVAL;
     if (N > 0 && (!q || !lens || !o || (width > 0 && !table))) return GDN_EINVAL;

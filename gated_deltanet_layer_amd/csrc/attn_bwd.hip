@@ -338,7 +338,8 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
     constexpr bool BF = sizeof(T) == 2;
     extern __shared__ char lds[];
     const int h = blockIdx.x % a.Hk, piece = CUT ? blockIdx.x / a.Hk % plan.kp : 0, per = plan.tokens;
-    const Item it = find_last(a.B, blockIdx.x / a.Hk / (CUT ? plan.kp : 1), [&](int b) { return AttnTiles(per, seq_lane(a, b)).count(); });
+    const int pieces = CUT ? plan.kp : 1;
+    const Item it = find_tile(a, per, blockIdx.x / a.Hk / pieces, gridDim.x / a.Hk / pieces);
     if (it.b < 0) return;
     const Seq sq = seq_of(a, it.b);
     const AttnTiles tl(per, sq);

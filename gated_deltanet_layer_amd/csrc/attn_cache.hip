@@ -133,10 +133,13 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_append_
     const int h = unit >> 1;
     const bool isv = unit & 1;
     Item it = {(int)blockIdx.x, 0};
-    if (a.cu) it = find_item(a.N, blockIdx.x, [&](int n) { return fresh_blocks(fresh(a, n)); });
-    if (it.b < 0) return;
+    if (a.cu) {   // n tokens touch n / 16 + 2 blocks at most: those of a sequence begin at
+        auto from = [&](int n) { return within(a.cu[n], a.T) / CACHE_BLOCK + 2 * n; };
+        it.b = find_slot(a.N, blockIdx.x, from);
+        it.i = (int)blockIdx.x - from(it.b);
+    }
     const Fresh f = fresh(a, it.b);
-    if (it.i >= fresh_blocks(f)) return;
+    if (it.i < 0 || it.i >= fresh_blocks(f)) return;
     const int blk = f.lo / CACHE_BLOCK + it.i, base = blk * CACHE_BLOCK;
     const int lo = max(f.lo - base, 0), hi = min(f.hi - base, CACHE_BLOCK);   // slots of new tokens
     const int gb = cache_block(a, it.b, h, blk);

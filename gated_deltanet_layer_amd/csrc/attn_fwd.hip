@@ -61,7 +61,7 @@ __global__ __launch_bounds__(FORM == HALVES ? 512 : 256, FORM == HALVES ? 1 : 2)
         cur = sh.r;
     } else {
         cur.h = blockIdx.x % a.Hk;
-        const Item it = find_last(a.B, blockIdx.x / a.Hk, [&](int b) { return make(seq_lane(a, b)).count(); });
+        const Item it = find_tile(a, per, blockIdx.x / a.Hk, gridDim.x / a.Hk);
         if (it.b < 0) return;
         cur.b = it.b;
         cur.t = uniform(it.i);

@@ -6,6 +6,10 @@
 
 namespace gdn {
 
+// Row tiles of one key head, at most, and the numbers that they have (find_tile): a sequence
+// of l tokens has ceil(l / tokens).
+inline long attn_row_tiles(int B, int Tq, int tokens) { return Tq / tokens + (long)(B <= 64 && Tq < B ? Tq : B); }
+
 // --- packed forward -------------------------------------------------------------
 
 // The G query heads that share a key head stand side by side in a row tile: row r of a
@@ -39,7 +43,7 @@ inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G
     const long wide = (long)Tq * G / 128 * Hk;
     p.nr = bf16 && wide >= 256 ? 2 : 1;
     p.tokens = 64 * p.nr / G;
-    p.tiles = Tq / p.tokens + (B < Tq ? B : Tq);
+    p.tiles = attn_row_tiles(B, Tq, p.tokens);
     const long wgs = ((Tq + p.tokens - 1) / p.tokens) * (long)Hk, each = B > 0 ? Tk / (B < 4 ? B : 4) : 0;
     const long least = !bf16 ? 20 * 32 : p.nr == 1 && wgs <= 256 ? 36 * 64 : 20 * 64;
     p.shares = wgs > 0 && wgs < ATTN_SHARES && each >= least ? ATTN_SHARES : 0;
@@ -75,7 +79,7 @@ inline AttnBwdPlan attn_bwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G
     AttnBwdPlan p;
     const int own = attn_own(bf16), st = attn_walk(bf16), least = bf16 ? 4 : 1;
     p.tokens = own / G;
-    p.qtiles = Tq / p.tokens + (B < Tq ? B : Tq);
+    p.qtiles = attn_row_tiles(B, Tq, p.tokens);
     // dq, below two workgroups a unit: pieces for up to eight sequences of equal length (the
     // lengths are on the device), the last with what a longer one has more, of four tiles (fp32
     // one) or more.  8 over 2 heads of 128: eight sequences of 300 65 us cut, 45 whole; one of

@@ -139,7 +139,7 @@ def test_bwd_rejects_invalid(L, kw):
 @pytest.mark.parametrize("kw", [
     dict(D=96), dict(D=256, qs=1536, ks=512, vs=512, dqs=1536, dks=512, dvs=512), dict(Hq=130, qs=130 * 128, dqs=130 * 128),
     dict(Hq=1 << 15, Hk=1 << 15, qs=1 << 22, ks=1 << 22, vs=1 << 22, dqs=1 << 22, dks=1 << 22, dvs=1 << 22, Tq=1, Tk=1),
-    dict(Tq=1 << 26), dict(Tk=1 << 27), dict(Tq=1 << 23, Tk=1 << 23, Hq=128, Hk=2, qs=1 << 14, dqs=1 << 14), dict(B=1 << 24),
+    dict(Tq=1 << 26), dict(Tk=1 << 25), dict(Tq=1 << 23, Tk=1 << 23, Hq=128, Hk=2, qs=1 << 14, dqs=1 << 14), dict(B=1 << 24),
     dict(qs=(1 << 21) + 8), dict(vs=1 << 22)])
 def test_sequences_unsupported(L, call, kw):
     if call is _fwd:
@@ -190,7 +190,7 @@ def test_step_rejects_invalid(L, kw):
     assert _step(L, **kw) == gdn.GDN_EINVAL
 
 
-@pytest.mark.parametrize("kw", CACHE_WIDE + [dict(D=32), dict(Hq=130), dict(N=1 << 20, width=1, Hq=32)])
+@pytest.mark.parametrize("kw", CACHE_WIDE + [dict(D=32), dict(Hq=130), dict(N=1 << 18, width=1, Hq=32, Hk=16)])
 def test_step_unsupported(L, kw):
     assert _step(L, **kw) == gdn.GDN_ENOTSUP
 

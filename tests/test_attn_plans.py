@@ -13,11 +13,14 @@ def test_grids_cover_every_split_of_the_rows(dt):
     rng = random.Random(0)
     for _ in range(400):
         B, G, Hk = rng.choice((1, 2, 7, 64, 300)), rng.choice((1, 2, 3, 5, 8, 16, 33, 64)), rng.choice((1, 2, 8))
-        lens = [rng.choice((0, 1, 2, 3, 17, 64, 65, 400)) for _ in range(B)]
+        lens = [rng.choice((0, 0, 0, 1, 2, 3, 17, 64, 65, 400)[:rng.choice((4, 10))]) for _ in range(B)]
         T = sum(lens)
         f, b = attn_plans.fwd(dt, B, T, T, G * Hk, Hk), attn_plans.bwd(dt, B, T, T, G * Hk, Hk)
         for tokens, tiles in ((f["tokens"], f["tiles"]), (b["tokens"], b["qtiles"])):
             assert tokens >= 1 and sum(-(-n // tokens) for n in lens) <= tiles
+            if B > 64:   # tile t of sequence b is number start / tokens + b + t
+                starts = [sum(lens[:b]) // tokens + b for b in range(B + 1)]
+                assert all(a + -(-n // tokens) <= e for a, e, n in zip(starts, starts[1:], lens)) and starts[-1] <= tiles
         assert f["tokens"] * G <= 64 * f["nr"] and b["tokens"] * G <= (128 if dt == "bf16" else 64)
         assert b["shares"] % 8 == 0 and 8 <= b["shares"] <= 256
         st = 64 if dt == "bf16" else 32
