@@ -86,17 +86,23 @@ def _packed(t, name):
     return t.shape
 
 
+_like = torch.empty_like   # contiguous for slices along the heads too, and quicker than new_empty
+
+
 def _space(workspace, dev):
     if workspace is not None:
         _check(workspace, "workspace", device=torch.device("cuda", dev))
+
+
+_current, _raw_stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(t, stream, call):
     """``call(handle)`` with t's GPU current, and the stream that the work goes to."""
     if stream is None:
         i = t.get_device()
-        if i == torch._C._cuda_getDevice():
-            return call(torch._C._cuda_getCurrentRawStream(i))
+        if i == _current():
+            return call(_raw_stream(i))
     return _on_slow(t, stream, call)
 
 
@@ -110,14 +116,17 @@ def _prologue_args(q_raw, k_raw, w_q, w_k, inv_freq, pos):
     dt, dev = q_raw.dtype, q_raw.get_device()
     qs = _step_of(q_raw, "q_raw", T, Hq, D, dt, dev)
     ks = _step_of(k_raw, "k_raw", T, Hk, D, dt, dev)
-    _need(w_q, "w_q", (D,), torch.float32, dev)
-    _need(w_k, "w_k", (D,), torch.float32, dev)
+    f = torch.float32
+    if not (w_q.shape == (D,) and w_k.shape == (D,) and w_q.dtype is f and w_k.dtype is f and w_q.get_device() == dev
+            and w_k.get_device() == dev and w_q.is_contiguous() and w_k.is_contiguous()):
+        _need(w_q, "w_q", (D,), f, dev)
+        _need(w_k, "w_k", (D,), f, dev)
     R = 0
     if inv_freq is not None:
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq must be [R / 2]")
         R = 2 * inv_freq.shape[0]
-        _need(inv_freq, "inv_freq", (R // 2,), torch.float32, dev)
+        _need(inv_freq, "inv_freq", inv_freq.shape, f, dev)
         if pos is None:
             raise ValueError("pos is required for the rotation")
         _need(pos, "pos", (T,), torch.int32, dev)
@@ -148,7 +157,7 @@ def attn_prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, eps=1e-6, stream=None):
     sizes, steps, code = _prologue_args(q_raw, k_raw, w_q, w_k, inv_freq, pos)
 
     def call(handle):
-        q, k = q_raw.new_empty(q_raw.shape), q_raw.new_empty(k_raw.shape)
+        q, k = _like(q_raw), _like(k_raw)
         _prologue(q_raw, k_raw, w_q, w_k, inv_freq, pos, q, k, eps, sizes, steps, code, handle)
         return q, k
 
@@ -199,7 +208,7 @@ def attn_prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, eps=1e-6,
     steps += (max(Hq, 1) * D, max(Hk, 1) * D)
 
     def call(handle):
-        g = dict(dq_raw=q_raw.new_empty(q_raw.shape), dk_raw=q_raw.new_empty(k_raw.shape), dw_q=w_q.new_empty(D), dw_k=w_q.new_empty(D))
+        g = dict(dq_raw=_like(q_raw), dk_raw=_like(k_raw), dw_q=_like(w_q), dw_k=_like(w_k))
         ws = workspace if workspace is not None else \
             _workspace(_query("gdn_attn_prologue_bwd_workspace_size", *sizes, code), q_raw.device)
         _prologue_bwd(q_raw, k_raw, w_q, w_k, inv_freq, pos, d_q, d_k, g["dq_raw"], g["dk_raw"], g["dw_q"], g["dw_k"], ws,
@@ -266,7 +275,7 @@ def attn_fwd(q, k, v, cu_q, cu_k=None, scale=None, workspace=None, stream=None):
     _space(workspace, q.get_device())
 
     def call(handle):
-        o, lse = q.new_empty(q.shape), q.new_empty(q.shape[:2], dtype=torch.float32)
+        o, lse = _like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         ws = workspace if workspace is not None else _workspace(_query("gdn_attn_fwd_workspace_size", *sizes, code), q.device)
         _fwd(q, k, v, cu_q, cu_k, o, lse, ws, _scale(scale, sizes[5]), sizes, steps, code, handle)
         return o, lse
@@ -311,7 +320,7 @@ def attn_bwd(q, k, v, o, lse, d_o, cu_q, cu_k=None, scale=None, workspace=None, 
     steps += (Hq * D, Hk * D, Hk * D)
 
     def call(handle):
-        dq, dk, dv = q.new_empty(q.shape), q.new_empty(k.shape), q.new_empty(k.shape)
+        dq, dk, dv = _like(q), _like(k), _like(v)
         ws = workspace if workspace is not None else _workspace(_query("gdn_attn_bwd_workspace_size", *sizes, code), q.device)
         _bwd(q, k, v, cu_q, cu_k, o, lse, d_o, dq, dk, dv, ws, _scale(scale, D), sizes, steps, code, handle)
         return dict(dq=dq, dk=dk, dv=dv)
@@ -332,12 +341,20 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, table, lens, dev):
     dt = k_cache.dtype
     if dt is not torch.float8_e4m3fn and dt is not torch.uint8:
         raise TypeError(f"k_cache must be float8_e4m3fn or uint8, got {dt}")
-    _need(k_cache, "k_cache", k_cache.shape, dt, dev)
-    _need(v_cache, "v_cache", (pages, Hk, page // BLOCK, D, BLOCK), dt, dev)
-    _need(k_scale, "k_scale", (pages, Hk, page // BLOCK), torch.float32, dev)
-    _need(v_scale, "v_scale", (pages, Hk, page // BLOCK), torch.float32, dev)
-    _need(table, "table", (N, width), torch.int32, dev)
-    _need(lens, "lens", (N,), torch.int32, dev)
+    blocks = (pages, Hk, page // BLOCK)
+    f, i = torch.float32, torch.int32
+    if not (v_cache.shape == (*blocks, D, BLOCK) and v_cache.dtype is dt and k_scale.shape == blocks and k_scale.dtype is f
+            and v_scale.shape == blocks and v_scale.dtype is f and table.dtype is i and lens.shape == (N,) and lens.dtype is i
+            and k_cache.get_device() == dev and v_cache.get_device() == dev and k_scale.get_device() == dev
+            and v_scale.get_device() == dev and table.get_device() == dev and lens.get_device() == dev
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and table.is_contiguous() and lens.is_contiguous()):
+        _need(k_cache, "k_cache", k_cache.shape, dt, dev)
+        _need(v_cache, "v_cache", (*blocks, D, BLOCK), dt, dev)
+        _need(k_scale, "k_scale", blocks, f, dev)
+        _need(v_scale, "v_scale", blocks, f, dev)
+        _need(table, "table", (N, width), i, dev)
+        _need(lens, "lens", (N,), i, dev)
     return N, Hk, D, pages, page, width
 
 
@@ -408,8 +425,8 @@ def attn_step(q, k_cache, v_cache, k_scale, v_scale, table, lens, scale=None, wa
     _space(workspace, q.get_device())
 
     def call(handle):
-        o = q.new_empty(q.shape)
-        lse = q.new_empty(q.shape[:2], dtype=torch.float32) if want_lse else None
+        o = _like(q)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
         N, Hq, Hk, D, _, page, width = sizes
         ws = workspace if workspace is not None else \
             _workspace(_query("gdn_attn_step_workspace_size", N, Hq, Hk, D, page, width), q.device)
