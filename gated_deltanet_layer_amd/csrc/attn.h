@@ -287,17 +287,22 @@ struct Share {
     long left;   // units of the share behind r
     int x;       // first unit of owner r.t behind r
 };
-__device__ __forceinline__ long scan_lanes(long x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const long v = __shfl_up(x, d, 64);
-        if ((int)(threadIdx.x & 63) >= d) x += v;
-    }
-    return x;
-}
 __device__ __forceinline__ long lane_of(long x, int l) {
     const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)x, l), hi = (unsigned)__builtin_amdgcn_readlane((int)(x >> 32), l);
     return (long)((unsigned long long)hi << 32 | lo);
+}
+
+template <int CTRL> __device__ __forceinline__ long row_shift(long x) {
+    return (long)((unsigned long long)(unsigned)row_shift<CTRL>((int)(x >> 32)) << 32 | (unsigned)row_shift<CTRL>((int)x));
+}
+__device__ __forceinline__ long scan_lanes(long x) {
+    x += row_shift<0x111>(x);
+    x += row_shift<0x112>(x);
+    x += row_shift<0x114>(x);
+    x += row_shift<0x118>(x);
+    const long a = lane_of(x, 15), b = a + lane_of(x, 31), c = b + lane_of(x, 47);
+    const int row = (threadIdx.x & 63) >> 4;
+    return x + (row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c);
 }
 
 // Units of a share: all of the call's over the shares, rounded up; `least` tiles or more.
@@ -347,9 +352,10 @@ template <int UT, typename M> __device__ __forceinline__ bool share_begin(const 
 {
     const int lane = threadIdx.x & 63;
     auto of = [&](int b) { return b < a.B ? a.Hk * make(seq_lane(a, b)).all() : 0L; };
-    long total = 0;
+    long total = 0, mine = 0, incl = 0;
     for (int b = 0; b < a.B; b += 64) {
-        const long mine = of(b + lane), incl = scan_lanes(mine);
+        mine = of(b + lane);
+        incl = scan_lanes(mine);
         if (share == 0 && b + lane < a.B) prefix[b + lane] = total + incl - mine;
         total += lane_of(incl, 63);
     }
@@ -359,7 +365,11 @@ template <int UT, typename M> __device__ __forceinline__ bool share_begin(const 
     long at = 0;
     sh.r.b = 0;
     for (int b = 0; b < a.B; b += 64) {
-        const long mine = of(b + lane), incl = scan_lanes(mine), sum = lane_of(incl, 63);
+        if (a.B > 64) {   // else there are those of before
+            mine = of(b + lane);
+            incl = scan_lanes(mine);
+        }
+        const long sum = lane_of(incl, 63);
         if (g0 < at + sum) {
             const int l = (int)__builtin_ctzll(__ballot(g0 < at + incl));
             sh.r.b = b + l;
