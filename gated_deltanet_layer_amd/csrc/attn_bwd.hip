@@ -349,6 +349,18 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
     const T *k = (const T *)a.k + sq.k0 * a.ks + h * D, *v = (const T *)a.v + sq.k0 * a.vs + h * D;
     const float c = a.scale * LOG2E;
 
+    const int all = uniform((tl.walk(it.i) + ST - 1) / ST);
+    const int j0 = CUT ? piece * (plan.kstep / ST) : 0, nt = CUT && piece + 1 < plan.kp ? min(all, j0 + plan.kstep / ST) : all;
+    if (CUT && piece > 0 && nt <= j0) return;   // the last kernel knows which pieces there are
+    auto load = [&](int j) {
+        char *to = lds + (j & 1) * C::BUF;
+        load_tile<C::CPR, ST>(to, (const char *)k, a.ks * C::ES, j * ST, n, threadIdx.x);
+        load_tile<C::CPR, ST>(to + C::OFF_V, (const char *)v, a.vs * C::ES, j * ST, n, threadIdx.x);
+    };
+    // Of few keys, D needs all of them first (below); two tiles then stay where they are.
+    const bool few = BF && all <= 2;
+    if (few ? all > 0 : nt > j0) load(few ? 0 : j0);
+
     int pos[NG];
     long row[NG];   // of [Tq Hq]
     float ls[NG], dd[NG];
@@ -386,18 +398,10 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
 #pragma unroll
         for (int i = 0; i < NC; ++i) dq[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int all = uniform((tl.walk(it.i) + ST - 1) / ST);
-    const int j0 = CUT ? piece * (plan.kstep / ST) : 0, nt = CUT && piece + 1 < plan.kp ? min(all, j0 + plan.kstep / ST) : all;
-    if (CUT && piece > 0 && nt <= j0) return;   // the last kernel knows which pieces there are
     // keys that some, that all of the wave's rows see
     const int wend = min(lr0 + 16 * NG, nlive) - 1;
     const int wlast = wend < lr0 ? 0 : off + t0 + quotient(max(wend, 0), a.g_mul, a.g_shift) + 1;
     const int wfull = off + t0 + quotient(lr0, a.g_mul, a.g_shift) + 1;
-    auto load = [&](int j) {
-        char *to = lds + (j & 1) * C::BUF;
-        load_tile<C::CPR, ST>(to, (const char *)k, a.ks * C::ES, j * ST, n, threadIdx.x);
-        load_tile<C::CPR, ST>(to + C::OFF_V, (const char *)v, a.vs * C::ES, j * ST, n, threadIdx.x);
-    };
     const int rb = row_base<T, C::CPR>(r16), cb = col_base<T, C::CPR>(4 * gq);
     // of 32 keys (block t of tile j): P, and dP in the same layout
     auto products = [&](int j, int t, f32x4 (&s)[2][NG], f32x4 (&dp)[2][NG]) {
@@ -438,7 +442,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
             }
         }
     };
-    if (BF && all <= 2) {
+    if (few) {
         // The first rows, of few keys: o, rounded to bf16, is as large as v there, and the
         // error that its rounding leaves in D, the same for all keys of a row, would be as
         // large as the rounding of dS.  They have D from P and dP themselves.  The others
@@ -448,7 +452,6 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
 #pragma unroll
         for (int g = 0; g < NG; ++g) sum[g] = 0.f;
         for (int j = 0; j < all; ++j) {
-            if (j == 0) load(0);
             wait_vm<0>();
             lds_barrier();
             if (j + 1 < all) load(j + 1);
@@ -464,7 +467,6 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
                         for (int e = 0; e < 4; ++e) sum[g] += s[u][g][e] * dp[u][g][e];
             }
         }
-        lds_barrier();
 #pragma unroll
         for (int g = 0; g < NG; ++g) dd[g] = rows_sum(sum[g]);
     }
@@ -473,12 +475,13 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
         for (int g = 0; g < NG; ++g)   // also of rows that see nothing: they stand in walked tiles
             if (lr0 + 16 * g + r16 < nlive) ((float *)a.ws)[row[g]] = dd[g];
     }
-    if (nt > j0) load(j0);
     for (int j = j0; j < nt; ++j) {
         const char *kt = lds + (j & 1) * C::BUF;
-        wait_vm<0>();
-        lds_barrier();
-        if (j + 1 < nt) load(j + 1);
+        if (!few) {
+            wait_vm<0>();
+            lds_barrier();
+            if (j + 1 < nt) load(j + 1);
+        }
         if (j * ST >= wlast) continue;
 #pragma unroll 1
         for (int t = 0; t < ST / 32; ++t) {
