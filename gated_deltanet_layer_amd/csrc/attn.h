@@ -417,4 +417,55 @@ __device__ __forceinline__ int seq_at(const int *cu, int B, int T, int row) {
 }
 #endif
 
+// The parts of a row put together: part p < n has o[place(p)][D] and a weight of
+// 2^lse[place(p)], or nothing where that is -infinity, and then o may never have been written.
+// D / 4 lanes a row take the parts in turn, or, of few rows with many parts each, a whole
+// workgroup of 256 does, in GR = 1024 / D groups that take every GR-th.  Returns whether the
+// lane holds the row's sum (the first group does), with the base-2 log of the weights.
+template <int D, int GR, typename Place>
+__device__ __forceinline__ bool join_parts(const float *o, const float *lse, int n, Place place, f32x4 &sum, float &lg)
+{
+    constexpr int LPR = D / 4;
+    const int at = threadIdx.x % LPR * 4, g = GR > 1 ? threadIdx.x / LPR : 0;
+    float top = -INFINITY, ls = 0.f;
+#pragma unroll 4
+    for (int p = g; p < n; p += GR) top = fmaxf(top, lse[place(p)]);
+    sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = g; p < n; p += GR) {
+        const long i = place(p);
+        const float x = lse[i], f = exp2_hw(x - top);
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(o + i * D + at);
+        if (x == -INFINITY) continue;
+        ls += f;
+        sum += f * v;
+    }
+    if constexpr (GR > 1) {
+        __shared__ float os[GR][D];
+        __shared__ float st[2][GR];
+        store4(os[g] + at, sum);
+        if (at == 0) {
+            st[0][g] = top;
+            st[1][g] = ls;
+        }
+        __syncthreads();
+        if (g > 0) return false;
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < GR; ++i) top = fmaxf(top, st[0][i]);
+        ls = 0.f;
+        sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < GR; ++i) {
+            if (st[1][i] == 0.f) continue;   // of none of the parts; a sum that is NaN stays
+            const float f = exp2_hw(st[0][i] - top);
+            ls += f * st[1][i];
+            sum += f * *reinterpret_cast<const f32x4 *>(os[i] + at);
+        }
+    }
+    if (ls != 0.f) sum = sum * (1.f / ls);
+    lg = ls != 0.f ? top + __builtin_amdgcn_logf(ls) : -INFINITY;
+    return true;
+}
+
 } // namespace gdn

@@ -233,9 +233,21 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_append_
 // --- one token ------------------------------------------------------------------
 
 constexpr int STEP_TILE = 64;       // tokens a tile: four blocks, one for each 16-lane row of a wave
-constexpr int STEP_WGS = 768;       // workgroups to share a call's tiles
 constexpr int STEP_LEAST = 4;       // tiles a workgroup, one for each wave
-constexpr int STEP_WHOLE = 16;      // tiles that a table may name and a workgroup takes at once
+
+// Tiles that a table may name and a workgroup takes at once, in one launch (32 over 8 heads of
+// 128, in bf16: eight users of 1000 8.7 us, cut 10.7; one of 2000 12.8, cut 10).
+constexpr int STEP_WHOLE = 16;
+
+// Rows, at most, that are joined by a workgroup each, not by D / 4 lanes (one user of 100000, 32
+// over 4 heads 32 us from 66, 8 over 1 37 from 101; 64 users of 16384 198 from 196).
+constexpr int STEP_JOIN = 2048;
+
+// Workgroups to share a call's tiles, `runs` being sequences times key heads.  Two fit a
+// compute unit, so 512 run at once; of many sequences with lengths of their own, 768 leave
+// smaller remainders (32 over 4 heads, 16 users of 8192 29 us, with 768 34; 64 users of up to
+// 16384 125, with 768 116).
+__host__ __device__ inline int step_wgs(int runs) { return runs <= 128 ? 512 : 768; }
 
 // Workspace of a call that is cut: int prefix[N + 1] (pieces before each sequence), then for
 // each workgroup float o[16][D] and float lse[16] (base 2).
@@ -243,7 +255,7 @@ struct StepWs {
     long o, lse, bytes;
     int wgs;
     __host__ __device__ StepWs(int N, int heads, int d) {
-        wgs = STEP_WGS + N * heads;
+        wgs = step_wgs(N * heads) + N * heads;
         o = ((long)(N + 1) * 4 + 255) & ~255L;
         lse = o + (long)wgs * 16 * d * 4;
         bytes = lse + (long)wgs * 16 * 4;
@@ -253,13 +265,15 @@ static bool step_cut(int page, int width) { return (long)page * width > STEP_WHO
 
 __device__ __forceinline__ int step_len(const AttnCacheArgs &a, int n) { return a.pages > 0 ? within(a.lens[n], a.width * a.page) : 0; }
 __device__ __forceinline__ int step_tiles(const AttnCacheArgs &a, int n) { return (step_len(a, n) + STEP_TILE - 1) / STEP_TILE; }
-// Tiles of a piece: all of the call's over the workgroups, rounded up.
+// Tiles of a piece: all of the call's over the workgroups, rounded up to as many for each wave.
 __device__ __forceinline__ int step_each(const AttnCacheArgs &a, int heads)
 {
     const int lane = threadIdx.x & 63;
-    float all = 0.f;   // rounded, but the same in every workgroup
-    for (int n = 0; n < a.N; n += 64) all += (float)sum_lanes(n + lane < a.N ? step_tiles(a, n + lane) : 0);
-    return max(STEP_LEAST, (int)ceilf(all * (float)heads * (1.f / STEP_WGS)) + 1);
+    long all = 0;
+    for (int n = 0; n < a.N; n += 64) all += sum_lanes(n + lane < a.N ? step_tiles(a, n + lane) : 0);
+    const int wgs = step_wgs(a.N * heads);
+    const long each = (all * heads + wgs - 1) / wgs;
+    return max(STEP_LEAST, (int)min((each + 3) & ~3L, 1L << 24));
 }
 __device__ __forceinline__ int step_pieces(int tiles, int each) { return max(1, (tiles + each - 1) / each); }
 
@@ -504,33 +518,25 @@ template <typename T, int D, bool CUT> __global__ __launch_bounds__(256, 2) void
     }
 }
 
-// Joins the pieces of a row; D / 4 lanes a row.
-template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_join_kernel(AttnCacheArgs a, int ntile)
+// Joins the pieces of a row: GR groups of D / 4 lanes a row.
+template <typename T, int D, int GR> __global__ __launch_bounds__(256) void attn_step_join_kernel(AttnCacheArgs a, int ntile)
 {
-    constexpr int LPR = D / 4;
+    constexpr int LPR = D / 4, ROWS = 256 / LPR / GR;   // of a workgroup
     const int Hq = a.Hk * a.G, heads = a.Hk * ntile, at = threadIdx.x % LPR * 4;
-    const long row = (long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const long row = (long)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / LPR : 0);
     if (row >= (long)a.N * Hq) return;
     const int n = (int)(row / Hq), head = (int)(row - (long)n * Hq), h = head / a.G, g = head - h * a.G;
     const int *prefix = (const int *)a.ws;
     const int p0 = prefix[n], pieces = prefix[n + 1] - p0;
     if (pieces == 1) return;   // written by its one workgroup
     const StepWs lay(a.N, heads, D);
-    const float *po = (const float *)((const char *)a.ws + lay.o), *pl = (const float *)((const char *)a.ws + lay.lse);
-    auto place = [&](int p) { return ((long)(p0 + p) * heads + h * ntile + (g >> 4)) * 16 + (g & 15); };
-    float top = -INFINITY, ls = 0.f;
-    for (int p = 0; p < pieces; ++p) top = fmaxf(top, pl[place(p)]);
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = 0; p < pieces; ++p) {
-        const float lg = pl[place(p)];
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(po + place(p) * D + at);
-        const float f = lg == -INFINITY ? 0.f : exp2_hw(lg - top);
-        ls += f;
-        sum += f * v;
-    }
-    store4((T *)a.o + row * D + at, ls != 0.f ? sum * (1.f / ls) : sum);
-    if (a.lse && at == 0) a.lse[row] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+    f32x4 sum;
+    float lg;
+    if (!join_parts<D, GR>((const float *)((const char *)a.ws + lay.o), (const float *)((const char *)a.ws + lay.lse), pieces,
+                           [&](int p) { return ((long)(p0 + p) * heads + h * ntile + (g >> 4)) * 16 + (g & 15); }, sum, lg))
+        return;
+    store4((T *)a.o + row * D + at, sum);
+    if (a.lse && at == 0) a.lse[row] = lg * LN2;
 }
 
 template <typename T, int D> static hipError_t append(AttnCacheArgs a, hipStream_t st)
@@ -554,8 +560,10 @@ template <typename T, int D> static hipError_t step(AttnCacheArgs a, hipStream_t
     hipLaunchKernelGGL((attn_step_kernel<T, D, true>), dim3((unsigned)lay.wgs), dim3(256), 0, st, a, ntile);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const long rows = (long)a.N * a.Hk * a.G, each = 256 / (D / 4);
-    hipLaunchKernelGGL((attn_step_join_kernel<T, D>), dim3((unsigned)((rows + each - 1) / each)), dim3(256), 0, st, a, ntile);
+    const long rows = (long)a.N * a.Hk * a.G;
+    constexpr int EACH = 1024 / D;
+    if (rows <= STEP_JOIN) hipLaunchKernelGGL((attn_step_join_kernel<T, D, EACH>), dim3((unsigned)rows), dim3(256), 0, st, a, ntile);
+    else hipLaunchKernelGGL((attn_step_join_kernel<T, D, 1>), dim3((unsigned)((rows + EACH - 1) / EACH)), dim3(256), 0, st, a, ntile);
     return hipGetLastError();
 }
 

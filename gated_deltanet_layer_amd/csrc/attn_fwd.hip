@@ -36,6 +36,10 @@ struct AttnFwdWs {
 };
 
 constexpr int FWD_LEAST = 4;   // key tiles of a share
+// Rows, at most, that are joined by a workgroup each, not by D / 4 lanes: few rows have many
+// parts (32 over 4 heads of 128, one token of 20000 keys 24 us from 52; 32 over 8, 64 tokens 53
+// from 55; with 128 tokens it would be 85 from 79).
+constexpr int FWD_JOIN = 2048;
 
 // KS: groups of four waves that take the key tiles of a row tile in turn, each with buffers of
 // its own, and put their sums together at the end: two for calls that leave compute units idle.
@@ -249,14 +253,14 @@ __global__ __launch_bounds__(FORM == HALVES ? 512 : 256, FORM == HALVES ? 1 : 2)
     }
 }
 
-// Joins the rows that several shares worked on and writes those that see no key; D / 4
-// lanes a row.
-template <typename T, int D, int NR> __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int per)
+// Joins the rows that several shares worked on and writes those that see no key: GR groups of
+// D / 4 lanes a row.
+template <typename T, int D, int NR, int GR> __global__ __launch_bounds__(256) void attn_fwd_join_kernel(AttnArgs a, int per)
 {
     typedef AttnFwdCfg<T, D, NR> C;
-    constexpr int LPR = D / 4, KT = C::KT;
+    constexpr int LPR = D / 4, KT = C::KT, ROWS = 256 / LPR / GR;   // rows of a workgroup
     const int Hq = a.Hk * a.G, at = threadIdx.x % LPR * 4;
-    const long row = (long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const long row = (long)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / LPR : 0);
     if (row >= (long)a.Tq * Hq) return;
     const int token = (int)(row / Hq), head = (int)(row - (long)token * Hq);
     const int b = seq_at(a.cu_q, a.B, a.Tq, token);
@@ -272,22 +276,13 @@ template <typename T, int D, int NR> __global__ __launch_bounds__(256) void attn
     }
     if (wf == wl) return;   // written by its one workgroup
     const AttnFwdWs lay(a.B, C::RT, D);
-    const float *po = (const float *)((const char *)a.ws + lay.o), *pl = (const float *)((const char *)a.ws + lay.lse);
-    auto place = [&](int w) { return (w * 2 + (w == wf)) * (long)C::RT + lr; };   // of share wf its last part
-    float top = -INFINITY, ls = 0.f;
-    for (int w = wf; w <= wl; ++w) top = fmaxf(top, pl[place(w)]);
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int w = wf; w <= wl; ++w) {
-        const float lg = pl[place(w)];
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(po + place(w) * D + at);
-        const float f = exp2_hw(lg - top);
-        if (lg == -INFINITY) continue;   // v was never written
-        ls += f;
-        sum += f * v;
-    }
-    store4((T *)a.o + row * D + at, ls != 0.f ? sum * (1.f / ls) : sum);
-    if (a.lse && at == 0) a.lse[row] = ls != 0.f ? (top + __builtin_amdgcn_logf(ls)) * LN2 : -INFINITY;
+    f32x4 sum;
+    float lg;
+    if (!join_parts<D, GR>((const float *)((const char *)a.ws + lay.o), (const float *)((const char *)a.ws + lay.lse), wl - wf + 1,
+                           [&](int p) { return ((wf + p) * 2 + (p == 0)) * (long)C::RT + lr; }, sum, lg))   // of share wf its last part
+        return;
+    store4((T *)a.o + row * D + at, sum);
+    if (a.lse && at == 0) a.lse[row] = lg * LN2;
 }
 
 template <typename T, int D, int NR, int FORM> static hipError_t fwd_enqueue(const AttnArgs &a, const AttnFwdPlan &plan, hipStream_t st)
@@ -301,8 +296,10 @@ template <typename T, int D, int NR, int FORM> static hipError_t fwd_enqueue(con
     }
     hipLaunchKernelGGL(k, dim3((unsigned)(FORM == SHARED ? plan.shares : plan.tiles * a.Hk)), dim3(KS * 256), BYTES, st, a, plan.tokens);
     if (FORM == SHARED) {
-        const long rows = (long)a.Tq * a.Hk * a.G, each = 256 / (D / 4);
-        hipLaunchKernelGGL((attn_fwd_join_kernel<T, D, NR>), dim3((unsigned)((rows + each - 1) / each)), dim3(256), 0, st, a, plan.tokens);
+        const long rows = (long)a.Tq * a.Hk * a.G;
+        constexpr int EACH = 1024 / D;
+        if (rows <= FWD_JOIN) hipLaunchKernelGGL((attn_fwd_join_kernel<T, D, NR, EACH>), dim3((unsigned)rows), dim3(256), 0, st, a, plan.tokens);
+        else hipLaunchKernelGGL((attn_fwd_join_kernel<T, D, NR, 1>), dim3((unsigned)((rows + EACH - 1) / EACH)), dim3(256), 0, st, a, plan.tokens);
     }
     return hipGetLastError();
 }

@@ -211,3 +211,28 @@ def test_prologue_of_equal_rows_is_equal():
                                  torch.full((T,), 77777, dtype=torch.int32, device=DEV))
         for a, b in zip(one, many):
             assert (a == b).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,Hq,Hk,D", [(257, 8, 2, 128), (9, 34, 2, 64)])
+def test_step_joined_by_lanes_and_by_workgroups(N, Hq, Hk, D, dt):
+    """Sequences in many pieces beside whole and empty ones, with more and fewer rows than are
+    joined by a workgroup each."""
+    _say(f"step joined N{N} Hq{Hq} Hk{Hk} D{D} {dt}")
+    g = torch.Generator().manual_seed(N)
+    c = _live(_cache(7, 40, 32, Hk, D, seed=N))
+    c["table"] = torch.randint(0, 280, (N, 160), generator=g).to(torch.int32)   # pages shared
+    lens = [5120 if i in (3, N - 1) else 1500 if i == 5 else (37 * i) % 130 for i in range(N)]
+    q = (torch.randn(N, Hq, D, generator=g) * 0.2).to(DT[dt])
+    _check_step(c, q, lens, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D", [([3], [9000], 8, 2, 64), ([1, 40, 0], [6000, 7, 900], 12, 1, 128),
+                                           ([1, 40, 0], [6000, 7, 1900], 12, 1, 128), ([130, 2], [5000, 4000], 17, 1, 64)])
+def test_few_rows_over_long_sequences(lq, lk, Hq, Hk, D, dt):
+    """A few tokens, some of which see nothing, behind long sequences: rows of many parts."""
+    _say(f"few rows lq {lq} lk {lk} Hq{Hq} Hk{Hk} D{D} {dt}")
+    form = "halves" if dt == "bf16" and sum(lk) < 36 * 64 * 3 else "shares"
+    assert attn_plans.fwd(dt, len(lq), sum(lq), sum(lk), Hq, Hk)["form"] == form
+    _check_fwd(_packed(lq, lk, Hq, Hk, D, dt, seed=31), dt)
