@@ -55,7 +55,7 @@ struct AttnCacheArgs {
 
 hipError_t attn_prologue_launch(bool bf16, int D, const AttnPrologueArgs &a, hipStream_t st);
 hipError_t attn_prologue_bwd_launch(bool bf16, int D, const AttnPrologueArgs &a, hipStream_t st);
-unsigned long long attn_prologue_bwd_workspace(int T, int D);
+unsigned long long attn_prologue_bwd_workspace(int T, int Hq, int D);
 hipError_t attn_fwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st);
 unsigned long long attn_fwd_workspace(bool bf16, int B, int Tq, int Tk, int Hk, int G, int D);
 hipError_t attn_bwd_launch(bool bf16, int D, const AttnArgs &a, hipStream_t st);

@@ -135,7 +135,7 @@ gdn_status gdn_attn_prologue_bwd_workspace_size(int T, int Hq, int Hk, int D, in
     if (!bytes) return GDN_EINVAL;
     const gdn_status st = prologue_sizes(T, Hq, Hk, D, R, dtype);
     if (st != GDN_OK) return st;
-    *bytes = (size_t)gdn::attn_prologue_bwd_workspace(T, D);
+    *bytes = (size_t)gdn::attn_prologue_bwd_workspace(T, Hq, D);
     return GDN_OK;
 }
 
@@ -160,7 +160,7 @@ gdn_status gdn_attn_prologue_bwd(const void *q_raw, const void *k_raw, const flo
     if (!all_aligned({q_raw, k_raw, w_q, w_k, d_q, d_k, dq_raw, dk_raw}, 16) || !all_aligned({inv_freq, pos, dw_q, dw_k}, 4) ||
         !all_aligned({workspace}, 256))
         return GDN_EINVAL;
-    const unsigned long long need = st == GDN_OK ? gdn::attn_prologue_bwd_workspace(T, D) : 0;
+    const unsigned long long need = st == GDN_OK ? gdn::attn_prologue_bwd_workspace(T, Hq, D) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EINVAL;
     const Rows in[] = {rows(q_raw, T, qrow, q_stride * es), rows(k_raw, T, krow, k_stride * es), block(w_q, D * 4), block(w_k, D * 4),
                        block(inv_freq, R * 2), block(pos, T * 4LL), block(d_q, T * qrow), block(d_k, T * krow)};

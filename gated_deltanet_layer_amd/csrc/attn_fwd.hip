@@ -12,6 +12,14 @@
 // on the accumulator's rows, query rows on its lanes): a lane holds four consecutive keys of
 // one row, the softmax needs two cross-lane steps a tile, and the weights feed the second
 // product (o^T = V^T P^T) as its B operand straight from the registers.
+//
+// Long rows are bound by the matrix cores and the exponentials that stand between their
+// products: 8192 packed tokens (one sequence of 4999 among seven) of 32 over 8 heads of 128, bf16,
+// take 250 to 290 us (0.82 to 0.94 PFLOP/s of the visible half; a library product reaches 1.34),
+// in which the matrix cores are busy for 43 % of the cycles.  Without its exponentials the
+// kernel takes 0.93 of that, without its reads of keys 0.86, without its copies 0.89: no one of
+// them bounds it alone.  Short rows are bound by latency, a key tile after the other, some 1 us
+// each in bf16.
 #include "attn.h"
 
 namespace gdn {

@@ -13,7 +13,8 @@
 // 64 bits, its fraction to fp32: at position 10^6 an fp32 product would be off by 0.06
 // radians), and then goes through the heads, D / 8 lanes a head with eight channels each.
 // A lane reads the partners of its channels itself: they are in the lines that its
-// neighbours read.
+// neighbours read.  16384 tokens of 32 and 8 heads of 128 in bf16 (336 MB) take 66 us, 5.1 TB/s;
+// their gradients (504 MB) 98 us, of which the last kernel, the sums of dw, 5.
 #include "attn.h"
 
 namespace gdn {
@@ -96,7 +97,6 @@ template <typename T, int D, int TPW> __global__ __launch_bounds__(256) void att
         Eight<float> wo, wp;
         wo.load(w + ln.at);
         wp.load(w + ln.other);
-#pragma unroll 2
         for (int h = first; h < H; h += GROUPS) {
             Eight<T> o, p;
             o.load(x + h * D + ln.at);
@@ -114,17 +114,24 @@ template <typename T, int D, int TPW> __global__ __launch_bounds__(256) void att
     heads((const T *)a.k_raw + t * a.k_stride, a.w_k, (T *)a.k + t * a.Hk * D, a.Hk);
 }
 
-constexpr int PRO_BWD_TPW = 4, PRO_BWD_WGS = 1024;   // four workgroups a compute unit
-static int pro_bwd_wgs(int T) {
-    const int n = (T + PRO_BWD_TPW - 1) / PRO_BWD_TPW;
+// Tokens at a time of a workgroup, and the workgroups: up to four a compute unit, which share
+// the tokens.  One token where there is one for each, if it has heads for all lanes (32 over 8
+// heads of 128, bf16: 64 tokens 7.3 us, four at a time 10.7; 1024 13.1, 14.6) or the call is
+// short (16 over 2 of 64: 64 tokens 6.7 us, 7.3; 512 9.2, 7.7); above, four (32 over 8 heads,
+// 4096 tokens 26.1 us, one at a time 27.9; with 512 workgroups 28.6, with 2048 26.0 and, of
+// 16384 tokens, 113.8 and 100.4 for 98.9).
+constexpr int PRO_BWD_WGS = 1024;
+static int pro_bwd_tokens(int T, int Hq, int D) { return T <= (Hq * D >= 4096 ? PRO_BWD_WGS : 128) ? 1 : 4; }
+static int pro_bwd_wgs(int T, int tokens) {
+    const int n = (T + tokens - 1) / tokens;
     return n < PRO_BWD_WGS ? n : PRO_BWD_WGS;
 }
 
 // Sums of dw: each lane adds up its channels over the tokens of its workgroup, the
 // workgroup its groups' sums, and attn_prologue_dw_kernel the workgroups', all in order.
-template <typename T, int D> __global__ __launch_bounds__(256) void attn_prologue_bwd_kernel(AttnPrologueArgs a)
+template <typename T, int D, int TPW> __global__ __launch_bounds__(256) void attn_prologue_bwd_kernel(AttnPrologueArgs a)
 {
-    constexpr int TPW = PRO_BWD_TPW, LPH = D / 8, NG = 256 / LPH, GROUPS = NG / TPW;
+    constexpr int LPH = D / 8, NG = 256 / LPH, GROUPS = NG / TPW;
     __shared__ float cs[TPW * D];
     __shared__ float sums[NG][D];
     const int group = threadIdx.x / LPH, tl = group / GROUPS, first = group % GROUPS;
@@ -139,7 +146,6 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_prologu
             if (first >= H) return;
             Eight<float> wo;
             wo.load(w + ln.at);
-#pragma unroll 2
             for (int h = first; h < H; h += GROUPS) {
                 Eight<T> o, z, p;
                 o.load(x + h * D + ln.at);
@@ -199,6 +205,9 @@ template <int D> __global__ __launch_bounds__(1024) void attn_prologue_dw_kernel
     (col < D ? a.dw_q : a.dw_k)[col % D] = s;
 }
 
+// Four tokens a workgroup once that leaves workgroups for four a compute unit (32 over 8 heads
+// of 128, bf16: 64 tokens 4.3 us one a workgroup, 7.7 four; 2048 11.1, 11.8; 4096 18.0, 16.2;
+// 16384 76, 65.7, which is 5.1 TB/s).
 template <typename T, int D> static hipError_t prologue(const AttnPrologueArgs &a, hipStream_t st)
 {
     if (a.T >= 4096) hipLaunchKernelGGL((attn_prologue_kernel<T, D, 4>), dim3((a.T + 3) / 4), dim3(256), 0, st, a);
@@ -208,8 +217,9 @@ template <typename T, int D> static hipError_t prologue(const AttnPrologueArgs &
 
 template <typename T, int D> static hipError_t prologue_bwd(const AttnPrologueArgs &a, hipStream_t st)
 {
-    const int wgs = pro_bwd_wgs(a.T);
-    if (wgs > 0) hipLaunchKernelGGL((attn_prologue_bwd_kernel<T, D>), dim3(wgs), dim3(256), 0, st, a);
+    const int tokens = pro_bwd_tokens(a.T, a.Hq, D), wgs = pro_bwd_wgs(a.T, tokens);
+    if (wgs > 0 && tokens == 1) hipLaunchKernelGGL((attn_prologue_bwd_kernel<T, D, 1>), dim3(wgs), dim3(256), 0, st, a);
+    else if (wgs > 0) hipLaunchKernelGGL((attn_prologue_bwd_kernel<T, D, 4>), dim3(wgs), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attn_prologue_dw_kernel<D>), dim3(2 * D / 16), dim3(1024), 0, st, a, wgs);
@@ -228,9 +238,9 @@ hipError_t attn_prologue_bwd_launch(bool bf16, int D, const AttnPrologueArgs &a,
     return D == 128 ? prologue_bwd<float, 128>(a, st) : prologue_bwd<float, 64>(a, st);
 }
 
-unsigned long long attn_prologue_bwd_workspace(int T, int D)
+unsigned long long attn_prologue_bwd_workspace(int T, int Hq, int D)
 {
-    return (unsigned long long)pro_bwd_wgs(T) * 2 * D * 4;
+    return (unsigned long long)pro_bwd_wgs(T, pro_bwd_tokens(T, Hq, D)) * 2 * D * 4;
 }
 
 } // namespace gdn

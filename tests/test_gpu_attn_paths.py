@@ -9,6 +9,7 @@ import torch
 
 import attn_plans
 import gated_deltanet_layer_amd as gdn
+import test_gpu_attn
 from oracle import attention as ref
 from test_gpu_attn import (DEV, DT, _append_args, _cache, _check_bwd, _check_fwd, _check_step, _cu, _dev, _live, _on, _packed,
                            _say, _values)
@@ -236,3 +237,9 @@ def test_few_rows_over_long_sequences(lq, lk, Hq, Hk, D, dt):
     form = "halves" if dt == "bf16" and sum(lk) < 36 * 64 * 3 else "shares"
     assert attn_plans.fwd(dt, len(lq), sum(lq), sum(lk), Hq, Hk)["form"] == form
     _check_fwd(_packed(lq, lk, Hq, Hk, D, dt, seed=31), dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,Hq,Hk,D", [(130, 32, 3, 128), (1024, 32, 1, 128), (1025, 64, 2, 64), (128, 3, 2, 64), (129, 3, 2, 64)])
+def test_prologue_of_one_and_of_four_tokens_a_workgroup(T, Hq, Hk, D, dt):
+    test_gpu_attn.test_prologue(T, Hq, Hk, D, D, 1000, dt)
