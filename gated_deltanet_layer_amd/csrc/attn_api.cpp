@@ -70,7 +70,7 @@ gdn_status attn_sizes(int B, int Tq, int Tk, int Hq, int Hk, int D, gdn_dtype dt
     if (prod(Tq, Hq, D, 4) < 0 || prod(Tk, Hk, D, 4) < 0) return GDN_EINVAL;
     if ((D != 64 && D != 128) || Hq / Hk > 64 || Hq > (1 << 14)) return GDN_ENOTSUP;
     // rows of a key head (token, head) in 30 bits, those of all heads in 28; grids: workgroups * threads < 2^32
-    // (64 threads a key where dk and dv are added up)
+    // (64 threads for four keys where dk and dv of many are added up)
     const bool bf16 = dtype == GDN_BF16;
     const int G = Hq / Hk;
     if (((long long)Tq + Tk) * G >= (1LL << 30) || prod(Tq, Hq) >= (1LL << 28) || prod(Tk, Hk) >= (1LL << 26)) return GDN_ENOTSUP;

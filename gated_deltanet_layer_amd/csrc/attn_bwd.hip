@@ -12,7 +12,7 @@
 //
 // Seven products for the five of the formulas, bound by the matrix cores: 8192 packed tokens (one
 // sequence of 4999 among seven) of 16 over 4 heads of 128, bf16, take 440 to 465 us: dq 175 (1.0
-// PFLOP/s over its three products), dk and dv 255 to 265 (0.9 over four), the sums 19.
+// PFLOP/s over its three products), dk and dv 255 to 265 (0.9 over four), the sums 15.
 #include "attn.h"
 
 namespace gdn {
@@ -529,43 +529,56 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
 }
 
 // The sums over pieces and shares, in order: of dq by the first ndq workgroups (D / 4 lanes a
-// row), of dk and dv by the others (2 D / 4 lanes a key), which also write the keys that no
-// row sees.  A piece counts for the rows that its workgroup has worked on.
-template <typename T, int D> __global__ __launch_bounds__(256) void attn_bwd_sum_kernel(AttnArgs a, AttnBwdPlan plan, int ndq)
+// row), of dk and dv by the others (2 D / 4 lanes take `run` tokens of a head, one after the
+// other), which also write the keys that no row sees.  A piece counts for the rows that its
+// workgroup has worked on.
+template <typename T, int D> __global__ __launch_bounds__(256) void attn_bwd_sum_kernel(AttnArgs a, AttnBwdPlan plan, int ndq, int run)
 {
     typedef AttnBwdCfg<T, D> C;
+    constexpr int LPR = D / 4;
     const AttnBwdWs lay(plan, a.B, a.Tq, a.Tk, a.Hk, a.G, D, C::OWN);
-    const bool isq = (int)blockIdx.x < ndq;
-    const int W = isq ? D : 2 * D, H = isq ? a.Hk * a.G : a.Hk, T_ = isq ? a.Tq : a.Tk;
-    const long at = ((long)(blockIdx.x - (isq ? 0 : ndq)) * 256 + threadIdx.x) * 4;
-    const int col = (int)(at % W);
-    const long row = at / W;
-    if (row >= (long)T_ * H) return;
-    const int token = (int)(row / H), head = (int)(row - (long)token * H);
-    const int b = seq_at(isq || !a.cu_k ? a.cu_q : a.cu_k, a.B, T_, token);
-    const Seq s = seq_lane(a, b);
-    const int i = token - (isq ? s.q0 : s.k0);
-    if (i < 0 || i >= (isq ? s.lq : s.lk)) return;   // of no sequence
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    if (isq) {   // the owner of the row walks the keys up to its last row's position; piece 0 always writes
+    if ((int)blockIdx.x < ndq) {
+        const unsigned id = blockIdx.x * 256 + threadIdx.x, row = id / LPR, H = a.Hk * a.G;   // the grid has less than 2^32 threads
+        if (row >= a.Tq * H) return;
+        const int token = (int)(row / H), head = (int)row - token * (int)H, col = (int)(id % LPR) * 4;
+        const Seq s = seq_lane(a, seq_at(a.cu_q, a.B, a.Tq, token));
+        const int i = token - s.q0;
+        if (i < 0 || i >= s.lq) return;   // of no sequence
+        // the owner of the row walks the keys up to its last row's position; piece 0 always writes
         const int end = min(plan.kp, max(1, (AttnTiles(plan.tokens, s).walk(i / plan.tokens) + plan.kstep - 1) / plan.kstep));
-        const float *part = (const float *)((const char *)a.ws + lay.dq) + at;
-        for (int p = 0; p < end; ++p) x += *reinterpret_cast<const f32x4 *>(part + p * (long)T_ * H * W);
+        const float *part = (const float *)((const char *)a.ws + lay.dq) + (long)row * D + col;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < end; ++p) x += *reinterpret_cast<const f32x4 *>(part + p * (long)a.Tq * H * D);
         store4((T *)a.dq + token * a.dqs + head * D + col, x);
         return;
     }
-    const KeyTiles<C::OWN> owners(s, a.G);
-    const int t = i / C::OWN;
-    if (s.lq > 0) {
-        const long *prefix = (const long *)((const char *)a.ws + lay.prefix);
-        int wf, wl;
-        share_range<C::ST>(prefix[b] + head * owners.all() + owners.before(t), owners, t, share_each<C::ST>(prefix[a.B], plan.shares, BWD_LEAST), wf, wl);
-        if (wf == wl) return;   // written by its one workgroup
-        const float *part = (const float *)((const char *)a.ws + lay.dkv) + (i - t * C::OWN) * 2 * D + col;
+    const unsigned id = (blockIdx.x - ndq) * 256 + threadIdx.x, group = id / (2 * LPR);
+    const int first = (int)(group / (unsigned)a.Hk), head = (int)group - first * a.Hk, col = (int)(id % (2 * LPR)) * 4;
+    const long *prefix = (const long *)((const char *)a.ws + lay.prefix);
+    const float *parts = (const float *)((const char *)a.ws + lay.dkv) + col;
+    Seq s = {0, 0, 0, 0};
+    int own = 0, end = 0, wf = 0, wl = -1;   // tokens of one owner, and its shares
+    for (int token = first * run; token < min(a.Tk, (first + 1) * run); ++token) {
+        if (token >= end) {
+            const int b = seq_at(a.cu_k ? a.cu_k : a.cu_q, a.B, a.Tk, token);
+            s = seq_lane(a, b);
+            const int i = token - s.k0;
+            if (i < 0 || i >= s.lk) continue;   // of no sequence
+            const KeyTiles<C::OWN> owners(s, a.G);
+            const int t = i / C::OWN;
+            own = s.k0 + t * C::OWN;
+            end = min(own + C::OWN, s.k0 + s.lk);
+            wf = 0, wl = -1;
+            if (s.lq > 0)
+                share_range<C::ST>(prefix[b] + head * owners.all() + owners.before(t), owners, t, share_each<C::ST>(prefix[a.B], plan.shares, BWD_LEAST), wf, wl);
+        }
+        if (s.lq > 0 && wf == wl) continue;   // written by its one workgroup
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        const float *part = parts + (token - own) * 2 * D;
 #pragma unroll 4
         for (int w = wf; w <= wl; ++w) x += *reinterpret_cast<const f32x4 *>(part + (w * 2 + (w == wf)) * (long)lay.rows * 2 * D);
+        store4(col < D ? (T *)a.dk + token * a.dks + head * D + col : (T *)a.dv + token * a.dvs + head * D + col - D, x);
     }
-    store4(col < D ? (T *)a.dk + token * a.dks + head * D + col : (T *)a.dv + token * a.dvs + head * D + col - D, x);
 }
 
 template <typename T, int D> static hipError_t bwd_launch(AttnArgs a, hipStream_t st)
@@ -583,9 +596,12 @@ template <typename T, int D> static hipError_t bwd_launch(AttnArgs a, hipStream_
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.Tk > 0) hipLaunchKernelGGL(kkv, dim3((unsigned)plan.shares), dim3(512), C::KV_LDS, st, a, plan);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+    // Four tokens for one search of their owner and its shares, where that leaves 4096 runs (16 of
+    // 512, 32 over 8 heads of 64, 137 us, one by one 143; 333 rows over 4 heads 35 us, 29).
+    const int run = (long)a.Tk * a.Hk >= 4 * 4096 ? 4 : 1;
     auto groups = [](long values) { return (int)((values + 1023) / 1024); };
-    const int ndq = plan.kp > 1 ? groups((long)a.Tq * a.Hk * a.G * D) : 0, ndkv = groups((long)a.Tk * a.Hk * 2 * D);
-    if (ndq + ndkv > 0) hipLaunchKernelGGL((attn_bwd_sum_kernel<T, D>), dim3(ndq + ndkv), dim3(256), 0, st, a, plan, ndq);
+    const int ndq = plan.kp > 1 ? groups((long)a.Tq * a.Hk * a.G * D) : 0, ndkv = groups((long)((a.Tk + run - 1) / run) * a.Hk * 2 * D);
+    if (ndq + ndkv > 0) hipLaunchKernelGGL((attn_bwd_sum_kernel<T, D>), dim3(ndq + ndkv), dim3(256), 0, st, a, plan, ndq, run);
     return hipGetLastError();
 }
 
