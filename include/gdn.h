@@ -559,9 +559,10 @@ GDN_API gdn_status gdn_attn_prologue_bwd(const void *q_raw, const void *k_raw, c
  * Row i of a sequence of lq rows and lk keys has position p = lk - lq + i and sees the keys
  * j <= p: a whole prompt (lq = lk), or the last rows of a longer sequence.  A row that sees
  * none (p < 0) gives o = 0, lse = -inf.  Rows of no sequence are left as they were.  Any
- * length may be 0.  GDN_ENOTSUP from Hq > 2^14, Tq Hq >= 2^28, Tk Hk >= 2^26, B >= 2^24, (Tq +
- * Tk) Hq / Hk >= 2^30 and 2^24 row tiles on.  Long rows of few heads are split over the keys; the pieces stand in the
- * workspace (at least gdn_attn_fwd_workspace_size bytes; NULL when that is 0).
+ * length may be 0.  GDN_ENOTSUP from Hq > 2^14, Tq Hq >= 2^28, Tk Hk >= 2^26, B >= 2^24,
+ * (Tq + Tk) Hq / Hk >= 2^30 and 2^24 row tiles on.  Long rows of few heads are split over the
+ * keys; the pieces stand in the workspace (at least gdn_attn_fwd_workspace_size bytes; NULL
+ * when that is 0).
  */
 GDN_API gdn_status gdn_attn_fwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int D, gdn_dtype dtype,
                                                size_t *bytes);
