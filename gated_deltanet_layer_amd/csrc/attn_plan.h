@@ -33,10 +33,12 @@ struct AttnFwdPlan {
 // Shares: with fewer row tiles than two a unit, the longest row is the call's time unless all
 // rows' key tiles are shared equally; but a share begins, changes rows and is joined for
 // some 12 us.  Lengths are on the device, so the rule takes the call for up to four sequences
-// of equal length, and shares from 20 key tiles a sequence on, or 36 where halves would do in
-// bf16 (8 over 2 heads of 128: one sequence of 1000 26 us, in halves 21; of 2048 36, 35; 4
-// over 1, of 4096 48, 62; whole, four of 1000 41, 29, one of 4096 64, 81; fp32, D = 64: one of
-// 1000 31, 44; three of 1000 53, 57).
+// of equal length, and shares from 20 key tiles a sequence on; where halves would do in bf16,
+// from 36 (8 over 2 heads of 128: one sequence of 1000 26 us, in halves 21; of 2048 36, 35; 4
+// over 1, of 4096 48, 62), or from 24 for a few row tiles, which are joined soonest (8 over 2
+// heads, 64 tokens of 2000 22 us, in halves 34; D = 64 17, 19, and 64 of 1500 16, 15).  Against
+// whole tiles: four of 1000 41, 29, one of 4096 64, 81; fp32, D = 64: one of 1000 31, 44; three
+// of 1000 53, 57.
 inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G)
 {
     AttnFwdPlan p;
@@ -45,7 +47,7 @@ inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G
     p.tokens = 64 * p.nr / G;
     p.tiles = attn_row_tiles(B, Tq, p.tokens);
     const long wgs = ((Tq + p.tokens - 1) / p.tokens) * (long)Hk, each = B > 0 ? Tk / (B < 4 ? B : 4) : 0;
-    const long least = !bf16 ? 20 * 32 : p.nr == 1 && wgs <= 256 ? 36 * 64 : 20 * 64;
+    const long least = !bf16 ? 20 * 32 : p.nr > 1 || wgs > 256 ? 20 * 64 : wgs > 16 ? 36 * 64 : 24 * 64;
     p.shares = wgs > 0 && wgs < ATTN_SHARES && each >= least ? ATTN_SHARES : 0;
     p.halves = !p.shares && p.nr == 1 && wgs <= 256;
     return p;

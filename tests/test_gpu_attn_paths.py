@@ -234,8 +234,7 @@ def test_step_joined_by_lanes_and_by_workgroups(N, Hq, Hk, D, dt):
 def test_few_rows_over_long_sequences(lq, lk, Hq, Hk, D, dt):
     """A few tokens, some of which see nothing, behind long sequences: rows of many parts."""
     _say(f"few rows lq {lq} lk {lk} Hq{Hq} Hk{Hk} D{D} {dt}")
-    form = "halves" if dt == "bf16" and sum(lk) < 36 * 64 * 3 else "shares"
-    assert attn_plans.fwd(dt, len(lq), sum(lq), sum(lk), Hq, Hk)["form"] == form
+    assert attn_plans.fwd(dt, len(lq), sum(lq), sum(lk), Hq, Hk)["form"] == "shares"
     _check_fwd(_packed(lq, lk, Hq, Hk, D, dt, seed=31), dt)
 
 
