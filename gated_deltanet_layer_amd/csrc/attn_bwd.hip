@@ -3,6 +3,9 @@
 //   P_ij = exp(s_ij - lse_i),  D_i = do_i . o_i,  dS_ij = scale P_ij (do_i . v_j - D_i)
 //   dv_j = sum_i P_ij do_i,  dk_j = sum_i dS_ij q_i,  dq_i = sum_j dS_ij k_j
 //
+// A row that sees one key (position 0) has P = 1 and dS = 0, as D = dP; from a rounded lse and o
+// there would be a residue in place of the zero, so both kernels leave its dS out.
+//
 // The sums of dk and dv run over the rows of all G query heads that share the key head: rows
 // (token, head) in one run, as in the forward's tiles.  No atomics, so results do not depend
 // on the order in which workgroups run: one kernel owns query rows and walks their keys (dq),
@@ -186,6 +189,8 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
         // first row that sees key j: its token is j - off
         auto sees = [&](int j) { return (j - off) * a.G; };
         auto seen = [&](int r) { return r + ST - 1 >= sees(w0) && w0 < n; };   // whether a row of the tile sees a key of the wave
+        // rows of one key at the run's begin: the first that walk by the first owner
+        const int single = cur.t == 0 && off <= 0 ? a.G - cur.j * ST : 0;
         const T *x = isv ? (const T *)a.k + sq.k0 * a.ks + h * D : (const T *)a.v + sq.k0 * a.vs + h * D;
         const long xs = isv ? a.ks : a.vs;
         Frag<T> xf[NG][NKB];   // k for the first of the pair, v for the second
@@ -295,6 +300,15 @@ __global__ __launch_bounds__(512, 1) void attn_bwd_kv_kernel(AttnArgs a, AttnBwd
                 for (int u = 0; u < NS; ++u) {
 #pragma unroll
                     for (int g = 0; g < NG; ++g) dp[u][g] *= take_over<T>(from + (u * NG + g) * C::HP);
+                }
+                if ((j - 1) * ST < single) {
+                    const int end = single - (j - 1) * ST - 4 * gq;
+#pragma unroll
+                    for (int u = 0; u < NS; ++u)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) dp[u][g][e] = 16 * u + e < end ? 0.f : dp[u][g][e];
                 }
 #pragma unroll
                 for (int u = 0; u < NS; u += 2) {
@@ -521,7 +535,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_q_kernel(AttnArgs a, AttnBwdP
         T *out = (T *)a.dq + (sq.q0 + (long)(t0 + i)) * a.dqs + (h * a.G + lr - i * a.G) * D;
 #pragma unroll
         for (int e = 0; e < NC; ++e) {
-            const f32x4 x = pos[g] >= 0 ? dq[e][g] * a.scale : f32x4{0.f, 0.f, 0.f, 0.f};
+            const f32x4 x = pos[g] > 0 ? dq[e][g] * a.scale : f32x4{0.f, 0.f, 0.f, 0.f};   // at 0: one key, dS = 0
             if (CUT) store4(sum + row[g] * D + 16 * e + 4 * gq, x);
             else store4(out + 16 * e + 4 * gq, x);
         }

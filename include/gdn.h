@@ -575,7 +575,8 @@ GDN_API gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, con
  * Gradients of gdn_attn_fwd.  q .. lse as given to and written by the forward (lse is
  * required), d_o [Tq, Hq, D] dtype; writes dq, dk and dv (strided; dk and dv are the sums over
  * the query heads that share them).  Gradients of rows that see nothing and of keys that no
- * row sees are 0; rows of no sequence are left as they were.  No atomics.
+ * row sees are 0, as are dq of a row that sees one key and its share in that key's dk (its
+ * weight is 1 whatever the score); rows of no sequence are left as they were.  No atomics.
  *
  * For GDN_BF16, P is rounded to bf16 for dv and dS for dq and dk, the P in dk's dS to fp16 of
  * 4096 P, and D = d_o . o is of o as stored, whose rounding reaches the gradients of a row
