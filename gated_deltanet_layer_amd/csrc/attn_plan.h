@@ -28,7 +28,8 @@ struct AttnFwdPlan {
 //
 // Halves: with a workgroup a unit or fewer, and one row group a wave, four more waves take
 // every other key tile (32 over 8 heads of 128, 333 rows 11.4 us from 12.8; 8 over 2, 1000
-// rows 20 from 26).
+// rows 20 from 26).  Tiles' numbers leave gaps where sequences are many (find_tile), and a launch
+// has less than 2^32 threads: 512 a tile until 2^23.
 //
 // Shares: with fewer row tiles than two a unit, the longest row is the call's time unless all
 // rows' key tiles are shared equally; but a share begins, changes rows and is joined for
@@ -49,7 +50,7 @@ inline AttnFwdPlan attn_fwd_plan(bool bf16, int B, int Tq, int Tk, int Hk, int G
     const long wgs = ((Tq + p.tokens - 1) / p.tokens) * (long)Hk, each = B > 0 ? Tk / (B < 4 ? B : 4) : 0;
     const long least = !bf16 ? 20 * 32 : p.nr > 1 || wgs > 256 ? 20 * 64 : wgs > 16 ? 36 * 64 : 24 * 64;
     p.shares = wgs > 0 && wgs < ATTN_SHARES && each >= least ? ATTN_SHARES : 0;
-    p.halves = !p.shares && p.nr == 1 && wgs <= 256;
+    p.halves = !p.shares && p.nr == 1 && wgs <= 256 && p.tiles * Hk < (1L << 23);
     return p;
 }
 

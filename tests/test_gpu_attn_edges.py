@@ -61,3 +61,26 @@ def test_rows_of_one_key_where_keys_are_cut(dt):
     g = gdn.attn_bwd(d["q"], d["k"], d["v"], o, lse, d["d_o"], d["cu_q"])
     assert (g["dq"][[0, 1100]] == 0).all() and (g["dk"][1100] == 0).all()
     assert (g["dq"][1:1100] != 0).any(-1).all() and (g["dk"][:1100] != 0).any(-1).all()
+
+
+# --- sizes ----------------------------------------------------------------------
+
+def test_a_million_sequences_of_which_most_are_empty():
+    """1000 single tokens among 1,100,000 sequences, 8 heads: more than 2^23 row tiles, which the
+    forward takes with 256 threads each.  o is v (a weight of 1 over a sum of 1, each to 16 e, and
+    the rounding), dv is d_o, the gradients of the score are 0."""
+    B, T, H, D = 1_100_000, 1000, 8, 64
+    p = attn_plans.fwd("bf16", B, T, T, H, H)
+    assert p["form"] == "whole" and 1 << 23 < p["tiles"] * H < 1 << 24
+    g = torch.Generator().manual_seed(3)
+    one = torch.zeros(B, dtype=torch.int32)
+    one[torch.randperm(B, generator=g)[:T]] = 1
+    cu = torch.cat((torch.zeros(1, dtype=torch.int32), one.cumsum(0).to(torch.int32))).to(DEV)
+    q, k, v, d_o = (torch.randn(T, H, D, generator=g).to(torch.bfloat16).to(DEV) for _ in range(4))
+    o, lse = gdn.attn_fwd(q, k, v, cu)
+    assert ((o.double() - v.double()).abs() <= 2 * U["bf16"] * v.double().abs()).all()
+    s, most = (f(q.double() * k.double()).sum(-1) * D ** -0.5 for f in (lambda x: x, torch.abs))
+    assert ((lse.double() - s).abs() <= (D + 4) * E * most + 16 * E + 4 * E * s.abs()).all()
+    grads = gdn.attn_bwd(q, k, v, o, lse, d_o, cu)
+    assert (grads["dq"] == 0).all() and (grads["dk"] == 0).all()
+    assert ((grads["dv"].double() - d_o.double()).abs() <= 2 * U["bf16"] * d_o.double().abs()).all()
