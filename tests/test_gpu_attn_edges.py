@@ -154,3 +154,122 @@ def test_gradients_of_peaked_rows(T, D, dt):
 @pytest.mark.parametrize("scale", [1e-3, 0.7, 5.0])
 def test_backward_of_other_scales(scale, dt):
     _check_gradients(_packed([330, 1, 70], None, 6, 2, 64, dt, seed=63), dt, scale)
+
+
+# --- work that is shared and cut ------------------------------------------------
+
+def _shared(dt, B, Tq, Tk, Hq, Hk):
+    """Sizes whose forward is in shares and whose backward is cut: both have workspaces that the
+    offsets fill."""
+    assert attn_plans.fwd(dt, B, Tq, Tk, Hq, Hk)["form"] == "shares" and attn_plans.bwd(dt, B, Tq, Tk, Hq, Hk)["kp"] > 1
+
+
+class _Guarded:
+    """Tensors with 0x5a bytes in front of them and behind."""
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, shape, dtype):
+        t = torch.full((2048 + torch.empty(shape, dtype=dtype, device="meta").nbytes,), 0x5a, dtype=torch.uint8, device=DEV)
+        self.all.append(t)
+        return t[1024:-1024].view(dtype).view(shape)
+
+    def check(self):
+        torch.cuda.synchronize()
+        for i, t in enumerate(self.all):
+            assert (t[:1024] == 0x5a).all() and (t[-1024:] == 0x5a).all(), i
+
+
+def _all_guarded(d, cu_q, cu_k, dt, scale=0.1):
+    """Forward and backward with outputs and workspaces, of just the size that is asked for, in guards."""
+    Tq, Hq, D = d["q"].shape
+    Tk, Hk, _ = d["k"].shape
+    room, sizes, t = _Guarded(), (len(cu_q) - 1, Tq, Tk, Hq, Hk, D, DT[dt]), DT[dt]
+    o, lse = room((Tq, Hq, D), t), room((Tq, Hq), torch.float32)
+    ws = room((gdn.gdn_attn_fwd_workspace_size(*sizes),), torch.uint8)
+    gdn.gdn_attn_fwd(d["q"], d["k"], d["v"], cu_q, cu_k, o, lse, ws, scale)
+    g = dict(dq=room((Tq, Hq, D), t), dk=room((Tk, Hk, D), t), dv=room((Tk, Hk, D), t))
+    ws = room((gdn.gdn_attn_bwd_workspace_size(*sizes),), torch.uint8)
+    gdn.gdn_attn_bwd(d["q"], d["k"], d["v"], cu_q, cu_k, o, lse, d["d_o"].contiguous(), *g.values(), ws, scale)
+    room.check()
+    return o, lse, g
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D", [
+    ([90, 1], [6000, 900], 4, 2, 64), ([64], [4001], 8, 2, 128), ([5, 0, 3], [3100, 7, 4000], 17, 1, 64), ([2500], [2500], 4, 1, 128),
+    ([1], [20000], 64, 1, 64)])
+def test_shared_work_stays_inside_its_buffers(lq, lk, Hq, Hk, D, dt):
+    _say(f"guards lq {lq} lk {lk} Hq{Hq} Hk{Hk} D{D} {dt}")
+    _shared(dt, len(lq), sum(lq), sum(lk), Hq, Hk)
+    d = _on(_packed(lq, lk, Hq, Hk, D, dt, seed=71))
+    o, lse, g = _all_guarded(d, d["cu_q"], d["cu_k"], dt)
+    o2, lse2 = gdn.attn_fwd(d["q"], d["k"], d["v"], d["cu_q"], d["cu_k"], scale=0.1)
+    g2 = gdn.attn_bwd(d["q"], d["k"], d["v"], o2, lse2, d["d_o"], d["cu_q"], d["cu_k"], scale=0.1)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(g[n], g2[n]) for n in g)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("cq,ck", [([-5, 70, 30, 1000, 100], [10, 9000, 2000, -7, 6500]), ([100, 0, 100, 0, 100], [7000, 0, 7000, 0, 7000]),
+                                   ([0, 100, 0, 100, 50], [0, 7000, 0, 7000, 1]), ([2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 0, 3], [-2 ** 31, 2 ** 31 - 1, 5, 4, 6])])
+def test_offsets_out_of_range_in_shared_work_stay_inside(cq, ck, dt):
+    """Offsets that fall or lie outside, sequences over each other among them."""
+    _shared(dt, 4, 100, 7000, 4, 2)
+    d = _on(_packed([100], [7000], 4, 2, 64, dt, seed=72))
+    cu_q, cu_k = (torch.tensor(c, dtype=torch.int32, device=DEV) for c in (cq, ck))
+    _all_guarded(d, cu_q, cu_k, dt)
+
+
+def test_shared_work_side_by_side():
+    """Two calls at once on two streams give what they give alone."""
+    _shared("bf16", 2, 73, 5000, 4, 2)
+    ds = [_on(_packed([70, 3], [4100, 900], 4, 2, 64, "bf16", seed=s)) for s in (1, 2)]
+
+    def both(d, s=None):
+        o, lse = gdn.attn_fwd(d["q"], d["k"], d["v"], d["cu_q"], d["cu_k"], stream=s)
+        return o, lse, *gdn.attn_bwd(d["q"], d["k"], d["v"], o, lse, d["d_o"], d["cu_q"], d["cu_k"], stream=s).values()
+
+    alone = [both(d) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    for _ in range(3):
+        got = [both(d, s) for d, s in zip(ds, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_shared_work_captured_with_offsets_that_change(dt):
+    """Forward and backward in a graph, with eager calls and synchronisations between the replays."""
+    Tq, Tk = 120, 7000
+    _shared(dt, 3, Tq, Tk, 4, 2)
+    d = _on(_packed([Tq], [Tk], 4, 2, 64, dt, seed=73))
+    cu_q, cu_k = torch.zeros(4, dtype=torch.int32, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+
+    def work():
+        o, lse = gdn.attn_fwd(d["q"], d["k"], d["v"], cu_q, cu_k)
+        return [o, lse, *gdn.attn_bwd(d["q"], d["k"], d["v"], o, lse, d["d_o"], cu_q, cu_k).values()]
+
+    def fill(q, k):
+        cu_q.copy_(torch.tensor([0, *q, Tq], dtype=torch.int32))
+        cu_k.copy_(torch.tensor([0, *k, Tk], dtype=torch.int32))
+
+    splits = [((40, 80), (2000, 5000)), ((0, 120), (0, 7000)), ((1, 1), (6000, 6100)), ((60, 110), (30, 6900)), ((40, 80), (2000, 5000))]
+    fill(*splits[0])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for q, k in splits:
+        fill(q, k)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = work()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), (q, k, i)
