@@ -273,3 +273,59 @@ def test_shared_work_captured_with_offsets_that_change(dt):
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(got, want)):
             assert torch.equal(a, b), (q, k, i)
+
+
+# --- strides --------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,T,step", [("bf16", 2100, 1 << 20), ("bf16", 1100, 1 << 21), ("fp32", 300, 1 << 21)])
+def test_inputs_and_gradients_at_large_steps(dt, T, step):
+    """q, k and v from slices of a tensor of more than 2^31 bytes, and gradients into others, up to
+    the largest step from token to token: the same bits as from contiguous tensors."""
+    Hq, Hk, D = 4, 2, 64
+    H = Hq + 2 * Hk
+    _say(f"steps of {step}, {T} tokens, {dt}")
+    big = torch.empty(T, step, dtype=DT[dt], device=DEV)
+    assert big.nbytes > 1 << 31
+    x, y = (big.as_strided((T, H, D), (step, D, 1), at) for at in (0, 2048))   # gradients beside the values
+    x.copy_(torch.randn(T, H, D, generator=torch.Generator().manual_seed(1)))
+    far = x[:, :Hq], x[:, Hq:Hq + Hk], x[:, Hq + Hk:]
+    near = [t.contiguous() for t in far]
+    cu = torch.tensor([0, T - 200, T], dtype=torch.int32, device=DEV)
+    d_o = torch.randn(T, Hq, D, generator=torch.Generator().manual_seed(2)).to(DT[dt]).to(DEV)
+    o, lse = gdn.attn_fwd(*near, cu)
+    o2, lse2 = gdn.attn_fwd(*far, cu)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    want = gdn.attn_bwd(*near, o, lse, d_o, cu)
+    got = gdn.attn_bwd(*far, o, lse, d_o, cu)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    ws = torch.empty(gdn.gdn_attn_bwd_workspace_size(2, T, T, Hq, Hk, D, DT[dt]), dtype=torch.uint8, device=DEV)
+    into = y[:, :Hq], y[:, Hq:Hq + Hk], y[:, Hq + Hk:]
+    gdn.gdn_attn_bwd(*far, cu, None, o, lse, d_o, *into, ws, D ** -0.5)
+    assert all(torch.equal(t, want[n]) for n, t in zip(("dq", "dk", "dv"), into))
+    w = torch.linspace(0.5, 1.5, D, device=DEV)
+    args = w, w, torch.rand(D // 2, generator=torch.Generator().manual_seed(3)).to(DEV), torch.arange(T, dtype=torch.int32, device=DEV)
+    q, k = gdn.attn_prologue(*near[:2], *args)
+    assert all(torch.equal(a, b) for a, b in zip((q, k), gdn.attn_prologue(*far[:2], *args)))
+    want = gdn.attn_prologue_bwd(*near[:2], *args, q, k)
+    got = gdn.attn_prologue_bwd(*far[:2], *args, q, k)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    ws = torch.empty(gdn.gdn_attn_prologue_bwd_workspace_size(T, Hq, Hk, D, D, DT[dt]), dtype=torch.uint8, device=DEV)
+    dw = torch.empty(2, D, device=DEV)
+    gdn.gdn_attn_prologue_bwd(*far[:2], *args, q, k, *into[:2], dw[0], dw[1], ws, 1e-6)
+    assert all(torch.equal(a, want[n]) for n, a in zip(("dq_raw", "dk_raw", "dw_q", "dw_k"), (*into[:2], *dw)))
+
+
+def test_append_at_large_steps():
+    """New tokens from slices at the largest step: the same bytes as from contiguous tensors."""
+    T, Hk, D, page, step = 1100, 2, 64, 16, 1 << 21
+    big = torch.empty(T, step, dtype=torch.bfloat16, device=DEV)
+    x = big.as_strided((T, 2 * Hk, D), (step, D, 1), 0)
+    x.copy_(torch.randn(T, 2 * Hk, D, generator=torch.Generator().manual_seed(1)))
+    table = torch.randperm(70, generator=torch.Generator().manual_seed(2)).to(torch.int32).to(DEV)[None]
+    lens, cu, out = torch.tensor([T + 3], dtype=torch.int32, device=DEV), torch.tensor([0, T], dtype=torch.int32, device=DEV), []
+    for k, v in ((x[:, :Hk], x[:, Hk:]), (x[:, :Hk].contiguous(), x[:, Hk:].contiguous())):
+        c = [torch.zeros(70, Hk, page, D, dtype=torch.uint8, device=DEV), torch.zeros(70, Hk, 1, D, 16, dtype=torch.uint8, device=DEV),
+             torch.zeros(70, Hk, 1, device=DEV), torch.zeros(70, Hk, 1, device=DEV)]
+        gdn.attn_append_(k, v, *c, table, lens, cu=cu)
+        out.append(c)
+    assert (out[0][0] != 0).any() and all(torch.equal(a, b) for a, b in zip(*out))
