@@ -65,3 +65,8 @@ def test_sizes_over_the_whole_range():
         t = _threads(dt, B, Tq, Tk, Hk * G, Hk, D)
         assert max(t.values()) < 1 << 32, (dt, B, Tq, Tk, G, Hk, t)
     assert seen > 2000
+
+
+def test_form_without_sequences():
+    assert attn_plans.fwd("bf16", 0, 0, 0, 8, 2)["form"] == "halves"
+    assert gdn.gdn_attn_fwd_workspace_size(0, 0, 0, 8, 2, 64, torch.bfloat16) == 0

@@ -275,6 +275,32 @@ def test_shared_work_captured_with_offsets_that_change(dt):
             assert torch.equal(a, b), (q, k, i)
 
 
+# --- the prologue's sums ---------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,Hq,Hk,D", [(16384, 8, 2, 64), (9001, 16, 3, 128), (1000, 32, 8, 128)])
+def test_norm_weight_gradients_of_long_calls(T, Hq, Hk, D, dt):
+    """dw is a sum of T H terms in 32 bits, but not one after the other: a lane adds up the heads
+    of its tokens, the workgroup its 256 / (D / 8) groups, then 64 runs of up to 1024 workgroups
+    are added up, and the runs.  Its rounding goes by the longest chain of these, n additions, so
+    it is off by (n + D + 40) e of the sum of absolute terms (D + 40: each term's own)."""
+    g = torch.Generator().manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    raw, dy, w = r(T, Hq + Hk, D).to(DT[dt]), r(T, Hq + Hk, D).to(DT[dt]), 1 + r(D) / 4
+    inv, pos = 10000.0 ** (-torch.arange(0, D, 2) / D), torch.arange(T, dtype=torch.int32)
+    x, y, wd = raw.to(DEV), dy.to(DEV), w.to(DEV)
+    got = gdn.attn_prologue_bwd(x[:, :Hq], x[:, Hq:], wd, wd, inv.to(DEV), pos.to(DEV), y[:, :Hq].contiguous(), y[:, Hq:].contiguous())
+    groups = 256 // (D // 8)
+    for n, a, b in (("dw_q", 0, Hq), ("dw_k", Hq, Hq + Hk)):
+        X, Z = ref.f64(raw[:, a:b]), ref.turn(ref.f64(dy[:, a:b]), inv, pos, back=True)
+        X = X / np.sqrt((X * X).mean(-1, keepdims=True) + 1e-6)
+        A = np.abs(ref.f64(dy[:, a:b]))
+        A = np.concatenate([A[..., :D // 2] + A[..., D // 2:]] * 2, -1)
+        # one token at a time or four: the chain of four in groups / 4 is as long or longer
+        chain = -(-T // 1024) * -(-(b - a) // (groups // 4)) + groups + 16 + 64
+        _close(n, got[n], (Z * X).sum((0, 1)), (chain + D + 40) * E * (A * np.abs(X)).sum((0, 1)))
+
+
 # --- strides --------------------------------------------------------------------
 
 @pytest.mark.parametrize("dt,T,step", [("bf16", 2100, 1 << 20), ("bf16", 1100, 1 << 21), ("fp32", 300, 1 << 21)])
