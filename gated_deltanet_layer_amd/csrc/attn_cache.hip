@@ -252,16 +252,23 @@ constexpr int STEP_JOIN = 2048;
 // 16384 125, with 768 116).
 __host__ __device__ inline int step_wgs(int runs) { return runs <= 128 ? 512 : 768; }
 
-// Workspace of a call that is cut: int prefix[N + 1] (pieces before each sequence), then for
-// each workgroup float o[16][D] and float lse[16] (base 2).
+// Workspace of a call that is cut: int prefix[N + 1] (pieces of cut sequences before each), then
+// for each of those pieces and 16 heads float o[16][D] and float lse[16] (base 2), of however
+// many heads (as many rows as there are would be an address by a factor only known at run time:
+// one user of 100000, 8 heads a key head, 31.9 us from 30.4).  A cut sequence has more tiles than
+// `each` (below), so fewer pieces than twice its tiles over `each`, and all of them fewer than
+// twice the workgroups that share the tiles.  Whole sequences have none: the workspace does not
+// grow with their number.
 struct StepWs {
     long o, lse, bytes;
     int wgs;
     __host__ __device__ StepWs(int N, int heads, int d) {
-        wgs = step_wgs(N * heads) + N * heads;
+        const int share = step_wgs(N * heads);
+        wgs = share + N * heads;
+        const long slots = share + (N * heads < share ? N * heads : share);
         o = ((long)(N + 1) * 4 + 255) & ~255L;
-        lse = o + (long)wgs * 16 * d * 4;
-        bytes = lse + (long)wgs * 16 * 4;
+        lse = o + slots * 16 * d * 4;
+        bytes = lse + slots * 16 * 4;
     }
 };
 static bool step_cut(int page, int width) { return (long)page * width > STEP_WHOLE * STEP_TILE; }
@@ -269,16 +276,17 @@ static bool step_cut(int page, int width) { return (long)page * width > STEP_WHO
 __device__ __forceinline__ int step_len(const AttnCacheArgs &a, int n) { return a.pages > 0 ? within(a.lens[n], a.width * a.page) : 0; }
 __device__ __forceinline__ int step_tiles(const AttnCacheArgs &a, int n) { return (step_len(a, n) + STEP_TILE - 1) / STEP_TILE; }
 // Tiles of a piece: all of the call's over the workgroups, rounded up to as many for each wave.
-__device__ __forceinline__ int step_each(const AttnCacheArgs &a, int heads)
+template <typename F> __device__ __forceinline__ int step_each(const AttnCacheArgs &a, int heads, F tiles)
 {
     const int lane = threadIdx.x & 63;
     long all = 0;
-    for (int n = 0; n < a.N; n += 64) all += sum_lanes(n + lane < a.N ? step_tiles(a, n + lane) : 0);
+    for (int n = 0; n < a.N; n += 64) all += sum_lanes(n + lane < a.N ? tiles(n + lane) : 0);
     const int wgs = step_wgs(a.N * heads);
     const long each = (all * heads + wgs - 1) / wgs;
     return max(STEP_LEAST, (int)min((each + 3) & ~3L, 1L << 24));
 }
 __device__ __forceinline__ int step_pieces(int tiles, int each) { return max(1, (tiles + each - 1) / each); }
+__device__ __forceinline__ int step_cuts(int tiles, int each) { return tiles > each ? step_pieces(tiles, each) : 0; }
 
 // bf16 pieces that add up to a value: one of bf16, three of fp32 (8 + 8 + 8 bits).
 template <typename T> struct Pieces {
@@ -316,23 +324,29 @@ template <typename T, int D, bool CUT> __global__ __launch_bounds__(256, 2) void
     __shared__ float stat[2][4][16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r16 = lane_r16(), gq = lane_gq();
     const int heads = a.Hk * ntile, hr = blockIdx.x % heads, h = hr / ntile, g0 = hr % ntile * 16, Hq = a.Hk * a.G;
-    int n = blockIdx.x / heads, t0 = 0, t1, pieces = 1;
+    int n = blockIdx.x / heads, t0 = 0, t1, pieces = 1, place = 0;   // place: among the pieces of cut sequences
     if constexpr (CUT) {
-        const int each = step_each(a, heads);
+        const int first = lane < a.N ? step_tiles(a, lane) : 0;   // most calls have no more sequences
+        auto tiles = [&](int b) { return b < 64 ? first : step_tiles(a, b); };   // b: a multiple of 64, and the lane
+        const int each = step_each(a, heads, tiles);
         if (blockIdx.x == 0 && wave == 0) {   // for the join
             int *prefix = (int *)a.ws, at = 0;
             for (int b = 0; b < a.N; b += 64) {
-                const int mine = b + lane < a.N ? step_pieces(step_tiles(a, b + lane), each) : 0, incl = scan_lanes(mine);
+                const int mine = b + lane < a.N ? step_cuts(tiles(b + lane), each) : 0, incl = scan_lanes(mine);
                 if (b + lane < a.N) prefix[b + lane] = at + incl - mine;
                 at += __builtin_amdgcn_readlane(incl, 63);
             }
             if (lane == 0) prefix[a.N] = at;
         }
-        const Item it = find_item(a.N, n, [&](int b) { return step_pieces(step_tiles(a, b), each); });
+        const Item it = find_item(a.N, n, [&](int b) { return step_pieces(tiles(b), each); });
         if (it.b < 0) return;
         n = it.b;
         const int nt = __builtin_amdgcn_readfirstlane(step_tiles(a, n));
         pieces = step_pieces(nt, each);
+        if (pieces > 1) {
+            place = it.i;
+            for (int b = 0; b < n; b += 64) place += sum_lanes(b + lane < n ? step_cuts(tiles(b + lane), each) : 0);
+        }
         const int per = (nt + pieces - 1) / pieces;
         t0 = it.i * per;
         t1 = min(nt, t0 + per);
@@ -507,8 +521,8 @@ template <typename T, int D, bool CUT> __global__ __launch_bounds__(256, 2) void
     }
     const bool seen = total != 0.f;   // a NaN is seen
     const float inv = seen ? 1.f / total : 0.f, lg = seen ? top + __builtin_amdgcn_logf(total) : -INFINITY;
-    const long orow = (long)n * Hq + h * a.G + g0 + r, slot = (long)blockIdx.x * 16 + r;
     const StepWs lay(a.N, heads, D);
+    const long orow = (long)n * Hq + h * a.G + g0 + r, slot = ((long)place * heads + hr) * 16 + r;
 #pragma unroll
     for (int i = 0; i < PER; i += 4) {
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
@@ -534,7 +548,7 @@ template <typename T, int D, int GR> __global__ __launch_bounds__(256) void attn
     const int n = (int)(row / Hq), head = (int)(row - (long)n * Hq), h = head / a.G, g = head - h * a.G;
     const int *prefix = (const int *)a.ws;
     const int p0 = prefix[n], pieces = prefix[n + 1] - p0;
-    if (pieces == 1) return;   // written by its one workgroup
+    if (pieces == 0) return;   // written by its one workgroup
     const StepWs lay(a.N, heads, D);
     f32x4 sum;
     float lg;

@@ -70,3 +70,11 @@ def test_sizes_over_the_whole_range():
 def test_form_without_sequences():
     assert attn_plans.fwd("bf16", 0, 0, 0, 8, 2)["form"] == "halves"
     assert gdn.gdn_attn_fwd_workspace_size(0, 0, 0, 8, 2, 64, torch.bfloat16) == 0
+
+
+@pytest.mark.parametrize("N,Hq,Hk,D,page,width", [(1024, 32, 32, 128, 64, 100), (4096, 64, 64, 128, 64, 100), (100_000, 64, 1, 128, 64, 100),
+                                                  (1, 32, 8, 128, 64, 2048)])
+def test_step_workspace_grows_with_what_is_shared(N, Hq, Hk, D, page, width):
+    """512 to 768 workgroups share the tiles, a sequence is cut into fewer than twice its part of
+    them, and a piece has rows for 16 heads; and four bytes a sequence."""
+    assert gdn.gdn_attn_step_workspace_size(N, Hq, Hk, D, page, width) <= 2 * 768 * 16 * (D + 1) * 4 + 4 * (N + 1) + 512

@@ -9,7 +9,8 @@ import torch
 import attn_plans
 import gated_deltanet_layer_amd as gdn
 from oracle import attention as ref
-from test_gpu_attn import DEV, DT, E, U, _bwd_tol, _close, _fwd_tol, _on, _packed, _parts, _say
+from test_gpu_attn import (DEV, DT, E, U, _append_args, _bwd_tol, _cache, _check_step, _close, _dev, _fwd_tol, _live, _on, _packed,
+                           _parts, _say)
 
 pytestmark = pytest.mark.gpu
 
@@ -355,3 +356,30 @@ def test_append_at_large_steps():
         gdn.attn_append_(k, v, *c, table, lens, cu=cu)
         out.append(c)
     assert (out[0][0] != 0).any() and all(torch.equal(a, b) for a, b in zip(*out))
+
+
+# --- one token ------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,Hq,Hk,D,longest", [(1, 1, 1, 64, 20000), (300, 3, 1, 64, 9000), (70, 34, 2, 64, 6000), (1000, 8, 8, 64, 4000), (64, 20, 4, 128, 2500),
+                                               (5, 64, 1, 128, 5000)])
+def test_cut_steps_stay_inside_their_workspace(N, Hq, Hk, D, longest, dt):
+    """A few long sequences in pieces among many short, whole and empty ones, with a workspace of
+    just the size that is asked for."""
+    _say(f"cut step N{N} Hq{Hq} Hk{Hk} D{D} {dt}")
+    g, page = torch.Generator().manual_seed(N), 16
+    width = longest // page
+    c = _live(_cache(5, 40, page, Hk, D, seed=N))
+    c["table"] = torch.randint(0, len(c["k_cache"]), (N, width), generator=g).to(torch.int32)   # pages shared
+    long = {N - 1: longest, N // 2: longest // 2 + 3, 3: longest - 1}
+    lens = [long.get(i, (37 * i) % 90) for i in range(N)]
+    q = (torch.randn(N, Hq, D, generator=g) * 0.2).to(DT[dt])
+    o, lse = _check_step(c, q, lens, dt)
+    x, room = _dev(c), _Guarded()
+    o2, lse2 = room((N, Hq, D), DT[dt]), room((N, Hq), torch.float32)
+    size = gdn.gdn_attn_step_workspace_size(N, Hq, Hk, D, page, width)
+    assert size > 0
+    gdn.gdn_attn_step(q.to(DEV), *_append_args(x), torch.tensor(lens, dtype=torch.int32, device=DEV), o2, lse2, room((size,), torch.uint8),
+                      D ** -0.5)
+    room.check()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
