@@ -383,3 +383,94 @@ def test_cut_steps_stay_inside_their_workspace(N, Hq, Hk, D, longest, dt):
                       D ** -0.5)
     room.check()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# --- calls that a user may make -------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("Hq,Hk,T", [(4, 0, 5), (0, 3, 5), (0, 2, 1), (6, 0, 5000), (0, 0, 7)])
+def test_prologue_of_queries_or_keys_alone(Hq, Hk, T, dt):
+    """No heads on one side: the other is as with both, the norm weight's gradient of none is 0."""
+    D, g = 64, torch.Generator().manual_seed(T)
+    both = torch.randn(T, 9, D, generator=g).to(DT[dt]).to(DEV)
+    w, inv, pos = torch.rand(2, D, generator=g).to(DEV), torch.rand(16, generator=g).to(DEV), torch.arange(T, dtype=torch.int32, device=DEV)
+    args = w[0], w[1], inv, pos
+    full = gdn.attn_prologue(both[:, :6], both[:, 6:], *args)
+    q, k = gdn.attn_prologue(both[:, :Hq], both[:, 6:6 + Hk], *args)
+    assert torch.equal(q, full[0][:, :Hq]) and torch.equal(k, full[1][:, :Hk])
+    want = gdn.attn_prologue_bwd(both[:, :6], both[:, 6:], *args, *full)
+    got = gdn.attn_prologue_bwd(both[:, :Hq], both[:, 6:6 + Hk], *args, q, k)
+    assert torch.equal(got["dq_raw"], want["dq_raw"][:, :Hq]) and torch.equal(got["dk_raw"], want["dk_raw"][:, :Hk])
+    assert (Hq or (got["dw_q"] == 0).all()) and (Hk or (got["dw_k"] == 0).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("lq,lk,form", [([600] * 5, None, "whole"), ([65, 1], [90, 70], "halves"), ([60, 3], [6300, 900], "shares")])
+def test_forward_without_lse(lq, lk, form, dt):
+    Hq, Hk = (64, 16) if form == "whole" else (4, 2)
+    assert attn_plans.fwd(dt, len(lq), sum(lq), sum(lk or lq), Hq, Hk)["form"] == form
+    d = _on(_packed(lq, lk, Hq, Hk, 64, dt, seed=81))
+    o, _ = gdn.attn_fwd(d["q"], d["k"], d["v"], d["cu_q"], d["cu_k"], scale=0.1)
+    n = gdn.gdn_attn_fwd_workspace_size(len(lq), sum(lq), sum(lk or lq), Hq, Hk, 64, DT[dt])
+    o2, ws = torch.empty_like(o), torch.empty(n, dtype=torch.uint8, device=DEV) if n else None
+    gdn.gdn_attn_fwd(d["q"], d["k"], d["v"], d["cu_q"], d["cu_k"], o2, None, ws, 0.1)
+    assert torch.equal(o, o2)
+
+
+def test_idle_sequences_of_a_serving_batch():
+    """Sequences of no tokens among those of a decoding batch: one new row each, of which theirs is
+    not stored, whatever their table says, and their token is 0; the others are as without them."""
+    N, Hq, Hk, D, page, width = 7, 8, 2, 64, 32, 3
+    idle = [0, 3, 6]
+    live = [i for i in range(N) if i not in idle]
+    g = torch.Generator().manual_seed(4)
+    c = _live(_cache(N, width, page, Hk, D, seed=9))
+    lens = torch.tensor([0 if i in idle else 17 * i for i in range(N)], dtype=torch.int32)
+    q, k, v = (torch.randn(N, H, D, generator=g).to(torch.bfloat16).to(DEV) for H in (Hq, Hk, Hk))
+    one, few = _dev(c), _dev({n: t.clone() for n, t in c.items()})
+    few["table"] = few["table"][live].contiguous()
+    one["table"][idle] = one["table"][live[0]].clone()   # another's pages
+    gdn.attn_append_(k, v, *_append_args(one), lens.to(DEV))
+    gdn.attn_append_(k[live], v[live], *_append_args(few), lens[live].to(DEV))
+    for n in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        assert torch.equal(one[n], few[n]), n
+    o, lse = gdn.attn_step(q, *_append_args(one), lens.to(DEV), want_lse=True)
+    o2, lse2 = gdn.attn_step(q[live], *_append_args(few), lens[live].to(DEV), want_lse=True)
+    assert torch.equal(o[live], o2) and torch.equal(lse[live], lse2)
+    assert (o[idle] == 0).all() and torch.isneginf(lse[idle]).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_prologue_captured(dt):
+    """The prologue and its gradients in a graph; positions and rows change between replays."""
+    T, Hq, Hk, D = 700, 4, 2, 64
+    raw, d_q, d_k = (torch.randn(T, H, D, generator=torch.Generator().manual_seed(H), dtype=torch.float32).to(DT[dt]).to(DEV)
+                     for H in (Hq + Hk, Hq, Hk))
+    w, inv, pos = torch.rand(2, D).to(DEV), torch.rand(D // 2).to(DEV), torch.zeros(T, dtype=torch.int32, device=DEV)
+    work = lambda: [*gdn.attn_prologue(raw[:, :Hq], raw[:, Hq:], w[0], w[1], inv, pos),  # noqa: E731
+                    *gdn.attn_prologue_bwd(raw[:, :Hq], raw[:, Hq:], w[0], w[1], inv, pos, d_q, d_k).values()]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for i in range(4):
+        pos.add_(1000 * i + 1)
+        raw.mul_(0.75)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, work())), i
+        torch.cuda.synchronize()
+
+
+def test_one_tensor_as_keys_and_values():
+    d = _on(_packed([130, 5], None, 4, 2, 64, "bf16", seed=83))
+    k = d["k"].contiguous()
+    o, lse = gdn.attn_fwd(d["q"], k, k, d["cu_q"])
+    o2, lse2 = gdn.attn_fwd(d["q"], k, k.clone(), d["cu_q"])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    g, g2 = (gdn.attn_bwd(d["q"], k, x, o, lse, d["d_o"], d["cu_q"]) for x in (k, k.clone()))
+    assert all(torch.equal(g[n], g2[n]) for n in g)
