@@ -13,8 +13,8 @@
 // 64 bits, its fraction to fp32: at position 10^6 an fp32 product would be off by 0.06
 // radians), and then goes through the heads, D / 8 lanes a head with eight channels each.
 // A lane reads the partners of its channels itself: they are in the lines that its
-// neighbours read.  16384 tokens of 32 and 8 heads of 128 in bf16 (336 MB) take 66 us, 5.1 TB/s;
-// their gradients (504 MB) 98 us, of which the last kernel, the sums of dw, 5.
+// neighbours read.  16384 tokens of 32 and 8 heads of 128 in bf16 (336 MB) take 69 us, 4.9 TB/s
+// (66 to 71 in single calls); their gradients (504 MB) 98 us, of which the last kernel, the sums of dw, 5.
 #include "attn.h"
 
 namespace gdn {
@@ -207,7 +207,7 @@ template <int D> __global__ __launch_bounds__(1024) void attn_prologue_dw_kernel
 
 // Four tokens a workgroup once that leaves workgroups for four a compute unit (32 over 8 heads
 // of 128, bf16: 64 tokens 4.3 us one a workgroup, 7.7 four; 2048 11.1, 11.8; 4096 18.0, 16.2;
-// 16384 76, 65.7, which is 5.1 TB/s).
+// 16384 76, 69, which is 4.9 TB/s).
 template <typename T, int D> static hipError_t prologue(const AttnPrologueArgs &a, hipStream_t st)
 {
     if (a.T >= 4096) hipLaunchKernelGGL((attn_prologue_kernel<T, D, 4>), dim3((a.T + 3) / 4), dim3(256), 0, st, a);

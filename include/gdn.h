@@ -514,8 +514,9 @@ GDN_API gdn_status gdn_latent_steps(const void *q, const void *draft, const long
  * overlap neither inputs nor each other (slices of one tensor with equal strides do not).
  * D: 64 or 128, Hq / Hk: at most 64 (GDN_ENOTSUP otherwise).  scale: > 0, with scale / ln 2
  * finite.  Results are the same on every call with the same arguments.  NOT checked: live
- * inputs are finite; offsets rise within the tensor (others give unspecified results, within
- * the outputs).
+ * inputs are finite (a value that is not may reach every row of its sequence, earlier ones
+ * too, since a masked weight of 0 times it is NaN, and no row of another); offsets rise within
+ * the tensor (others give unspecified results, within the outputs).
  *
  * The prologue: RMS norm of every query and key head and the rotation by its position.
  *
@@ -631,7 +632,8 @@ GDN_API gdn_status gdn_attn_append(const void *k, const void *v, const int *cu, 
  * entries behind a sequence's last page are not read, and slots and scales behind its last
  * token may hold anything.  A sequence with no token gives o = 0, lse = -inf.  For GDN_BF16
  * the softmax weights, times the values' scale, are rounded to bf16 for the matrix cores;
- * GDN_F32 rounds nothing to fewer bits.  GDN_ENOTSUP also from N * Hq >= 2^23 on.
+ * GDN_F32 rounds nothing to fewer bits.  GDN_ENOTSUP also from N * Hq >= 2^23 on.  The
+ * workspace (none where width * page <= 1024) is 13 MB at most and four bytes a sequence.
  */
 GDN_API gdn_status gdn_attn_step_workspace_size(int N, int Hq, int Hk, int D, int page, int width, size_t *bytes);
 GDN_API gdn_status gdn_attn_step(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
