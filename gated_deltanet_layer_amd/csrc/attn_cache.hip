@@ -324,7 +324,7 @@ template <typename T, int D, bool CUT> __global__ __launch_bounds__(256, 2) void
     __shared__ float stat[2][4][16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r16 = lane_r16(), gq = lane_gq();
     const int heads = a.Hk * ntile, hr = blockIdx.x % heads, h = hr / ntile, g0 = hr % ntile * 16, Hq = a.Hk * a.G;
-    int n = blockIdx.x / heads, t0 = 0, t1, pieces = 1, place = 0;   // place: among the pieces of cut sequences
+    int n = blockIdx.x / heads, t0 = 0, t1, pieces = 1, place = 0;   // place: of a piece among those of cut sequences
     if constexpr (CUT) {
         const int first = lane < a.N ? step_tiles(a, lane) : 0;   // most calls have no more sequences
         auto tiles = [&](int b) { return b < 64 ? first : step_tiles(a, b); };   // b: a multiple of 64, and the lane
@@ -338,15 +338,25 @@ template <typename T, int D, bool CUT> __global__ __launch_bounds__(256, 2) void
             }
             if (lane == 0) prefix[a.N] = at;
         }
-        const Item it = find_item(a.N, n, [&](int b) { return step_pieces(tiles(b), each); });
+        // item n of the list of pieces, as find_item does; the whole sequences before it have no place
+        Item it = {-1, 0};
+        for (int b = 0, at = 0, wholes = 0; b < a.N; b += 64) {
+            const int mine = b + lane < a.N ? step_pieces(tiles(b + lane), each) : 0, incl = scan_lanes(mine);
+            const int sum = __builtin_amdgcn_readlane(incl, 63);
+            const unsigned long long whole = __ballot(mine == 1);
+            if (n < at + sum) {
+                const int l = (int)__builtin_ctzll(__ballot(n < at + incl));
+                it = {b + l, n - at - __builtin_amdgcn_readlane(incl - mine, l)};
+                place = n - wholes - (int)__builtin_popcountll(whole & ((1ULL << l) - 1));
+                break;
+            }
+            at += sum;
+            wholes += (int)__builtin_popcountll(whole);
+        }
         if (it.b < 0) return;
         n = it.b;
         const int nt = __builtin_amdgcn_readfirstlane(step_tiles(a, n));
         pieces = step_pieces(nt, each);
-        if (pieces > 1) {
-            place = it.i;
-            for (int b = 0; b < n; b += 64) place += sum_lanes(b + lane < n ? step_cuts(tiles(b + lane), each) : 0);
-        }
         const int per = (nt + pieces - 1) / pieces;
         t0 = it.i * per;
         t1 = min(nt, t0 + per);
