@@ -14,7 +14,7 @@
 // cut into pieces; the sums of what is cut a third kernel adds up in order.
 //
 // Seven products for the five of the formulas, bound by the matrix cores: 8192 packed tokens (one
-// sequence of 4999 among seven) of 16 over 4 heads of 128, bf16, take 433 us; in a trace
+// sequence of 4999 among seven) of 16 over 4 heads of 128, bf16, take 432 to 440 us; in a trace
 // dq 191 (0.93 PFLOP/s over its three products), dk and dv 246 (0.96 over four), the sums 16.
 #include "attn.h"
 
